@@ -357,6 +357,132 @@ int sai_topk_transform_noalloc(const float* scores, int64_t rows, int64_t score_
                                int64_t pt_stride, const int32_t* row_to_batch, int32_t page_size, int32_t k,
                                int32_t* out_slots, int32_t* out_indices, sai_stream_t stream);
 
+/*
+ * Paged key/value caches and the attention over them.
+ *
+ * What the indexer's caller does next to the calls above: the step's keys and
+ * values go into a paged cache (sai_append_kv), the attention reads the slots
+ * that the top-k picked (sai_sparse_attention), and layers without the
+ * indexer attend over all keys or a sliding window of them
+ * (sai_paged_attention). Rows, seq_lens, row_to_batch and block_table mean
+ * what they mean for sai_index_score_topk: row i belongs to request
+ * b = row_to_batch ? row_to_batch[i] : i and sits at position seq_lens[i] - 1
+ * of it, token t of request b is cell t % block_size of block
+ * block_table[b*bt_stride + t/block_size], and its slot is
+ * block * block_size + cell. A row with seq_lens[i] = 0 is padding.
+ *
+ * sai_kv_cache describes one layer's cache; the arrays belong to the caller.
+ *
+ * k, v        [num_blocks, heads, block_size, dim], bf16 or e4m3 codes; the
+ *             last axis has unit stride, the strides of the others (in
+ *             elements) are given, so that heads and tokens may be in either
+ *             order and k and v may share one array. 16-byte aligned, every
+ *             stride a multiple of 16 bytes.
+ * k_scale,    fp32 [num_blocks, heads], contiguous: value = code * scale, one
+ * v_scale     scale for each block of tokens and kv head. e4m3 only.
+ * block_size  16, 32, 64 or 128; dim 64 or 128.
+ */
+#define SAI_CACHE_BF16 0
+#define SAI_CACHE_E4M3 1
+
+typedef struct {
+  void* k;
+  void* v;
+  float* k_scale;
+  float* v_scale;
+  int64_t num_blocks;
+  int64_t k_stride[3]; /* between blocks, heads, tokens */
+  int64_t v_stride[3];
+  int32_t heads;
+  int32_t block_size;
+  int32_t dim;
+  int32_t dtype; /* SAI_CACHE_BF16 or SAI_CACHE_E4M3 */
+} sai_kv_cache;
+
+/*
+ * sai_append_kv -- rotate the rows' keys (and queries) by their positions and
+ * write keys and values into the cache.
+ *
+ * With p = seq_lens[i] - 1 and c_j, s_j = cos_sin[p*rot_dim + j],
+ * cos_sin[p*rot_dim + rot_dim/2 + j], each head of k (and of q) becomes, for
+ * the pairs (x1, x2) = (x[j], x[j + rot_dim/2]), or (x[2j], x[2j+1]) when
+ * interleaved, j < rot_dim/2:
+ *   (x1*c_j - x2*s_j, x2*c_j + x1*s_j)
+ * and the dims at rot_dim and above stay. Products and sums are single fp32
+ * operations. A bf16 cache takes the result rounded to nearest.
+ *
+ * An e4m3 cache takes round(x / s) with the block's scale s, a power of two:
+ * need = the least 2^e, e >= -64, with |x| <= 448 * 2^e for every finite x
+ * that the call puts into this block and head; s = need when the call writes
+ * the block's first cell, else max(old scale, need), and then the codes of the
+ * cells before the call's first one are rounded to the new scale (exact
+ * but for values that become subnormal). Infinities saturate, NaN stays NaN.
+ *
+ * k, v        bf16 [rows, heads, dim]; heads and dims contiguous, the stride
+ *             between rows given in elements (a slice of a fused projection).
+ *             16-byte aligned, strides multiples of 8 elements.
+ * q, out_q    bf16 [rows, q_heads, dim] like k, and the rotated queries
+ *             (contiguous; zeros for padding rows), or both NULL.
+ * cos_sin     fp32 [max_pos, rot_dim], 16-byte aligned, or NULL with
+ *             rot_dim = 0: no rotation. rot_dim is a multiple of 16 up to dim.
+ * The rows of one request that meet in one block are neighbours in the order
+ * of their positions, without gaps (a decode row by itself, or a packed
+ * chunk). A row with a length below 0 or above bt_stride*block_size or
+ * (with cos_sin) max_pos, or with a request outside [0, bt_rows), sets status
+ * bit 1 and is skipped; a block id outside [0, num_blocks) sets bit 4 and its
+ * rows are skipped.
+ */
+int sai_append_kv(const sai_kv_cache* cache, const uint16_t* k, int64_t k_row_stride, const uint16_t* v,
+                  int64_t v_row_stride, const uint16_t* q, int64_t q_row_stride, int32_t q_heads, uint16_t* out_q,
+                  const float* cos_sin, int64_t max_pos, int32_t rot_dim, int32_t interleaved,
+                  const int32_t* block_table, int64_t bt_rows, int64_t bt_stride, const int32_t* row_to_batch,
+                  const int32_t* seq_lens, int64_t rows, sai_stream_t stream);
+
+/*
+ * sai_paged_attention -- softmax attention of each row over its request's keys.
+ *
+ * Row i with n = seq_lens[i] sees key t when t < n and (window = 0, or
+ * t >= n - window, or t < sinks). For query head a, which reads kv head
+ * a / (q_heads / heads):
+ *   out[i, a] = sum_t e_t v_t / sum_t e_t,  e_t = exp(sm_scale * q[i, a].k_t)
+ *   out_lse[i, a] = log sum_t e_t
+ * with fp32 sums. A row that sees no key, and a bad row (status bit 1), gets
+ * zeros and -inf. What an unseen cell holds, NaN included, does not matter.
+ * Keys on a block id outside [0, num_blocks) are not seen and set bit 4.
+ *
+ * q           bf16 [rows, q_heads, dim], row stride in elements as above.
+ * max_seq_len host-side bound of seq_lens (longer rows are bad rows).
+ * packed      0: each row by itself (decode; its keys are split over CTAs).
+ *             1: neighbouring rows mostly share a request and have
+ *             neighbouring lengths (prefill): they are taken as tiles, which
+ *             needs row_to_batch. Any rows give right results either way.
+ * out         bf16 [rows, q_heads, dim]; out_lse fp32 [rows, q_heads] or NULL.
+ * workspace   sai_paged_attention_workspace(...) bytes (same arguments, same
+ *             device), 16-byte aligned; NULL when that is 0. Calls that share
+ *             a workspace must not overlap on the GPU.
+ */
+size_t sai_paged_attention_workspace(int64_t rows, int32_t q_heads, int32_t heads, int32_t dim, int32_t dtype,
+                                     int32_t max_seq_len, int32_t window, int32_t sinks, int32_t packed);
+int sai_paged_attention(const uint16_t* q, int64_t q_row_stride, int32_t q_heads, const sai_kv_cache* cache,
+                        const int32_t* block_table, int64_t bt_rows, int64_t bt_stride, const int32_t* row_to_batch,
+                        const int32_t* seq_lens, int64_t rows, int32_t max_seq_len, int32_t window, int32_t sinks,
+                        float sm_scale, int32_t packed, uint16_t* out, float* out_lse, void* workspace,
+                        size_t workspace_bytes, sai_stream_t stream);
+
+/*
+ * sai_sparse_attention -- the same attention over chosen slots: row i sees
+ * the slots[i*slots_stride + j], j < k, that are >= 0 (the out_slots of
+ * sai_topk_transform or sai_index_score_topk with block_size pages; a slot
+ * named twice counts twice). Slots at or above num_blocks*block_size are not
+ * seen and set bit 4. 1 <= k <= 65536.
+ */
+size_t sai_sparse_attention_workspace(int64_t rows, int32_t q_heads, int32_t heads, int32_t dim, int32_t dtype,
+                                      int32_t k);
+int sai_sparse_attention(const uint16_t* q, int64_t q_row_stride, int32_t q_heads, const sai_kv_cache* cache,
+                         const int32_t* slots, int64_t slots_stride, int32_t k, int64_t rows, float sm_scale,
+                         uint16_t* out, float* out_lse, void* workspace, size_t workspace_bytes,
+                         sai_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

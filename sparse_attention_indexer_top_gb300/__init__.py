@@ -15,6 +15,14 @@ from typing import Optional
 import torch
 
 from ._lib import SaiError, check, load, status_string  # noqa: F401
+from .attention import (  # noqa: F401
+    KVCache,
+    append_kv,
+    paged_attention,
+    paged_attention_workspace,
+    sparse_attention,
+    sparse_attention_workspace,
+)
 
 TOPK = 512
 

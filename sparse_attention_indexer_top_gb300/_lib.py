@@ -14,6 +14,17 @@ _c_i32 = ctypes.c_int32
 _c_size = ctypes.c_size_t
 _vp = ctypes.c_void_p
 
+_f32 = ctypes.c_float
+
+
+class KVCacheDesc(ctypes.Structure):
+    """sai_kv_cache of include/sai.h."""
+
+    _fields_ = [("k", _vp), ("v", _vp), ("k_scale", _vp), ("v_scale", _vp), ("num_blocks", _c_i64),
+                ("k_stride", _c_i64 * 3), ("v_stride", _c_i64 * 3), ("heads", _c_i32), ("block_size", _c_i32),
+                ("dim", _c_i32), ("dtype", _c_i32)]
+
+
 # name -> (restype, argtypes); mirrors include/sai.h
 SIGNATURES = {
     "sai_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -48,6 +59,15 @@ SIGNATURES = {
     "sai_topk_transform_noalloc": (ctypes.c_int, [_vp, _c_i64, _c_i64, _vp, _vp, _vp, _c_i64, _c_i64, _vp, _c_i32,
                                                   _c_i32, _vp, _vp, _vp]),
     "sai_sparse_blocks": (ctypes.c_int, [_vp, _c_i64, _c_i32, _c_i32, _vp, _vp, _vp]),
+    "sai_append_kv": (ctypes.c_int, [_vp, _vp, _c_i64, _vp, _c_i64, _vp, _c_i64, _c_i32, _vp, _vp, _c_i64, _c_i32,
+                                     _c_i32, _vp, _c_i64, _c_i64, _vp, _vp, _c_i64, _vp]),
+    "sai_paged_attention_workspace": (_c_size, [_c_i64, _c_i32, _c_i32, _c_i32, _c_i32, _c_i32, _c_i32, _c_i32,
+                                                _c_i32]),
+    "sai_paged_attention": (ctypes.c_int, [_vp, _c_i64, _c_i32, _vp, _vp, _c_i64, _c_i64, _vp, _vp, _c_i64, _c_i32,
+                                           _c_i32, _c_i32, _f32, _c_i32, _vp, _vp, _vp, _c_size, _vp]),
+    "sai_sparse_attention_workspace": (_c_size, [_c_i64, _c_i32, _c_i32, _c_i32, _c_i32, _c_i32]),
+    "sai_sparse_attention": (ctypes.c_int, [_vp, _c_i64, _c_i32, _vp, _vp, _c_i64, _c_i32, _c_i64, _f32, _vp, _vp,
+                                            _vp, _c_size, _vp]),
 }
 
 _lib = None

@@ -19,8 +19,10 @@ int* g_status_ptr[kMaxDevices];
 int g_num_sms[kMaxDevices];
 std::mutex g_mu;
 
+}  // namespace
+
 // Per-device set-up, done once with that device current.
-bool device_setup(int* dev_out, int** status, int* sms) {
+bool sai::device_setup(int* dev_out, int** status, int* sms) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return false;
   std::lock_guard<std::mutex> lock(g_mu);
@@ -38,19 +40,24 @@ bool device_setup(int* dev_out, int** status, int* sms) {
   return true;
 }
 
+namespace {
+
+using sai::cuda_status;
+using sai::device_setup;
+
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 thread_local const char* t_last_error = "";
 thread_local int t_stall_unit = -1;  // test hook, consumed by the thread's next fused top-k call
 
+}  // namespace
+
 // Map a CUDA error to a status, remembering its text for sai_last_error.
-int cuda_status(cudaError_t e) {
+int sai::cuda_status(cudaError_t e) {
   if (e == cudaSuccess) return SAI_OK;
   t_last_error = cudaGetErrorString(e);
   return SAI_ERR_CUDA;
 }
-
-}  // namespace
 
 extern "C" {
 

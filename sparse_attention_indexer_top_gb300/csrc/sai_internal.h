@@ -120,4 +120,74 @@ cudaError_t launch_per_head_expand(const int* seq_lens, const int* row_to_batch,
                                    long long bt_rows, long long bt_stride, int* out_lens, int* out_batch,
                                    cudaStream_t stream);
 
+// Per-device set-up shared by the C-ABI files (sai_api.cu): the current
+// device, its status word and SM count; false when CUDA refuses.
+bool device_setup(int* dev_out, int** status, int* sms);
+// Map a CUDA error to a sai_status, remembering its text for sai_last_error.
+int cuda_status(cudaError_t e);
+
+// ------------------------------------------------- caches and attention
+struct CacheView {
+  char* k;
+  char* v;
+  float* ks;  // [num_blocks, heads] or null (bf16)
+  float* vs;
+  long long num_blocks;
+  long long kst[3], vst[3];  // bytes between blocks, heads, tokens
+  int heads, bs_log2, dim;
+  bool f8;
+};
+
+struct AppendLaunch {
+  CacheView c;
+  const uint16_t* k;
+  const uint16_t* v;
+  const uint16_t* q;  // or null
+  uint16_t* out_q;
+  long long k_row, v_row, q_row;  // elements between rows
+  int q_heads;
+  const float* cos_sin;  // [max_pos, rot] or null
+  long long max_pos;
+  int rot, interleaved;
+  const int* block_table;
+  long long bt_rows, bt_stride;
+  const int* row_to_batch;
+  const int* seq_lens;
+  int rows;
+  int* status;
+};
+cudaError_t launch_append_kv(const AppendLaunch& p, cudaStream_t stream);
+
+// One attention call; the keys of a row are its request's (block_table) or
+// its slots.
+struct AttnLaunch {
+  CacheView c;
+  const uint16_t* q;
+  long long q_row;
+  int q_heads, group;  // group = q_heads / kv heads
+  const int* block_table;
+  long long bt_rows, bt_stride;
+  const int* row_to_batch;
+  const int* seq_lens;
+  int max_len, window, sinks;
+  const int* slots;  // or null
+  long long slots_stride;
+  int slots_k;
+  int rows;
+  float scale_log2;  // sm_scale * log2(e)
+  uint16_t* out;
+  float* lse;
+  int chunks;      // key chunks per row; > 1: partial results
+  float* part_o;   // [rows, q_heads, chunks, dim]
+  float2* part_ml; // [rows, q_heads, chunks]: running maximum (log2 units) and sum
+  int* status;
+};
+// Chunks per row of the row kernel, and its partial results' bytes.
+struct AttnPlan {
+  int chunks;
+  size_t workspace_bytes;
+};
+AttnPlan attn_rows_plan(long long rows, int q_heads, int heads, int dim, bool f8, long long max_keys, int num_sms);
+cudaError_t launch_attn_rows(const AttnLaunch& p, cudaStream_t stream);
+
 }  // namespace sai
