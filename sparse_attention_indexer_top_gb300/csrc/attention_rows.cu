@@ -542,15 +542,18 @@ __global__ void __launch_bounds__(kThreads) attn_rows_kernel(const AttnLaunch p)
 
 // Joins the chunks of each (row, head): one warp each.
 template <int D>
-__global__ void __launch_bounds__(128) attn_join_kernel(const AttnLaunch p) {
+__global__ void __launch_bounds__(128) attn_join_kernel(const AttnLaunch p, bool all_chunks) {
   const long long head = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
   if (head >= static_cast<long long>(p.rows) * p.q_heads) return;
-  RowKeys rk = row_keys(p, static_cast<int>(head / p.q_heads));
-  int used = 0;
-  if (rk.count > 0) {
-    const int per = chunk_keys(rk.count, p.chunks);
-    used = (rk.count + per - 1) / per;
+  int used = p.chunks;
+  if (!all_chunks) {
+    const RowKeys rk = row_keys(p, static_cast<int>(head / p.q_heads));
+    used = 0;
+    if (rk.count > 0) {
+      const int per = chunk_keys(rk.count, p.chunks);
+      used = (rk.count + per - 1) / per;
+    }
   }
   pdl_wait();
   constexpr int V = D / 32;
@@ -637,6 +640,10 @@ cudaError_t launch_attn_rows(const AttnLaunch& p, cudaStream_t stream) {
   else
     e = p.c.f8 ? launch_rows_d<64, true>(p, stream) : launch_rows_d<64, false>(p, stream);
   if (e != cudaSuccess || p.chunks == 1) return e;
+  return launch_attn_join(p, false, stream);
+}
+
+cudaError_t launch_attn_join(const AttnLaunch& p, bool all_chunks, cudaStream_t stream) {
   // the joining kernel starts while the last chunks run, and waits for them
   // before it reads their results
   cudaLaunchConfig_t cfg{};
@@ -648,8 +655,8 @@ cudaError_t launch_attn_rows(const AttnLaunch& p, cudaStream_t stream) {
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return p.c.dim == 128 ? cudaLaunchKernelEx(&cfg, attn_join_kernel<128>, p)
-                        : cudaLaunchKernelEx(&cfg, attn_join_kernel<64>, p);
+  return p.c.dim == 128 ? cudaLaunchKernelEx(&cfg, attn_join_kernel<128>, p, all_chunks)
+                        : cudaLaunchKernelEx(&cfg, attn_join_kernel<64>, p, all_chunks);
 }
 
 }  // namespace sai

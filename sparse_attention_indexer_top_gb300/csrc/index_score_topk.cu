@@ -66,6 +66,7 @@
 
 #include "sai_internal.h"
 #include "sai_ptx.cuh"
+#include "sai_tmap.h"
 #include "sai_select.cuh"
 
 namespace sai {
@@ -860,23 +861,6 @@ __global__ void __launch_bounds__(fused_threads<R>(), (fused_ctas_per_sm<R, BF16
 }
 
 // ---------------------------------------------------------------- host side
-using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-  static EncodeTiledFn fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult q{};
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(f);
-  });
-  return fn;
-}
-
 // 2-D map over [rows, 128] elements (uint8 FP8 codes or bf16) with a box of
 // box_rows rows x 128 bytes (all 128 FP8 dims, or 64 bf16 dims), 128-byte swizzle.
 bool make_map(CUtensorMap* map, const void* base, long long rows, int box_rows, bool bf16) {
