@@ -160,7 +160,7 @@ size_t sai_paged_attention_workspace(int64_t rows, int32_t q_heads, int32_t head
   const long long keys = most_keys(max_seq_len, window, sinks);
   size_t bytes = sai::attn_rows_plan(rows, q_heads, heads, dim, f8, keys, sms).workspace_bytes;
   // enough for either kernel: the tile kernel leaves calls with sm_scale <= 0 to the row kernel
-  if (packed && sai::attn_tiles_apply(q_heads / heads, f8, 1.f))
+  if (packed && sai::attn_tiles_apply(q_heads / heads, 1.f))
     bytes = std::max(bytes, sai::attn_tiles_plan(rows, q_heads, heads, dim, keys, sms).workspace_bytes);
   return bytes;
 }
@@ -196,7 +196,7 @@ int sai_paged_attention(const uint16_t* q, int64_t q_row_stride, int32_t q_heads
   p.scale_log2 = sm_scale * 1.44269504088896340736f;
   p.out = out;
   p.lse = out_lse;
-  const bool tiles = packed && sai::attn_tiles_apply(p.group, p.c.f8, p.scale_log2);
+  const bool tiles = packed && sai::attn_tiles_apply(p.group, p.scale_log2);
   return run_attention(p, tiles, most_keys(max_seq_len, window, sinks), workspace, workspace_bytes, sms, stream);
 }
 

@@ -19,13 +19,24 @@
 // CTA complete in order, so a tile's S(j+1) being there means its PV(j) is
 // too, and O may be rescaled without another wait.
 //
-// Roles (12 warps): 0-3 softmax of tile A, 4-7 softmax of tile B, 8 TMA, 9
-// MMA, 10-11 make the value tile safe to multiply: a weight of 0 times a
-// NaN or infinity that a row must not see would still be NaN, so in tiles that
-// some row sees only in part, rows of V past the request's end become 0, and
-// rows with a non-finite value too; if such a row of V is seen by some query
-// row, its share is added at the end from global memory.
+// Roles (bf16 cache, 12 warps): 0-3 softmax of tile A, 4-7 softmax of tile B,
+// 8 TMA, 9 MMA, 10-11 "prep", which makes the value tile safe to multiply: a
+// weight of 0 times a NaN or infinity that a row must not see would still be
+// NaN, so in tiles that some row sees only in part, rows of V past the
+// request's end become 0, and rows with a non-finite value too; if such a row
+// of V is seen by some query row, its share is added at the end from
+// global memory.
+//
+// e4m3 cache (16 warps): the products run in f16, which holds e4m3 codes
+// exactly; 12-15 are the prep warps and turn the codes of each K and V tile
+// into halves in the MMA's layout (one conversion for two tiles of rows). The
+// queries are brought to [2^14, 2^15) by a power of two for each (row, head)
+// and stored as halves. The block scales stay out of the tiles: a key scale is
+// part of the softmax's multiplier, and with w_t = 2^(s_t - m) * vscale_t, taken
+// as one exponent s_t + log2(vscale_t) - m with m the maximum of s + log2
+// vscale, weights are at most 2^8 whatever the scales; l adds w_t / vscale_t.
 #include <cuda.h>
+#include <cuda_fp16.h>
 
 #include <algorithm>
 #include <climits>
@@ -43,10 +54,16 @@ constexpr int kMaxRows = 256;    // query rows of a CTA (group 1)
 constexpr int kSoftmaxWarps = 8;
 constexpr int kTmaWarp = 8;
 constexpr int kMmaWarp = 9;
-constexpr int kPrepWarp = 10;
-constexpr int kPrepWarps = 2;
-constexpr int kThreads = (kPrepWarp + kPrepWarps) * 32;
-constexpr int kStages = 2;       // K and V tiles in flight each
+template <bool F8>
+struct Roles {
+  static constexpr int kPrepWarp = F8 ? 12 : 10;
+  static constexpr int kPrepWarps = F8 ? 4 : 2;
+  static constexpr int kThreads = (kPrepWarp + kPrepWarps) * 32;
+  // K and V tiles of the MMA: two each by TMA, or one each of halves, fed from
+  // a ring of five code tiles that K and V take in turn
+  static constexpr int kStages = F8 ? 1 : 2;
+  static constexpr int kRaw = F8 ? 5 : 0;
+};
 constexpr float kLn2 = 0.69314718055994530942f;
 
 // TMEM columns: S (and P over it) of tiles A and B, then their O.
@@ -58,15 +75,19 @@ struct TilesLaunch {
   int row_tiles;      // CTAs along the rows
 };
 
-template <int D>
+template <int D, bool F8>
 struct Shared {
   static constexpr int kSlabs = D / 64;
   static constexpr int kTileBytes = kSlabs * kTile * 128;
+  static constexpr int kStages = Roles<F8>::kStages, kRaw = Roles<F8>::kRaw;
   unsigned char q[2][kTileBytes];
   unsigned char k[kStages][kTileBytes];
   unsigned char v[kStages][kTileBytes];
-  uint64_t q_full, k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages], v_safe[kStages];
-  uint64_t s_ready[2], p_ready[2], o_done[2];
+  unsigned char raw[kRaw ? kRaw : 1][kRaw ? kTile * D : 16];
+  // full: TMA (bf16) or prep (e4m3) has filled it; v_safe: prep is done with it
+  uint64_t q_full, q_ready, k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages], v_safe[kStages];
+  uint64_t raw_full[kRaw ? kRaw : 1], raw_empty[kRaw ? kRaw : 1];
+  uint64_t s_ready[2], p_ready[2][2], o_done[2];  // p_ready: first and second half of the keys
   uint32_t tmem;
   int nonfinite;  // number of the last pass (from 1) that met a non-finite value row
   int segs;
@@ -96,8 +117,8 @@ struct Pass {
   }
 };
 
-template <int D>
-__device__ __forceinline__ Pass get_pass(const Shared<D>& S, const TilesLaunch& L, int seg, int chunk) {
+template <int D, bool F8>
+__device__ __forceinline__ Pass get_pass(const Shared<D, F8>& S, const TilesLaunch& L, int seg, int chunk) {
   const AttnLaunch& p = L.a;
   Pass r;
   r.s = S.seg_start[seg];
@@ -134,12 +155,29 @@ __device__ __forceinline__ void tma_3d(void* dst, const void* map, int c0, int c
       "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar))
       : "memory");
 }
-// D[tmem] (+)= A[tmem] x B[smem], 16-bit A packed two to a column.
-__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+// Shared-memory matrix descriptors of 128-byte swizzled tiles (rows of 128
+// bytes in atoms of 8 rows, 1024 bytes apart). Low word: start address and
+// "leading" offset (N-major tiles: bytes between 64-dim slabs); the high word is
+// the same for all: stride offset 1024, version 1, 128-byte swizzle.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_lo(uint32_t smem_addr, uint32_t leading) {
+  return ((smem_addr & 0x3FFFFu) >> 4) | ((leading >> 4) << 16);
+}
+// D[tmem] (+)= A[smem] x B[smem], 16-bit types.
+__device__ __forceinline__ void umma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tmov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %5};\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d),
+      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate), "r"(kDescHi)
+      : "memory");
+}
+// D[tmem] (+)= A[tmem] x B[smem], 16-bit A packed two to a column.
+__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tmov.b64 b, {%2, %5};\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b_lo), "r"(idesc), "r"(accumulate), "r"(kDescHi)
       : "memory");
 }
 __device__ __forceinline__ void tmem_ld32(uint32_t a, uint32_t* r) {
@@ -152,14 +190,12 @@ __device__ __forceinline__ void tmem_ld32(uint32_t a, uint32_t* r) {
         "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(a));
 }
-__device__ __forceinline__ void tmem_st32(uint32_t a, const uint32_t* r) {
+__device__ __forceinline__ void tmem_st16(uint32_t a, const uint32_t* r) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(a),
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16};" ::"r"(a),
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
@@ -172,18 +208,6 @@ __device__ __forceinline__ void tmem_ld_wait32(uint32_t* r) {
                  "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]),
                  "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
                  "+r"(r[30]), "+r"(r[31])::"memory");
-}
-// Shared-memory descriptor of a [keys x dim] tile used with dim as its outer
-// (N) axis: rows of 64 dims in 128-byte swizzled atoms of 8 keys, atoms 1024
-// bytes apart along the keys, 64-dim slabs `slab` bytes apart.
-__device__ __forceinline__ uint64_t umma_desc_sw128_mnmajor(uint32_t smem_addr, uint32_t slab) {
-  uint64_t d = 0;
-  d |= static_cast<uint64_t>((smem_addr & 0x3FFFFu) >> 4);
-  d |= static_cast<uint64_t>(slab >> 4) << 16;
-  d |= static_cast<uint64_t>(1024 >> 4) << 32;
-  d |= static_cast<uint64_t>(1) << 46;
-  d |= static_cast<uint64_t>(2) << 61;
-  return d;
 }
 constexpr uint32_t kTransposeB = 1u << 16;  // instruction descriptor: B is N-major
 
@@ -222,6 +246,25 @@ __device__ __forceinline__ bool nonfinite2(uint32_t x) {
   return (x & 0x7f80u) == 0x7f80u || (x & 0x7f800000u) == 0x7f800000u;
 }
 
+// log2 of a block scale: the exponent exactly, so powers of two are exact
+// (scales below 2^-100 count as 2^-100).
+__device__ __forceinline__ float log2_scale(float s) {
+  s = fmaxf(s, 7.888609052210118e-31f);
+  const uint32_t u = __float_as_uint(s);
+  return static_cast<float>(static_cast<int>(u >> 23) - 127) + log2f(__uint_as_float((u & 0x7fffffu) | 0x3f800000u));
+}
+// Two e4m3 codes of each 16-bit half to halves, exactly.
+__device__ __forceinline__ void e4m3x4_f16x4(uint32_t c, uint32_t& a, uint32_t& b) {
+  asm("{\n\t.reg .b16 x, y;\n\tmov.b32 {x, y}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, x;\n\tcvt.rn.f16x2.e4m3x2 %1, y;\n\t}"
+      : "=r"(a), "=r"(b)
+      : "r"(c));
+}
+__device__ __forceinline__ uint32_t pack_f16(float a, float b) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+  return r;
+}
+
 // ------------------------------------------------------------------ softmax
 // Thread of one (row, head) pair.
 struct Lane {
@@ -231,11 +274,24 @@ struct Lane {
   bool live;       // belongs to the pass
 };
 
-// Adds to o[] the values that were kept out of the product for being
-// non-finite: every such key of the tiles that were checked.
-template <int D>
+// Two values of a cache row: bf16 pair d, or e4m3 codes 2d and 2d + 1.
+template <bool F8>
+__device__ __forceinline__ float2 values2(const char* row, int d) {
+  if (F8) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(reinterpret_cast<const uint16_t*>(row)[d]));
+    return __half22float2(*reinterpret_cast<__half2*>(&r));
+  }
+  const uint32_t x = reinterpret_cast<const uint32_t*>(row)[d];
+  return make_float2(bf16_lo(x), bf16_hi(x));
+}
+
+// Adds to o[], 32 columns of O from column c0, the values that were kept out
+// of the product for being non-finite: every such key of the tiles that were
+// checked.
+template <int D, bool F8>
 __device__ __noinline__ void add_nonfinite(const AttnLaunch& p, const Pass& ps, int kvh, const Lane& ln, float m,
-                                           float (&o)[D]) {
+                                           int c0, float (&o)[32]) {
   const int lane = threadIdx.x & 31;
   const uint16_t* q = p.q + static_cast<long long>(ln.row) * p.q_row +
                       (ln.head - static_cast<long long>(ln.row) * p.q_heads) * D;
@@ -246,57 +302,101 @@ __device__ __noinline__ void add_nonfinite(const AttnLaunch& p, const Pass& ps, 
       const int blk = p.block_table[ps.batch * p.bt_stride + (t >> p.c.bs_log2)];
       if (blk < 0 || blk >= p.c.num_blocks) continue;
       const long long off = t & ((1 << p.c.bs_log2) - 1);
-      const uint32_t* v = reinterpret_cast<const uint32_t*>(p.c.v + blk * p.c.vst[0] + kvh * p.c.vst[1] + off * p.c.vst[2]);
-      const uint32_t* k = reinterpret_cast<const uint32_t*>(p.c.k + blk * p.c.kst[0] + kvh * p.c.kst[1] + off * p.c.kst[2]);
+      const char* v = p.c.v + blk * p.c.vst[0] + kvh * p.c.vst[1] + off * p.c.vst[2];
+      const char* k = p.c.k + blk * p.c.kst[0] + kvh * p.c.kst[1] + off * p.c.kst[2];
       bool bad = false;
-      for (int d = lane; d < D / 2; d += 32) bad = bad || nonfinite2(v[d]);
+      for (int d = lane; d < D / 2; d += 32) {
+        const float2 x = values2<F8>(v, d);
+        bad = bad || !(fabsf(x.x) <= 3.402823466e38f) || !(fabsf(x.y) <= 3.402823466e38f);
+      }
       if (!__any_sync(0xffffffffu, bad)) continue;
       if (!ln.live || t >= ln.n || (t < ln.first && t >= ln.sinks)) continue;
       float s = 0.f;
       for (int d = 0; d < D / 2; ++d) {
-        const uint32_t a = reinterpret_cast<const uint32_t*>(q)[d], b = k[d];
-        s = fmaf(bf16_lo(a), bf16_lo(b), fmaf(bf16_hi(a), bf16_hi(b), s));
+        const uint32_t a = reinterpret_cast<const uint32_t*>(q)[d];
+        const float2 b = values2<F8>(k, d);
+        s = fmaf(bf16_lo(a), b.x, fmaf(bf16_hi(a), b.y, s));
       }
-      const float w = ex2(s * p.scale_log2 - (m == -INFINITY ? 0.f : m));
+      float e = s * p.scale_log2, vl = 0.f;
+      if (F8) {
+        const long long at = static_cast<long long>(blk) * p.c.heads + kvh;
+        e *= p.c.ks[at];
+        vl = log2_scale(p.c.vs[at]);
+      }
+      const float w = ex2(e + vl - (m == -INFINITY ? 0.f : m));
 #pragma unroll
-      for (int d = 0; d < D / 2; ++d) {
-        const uint32_t x = v[d];
-        o[2 * d] = fmaf(w, bf16_lo(x), o[2 * d]);
-        o[2 * d + 1] = fmaf(w, bf16_hi(x), o[2 * d + 1]);
+      for (int d = 0; d < 16; ++d) {
+        const float2 x = values2<F8>(v, c0 / 2 + d);
+        o[2 * d] = fmaf(w, x.x, o[2 * d]);
+        o[2 * d + 1] = fmaf(w, x.y, o[2 * d + 1]);
       }
     }
   }
 }
 
+// 32 columns of the thread's row, from column c0; an unseen row's O may hold anything.
 template <int D>
-__device__ __forceinline__ void write_rows(const AttnLaunch& p, const Lane& ln, int chunk, float m, float l,
-                                           float (&o)[D]) {
+__device__ __forceinline__ void write_columns(const AttnLaunch& p, const Lane& ln, int chunk, float l, int c0,
+                                              const float (&o)[32]) {
   if (!ln.live) return;
+  const bool none = l == 0.f;
   if (p.chunks > 1) {
-    float4* dst = reinterpret_cast<float4*>(p.part_o + (ln.head * p.chunks + chunk) * D);
+    float4* dst = reinterpret_cast<float4*>(p.part_o + (ln.head * p.chunks + chunk) * D + c0);
 #pragma unroll
-    for (int d = 0; d < D / 4; ++d)
-      dst[d] = l == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)
-                        : make_float4(o[4 * d], o[4 * d + 1], o[4 * d + 2], o[4 * d + 3]);
-    p.part_ml[ln.head * p.chunks + chunk] = make_float2(m, l);
+    for (int d = 0; d < 8; ++d)
+      dst[d] = none ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(o[4 * d], o[4 * d + 1], o[4 * d + 2], o[4 * d + 3]);
     return;
   }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  uint4* dst = reinterpret_cast<uint4*>(p.out + ln.head * D);
+  const float inv = none ? 0.f : 1.f / l;
+  uint4* dst = reinterpret_cast<uint4*>(p.out + ln.head * D + c0);
 #pragma unroll
-  for (int d = 0; d < D / 8; ++d) {
+  for (int d = 0; d < 4; ++d) {
     uint4 x;
     x.x = pack_bf16(o[8 * d] * inv, o[8 * d + 1] * inv);
     x.y = pack_bf16(o[8 * d + 2] * inv, o[8 * d + 3] * inv);
     x.z = pack_bf16(o[8 * d + 4] * inv, o[8 * d + 5] * inv);
     x.w = pack_bf16(o[8 * d + 6] * inv, o[8 * d + 7] * inv);
-    dst[d] = l == 0.f ? make_uint4(0, 0, 0, 0) : x;  // an unseen row's O may hold anything
+    dst[d] = none ? make_uint4(0, 0, 0, 0) : x;
   }
-  if (p.lse) p.lse[ln.head] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+}
+__device__ __forceinline__ void write_sums(const AttnLaunch& p, const Lane& ln, int chunk, float m, float l) {
+  if (!ln.live) return;
+  if (p.chunks > 1)
+    p.part_ml[ln.head * p.chunks + chunk] = make_float2(m, l);
+  else if (p.lse)
+    p.lse[ln.head] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
+// Brings this thread's row of the query tile from bf16 to halves, times a
+// power of two that puts its largest magnitude into [2^14, 2^15); returns the
+// factor's inverse. Values down to 2^-28 of the largest are exact, the rest
+// off by at most 2^-39 of it.
 template <int D>
-__device__ __forceinline__ bool softmax_role(Shared<D>& S, const TilesLaunch& L, int x, int kvh, int chunk, int row0) {
+__device__ __forceinline__ float query_to_f16(unsigned char* tile, int r) {
+  float amax = 0.f;
+#pragma unroll
+  for (int c = 0; c < D / 8; ++c) {
+    const uint4 x = *reinterpret_cast<const uint4*>(tile + (c / 8) * kTile * 128 + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(w[e])), fabsf(bf16_hi(w[e]))));
+  }
+  const int e = static_cast<int>(__float_as_uint(amax) >> 23);
+  const int up = (e == 0 || e == 255) ? 0 : max(-100, min(100, 14 - (e - 127)));
+  const float f = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
+#pragma unroll
+  for (int c = 0; c < D / 8; ++c) {
+    uint4* at = reinterpret_cast<uint4*>(tile + (c / 8) * kTile * 128 + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+    const uint4 x = *at;
+    *at = make_uint4(pack_f16(bf16_lo(x.x) * f, bf16_hi(x.x) * f), pack_f16(bf16_lo(x.y) * f, bf16_hi(x.y) * f),
+                     pack_f16(bf16_lo(x.z) * f, bf16_hi(x.z) * f), pack_f16(bf16_lo(x.w) * f, bf16_hi(x.w) * f));
+  }
+  return __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
+}
+
+template <int D, bool F8>
+__device__ __forceinline__ bool softmax_role(Shared<D, F8>& S, const TilesLaunch& L, int x, int kvh, int chunk,
+                                             int row0) {
   const AttnLaunch& p = L.a;
   const int lane = threadIdx.x & 31, quad = (threadIdx.x >> 5) & 3;
   const int r = quad * 32 + lane;  // the thread's TMEM lane
@@ -306,7 +406,14 @@ __device__ __forceinline__ bool softmax_role(Shared<D>& S, const TilesLaunch& L,
   const int local = x * L.rows_per_tile + r / p.group;
   const bool in_tile = r < L.rows_per_tile * p.group;
   int tiles_done = 0, passes_done = 0;
-  const uint64_t scale2 = pair(p.scale_log2, p.scale_log2);
+  float scale = p.scale_log2;
+  if (F8) {
+    const bool ok = mbar_wait(&S.q_full, 0);
+    if (!__all_sync(0xffffffffu, ok)) return false;
+    scale *= query_to_f16<D>(S.q[x], r);
+    fence_proxy_async_smem();
+    mbar_arrive(&S.q_ready);
+  }
 
   for (int seg = 0; seg < S.segs; ++seg) {
     const Pass ps = get_pass(S, L, seg, chunk);
@@ -320,121 +427,192 @@ __device__ __forceinline__ bool softmax_role(Shared<D>& S, const TilesLaunch& L,
     ln.head = static_cast<long long>(ln.row) * p.q_heads + kvh * p.group + r % p.group;
     float m = -INFINITY, l = 0.f;
     if (ps.i0 == ps.i1) {
-      float o[D];
-#pragma unroll
-      for (int d = 0; d < D; ++d) o[d] = 0.f;
-      write_rows<D>(p, ln, chunk, m, l, o);
+      const float o[32] = {};
+#pragma unroll 1
+      for (int c = 0; c < D; c += 32) write_columns<D>(p, ln, chunk, l, c, o);
+      write_sums(p, ln, chunk, m, l);
       continue;
     }
-    // block ids of the tile's eight 16-key groups, read one tile ahead
-    auto blocks_bad = [&](int i) -> bool {
-      if (i >= ps.i1 || lane >= 8) return false;
+    // lanes 0-7: block of the tile's 16-key group (-1: none, -2: bad), read
+    // two tiles ahead, and its scales, read one ahead
+    auto block_of = [&](int i) -> int {
+      if (i >= ps.i1 || lane >= 8) return -1;
       const int t = ps.tile0(i) + 16 * lane;
-      if (t >= ps.most) return false;
+      if (t >= ps.most) return -1;
       const int blk = p.block_table[ps.batch * p.bt_stride + (t >> p.c.bs_log2)];
-      return blk < 0 || blk >= p.c.num_blocks;
+      return blk < 0 || blk >= p.c.num_blocks ? -2 : blk;
     };
-    bool bad_next = blocks_bad(ps.i0);
+    auto scales_of = [&](int blk) -> float2 {
+      if (!F8 || blk < 0) return make_float2(1.f, 1.f);
+      const long long at = static_cast<long long>(blk) * p.c.heads + kvh;
+      return make_float2(p.c.ks[at], p.c.vs[at]);
+    };
+    int blk1 = block_of(ps.i0), blk2 = block_of(ps.i0 + 1);
+    float2 sc1 = scales_of(blk1);
     for (int i = ps.i0; i < ps.i1; ++i) {
-      const uint32_t bad = __ballot_sync(0xffffffffu, bad_next);
-      bad_next = blocks_bad(i + 1);
+      const uint32_t bad = __ballot_sync(0xffffffffu, blk1 == -2);
+      float ks_l = sc1.x, vl_l = 0.f, vi_l = 1.f;
+      if (F8) {
+        vl_l = log2_scale(sc1.y);
+        vi_l = 1.f / fmaxf(sc1.y, 7.888609052210118e-31f);
+        sc1 = scales_of(blk2);
+      }
+      blk1 = blk2;
+      blk2 = block_of(i + 2);
       const bool ok = mbar_wait(&S.s_ready[x], tiles_done & 1);
       if (!__all_sync(0xffffffffu, ok)) return false;
       ++tiles_done;
       tc_fence_after();
-      uint32_t s[kTile];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_ld32(ts + 32 * c, s + 32 * c);
-#pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_ld_wait32(s + 32 * c);
       const int t0 = ps.tile0(i);
       const bool whole = t0 + kTile <= ln.n && (t0 >= ln.first || t0 + kTile <= ln.sinks);
-      if (!__all_sync(0xffffffffu, whole) || bad) {
-        const int hi = ln.n - t0, lo = ln.first - t0, sk = ln.sinks - t0;
+      const bool masked = !__all_sync(0xffffffffu, whole) || bad;
+      if (bad && lane == 0) atomicOr(p.status, kDevBadPage);
+      // scores of columns [c0, c0 + 32) that the row does not see become -inf
+      auto mask = [&](uint32_t* s, int c0) {
+        const int hi = ln.n - t0 - c0, lo = ln.first - t0 - c0, sk = ln.sinks - t0 - c0;
+        const uint32_t dead = bad >> (c0 / 16);
 #pragma unroll
-        for (int c = 0; c < kTile; ++c) {
-          const bool see = c < hi && (c >= lo || c < sk) && !((bad >> (c / 16)) & 1);
+        for (int c = 0; c < 32; ++c) {
+          const bool see = c < hi && (c >= lo || c < sk) && !((dead >> (c / 16)) & 1);
           if (!see) s[c] = 0xff800000u;
         }
-        if (bad && lane == 0) atomicOr(p.status, kDevBadPage);
+      };
+      // largest exponent of 32 columns
+      auto largest = [&](const uint32_t* s, int c0, float top) {
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          float a = __uint_as_float(s[16 * g]), b = __uint_as_float(s[16 * g + 1]);
+          a = fmaxf(a, __uint_as_float(s[16 * g + 2]));
+          b = fmaxf(b, __uint_as_float(s[16 * g + 3]));
+#pragma unroll
+          for (int e = 4; e < 16; e += 4) {
+            a = fmaxf(fmaxf(a, __uint_as_float(s[16 * g + e])), __uint_as_float(s[16 * g + e + 1]));
+            b = fmaxf(fmaxf(b, __uint_as_float(s[16 * g + e + 2])), __uint_as_float(s[16 * g + e + 3]));
+          }
+          const float k = F8 ? scale * __shfl_sync(0xffffffffu, ks_l, c0 / 16 + g) : scale;
+          const float v = F8 ? __shfl_sync(0xffffffffu, vl_l, c0 / 16 + g) : 0.f;
+          top = fmaxf(top, fmaf(fmaxf(a, b), k, v));
+        }
+        return top;
+      };
+      // The first 64 columns stay in registers; the others are read for the
+      // maximum and read again for their weights, which keeps the row's
+      // registers at half of S.
+      uint32_t s[64], u[32];
+      tmem_ld32(ts, s);
+      tmem_ld32(ts + 32, s + 32);
+      tmem_ld32(ts + 64, u);
+      tmem_ld_wait32(s);
+      tmem_ld_wait32(s + 32);
+      tmem_ld_wait32(u);
+      if (masked) mask(u, 64);
+      float top = largest(u, 64, -INFINITY);
+      tmem_ld32(ts + 96, u);
+      if (masked) {
+        mask(s, 0);
+        mask(s + 32, 32);
       }
-      float mx[4];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) mx[c] = __uint_as_float(s[c]);
-#pragma unroll
-      for (int c = 4; c < kTile; c += 8)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          mx[e] = fmaxf(mx[e], c + 4 + e < kTile ? fmaxf(__uint_as_float(s[c + e]), __uint_as_float(s[c + 4 + e]))
-                                                 : __uint_as_float(s[c + e]));
-      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
+      top = largest(s, 0, top);
+      top = largest(s + 32, 32, top);
+      tmem_ld_wait32(u);
+      if (masked) mask(u, 96);
+      top = largest(u, 96, top);
       // the maximum moves only when it is passed by more than 2^8: weights up
-      // to 256 are as exact in bf16 as weights up to 1, and O is rarely rescaled
+      // to 256 are as exact in 16 bits as weights up to 1, and O is rarely
+      // rescaled
       const bool up = top > m + 8.f;
       if (__any_sync(0xffffffffu, up)) {
         const float f = up ? (m == -INFINITY ? 0.f : ex2(m - top)) : 1.f;
         if (up) m = top;
         l *= f;
         if (i > ps.i0) {
-#pragma unroll
+#pragma unroll 1
           for (int c = 0; c < D; c += 32) {
-            uint32_t o[32];
-            tmem_ld32(to + c, o);
-            tmem_ld_wait32(o);
+            tmem_ld32(to + c, u);
+            tmem_ld_wait32(u);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-            tmem_st32(to + c, o);
+            for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(__uint_as_float(u[e]) * f);
+            tmem_st16(to + c, u);
+            tmem_st16(to + c + 16, u + 16);
           }
         }
       }
       const float base = m == -INFINITY ? 0.f : m;
-      const uint64_t base2 = pair(-base, -base);
-      uint64_t sum[2] = {pair(l, 0.f), pair(0.f, 0.f)};
+      // weights of 32 columns, 16 bits each (relative error 2^-9, f16 2^-12;
+      // under the output's own), over the scores' TMEM columns
+      auto weights = [&](uint32_t* s, int c0) {
+        uint64_t sum[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
+        uint64_t scale2 = pair(scale, scale), base2 = pair(-base, -base);
+        float a, b;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-#pragma unroll
-        for (int c = 0; c < 64; c += 2) {
-          float a, b;
-          unpair(fma2(pair(__uint_as_float(s[64 * h + c]), __uint_as_float(s[64 * h + c + 1])), scale2, base2), a, b);
+        for (int c = 0; c < 32; c += 2) {
+          if (F8 && c % 16 == 0) {
+            const int g = (c0 + c) / 16;
+            const float k = scale * __shfl_sync(0xffffffffu, ks_l, g), v = __shfl_sync(0xffffffffu, vl_l, g) - base;
+            scale2 = pair(k, k);
+            base2 = pair(v, v);
+          }
+          unpair(fma2(pair(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), scale2, base2), a, b);
           a = ex2(a);
           b = ex2(b);
           sum[(c >> 1) & 1] = add2(sum[(c >> 1) & 1], pair(a, b));
-          // weights in bf16 (relative error 2^-9, under the output's own)
-          s[32 * h + c / 2] = pack_bf16(a, b);
+          s[c / 2] = F8 ? pack_f16(a, b) : pack_bf16(a, b);
+          if (c % 16 == 14 && (F8 || c == 30)) {
+            unpair(add2(sum[0], sum[1]), a, b);
+            l = F8 ? fmaf(a + b, __shfl_sync(0xffffffffu, vi_l, (c0 + c) / 16), l) : l + (a + b);
+            sum[0] = sum[1] = pair(0.f, 0.f);
+          }
         }
-        tmem_st32(ts + 32 * h, s + 32 * h);
-      }
-      float a, b;
-      unpair(add2(sum[0], sum[1]), a, b);
-      l = a + b;
+        tmem_st16(ts + c0 / 2, s);
+      };
+      tmem_ld32(ts + 64, u);
+      weights(s, 0);
+      weights(s + 32, 32);
       tmem_st_wait();
       tc_fence_before();
-      mbar_arrive(&S.p_ready[x]);
+      mbar_arrive(&S.p_ready[x][0]);
+      tmem_ld_wait32(u);
+      tmem_ld32(ts + 96, s);
+      if (masked) mask(u, 64);
+      weights(u, 64);
+      tmem_ld_wait32(s);
+      if (masked) mask(s, 96);
+      weights(s, 96);
+      tmem_st_wait();
+      tc_fence_before();
+      mbar_arrive(&S.p_ready[x][1]);
     }
     const bool ok = mbar_wait(&S.o_done[x], passes_done & 1);
     if (!__all_sync(0xffffffffu, ok)) return false;
     ++passes_done;
     tc_fence_after();
-    float o[D];
+    const bool extra = *reinterpret_cast<volatile int*>(&S.nonfinite) == seg + 1;
+#pragma unroll 1
+    for (int c = 0; c < D; c += 32) {
+      uint32_t u[32];
+      tmem_ld32(to + c, u);
+      tmem_ld_wait32(u);
+      float o[32];
 #pragma unroll
-    for (int c = 0; c < D; c += 32) tmem_ld32(to + c, reinterpret_cast<uint32_t*>(o) + c);
-#pragma unroll
-    for (int c = 0; c < D; c += 32) tmem_ld_wait32(reinterpret_cast<uint32_t*>(o) + c);
+      for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(u[e]);
+      if (extra) add_nonfinite<D, F8>(p, get_pass(S, L, seg, chunk), kvh, ln, m, c, o);
+      write_columns<D>(p, ln, chunk, l, c, o);
+    }
     tc_fence_before();
-    if (*reinterpret_cast<volatile int*>(&S.nonfinite) == seg + 1) add_nonfinite<D>(p, ps, kvh, ln, m, o);
-    write_rows<D>(p, ln, chunk, m, l, o);
+    write_sums(p, ln, chunk, m, l);
   }
   return true;
 }
 
 // ---------------------------------------------------------------------- TMA
-template <int D>
-__device__ __forceinline__ bool tma_role(Shared<D>& S, const TilesLaunch& L, const CUtensorMap* qmap,
+template <int D, bool F8>
+__device__ __forceinline__ bool tma_role(Shared<D, F8>& S, const TilesLaunch& L, const CUtensorMap* qmap,
                                          const CUtensorMap* kmap, const CUtensorMap* vmap, int kvh, int chunk,
                                          int row0) {
   const AttnLaunch& p = L.a;
   const int lane = threadIdx.x & 31;
   constexpr int kSlabs = D / 64;
+  constexpr int kStages = Shared<D, F8>::kStages, kRaw = Shared<D, F8>::kRaw;
   if (lane == 0) {
     mbar_arrive_expect_tx(&S.q_full, 2 * kSlabs * L.rows_per_tile * p.group * 128);
     for (int x = 0; x < 2; ++x)
@@ -451,26 +629,43 @@ __device__ __forceinline__ bool tma_role(Shared<D>& S, const TilesLaunch& L, con
       const int t = ps.tile0(i) + lane * bs;
       if (t >= ps.most) return -1;
       const int blk = p.block_table[ps.batch * p.bt_stride + (t >> p.c.bs_log2)];
-      return blk >= p.c.num_blocks ? -1 : blk;
+      // a bad block is read as the one past the end, which the copy fills with zeros
+      return blk < 0 || blk >= p.c.num_blocks ? static_cast<int>(p.c.num_blocks) : blk;
     };
     int next = block_of(ps.i0);
     for (int i = ps.i0; i < ps.i1; ++i, ++done) {
       const int blk = next;
       next = block_of(i + 1);
-      const int st = done % kStages;
-      const uint32_t ph = ((done / kStages) & 1) ^ 1;
-      const int bytes = __popc(__ballot_sync(0xffffffffu, blk >= 0)) * bs * 128 * kSlabs;
+      const int count = __popc(__ballot_sync(0xffffffffu, blk >= 0));
 #pragma unroll
       for (int kv = 0; kv < 2; ++kv) {
-        const bool ok = mbar_wait(kv ? &S.v_empty[st] : &S.k_empty[st], ph);
+        uint64_t *empty, *full;
+        unsigned char* dst;
+        uint32_t ph;
+        if (F8) {
+          const int idx = 2 * done + kv, st = idx % (kRaw ? kRaw : 1);
+          empty = &S.raw_empty[st];
+          full = &S.raw_full[st];
+          dst = S.raw[st] + lane * bs * D;
+          ph = (idx / (kRaw ? kRaw : 1)) & 1;
+        } else {
+          const int st = done % kStages;
+          empty = kv ? &S.v_empty[st] : &S.k_empty[st];
+          full = kv ? &S.v_full[st] : &S.k_full[st];
+          dst = (kv ? S.v[st] : S.k[st]) + lane * bs * 128;
+          ph = (done / kStages) & 1;
+        }
+        const bool ok = mbar_wait(empty, ph ^ 1);
         if (!__all_sync(0xffffffffu, ok)) return false;
-        uint64_t* full = kv ? &S.v_full[st] : &S.k_full[st];
-        if (lane == 0) mbar_arrive_expect_tx(full, bytes);
+        if (lane == 0) mbar_arrive_expect_tx(full, count * bs * D * (F8 ? 1 : 2));
         __syncwarp();
         if (blk >= 0) {
-          unsigned char* dst = (kv ? S.v[st] : S.k[st]) + lane * bs * 128;
+          if (F8) {
+            tma_4d(dst, kv ? vmap : kmap, 0, 0, kvh, blk, full);
+          } else {
 #pragma unroll
-          for (int c = 0; c < kSlabs; ++c) tma_4d(dst + c * kTile * 128, kv ? vmap : kmap, 64 * c, 0, kvh, blk, full);
+            for (int c = 0; c < kSlabs; ++c) tma_4d(dst + c * kTile * 128, kv ? vmap : kmap, 64 * c, 0, kvh, blk, full);
+          }
         }
       }
     }
@@ -479,28 +674,38 @@ __device__ __forceinline__ bool tma_role(Shared<D>& S, const TilesLaunch& L, con
 }
 
 // ---------------------------------------------------------------------- MMA
-template <int D>
-__device__ __forceinline__ bool mma_role(Shared<D>& S, const TilesLaunch& L, int chunk) {
-  constexpr uint32_t kIdescQk = umma_idesc_bf16(kTile, kTile);
-  constexpr uint32_t kIdescPv = umma_idesc_bf16(kTile, D) | kTransposeB;
+template <int D, bool F8>
+__device__ __forceinline__ bool mma_role(Shared<D, F8>& S, const TilesLaunch& L, int chunk) {
+  constexpr int kStages = Shared<D, F8>::kStages;
+  constexpr uint32_t kF16 = F8 ? (1u << 7) | (1u << 10) : 0u;  // format fields: 1 bf16, 0 f16
+  constexpr uint32_t kIdescQk = umma_idesc_bf16(kTile, kTile) ^ kF16;
+  constexpr uint32_t kIdescPv = (umma_idesc_bf16(kTile, D) ^ kF16) | kTransposeB;
   constexpr uint32_t kSlab = kTile * 128;
   const uint32_t tmem = S.tmem;
+  // first words of the descriptors; kept opaque, so that each step's is one
+  // addition and not a register of its own through the loop
+  uint32_t q_lo = desc_lo(smem_u32(S.q[0]), 16), k_lo = desc_lo(smem_u32(S.k[0]), 16),
+           v_lo = desc_lo(smem_u32(S.v[0]), kSlab);
+  constexpr uint32_t kTileLo = Shared<D, F8>::kTileBytes >> 4;
   auto qk = [&](int x, int st) {
+    asm volatile("" : "+r"(q_lo), "+r"(k_lo));
+    const uint32_t a = q_lo + x * kTileLo, b = k_lo + st * kTileLo;
 #pragma unroll
     for (int s = 0; s < D / 16; ++s) {
-      const uint32_t off = (s / 4) * kSlab + (s % 4) * 32;
-      umma_bf16(tmem + kColS + 128 * x, umma_desc_sw128_kmajor(smem_u32(S.q[x]) + off),
-                umma_desc_sw128_kmajor(smem_u32(S.k[st]) + off), kIdescQk, s > 0);
+      const uint32_t off = ((s / 4) * kSlab + (s % 4) * 32) >> 4;
+      umma_ss(tmem + kColS + 128 * x, a + off, b + off, kIdescQk, s > 0);
     }
     umma_commit(&S.s_ready[x]);
   };
-  auto pv = [&](int x, int st, bool first) {
+  auto pv = [&](int x, int st, int half, bool first) {
+    asm volatile("" : "+r"(v_lo));
+    const uint32_t b = v_lo + st * kTileLo;
 #pragma unroll
-    for (int s = 0; s < kTile / 16; ++s)
-      umma_ts(tmem + kColO + 128 * x, tmem + kColS + 128 * x + 8 * s,
-              umma_desc_sw128_mnmajor(smem_u32(S.v[st]) + s * 2048, kSlab), kIdescPv, !(first && s == 0));
+    for (int s = 4 * half; s < 4 * half + 4; ++s)
+      umma_ts(tmem + kColO + 128 * x, tmem + kColS + 128 * x + 8 * s, b + ((s * 2048) >> 4), kIdescPv,
+              !(first && s == 0));
   };
-  if (!mbar_wait(&S.q_full, 0)) return false;
+  if (!mbar_wait(F8 ? &S.q_ready : &S.q_full, 0)) return false;
   int done = 0, p_done[2] = {0, 0};
   for (int seg = 0; seg < S.segs; ++seg) {
     const Pass ps = get_pass(S, L, seg, chunk);
@@ -515,21 +720,27 @@ __device__ __forceinline__ bool mma_role(Shared<D>& S, const TilesLaunch& L, int
     for (int i = 0; i < n; ++i, ++done) {
       const int st = done % kStages, nst = (done + 1) % kStages;
       const bool more = i + 1 < n;
-      if (more && !mbar_wait(&S.k_full[nst], ((done + 1) / kStages) & 1)) return false;
+      bool k_there = false;
       if (!mbar_wait(&S.v_safe[st], (done / kStages) & 1)) return false;
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         if (!ps.act[x]) continue;
-        if (!mbar_wait(&S.p_ready[x], p_done[x] & 1)) return false;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          if (!mbar_wait(&S.p_ready[x][half], p_done[x] & 1)) return false;
+          tc_fence_after();
+          pv(x, st, half, i == 0);
+        }
         ++p_done[x];
-        tc_fence_after();
-        pv(x, st, i == 0);
-        if (more)
+        if (x == 1 || !ps.act[1]) umma_commit(&S.v_empty[st]);
+        if (more) {
+          if (!k_there && !mbar_wait(&S.k_full[nst], ((done + 1) / kStages) & 1)) return false;
+          k_there = true;
+          tc_fence_after();
           qk(x, nst);
-        else
+        } else
           umma_commit(&S.o_done[x]);
       }
-      umma_commit(&S.v_empty[st]);
       if (more) umma_commit(&S.k_empty[nst]);
     }
   }
@@ -538,9 +749,10 @@ __device__ __forceinline__ bool mma_role(Shared<D>& S, const TilesLaunch& L, int
 
 // --------------------------------------------------------------------- prep
 template <int D>
-__device__ __forceinline__ bool prep_role(Shared<D>& S, const TilesLaunch& L, int chunk) {
+__device__ __forceinline__ bool prep_role(Shared<D, false>& S, const TilesLaunch& L, int chunk) {
   const AttnLaunch& p = L.a;
-  const int tid = threadIdx.x - kPrepWarp * 32;
+  constexpr int kStages = Roles<false>::kStages, kPrepWarps = Roles<false>::kPrepWarps;
+  const int tid = threadIdx.x - Roles<false>::kPrepWarp * 32;
   int done = 0;
   for (int seg = 0; seg < S.segs; ++seg) {
     const Pass ps = get_pass(S, L, seg, chunk);
@@ -589,12 +801,82 @@ __device__ __forceinline__ bool prep_role(Shared<D>& S, const TilesLaunch& L, in
   return true;
 }
 
+// e4m3: codes of the ring to halves in the MMA's layout (128-byte swizzled
+// rows of 64 dims), K and V in turn. Lanes of one key row read its 16-byte
+// pieces; a piece becomes two 16-byte chunks, written in an order that keeps
+// the eight lanes of a store on different banks.
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1)
+__device__ __forceinline__ bool prep_role(Shared<D, true>& S, const TilesLaunch& L, int chunk) {
+  const AttnLaunch& p = L.a;
+  constexpr int kRaw = Roles<true>::kRaw, kThreadsHere = Roles<true>::kPrepWarps * 32;
+  constexpr int kPieces = D / 16;  // 16-code pieces of a key row
+  const int tid = threadIdx.x - Roles<true>::kPrepWarp * 32;
+  const int piece = tid % kPieces;
+  int done = 0;
+  for (int seg = 0; seg < S.segs; ++seg) {
+    const Pass ps = get_pass(S, L, seg, chunk);
+    for (int i = ps.i0; i < ps.i1; ++i, ++done) {
+      const int t0 = ps.tile0(i);
+      const bool check = ps.partial(t0, p);
+#pragma unroll
+      for (int kv = 0; kv < 2; ++kv) {
+        const int idx = 2 * done + kv, st = idx % kRaw;
+        bool ok = mbar_wait(&S.raw_full[st], (idx / kRaw) & 1);
+        uint4 x[kTile * kPieces / kThreadsHere];
+        if (ok) {
+#pragma unroll
+          for (int j = 0; j < kTile * kPieces / kThreadsHere; ++j)
+            x[j] = *reinterpret_cast<const uint4*>(S.raw[st] + (j * kThreadsHere + tid) * 16);
+          ok = mbar_wait(kv ? &S.v_empty[0] : &S.k_empty[0], (done & 1) ^ 1);
+        }
+        if (!__all_sync(0xffffffffu, ok)) return false;
+        if ((threadIdx.x & 31) == 0) mbar_arrive(&S.raw_empty[st]);  // every lane has its pieces
+        unsigned char* out = (kv ? S.v[0] : S.k[0]) + (piece / 4) * kTile * 128;
+#pragma unroll
+        for (int j = 0; j < kTile * kPieces / kThreadsHere; ++j) {
+          const int key = (j * kThreadsHere + tid) / kPieces;
+          if (kv && check) {
+            const uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
+            bool nan = false;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const uint32_t y = (w[e] & 0x7f7f7f7fu) ^ 0x7f7f7f7fu;  // a zero byte: NaN
+              nan = nan || (((y - 0x01010101u) & ~y & 0x80808080u) != 0u);
+            }
+            bool zero = t0 + key >= ps.most;
+            const uint32_t b = __ballot_sync(0xffffffffu, nan && !zero);
+            if ((b >> ((threadIdx.x & 31) / kPieces * kPieces)) & ((1u << kPieces) - 1u)) {
+              zero = true;
+              *reinterpret_cast<volatile int*>(&S.nonfinite) = seg + 1;
+            }
+            if (zero) x[j] = make_uint4(0, 0, 0, 0);
+          }
+          uint4 a, b;
+          e4m3x4_f16x4(x[j].x, a.x, a.y);
+          e4m3x4_f16x4(x[j].y, a.z, a.w);
+          e4m3x4_f16x4(x[j].z, b.x, b.y);
+          e4m3x4_f16x4(x[j].w, b.z, b.w);
+          const int odd = D == 128 ? piece >> 2 : 0;  // dims above 64 write their second chunk first
+          const int c0 = 2 * (piece & 3) + odd;
+          *reinterpret_cast<uint4*>(out + key * 128 + ((c0 ^ (key & 7)) << 4)) = odd ? b : a;
+          *reinterpret_cast<uint4*>(out + key * 128 + (((c0 ^ 1) ^ (key & 7)) << 4)) = odd ? a : b;
+        }
+        fence_proxy_async_smem();  // the MMA reads these stores through the async proxy
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) mbar_arrive(kv ? &S.v_safe[0] : &S.k_full[0]);
+      }
+    }
+  }
+  return true;
+}
+
+template <int D, bool F8>
+__global__ void __launch_bounds__(Roles<F8>::kThreads, 1)
     attn_tiles_kernel(const __grid_constant__ TilesLaunch L, const __grid_constant__ CUtensorMap qmap,
                       const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
   extern __shared__ unsigned char raw[];
-  Shared<D>& S = *reinterpret_cast<Shared<D>*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  using Sh = Shared<D, F8>;
+  Sh& S = *reinterpret_cast<Sh*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const AttnLaunch& p = L.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   int u = blockIdx.x;
@@ -608,16 +890,22 @@ __global__ void __launch_bounds__(kThreads, 1)
   // ---- set-up: barriers, TMEM, the rows' lengths and the runs of one request
   if (tid == 0) {
     mbar_init(&S.q_full, 1);
-    for (int i = 0; i < kStages; ++i) {
-      mbar_init(&S.k_full[i], 1);
+    mbar_init(&S.q_ready, kSoftmaxWarps * 32);
+    for (int i = 0; i < Sh::kStages; ++i) {
+      mbar_init(&S.k_full[i], F8 ? Roles<F8>::kPrepWarps : 1);
       mbar_init(&S.k_empty[i], 1);
       mbar_init(&S.v_full[i], 1);
       mbar_init(&S.v_empty[i], 1);
-      mbar_init(&S.v_safe[i], kPrepWarps);
+      mbar_init(&S.v_safe[i], Roles<F8>::kPrepWarps);
+    }
+    for (int i = 0; i < Sh::kRaw; ++i) {
+      mbar_init(&S.raw_full[i], 1);
+      mbar_init(&S.raw_empty[i], Roles<F8>::kPrepWarps);
     }
     for (int x = 0; x < 2; ++x) {
       mbar_init(&S.s_ready[x], 1);
-      mbar_init(&S.p_ready[x], 128);
+      mbar_init(&S.p_ready[x][0], 128);
+      mbar_init(&S.p_ready[x][1], 128);
       mbar_init(&S.o_done[x], 1);
     }
     S.nonfinite = 0;
@@ -679,19 +967,29 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
 
   bool ok = true;
-  // registers: 168 a thread at launch; the softmax warps hold a row of S (128)
-  // and take 216, the others give up the difference (2 * 216 + 72 = 3 * 168)
-  if (warp < kSoftmaxWarps)
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
-  else
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+  // the softmax warps hold a row of S (128 registers); the others give up what
+  // they take beyond the launch's share: 2 * 200 + 104 = 3 * 168 (12 warps),
+  // 2 * 160 + 88 + 104 = 4 * 128 (16 warps)
   if (warp < kSoftmaxWarps) {
-    ok = softmax_role<D>(S, L, warp >> 2, kvh, chunk, row0);
-  } else if (warp == kTmaWarp) {
-    ok = tma_role<D>(S, L, &qmap, &kmap, &vmap, kvh, chunk, row0);
-  } else if (warp == kMmaWarp) {
-    if (lane == 0) ok = mma_role<D>(S, L, chunk);
+    if (F8)
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
+    else
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+    ok = softmax_role<D, F8>(S, L, warp >> 2, kvh, chunk, row0);
+  } else if (warp < 12) {
+    if (F8)
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    else
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+    if (warp == kTmaWarp) {
+      ok = tma_role<D, F8>(S, L, &qmap, &kmap, &vmap, kvh, chunk, row0);
+    } else if (warp == kMmaWarp) {
+      if (lane == 0) ok = mma_role<D, F8>(S, L, chunk);
+    } else if (!F8) {
+      ok = prep_role<D>(S, L, chunk);
+    }
   } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
     ok = prep_role<D>(S, L, chunk);
   }
   if (!ok) atomicOr(p.status, kDevWaitTimeout);
@@ -705,8 +1003,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (p.chunks > 1) pdl_trigger();
 }
 
-// 4-D map of a cache: (dim, token, head, block), boxes of 64 dims of one
-// block's tokens, 128-byte swizzle.
+// 4-D map of a cache: (dim, token, head, block), boxes of one block's tokens.
 bool cache_map(CUtensorMap* map, const void* base, const CacheView& c, const long long* st) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return false;
@@ -715,10 +1012,12 @@ bool cache_map(CUtensorMap* map, const void* base, const CacheView& c, const lon
                               static_cast<cuuint64_t>(c.num_blocks)};
   const cuuint64_t strides[3] = {static_cast<cuuint64_t>(st[2]), static_cast<cuuint64_t>(st[1]),
                                  static_cast<cuuint64_t>(st[0])};
-  const cuuint32_t box[4] = {64, bs, 1, 1};
+  // bf16: 64-dim slabs in the MMA's layout; codes: plain rows for the prep warps
+  const cuuint32_t box[4] = {c.f8 ? static_cast<cuuint32_t>(c.dim) : 64, bs, 1, 1};
   const cuuint32_t one[4] = {1, 1, 1, 1};
-  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, one,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+  return fn(map, c.f8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base),
+            dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            c.f8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -737,7 +1036,7 @@ bool query_map(CUtensorMap* map, const AttnLaunch& p, int rows_per_tile) {
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D>
+template <int D, bool F8>
 cudaError_t launch_tiles_t(const AttnLaunch& p, cudaStream_t stream) {
   TilesLaunch L{p, kTile / p.group, 0};
   L.row_tiles = (p.rows + 2 * L.rows_per_tile - 1) / (2 * L.rows_per_tile);
@@ -745,25 +1044,26 @@ cudaError_t launch_tiles_t(const AttnLaunch& p, cudaStream_t stream) {
   if (!query_map(&qmap, p, L.rows_per_tile) || !cache_map(&kmap, p.c.k, p.c, p.c.kst) ||
       !cache_map(&vmap, p.c.v, p.c, p.c.vst))
     return cudaErrorInvalidValue;
-  constexpr size_t smem = sizeof(Shared<D>) + 1024;
+  static_assert(sizeof(Shared<D, F8>) + 1024 <= 227 * 1024, "shared memory of a CTA");
+  constexpr size_t smem = sizeof(Shared<D, F8>) + 1024;
   static bool attr_done[64];
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev >= 64 || !attr_done[dev]) {
-    cudaError_t e = cudaFuncSetAttribute(attn_tiles_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    cudaError_t e = cudaFuncSetAttribute(attn_tiles_kernel<D, F8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          static_cast<int>(smem));
     if (e != cudaSuccess) return e;
     if (dev < 64) attr_done[dev] = true;
   }
   const long long grid = static_cast<long long>(L.row_tiles) * p.c.heads * p.chunks;
   if (grid > INT_MAX) return cudaErrorInvalidConfiguration;
-  attn_tiles_kernel<D><<<static_cast<unsigned>(grid), kThreads, smem, stream>>>(L, qmap, kmap, vmap);
+  attn_tiles_kernel<D, F8><<<static_cast<unsigned>(grid), Roles<F8>::kThreads, smem, stream>>>(L, qmap, kmap, vmap);
   return cudaGetLastError();
 }
 
 }  // namespace
 
-bool attn_tiles_apply(int group, bool f8, float scale_log2) { return group <= kTile && !f8 && scale_log2 > 0.f; }
+bool attn_tiles_apply(int group, float scale_log2) { return group <= kTile && scale_log2 > 0.f; }
 
 AttnPlan attn_tiles_plan(long long rows, int q_heads, int heads, int dim, long long max_keys, int num_sms) {
   const int per = kTile / (q_heads / heads);
@@ -788,7 +1088,11 @@ AttnPlan attn_tiles_plan(long long rows, int q_heads, int heads, int dim, long l
 }
 
 cudaError_t launch_attn_tiles(const AttnLaunch& p, cudaStream_t stream) {
-  const cudaError_t e = p.c.dim == 128 ? launch_tiles_t<128>(p, stream) : launch_tiles_t<64>(p, stream);
+  cudaError_t e;
+  if (p.c.dim == 128)
+    e = p.c.f8 ? launch_tiles_t<128, true>(p, stream) : launch_tiles_t<128, false>(p, stream);
+  else
+    e = p.c.f8 ? launch_tiles_t<64, true>(p, stream) : launch_tiles_t<64, false>(p, stream);
   if (e != cudaSuccess || p.chunks == 1) return e;
   return launch_attn_join(p, true, stream);
 }

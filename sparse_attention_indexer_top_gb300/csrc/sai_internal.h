@@ -193,7 +193,7 @@ cudaError_t launch_attn_rows(const AttnLaunch& p, cudaStream_t stream);
 // for every row (else those that hold keys of the row).
 cudaError_t launch_attn_join(const AttnLaunch& p, bool all_chunks, cudaStream_t stream);
 // The tile kernel of packed rows: whether it takes a call, its chunks, and its launch.
-bool attn_tiles_apply(int group, bool f8, float scale_log2);
+bool attn_tiles_apply(int group, float scale_log2);
 AttnPlan attn_tiles_plan(long long rows, int q_heads, int heads, int dim, long long max_keys, int num_sms);
 cudaError_t launch_attn_tiles(const AttnLaunch& p, cudaStream_t stream);
 
