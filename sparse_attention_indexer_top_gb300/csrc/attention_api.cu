@@ -93,6 +93,7 @@ int run_attention(sai::AttnLaunch& p, bool tiles, long long max_keys, void* work
   if (plan.workspace_bytes && (!workspace || workspace_bytes < plan.workspace_bytes || !aligned(workspace, 16)))
     return SAI_ERR_WORKSPACE;
   p.chunks = plan.chunks;
+  p.own = plan.own;
   if (plan.chunks > 1) {
     p.part_o = static_cast<float*>(workspace);
     p.part_ml = reinterpret_cast<float2*>(p.part_o + static_cast<size_t>(p.rows) * p.q_heads * plan.chunks * p.c.dim);

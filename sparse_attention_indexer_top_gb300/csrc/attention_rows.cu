@@ -142,7 +142,9 @@ __device__ __forceinline__ float join_factor(float2 ml, float base) {
   return ml.y != ml.y ? ml.y : (ml.x == -INFINITY ? 0.f : ex2(ml.x - base));
 }
 
-template <int D, bool F8, int MT>
+// OWN: each team has a unit (row, kv head, head group) of its own; else the
+// teams of a CTA share one unit's keys and join at the end.
+template <int D, bool F8, int MT, bool OWN>
 __global__ void __launch_bounds__(kThreads) attn_rows_kernel(const AttnLaunch p) {
   constexpr int E = F8 ? 1 : 2;
   constexpr int RB = D * E;         // bytes of a key row
@@ -160,18 +162,28 @@ __global__ void __launch_bounds__(kThreads) attn_rows_kernel(const AttnLaunch p)
   const int g = lane >> 2, t = lane & 3;
 
   const int hg_count = (p.group + 16 * MT - 1) / (16 * MT);
-  long long u = blockIdx.x;
-  const int chunk = static_cast<int>(u % p.chunks);
-  u /= p.chunks;
-  const int hg = static_cast<int>(u % hg_count);
-  u /= hg_count;
-  const int kvh = static_cast<int>(u % p.c.heads);
-  const int row = static_cast<int>(u / p.c.heads);
+  int chunk = 0, hg, kvh, row;
+  if (OWN) {
+    // kv head by kv head, so that the rows at work share one head's keys in L2
+    const long long u = static_cast<long long>(blockIdx.x) * TEAMS + team;
+    if (u >= static_cast<long long>(p.rows) * p.c.heads * hg_count) return;
+    hg = static_cast<int>(u % hg_count);
+    row = static_cast<int>(u / hg_count % p.rows);
+    kvh = static_cast<int>(u / hg_count / p.rows);
+  } else {
+    long long u = blockIdx.x;
+    chunk = static_cast<int>(u % p.chunks);
+    u /= p.chunks;
+    hg = static_cast<int>(u % hg_count);
+    u /= hg_count;
+    kvh = static_cast<int>(u % p.c.heads);
+    row = static_cast<int>(u / p.c.heads);
+  }
 
   RowKeys rk = row_keys(p, row);
   if (rk.count < 0) {
     rk.count = 0;
-    if (threadIdx.x == 0) atomicOr(p.status, kDevBadRowMeta);
+    if (lane == 0) atomicOr(p.status, kDevBadRowMeta);
   }
   int k_begin = 0, k_end = rk.count;
   if (p.chunks > 1) {
@@ -250,13 +262,15 @@ __global__ void __launch_bounds__(kThreads) attn_rows_kernel(const AttnLaunch p)
   const char* vbase = p.c.v + kvh * p.c.vst[1];
   const long long slot_limit = p.c.num_blocks << p.c.bs_log2;
   const int bs_mask = (1 << p.c.bs_log2) - 1;
+  constexpr int STEP = OWN ? 1 : TEAMS;  // a team's stages are STEP apart
+  const int first = OWN ? 0 : team;
   const int stages = (k_end - k_begin + SK - 1) / SK;
-  const int my_stages = stages > team ? (stages - team + TEAMS - 1) / TEAMS : 0;
+  const int my_stages = stages > first ? (stages - first + STEP - 1) / STEP : 0;
   bool bad_slot = false;
 
   // slot of this lane's key (lane & 15) in the team's stage s, -1: none
   auto slot_of = [&](int s) -> int {
-    const int j = k_begin + (team + s * TEAMS) * SK + mt * 16 + (lane & 15);
+    const int j = k_begin + (first + s * STEP) * SK + mt * 16 + (lane & 15);
     if (s >= my_stages || j >= k_end) return -1;
     long long slot;
     if (p.slots) {
@@ -475,13 +489,22 @@ __global__ void __launch_bounds__(kThreads) attn_rows_kernel(const AttnLaunch p)
   l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
   l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
 
-  // ---- join the teams' results (same head tile mt, different keys)
-  __syncthreads();  // the rings are done with; their memory holds the partial results
+  // ---- join the teams' results (same head tile mt, different keys); with
+  // OWN the same way through the team's own ring, for whole-line stores
+  constexpr int JOIN = OWN ? 1 : TEAMS;
+  auto part_sync = [&]() {
+    if (OWN)
+      team_sync();
+    else
+      __syncthreads();
+  };
+  part_sync();  // the ring is done with; its memory holds the partial results
   constexpr int OS = D + 4;  // floats between rows
-  float* po = reinterpret_cast<float*>(smem);                    // [kWarps][16][OS]
-  float2* pml = reinterpret_cast<float2*>(po + kWarps * 16 * OS);  // [kWarps][16]
+  float* po = reinterpret_cast<float*>(OWN ? ring : smem);          // [JOIN * MT][16][OS]
+  float2* pml = reinterpret_cast<float2*>(po + JOIN * MT * 16 * OS);  // [JOIN * MT][16]
   {
-    float* w = po + warp * 16 * OS;
+    const int slot = OWN ? mt : warp;
+    float* w = po + slot * 16 * OS;
 #pragma unroll
     for (int s = 0; s < NS; ++s) {
       if (!F8) {
@@ -498,25 +521,25 @@ __global__ void __launch_bounds__(kThreads) attn_rows_kernel(const AttnLaunch p)
       }
     }
     if (t == 0) {
-      pml[warp * 16 + g] = make_float2(m0, l0);
-      pml[warp * 16 + g + 8] = make_float2(m1, l1);
+      pml[slot * 16 + g] = make_float2(m0, l0);
+      pml[slot * 16 + g + 8] = make_float2(m1, l1);
     }
   }
-  __syncthreads();
+  part_sync();
   constexpr int LPR = D / 4;  // lanes of four dims to a head row
-  for (int i = threadIdx.x; i < 16 * MT * LPR; i += kThreads) {
+  for (int i = OWN ? mt * 32 + lane : threadIdx.x; i < min(16 * MT, p.group - hg * 16 * MT) * LPR;
+       i += OWN ? 32 * MT : kThreads) {
     const int hr = i / LPR, d = (i % LPR) * 4;
     const int tile = hr / 16, r = hr % 16;
     const int hin = hg * 16 * MT + hr;
-    if (hin >= p.group) continue;
     float m = -INFINITY;
 #pragma unroll
-    for (int k = 0; k < TEAMS; ++k) m = fmaxf(m, pml[(k * MT + tile) * 16 + r].x);
+    for (int k = 0; k < JOIN; ++k) m = fmaxf(m, pml[(k * MT + tile) * 16 + r].x);
     const float base = m == -INFINITY ? 0.f : m;
     float l = 0.f;
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-    for (int k = 0; k < TEAMS; ++k) {
+    for (int k = 0; k < JOIN; ++k) {
       const float2 ml = pml[(k * MT + tile) * 16 + r];
       const float f = join_factor(ml, base);
       const float4 x = *reinterpret_cast<const float4*>(po + ((k * MT + tile) * 16 + r) * OS + d);
@@ -594,29 +617,35 @@ constexpr size_t rows_smem() {
   return ring > join ? ring : join;
 }
 
-template <int D, bool F8, int MT>
+template <int D, bool F8, int MT, bool OWN>
 cudaError_t launch_rows_t(const AttnLaunch& p, cudaStream_t stream) {
   constexpr size_t smem = rows_smem<D, F8, MT>();
   static bool attr_done[64];
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev >= 64 || !attr_done[dev]) {
-    cudaError_t e = cudaFuncSetAttribute(attn_rows_kernel<D, F8, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    cudaError_t e = cudaFuncSetAttribute(attn_rows_kernel<D, F8, MT, OWN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          static_cast<int>(smem));
     if (e != cudaSuccess) return e;
     if (dev < 64) attr_done[dev] = true;
   }
   const long long groups = (p.group + 16 * MT - 1) / (16 * MT);
-  const long long grid = static_cast<long long>(p.rows) * p.c.heads * groups * p.chunks;
-  attn_rows_kernel<D, F8, MT><<<static_cast<unsigned>(grid), kThreads, smem, stream>>>(p);
+  long long grid = static_cast<long long>(p.rows) * p.c.heads * groups * p.chunks;
+  if (OWN) grid = (grid * MT + kWarps - 1) / kWarps;
+  attn_rows_kernel<D, F8, MT, OWN><<<static_cast<unsigned>(grid), kThreads, smem, stream>>>(p);
   return cudaGetLastError();
+}
+
+template <int D, bool F8, int MT>
+cudaError_t launch_rows_m(const AttnLaunch& p, cudaStream_t stream) {
+  return p.own ? launch_rows_t<D, F8, MT, true>(p, stream) : launch_rows_t<D, F8, MT, false>(p, stream);
 }
 
 template <int D, bool F8>
 cudaError_t launch_rows_d(const AttnLaunch& p, cudaStream_t stream) {
-  if (p.group <= 16) return launch_rows_t<D, F8, 1>(p, stream);
-  if (p.group <= 32) return launch_rows_t<D, F8, 2>(p, stream);
-  return launch_rows_t<D, F8, 4>(p, stream);
+  if (p.group <= 16) return launch_rows_m<D, F8, 1>(p, stream);
+  if (p.group <= 32) return launch_rows_m<D, F8, 2>(p, stream);
+  return launch_rows_m<D, F8, 4>(p, stream);
 }
 
 }  // namespace
@@ -627,7 +656,10 @@ AttnPlan attn_rows_plan(long long rows, int q_heads, int heads, int dim, bool f8
   const long long target = 12LL * num_sms;  // about four waves of three CTAs per SM
   long long chunks = units > 0 ? (target + units - 1) / units : 1;
   chunks = std::max<long long>(1, std::min<long long>({chunks, 64LL, (max_keys + 127) / 128}));
-  AttnPlan pl{static_cast<int>(chunks), 0};
+  AttnPlan pl{static_cast<int>(chunks), 0, false};
+  // enough units for every team to have its own: no joining
+  const int teams = group <= 16 ? 4 : group <= 32 ? 2 : 1;
+  pl.own = chunks == 1 && units >= 4LL * num_sms * teams;
   if (chunks > 1)
     pl.workspace_bytes = static_cast<size_t>(rows) * q_heads * chunks * (static_cast<size_t>(dim) * 4 + 8);
   return pl;

@@ -1071,7 +1071,7 @@ AttnPlan attn_tiles_plan(long long rows, int q_heads, int heads, int dim, long l
   const long long tiles = std::max<long long>(1, (max_keys + kTile - 1) / kTile);
   // cost in tile steps: waves of CTAs, each its share of the tiles and about
   // four steps of start and end, and the partial results' traffic
-  AttnPlan pl{1, 0};
+  AttnPlan pl{1, 0, false};
   double best = 1e300;
   for (long long c = 1; c <= std::min<long long>(tiles, 32); ++c) {
     const double waves = static_cast<double>((units * c + num_sms - 1) / num_sms);

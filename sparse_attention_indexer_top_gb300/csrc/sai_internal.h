@@ -178,6 +178,7 @@ struct AttnLaunch {
   uint16_t* out;
   float* lse;
   int chunks;      // key chunks per row; > 1: partial results
+  bool own;        // row kernel: see AttnPlan
   float* part_o;   // [rows, q_heads, chunks, dim]
   float2* part_ml; // [rows, q_heads, chunks]: running maximum (log2 units) and sum
   int* status;
@@ -186,6 +187,7 @@ struct AttnLaunch {
 struct AttnPlan {
   int chunks;
   size_t workspace_bytes;
+  bool own;  // row kernel: a unit for each team of warps instead of each CTA
 };
 AttnPlan attn_rows_plan(long long rows, int q_heads, int heads, int dim, bool f8, long long max_keys, int num_sms);
 cudaError_t launch_attn_rows(const AttnLaunch& p, cudaStream_t stream);
