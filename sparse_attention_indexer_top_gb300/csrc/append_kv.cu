@@ -136,47 +136,63 @@ __device__ __forceinline__ void rotate(float (&a)[8], float (&b)[8], const Angle
 }
 
 // ------------------------------------------------------------- row CTAs
-// One row: its query heads, and with a bf16 cache its keys and values.
-__device__ void row_cta(const AppendLaunch& p, int row) {
+// `rows` neighbouring rows: their query heads, and with a bf16 cache their
+// keys and values. A thread stays with one row and one place in the heads, so
+// it loads its angles once; four heads' loads are in flight at a time.
+__device__ void row_cta(const AppendLaunch& p, int row0, int rows) {
   const int lph = p.c.dim / 16;  // lanes to a head
-  const int l = threadIdx.x % lph, first = threadIdx.x / lph, step = kThreads / lph;
-  const RowPlace r = row_place(p, row, threadIdx.x == 0);
+  const int slots = kThreads / lph / rows;  // heads of a row at once
+  const int l = threadIdx.x % lph, slot = threadIdx.x / lph;
+  const int row = row0 + slot / slots;
+  if (row >= p.rows || slot >= slots * rows) return;
+  const RowPlace r = row_place(p, row, l == 0 && slot % slots == 0);
   const Chunks ch = chunks_of(l, p.rot, p.c.dim);
   const bool turn = ch.rotated && r.pos >= 0;
   Angles ang;
   if (turn) load_angles(p, r.pos, ch, ang);
   const int kv = p.c.f8 ? 0 : p.c.heads;
   const int off = r.pos & ((1 << p.c.bs_log2) - 1);
-  for (int h = first; h < p.q_heads + 2 * kv; h += step) {
-    const bool is_q = h < p.q_heads;
-    const bool is_k = !is_q && h < p.q_heads + kv;
-    const int hh = is_q ? h : (is_k ? h - p.q_heads : h - p.q_heads - kv);
-    const uint16_t* src;
-    char* dst;
-    if (is_q) {
-      src = p.q + row * p.q_row + static_cast<long long>(hh) * p.c.dim;
-      dst = reinterpret_cast<char*>(p.out_q + (static_cast<long long>(row) * p.q_heads + hh) * p.c.dim);
-    } else {
-      if (r.pos < 0) continue;
-      src = (is_k ? p.k + row * p.k_row : p.v + row * p.v_row) + static_cast<long long>(hh) * p.c.dim;
-      const long long* st = is_k ? p.c.kst : p.c.vst;
-      dst = (is_k ? p.c.k : p.c.v) + r.blk * st[0] + hh * st[1] + off * st[2];
-    }
-    uint4 xa = make_uint4(0, 0, 0, 0), xb = xa;
-    if (r.pos >= 0) {
-      xa = __ldg(reinterpret_cast<const uint4*>(src) + ch.a);
-      xb = __ldg(reinterpret_cast<const uint4*>(src) + ch.b);
-      if (turn && (is_q || is_k)) {
-        float a[8], b[8];
-        unpack8(xa, a);
-        unpack8(xb, b);
-        rotate(a, b, ang, p.interleaved);
-        xa = pack8(a);
-        xb = pack8(b);
+  const int all = p.q_heads + 2 * kv;
+  constexpr int kAhead = 4;
+  for (int h0 = slot % slots; h0 < all; h0 += kAhead * slots) {
+    uint4 xa[kAhead], xb[kAhead];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      const int h = h0 + j * slots;
+      xa[j] = xb[j] = make_uint4(0, 0, 0, 0);
+      if (h < all && r.pos >= 0) {
+        const uint16_t* src = h < p.q_heads        ? p.q + row * p.q_row + static_cast<long long>(h) * p.c.dim
+                              : h < p.q_heads + kv ? p.k + row * p.k_row + static_cast<long long>(h - p.q_heads) * p.c.dim
+                                                   : p.v + row * p.v_row +
+                                                         static_cast<long long>(h - p.q_heads - kv) * p.c.dim;
+        xa[j] = __ldg(reinterpret_cast<const uint4*>(src) + ch.a);
+        xb[j] = __ldg(reinterpret_cast<const uint4*>(src) + ch.b);
       }
     }
-    reinterpret_cast<uint4*>(dst)[ch.a] = xa;
-    reinterpret_cast<uint4*>(dst)[ch.b] = xb;
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      const int h = h0 + j * slots;
+      if (h >= all) break;
+      const bool is_q = h < p.q_heads, is_v = h >= p.q_heads + kv;
+      if (!is_q && r.pos < 0) continue;
+      if (turn && !is_v) {
+        float a[8], b[8];
+        unpack8(xa[j], a);
+        unpack8(xb[j], b);
+        rotate(a, b, ang, p.interleaved);
+        xa[j] = pack8(a);
+        xb[j] = pack8(b);
+      }
+      char* dst;
+      if (is_q) {
+        dst = reinterpret_cast<char*>(p.out_q + (static_cast<long long>(row) * p.q_heads + h) * p.c.dim);
+      } else {
+        const long long* st = is_v ? p.c.vst : p.c.kst;
+        dst = (is_v ? p.c.v : p.c.k) + r.blk * st[0] + (h - p.q_heads - (is_v ? kv : 0)) * st[1] + off * st[2];
+      }
+      reinterpret_cast<uint4*>(dst)[ch.a] = xa[j];
+      reinterpret_cast<uint4*>(dst)[ch.b] = xb[j];
+    }
   }
 }
 
@@ -348,12 +364,14 @@ __device__ void block_cta(const AppendLaunch& p, int r0, int window, int h) {
 }
 
 template <int TPT>
-__global__ void __launch_bounds__(kThreads) append_kv_kernel(const AppendLaunch p, int row_ctas, int window) {
-  if (static_cast<int>(blockIdx.x) < row_ctas) {
-    row_cta(p, blockIdx.x);
+__global__ void __launch_bounds__(kThreads) append_kv_kernel(const AppendLaunch p, int rows_per_cta,
+                                                              int block_ctas, int window) {
+  // the block CTAs first: they are the longer ones
+  if (static_cast<int>(blockIdx.x) >= block_ctas) {
+    row_cta(p, (blockIdx.x - block_ctas) * rows_per_cta, rows_per_cta);
     return;
   }
-  const int u = blockIdx.x - row_ctas;
+  const int u = blockIdx.x;
   const int h = u % p.c.heads;
   const int w = (u / p.c.heads) >> 1;
   if ((u / p.c.heads) & 1)
@@ -365,23 +383,26 @@ __global__ void __launch_bounds__(kThreads) append_kv_kernel(const AppendLaunch 
 }  // namespace
 
 cudaError_t launch_append_kv(const AppendLaunch& p, cudaStream_t stream) {
-  const int row_ctas = (p.q || !p.c.f8) ? p.rows : 0;
+  // one row per CTA while that gives every SM at most a few, else four: fewer
+  // CTAs, whose threads have more heads each to keep in flight
+  const int rows_per_cta = p.rows <= 512 ? 1 : 4;
+  const int row_ctas = (p.q || !p.c.f8) ? (p.rows + rows_per_cta - 1) / rows_per_cta : 0;
   // decode rows are units of their own, one per warp; packed rows make units
   // of up to a block, so a wider window wastes fewer CTAs on rows that only
   // continue one
   const int window = p.row_to_batch ? 32 : kWarps;
-  long long grid = row_ctas;
-  if (p.c.f8) grid += (static_cast<long long>(p.rows) + window - 1) / window * p.c.heads * 2;
+  const long long block_ctas = p.c.f8 ? (static_cast<long long>(p.rows) + window - 1) / window * p.c.heads * 2 : 0;
+  const long long grid = row_ctas + block_ctas;
   if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   // tokens of a block per thread: block_size / (256 threads / (dim / 16) lanes)
   const int tpt = std::max(1, (1 << p.c.bs_log2) * (p.c.dim / 16) / kThreads);
   const unsigned g = static_cast<unsigned>(grid);
   if (tpt == 1)
-    append_kv_kernel<1><<<g, kThreads, 0, stream>>>(p, row_ctas, window);
+    append_kv_kernel<1><<<g, kThreads, 0, stream>>>(p, rows_per_cta, static_cast<int>(block_ctas), window);
   else if (tpt == 2)
-    append_kv_kernel<2><<<g, kThreads, 0, stream>>>(p, row_ctas, window);
+    append_kv_kernel<2><<<g, kThreads, 0, stream>>>(p, rows_per_cta, static_cast<int>(block_ctas), window);
   else
-    append_kv_kernel<4><<<g, kThreads, 0, stream>>>(p, row_ctas, window);
+    append_kv_kernel<4><<<g, kThreads, 0, stream>>>(p, rows_per_cta, static_cast<int>(block_ctas), window);
   return cudaGetLastError();
 }
 
