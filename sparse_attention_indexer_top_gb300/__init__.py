@@ -14,7 +14,7 @@ from typing import Optional
 
 import torch
 
-from ._lib import SaiError, check, load, status_string  # noqa: F401
+from ._lib import SaiError, binding, check, load, status_string  # noqa: F401
 from .attention import (  # noqa: F401
     KVCache,
     append_kv,

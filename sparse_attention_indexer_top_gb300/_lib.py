@@ -97,6 +97,23 @@ def load() -> ctypes.CDLL:
     return _lib
 
 
+_binding = None
+
+
+def binding():
+    """The compiled module of the calls that a decode step makes per layer; raises if it has not been built."""
+    global _binding
+    if _binding is None:
+        load()
+        try:
+            from . import _binding as module
+        except ImportError as e:
+            raise RuntimeError(f"{os.path.join(_HERE, '_binding.so')} cannot be loaded ({e}): build it with "
+                               "sparse_attention_indexer_top_gb300.build.build()") from e
+        _binding = module
+    return _binding
+
+
 def status_string(status: int) -> str:
     return load().sai_status_string(int(status)).decode()
 

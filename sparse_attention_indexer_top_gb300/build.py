@@ -1,9 +1,11 @@
-"""Build libsai.so (the C-ABI library) in-tree for sm_103a with nvcc.
+"""Build libsai.so (the C-ABI library) in-tree for sm_103a with nvcc, and the
+Python module of its per-layer calls with g++.
 
 Each ``csrc/*.cu`` translation unit is compiled in parallel to an object
 file, then linked into ``libsai.so`` next to this file. Objects live in
 ``_build/`` (git-ignored). A unit is rebuilt when it or any header is newer
-than its object.
+than its object. ``csrc/binding.cpp`` becomes ``_binding.so``, against the
+installed torch; it is also rebuilt when torch's version has changed.
 """
 
 from __future__ import annotations
@@ -14,12 +16,14 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libsai.so")
+BINDING = os.path.join(HERE, "_binding.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xptxas", "-warn-spills",
          "-I" + os.path.join(ROOT, "include")]
@@ -38,6 +42,22 @@ def _newest_header() -> float:
     return max((os.path.getmtime(h) for h in hs), default=0.0)
 
 
+def _binding_job(hdr: float):
+    """Command that compiles binding.cpp to an object, its object, and whether it is out of date."""
+    import torch
+
+    src, obj = os.path.join(CSRC, "binding.cpp"), os.path.join(BUILD, f"binding-torch-{torch.__version__}.o")
+    top = os.path.dirname(torch.__file__)
+    inc = [os.path.join(top, "include"), sysconfig.get_paths()["include"],
+           os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include"), "/usr/local/cuda/include"]
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *["-I" + i for i in inc], "-c", src, "-o", obj]
+    link = ["-L" + os.path.join(top, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10", "-L" + HERE,
+            "-l:libsai.so", "-Wl,-rpath,$ORIGIN"]
+    stale = not os.path.exists(obj) or os.path.getmtime(obj) < max(os.path.getmtime(src), hdr)
+    return cmd, obj, link, stale
+
+
 def build(verbose: bool = False, force: bool = False) -> str:
     """Compile and link; returns the path of libsai.so."""
     nvcc = _nvcc()
@@ -52,10 +72,14 @@ def build(verbose: bool = False, force: bool = False) -> str:
         if force or not os.path.exists(o) or os.path.getmtime(o) < max(os.path.getmtime(s), hdr):
             jobs.append([nvcc, *ARCH, *FLAGS, "-c", s, "-o", o])
 
+    cmd, bobj, link, stale = _binding_job(hdr)
+    if stale:
+        jobs.append(cmd)
+
     def run(cmd):
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
-            raise RuntimeError("nvcc failed:\n" + " ".join(cmd) + "\n" + r.stdout + r.stderr)
+            raise RuntimeError("compiler failed:\n" + " ".join(cmd) + "\n" + r.stdout + r.stderr)
         if verbose:
             sys.stderr.write(r.stdout + r.stderr)
 
@@ -65,6 +89,10 @@ def build(verbose: bool = False, force: bool = False) -> str:
         tmp = LIB + ".tmp"
         run([nvcc, *ARCH, "-shared", "-o", tmp, *objs])
         os.replace(tmp, LIB)
+    if not os.path.exists(BINDING) or os.path.getmtime(BINDING) < max(os.path.getmtime(bobj), os.path.getmtime(LIB)):
+        tmp = BINDING + ".tmp"
+        run(["g++", "-shared", "-o", tmp, bobj, *link])
+        os.replace(tmp, BINDING)
     return LIB
 
 
