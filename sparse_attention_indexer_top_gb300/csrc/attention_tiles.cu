@@ -19,6 +19,13 @@
 // CTA complete in order, so a tile's S(j+1) being there means its PV(j) is
 // too, and O may be rescaled without another wait.
 //
+// At dim 128 two CTAs of a cluster pair up (cta_group::2): an MMA tile is 256
+// pairs, 128 in each CTA's TMEM, and each CTA holds half of every K tile (64
+// keys) and of every V tile (64 dims). One CTA alone reads 128 bytes of shared
+// memory per clock for Q K^T, all there is, besides what the copies write; the
+// pair needs 96 and half the copies. The first CTA's MMA thread issues for
+// both; the second CTA's softmax and prep warps report to its barriers.
+//
 // Roles (bf16 cache, 12 warps): 0-3 softmax of tile A, 4-7 softmax of tile B,
 // 8 TMA, 9 MMA, 10-11 "prep", which makes the value tile safe to multiply: a
 // weight of 0 times a NaN or infinity that a row must not see would still be
@@ -50,7 +57,10 @@ namespace sai {
 namespace {
 
 constexpr int kTile = 128;       // keys of a tile, and (row, head) pairs of an MMA tile
-constexpr int kMaxRows = 256;    // query rows of a CTA (group 1)
+template <int D>
+constexpr int kPair = D == 128 ? 2 : 1;               // CTAs of a pair
+template <int D>
+constexpr int kMaxRows = 2 * kTile * kPair<D>;        // query rows of a pair (group 1)
 constexpr int kSoftmaxWarps = 8;
 constexpr int kTmaWarp = 8;
 constexpr int kMmaWarp = 9;
@@ -59,10 +69,6 @@ struct Roles {
   static constexpr int kPrepWarp = F8 ? 12 : 10;
   static constexpr int kPrepWarps = F8 ? 4 : 2;
   static constexpr int kThreads = (kPrepWarp + kPrepWarps) * 32;
-  // K and V tiles of the MMA: two each by TMA, or one each of halves, fed from
-  // a ring of five code tiles that K and V take in turn
-  static constexpr int kStages = F8 ? 1 : 2;
-  static constexpr int kRaw = F8 ? 5 : 0;
 };
 constexpr float kLn2 = 0.69314718055994530942f;
 
@@ -71,34 +77,44 @@ constexpr uint32_t kColS = 0, kColO = 256, kTmemCols = 512;
 
 struct TilesLaunch {
   AttnLaunch a;
-  int rows_per_tile;  // floor(128 / group)
-  int row_tiles;      // CTAs along the rows
+  int rows_per_tile;  // floor(128 / group): rows of one CTA's part of an MMA tile
+  int row_tiles;      // CTAs (pairs) along the rows
 };
 
 template <int D, bool F8>
 struct Shared {
+  static constexpr int kPairN = kPair<D>;
+  static constexpr int kKeys = kTile / kPairN;  // keys of a K tile in this CTA
+  static constexpr int kDims = D / kPairN;      // dims of a V tile in this CTA (64)
+  static_assert(kDims == 64, "V is one slab of 64 dims");
   static constexpr int kSlabs = D / 64;
-  static constexpr int kTileBytes = kSlabs * kTile * 128;
-  static constexpr int kStages = Roles<F8>::kStages, kRaw = Roles<F8>::kRaw;
-  unsigned char q[2][kTileBytes];
-  unsigned char k[kStages][kTileBytes];
-  unsigned char v[kStages][kTileBytes];
-  unsigned char raw[kRaw ? kRaw : 1][kRaw ? kTile * D : 16];
-  // full: TMA (bf16) or prep (e4m3) has filled it; v_safe: prep is done with it
+  static constexpr int kQBytes = kSlabs * kTile * 128;
+  static constexpr int kKBytes = kSlabs * kKeys * 128, kVBytes = kTile * 128;
+  // K and V tiles of the MMA; of e4m3 fewer, fed from a ring of code tiles
+  // that K and V take in turn
+  static constexpr int kStages = F8 ? 2 : D == 128 ? 4 : 3;
+  static constexpr int kRaw = F8 ? 8 : 0;
+  unsigned char q[2][kQBytes];
+  unsigned char k[kStages][kKBytes];
+  unsigned char v[kStages][kVBytes];
+  unsigned char raw[kRaw ? kRaw : 1][kRaw ? kKeys * D : 16];
+  // In the first CTA of a pair, for both (the MMA waits there): q_ready, k_full,
+  // v_safe, p_ready. In each CTA for itself: the others.
   uint64_t q_full, q_ready, k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages], v_safe[kStages];
   uint64_t raw_full[kRaw ? kRaw : 1], raw_empty[kRaw ? kRaw : 1];
   uint64_t s_ready[2], p_ready[2][2], o_done[2];  // p_ready: first and second half of the keys
   uint32_t tmem;
   int nonfinite;  // number of the last pass (from 1) that met a non-finite value row
   int segs;
-  int warp_starts[8];
-  int row_n[kMaxRows], row_b[kMaxRows];
-  int seg_start[kMaxRows + 1], seg_most[kMaxRows], seg_least[kMaxRows], seg_low[kMaxRows];
+  int warp_starts[16];
+  int row_n[kMaxRows<D>], row_b[kMaxRows<D>];
+  int seg_start[kMaxRows<D> + 1], seg_most[kMaxRows<D>], seg_least[kMaxRows<D>], seg_low[kMaxRows<D>];
+  float4 scales[F8 ? kSoftmaxWarps : 1][8];  // per softmax warp: k scale, log2 v scale, 1 / v scale of 16 keys
 };
 
-// One request's rows of the CTA and the tiles that this CTA's chunk walks.
+// One request's rows of the CTA (pair) and the tiles that its chunk walks.
 struct Pass {
-  int s, e;        // rows [s, e) of the CTA
+  int s, e;        // rows [s, e) of the pair
   int batch;
   int most, least; // longest and shortest (above 0) row
   int low;         // least first key of a row's window (0: no window)
@@ -127,8 +143,9 @@ __device__ __forceinline__ Pass get_pass(const Shared<D, F8>& S, const TilesLaun
   r.most = S.seg_most[seg];
   r.least = S.seg_least[seg];
   r.low = S.seg_low[seg];
-  r.act[0] = r.s < L.rows_per_tile;
-  r.act[1] = r.e > L.rows_per_tile;
+  const int per = kPair<D> * L.rows_per_tile;
+  r.act[0] = r.s < per;
+  r.act[1] = r.e > per;
   int tiles = 0;
   r.first_tiles = r.low_tile = 0;
   if (r.most > 0) {
@@ -141,44 +158,129 @@ __device__ __forceinline__ Pass get_pass(const Shared<D, F8>& S, const TilesLaun
   return r;
 }
 
-__device__ __forceinline__ void tma_4d(void* dst, const void* map, int c0, int c1, int c2, int c3, uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
-      "[%6];" ::"r"(smem_u32(dst)),
-      "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_u32(bar))
-      : "memory");
+// TMA loads into this CTA; `bar` is a shared::cluster address, in a pair
+// possibly the first CTA's barrier.
+template <int PAIR>
+__device__ __forceinline__ void tma_4d(void* dst, const void* map, int c0, int c1, int c2, int c3, uint32_t bar) {
+  if (PAIR == 2)
+    asm volatile(
+        "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_u32(dst)),
+        "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_u32(dst)),
+        "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
+        : "memory");
 }
-__device__ __forceinline__ void tma_3d(void* dst, const void* map, int c0, int c1, int c2, uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
-      "[%5];" ::"r"(smem_u32(dst)),
-      "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar))
-      : "memory");
+template <int PAIR>
+__device__ __forceinline__ void tma_3d(void* dst, const void* map, int c0, int c1, int c2, uint32_t bar) {
+  if (PAIR == 2)
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
+        "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
+        "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ uint32_t cta_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+// shared::cluster address of the same variable in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t peer_addr(const void* p, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
+  return r;
+}
+// Barrier address in the first CTA of the pair (this CTA without a pair).
+template <int PAIR>
+__device__ __forceinline__ uint32_t first_cta(const uint64_t* bar) {
+  return PAIR == 2 ? peer_addr(bar, 0) : smem_u32(bar);
+}
+template <int PAIR>
+__device__ __forceinline__ void arrive_first(uint64_t* bar) {
+  if (PAIR == 2)
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(peer_addr(bar, 0)) : "memory");
+  else
+    mbar_arrive(bar);
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Arrive, in every CTA of the pair, when the products issued so far are done.
+template <int PAIR>
+__device__ __forceinline__ void commit_all(uint64_t* bar) {
+  if (PAIR == 2)
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            smem_u32(bar)),
+        "h"(static_cast<uint16_t>(3))
+        : "memory");
+  else
+    umma_commit(bar);
+}
+template <int PAIR>
+__device__ __forceinline__ void tmem_take(uint32_t* result) {
+  if (PAIR == 2) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(result)), "r"(kTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  } else {
+    tmem_alloc(result, kTmemCols);
+    tmem_relinquish();
+  }
+}
+template <int PAIR>
+__device__ __forceinline__ void tmem_give(uint32_t addr) {
+  if (PAIR == 2)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(kTmemCols) : "memory");
+  else
+    tmem_dealloc(addr, kTmemCols);
 }
 // Shared-memory matrix descriptors of 128-byte swizzled tiles (rows of 128
 // bytes in atoms of 8 rows, 1024 bytes apart). Low word: start address and
-// "leading" offset (N-major tiles: bytes between 64-dim slabs); the high word is
-// the same for all: stride offset 1024, version 1, 128-byte swizzle.
+// leading offset (not used: a tile's outer extent is one 128-byte row); the high
+// word is the same for all: stride offset 1024, version 1, 128-byte swizzle.
 constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
-__device__ __forceinline__ uint32_t desc_lo(uint32_t smem_addr, uint32_t leading) {
-  return ((smem_addr & 0x3FFFFu) >> 4) | ((leading >> 4) << 16);
-}
+__device__ __forceinline__ uint32_t desc_lo(uint32_t smem_addr) { return ((smem_addr & 0x3FFFFu) >> 4) | (1u << 16); }
 // D[tmem] (+)= A[smem] x B[smem], 16-bit types.
+template <int PAIR>
 __device__ __forceinline__ void umma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tmov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %5};\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d),
-      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate), "r"(kDescHi)
-      : "memory");
+#define SAI_UMMA_SS(N)                                                                                    \
+  asm volatile(                                                                                           \
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tmov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %5};\n\t"            \
+      "setp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::" #N ".kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d),  \
+      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate), "r"(kDescHi)                                      \
+      : "memory")
+  if (PAIR == 2)
+    SAI_UMMA_SS(2);
+  else
+    SAI_UMMA_SS(1);
+#undef SAI_UMMA_SS
 }
 // D[tmem] (+)= A[tmem] x B[smem], 16-bit A packed two to a column.
+template <int PAIR>
 __device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tmov.b64 b, {%2, %5};\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "r"(b_lo), "r"(idesc), "r"(accumulate), "r"(kDescHi)
-      : "memory");
+#define SAI_UMMA_TS(N)                                                                                    \
+  asm volatile(                                                                                           \
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tmov.b64 b, {%2, %5};\n\tsetp.ne.b32 p, %4, 0;\n\t"            \
+      "tcgen05.mma.cta_group::" #N ".kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d),                        \
+      "r"(a), "r"(b_lo), "r"(idesc), "r"(accumulate), "r"(kDescHi)                                         \
+      : "memory")
+  if (PAIR == 2)
+    SAI_UMMA_TS(2);
+  else
+    SAI_UMMA_TS(1);
+#undef SAI_UMMA_TS
 }
 __device__ __forceinline__ void tmem_ld32(uint32_t a, uint32_t* r) {
   asm volatile(
@@ -215,6 +317,11 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
 }
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   uint32_t r;
@@ -305,7 +412,8 @@ __device__ __noinline__ void add_nonfinite(const AttnLaunch& p, const Pass& ps, 
       const char* v = p.c.v + blk * p.c.vst[0] + kvh * p.c.vst[1] + off * p.c.vst[2];
       const char* k = p.c.k + blk * p.c.kst[0] + kvh * p.c.kst[1] + off * p.c.kst[2];
       bool bad = false;
-      for (int d = lane; d < D / 2; d += 32) {
+      // what was kept out goes by the 64 dims of one V tile
+      for (int d = c0 / 64 * 32 + lane; d < c0 / 64 * 32 + 32; d += 32) {
         const float2 x = values2<F8>(v, d);
         bad = bad || !(fabsf(x.x) <= 3.402823466e38f) || !(fabsf(x.y) <= 3.402823466e38f);
       }
@@ -396,14 +504,15 @@ __device__ __forceinline__ float query_to_f16(unsigned char* tile, int r) {
 
 template <int D, bool F8>
 __device__ __forceinline__ bool softmax_role(Shared<D, F8>& S, const TilesLaunch& L, int x, int kvh, int chunk,
-                                             int row0) {
+                                             int row0, int rank) {
+  constexpr int PAIR = kPair<D>;
   const AttnLaunch& p = L.a;
-  const int lane = threadIdx.x & 31, quad = (threadIdx.x >> 5) & 3;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, quad = warp & 3;
   const int r = quad * 32 + lane;  // the thread's TMEM lane
   const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
   const uint32_t ts = S.tmem + lanes + kColS + 128 * x;
   const uint32_t to = S.tmem + lanes + kColO + 128 * x;
-  const int local = x * L.rows_per_tile + r / p.group;
+  const int local = (x * PAIR + rank) * L.rows_per_tile + r / p.group;
   const bool in_tile = r < L.rows_per_tile * p.group;
   int tiles_done = 0, passes_done = 0;
   float scale = p.scale_log2;
@@ -412,7 +521,8 @@ __device__ __forceinline__ bool softmax_role(Shared<D, F8>& S, const TilesLaunch
     if (!__all_sync(0xffffffffu, ok)) return false;
     scale *= query_to_f16<D>(S.q[x], r);
     fence_proxy_async_smem();
-    mbar_arrive(&S.q_ready);
+    __syncwarp();
+    if (lane == 0) arrive_first<PAIR>(&S.q_ready);
   }
 
   for (int seg = 0; seg < S.segs; ++seg) {
@@ -451,10 +561,13 @@ __device__ __forceinline__ bool softmax_role(Shared<D, F8>& S, const TilesLaunch
     float2 sc1 = scales_of(blk1);
     for (int i = ps.i0; i < ps.i1; ++i) {
       const uint32_t bad = __ballot_sync(0xffffffffu, blk1 == -2);
-      float ks_l = sc1.x, vl_l = 0.f, vi_l = 1.f;
+      const float4* gs = S.scales[F8 ? warp : 0];
       if (F8) {
-        vl_l = log2_scale(sc1.y);
-        vi_l = 1.f / fmaxf(sc1.y, 7.888609052210118e-31f);
+        __syncwarp();  // the last tile's have been read
+        if (lane < 8)
+          S.scales[warp][lane] =
+              make_float4(sc1.x, log2_scale(sc1.y), 1.f / fmaxf(sc1.y, 7.888609052210118e-31f), 0.f);
+        __syncwarp();
         sc1 = scales_of(blk2);
       }
       blk1 = blk2;
@@ -481,42 +594,55 @@ __device__ __forceinline__ bool softmax_role(Shared<D, F8>& S, const TilesLaunch
       auto largest = [&](const uint32_t* s, int c0, float top) {
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
-          float a = __uint_as_float(s[16 * g]), b = __uint_as_float(s[16 * g + 1]);
-          a = fmaxf(a, __uint_as_float(s[16 * g + 2]));
-          b = fmaxf(b, __uint_as_float(s[16 * g + 3]));
-#pragma unroll
-          for (int e = 4; e < 16; e += 4) {
-            a = fmaxf(fmaxf(a, __uint_as_float(s[16 * g + e])), __uint_as_float(s[16 * g + e + 1]));
-            b = fmaxf(fmaxf(b, __uint_as_float(s[16 * g + e + 2])), __uint_as_float(s[16 * g + e + 3]));
+          auto at = [&](int e) { return __uint_as_float(s[16 * g + e]); };
+          float a = max3(at(0), at(1), at(2)), b = max3(at(3), at(4), at(5));
+          a = max3(a, at(6), at(7));
+          b = max3(b, at(8), at(9));
+          a = max3(a, at(10), at(11));
+          b = max3(b, at(12), at(13));
+          a = max3(a, at(14), at(15));
+          if (F8) {
+            const float4 k = gs[c0 / 16 + g];
+            top = fmaxf(top, fmaf(fmaxf(a, b), scale * k.x, k.y));
+          } else {
+            top = max3(top, a, b);
           }
-          const float k = F8 ? scale * __shfl_sync(0xffffffffu, ks_l, c0 / 16 + g) : scale;
-          const float v = F8 ? __shfl_sync(0xffffffffu, vl_l, c0 / 16 + g) : 0.f;
-          top = fmaxf(top, fmaf(fmaxf(a, b), k, v));
         }
         return top;
       };
-      // The first 64 columns stay in registers; the others are read for the
-      // maximum and read again for their weights, which keeps the row's
-      // registers at half of S.
-      uint32_t s[64], u[32];
-      tmem_ld32(ts, s);
-      tmem_ld32(ts + 32, s + 32);
-      tmem_ld32(ts + 64, u);
-      tmem_ld_wait32(s);
-      tmem_ld_wait32(s + 32);
-      tmem_ld_wait32(u);
-      if (masked) mask(u, 64);
-      float top = largest(u, 64, -INFINITY);
-      tmem_ld32(ts + 96, u);
-      if (masked) {
-        mask(s, 0);
-        mask(s + 32, 32);
+      // bf16: the row of S stays in registers. e4m3 (more warps, fewer
+      // registers each): its first half does; the other columns are read for
+      // the maximum and read again for their weights.
+      constexpr int kHeld = F8 ? 64 : 128;
+      uint32_t s[kHeld], u[32];
+#pragma unroll
+      for (int c = 0; c < kHeld; c += 32) tmem_ld32(ts + c, s + c);
+      float top = -INFINITY;
+      if (F8) {
+        tmem_ld32(ts + 64, u);
+        tmem_ld_wait32(u);
+#pragma unroll
+        for (int c = 0; c < kHeld; c += 32) tmem_ld_wait32(s + c);
+        if (masked) mask(u, 64);
+        top = largest(u, 64, top);
+        tmem_ld32(ts + 96, u);
+      } else {
+#pragma unroll
+        for (int c = 0; c < kHeld; c += 32) tmem_ld_wait32(s + c);
       }
-      top = largest(s, 0, top);
-      top = largest(s + 32, 32, top);
-      tmem_ld_wait32(u);
-      if (masked) mask(u, 96);
-      top = largest(u, 96, top);
+      if (masked) {
+#pragma unroll
+        for (int c = 0; c < kHeld; c += 32) mask(s + c, c);
+      }
+#pragma unroll
+      for (int c = 0; c < kHeld; c += 32) top = largest(s + c, c, top);
+      if (F8) {
+        tmem_ld_wait32(u);
+        if (masked) mask(u, 96);
+        top = largest(u, 96, top);
+      } else {
+        top *= scale;
+      }
       // the maximum moves only when it is passed by more than 2^8: weights up
       // to 256 are as exact in 16 bits as weights up to 1, and O is rarely
       // rescaled
@@ -543,14 +669,14 @@ __device__ __forceinline__ bool softmax_role(Shared<D, F8>& S, const TilesLaunch
       auto weights = [&](uint32_t* s, int c0) {
         uint64_t sum[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
         uint64_t scale2 = pair(scale, scale), base2 = pair(-base, -base);
-        float a, b;
+        float a, b, inv = 1.f;
 #pragma unroll
         for (int c = 0; c < 32; c += 2) {
           if (F8 && c % 16 == 0) {
-            const int g = (c0 + c) / 16;
-            const float k = scale * __shfl_sync(0xffffffffu, ks_l, g), v = __shfl_sync(0xffffffffu, vl_l, g) - base;
-            scale2 = pair(k, k);
-            base2 = pair(v, v);
+            const float4 k = gs[(c0 + c) / 16];
+            scale2 = pair(scale * k.x, scale * k.x);
+            base2 = pair(k.y - base, k.y - base);
+            inv = k.z;
           }
           unpair(fma2(pair(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), scale2, base2), a, b);
           a = ex2(a);
@@ -559,34 +685,46 @@ __device__ __forceinline__ bool softmax_role(Shared<D, F8>& S, const TilesLaunch
           s[c / 2] = F8 ? pack_f16(a, b) : pack_bf16(a, b);
           if (c % 16 == 14 && (F8 || c == 30)) {
             unpair(add2(sum[0], sum[1]), a, b);
-            l = F8 ? fmaf(a + b, __shfl_sync(0xffffffffu, vi_l, (c0 + c) / 16), l) : l + (a + b);
+            l = F8 ? fmaf(a + b, inv, l) : l + (a + b);
             sum[0] = sum[1] = pair(0.f, 0.f);
           }
         }
         tmem_st16(ts + c0 / 2, s);
       };
-      tmem_ld32(ts + 64, u);
+      auto hand_over = [&](int half) {
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_first<PAIR>(&S.p_ready[x][half]);
+      };
+      if (F8) tmem_ld32(ts + 64, u);
       weights(s, 0);
       weights(s + 32, 32);
-      tmem_st_wait();
-      tc_fence_before();
-      mbar_arrive(&S.p_ready[x][0]);
-      tmem_ld_wait32(u);
-      tmem_ld32(ts + 96, s);
-      if (masked) mask(u, 64);
-      weights(u, 64);
-      tmem_ld_wait32(s);
-      if (masked) mask(s, 96);
-      weights(s, 96);
-      tmem_st_wait();
-      tc_fence_before();
-      mbar_arrive(&S.p_ready[x][1]);
+      hand_over(0);
+      if (F8) {
+        tmem_ld_wait32(u);
+        tmem_ld32(ts + 96, s);
+        if (masked) mask(u, 64);
+        weights(u, 64);
+        tmem_ld_wait32(s);
+        if (masked) mask(s, 96);
+        weights(s, 96);
+      } else {
+        weights(s + kHeld / 2, 64);
+        weights(s + kHeld - 32, 96);
+      }
+      hand_over(1);
     }
     const bool ok = mbar_wait(&S.o_done[x], passes_done & 1);
     if (!__all_sync(0xffffffffu, ok)) return false;
     ++passes_done;
     tc_fence_after();
-    const bool extra = *reinterpret_cast<volatile int*>(&S.nonfinite) == seg + 1;
+    bool extra = *reinterpret_cast<volatile int*>(&S.nonfinite) == seg + 1;
+    if (PAIR == 2) {
+      int other;
+      asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(other) : "r"(peer_addr(&S.nonfinite, rank ^ 1)) : "memory");
+      extra = extra || other == seg + 1;
+    }
 #pragma unroll 1
     for (int c = 0; c < D; c += 32) {
       uint32_t u[32];
@@ -608,64 +746,83 @@ __device__ __forceinline__ bool softmax_role(Shared<D, F8>& S, const TilesLaunch
 template <int D, bool F8>
 __device__ __forceinline__ bool tma_role(Shared<D, F8>& S, const TilesLaunch& L, const CUtensorMap* qmap,
                                          const CUtensorMap* kmap, const CUtensorMap* vmap, int kvh, int chunk,
-                                         int row0) {
+                                         int row0, int rank) {
+  using Sh = Shared<D, F8>;
+  constexpr int PAIR = kPair<D>, kStages = Sh::kStages, kRaw = F8 ? Sh::kRaw : 1;
   const AttnLaunch& p = L.a;
   const int lane = threadIdx.x & 31;
-  constexpr int kSlabs = D / 64;
-  constexpr int kStages = Shared<D, F8>::kStages, kRaw = Shared<D, F8>::kRaw;
   if (lane == 0) {
-    mbar_arrive_expect_tx(&S.q_full, 2 * kSlabs * L.rows_per_tile * p.group * 128);
+    // bf16: the MMA waits for both CTAs' queries; e4m3: each CTA converts its own first
+    const uint32_t bar = F8 ? smem_u32(&S.q_full) : first_cta<PAIR>(&S.q_full);
+    const int bytes = 2 * Sh::kSlabs * L.rows_per_tile * p.group * 128;
+    if (F8)
+      mbar_arrive_expect_tx(&S.q_full, bytes);
+    else if (rank == 0)
+      mbar_arrive_expect_tx(&S.q_full, PAIR * bytes);
     for (int x = 0; x < 2; ++x)
-      for (int c = 0; c < kSlabs; ++c)
-        tma_3d(S.q[x] + c * kTile * 128, qmap, 64 * c, kvh * p.group, row0 + x * L.rows_per_tile, &S.q_full);
+      for (int c = 0; c < Sh::kSlabs; ++c)
+        tma_3d<PAIR>(S.q[x] + c * kTile * 128, qmap, 64 * c, kvh * p.group, row0 + (x * PAIR + rank) * L.rows_per_tile,
+                     bar);
   }
   const int bs = 1 << p.c.bs_log2;
-  const int blocks = kTile >> p.c.bs_log2;  // blocks of a tile
+  const int k_box = min(bs, Sh::kKeys);  // keys of one K copy; a V copy takes a block
   int done = 0;
   for (int seg = 0; seg < S.segs; ++seg) {
     const Pass ps = get_pass(S, L, seg, chunk);
-    auto block_of = [&](int i) -> int {
-      if (i >= ps.i1 || lane >= blocks) return -1;
-      const int t = ps.tile0(i) + lane * bs;
+    // block of the lane's copy, copies being `box` keys each; -1: none. A bad
+    // block is read as the one past the end, which the copy fills with zeros.
+    auto block_of = [&](int i, int box) -> int {
+      if (i >= ps.i1 || lane >= kTile / box) return -1;
+      const int t = ps.tile0(i) + lane * box;
       if (t >= ps.most) return -1;
       const int blk = p.block_table[ps.batch * p.bt_stride + (t >> p.c.bs_log2)];
-      // a bad block is read as the one past the end, which the copy fills with zeros
       return blk < 0 || blk >= p.c.num_blocks ? static_cast<int>(p.c.num_blocks) : blk;
     };
-    int next = block_of(ps.i0);
+    int next_k = block_of(ps.i0, k_box), next_v = block_of(ps.i0, bs);
     for (int i = ps.i0; i < ps.i1; ++i, ++done) {
-      const int blk = next;
-      next = block_of(i + 1);
-      const int count = __popc(__ballot_sync(0xffffffffu, blk >= 0));
+      const int blk[2] = {next_k, next_v};
+      next_k = block_of(i + 1, k_box);
+      next_v = block_of(i + 1, bs);
 #pragma unroll
       for (int kv = 0; kv < 2; ++kv) {
+        const int box = kv ? bs : k_box;
+        const bool mine = blk[kv] >= 0 && (kv || PAIR == 1 || lane * box / Sh::kKeys == rank);
+        // bf16 keys report to the first CTA, which expects both CTAs' bytes
+        const bool shared = !F8 && !kv;
+        const int copies = __popc(__ballot_sync(0xffffffffu, shared ? blk[kv] >= 0 : mine));
+        const int bytes = copies * box * (kv ? Sh::kDims : D) * (F8 ? 1 : 2);
         uint64_t *empty, *full;
         unsigned char* dst;
         uint32_t ph;
+        const int at = kv ? lane * box : lane * box % Sh::kKeys;  // row of the copy in the tile
         if (F8) {
-          const int idx = 2 * done + kv, st = idx % (kRaw ? kRaw : 1);
+          const int idx = 2 * done + kv, st = idx % kRaw;
           empty = &S.raw_empty[st];
           full = &S.raw_full[st];
-          dst = S.raw[st] + lane * bs * D;
-          ph = (idx / (kRaw ? kRaw : 1)) & 1;
+          dst = S.raw[st] + at * (kv ? Sh::kDims : D);
+          ph = (idx / kRaw) & 1;
         } else {
           const int st = done % kStages;
           empty = kv ? &S.v_empty[st] : &S.k_empty[st];
           full = kv ? &S.v_full[st] : &S.k_full[st];
-          dst = (kv ? S.v[st] : S.k[st]) + lane * bs * 128;
+          dst = (kv ? S.v[st] : S.k[st]) + at * 128;
           ph = (done / kStages) & 1;
         }
         const bool ok = mbar_wait(empty, ph ^ 1);
         if (!__all_sync(0xffffffffu, ok)) return false;
-        if (lane == 0) mbar_arrive_expect_tx(full, count * bs * D * (F8 ? 1 : 2));
+        if (lane == 0 && (!shared || rank == 0)) mbar_arrive_expect_tx(full, bytes);
         __syncwarp();
-        if (blk >= 0) {
-          if (F8) {
-            tma_4d(dst, kv ? vmap : kmap, 0, 0, kvh, blk, full);
-          } else {
+        if (mine) {
+          const uint32_t bar = shared ? first_cta<PAIR>(full) : smem_u32(full);
+          const int tok = lane * box & (bs - 1);
+          if (kv)
+            tma_4d<PAIR>(dst, vmap, Sh::kDims * rank, 0, kvh, blk[kv], bar);
+          else if (F8)
+            tma_4d<PAIR>(dst, kmap, 0, tok, kvh, blk[kv], bar);
+          else
 #pragma unroll
-            for (int c = 0; c < kSlabs; ++c) tma_4d(dst + c * kTile * 128, kv ? vmap : kmap, 64 * c, 0, kvh, blk, full);
-          }
+            for (int c = 0; c < Sh::kSlabs; ++c)
+              tma_4d<PAIR>(dst + c * Sh::kKeys * 128, kmap, 64 * c, tok, kvh, blk[kv], bar);
         }
       }
     }
@@ -676,34 +833,31 @@ __device__ __forceinline__ bool tma_role(Shared<D, F8>& S, const TilesLaunch& L,
 // ---------------------------------------------------------------------- MMA
 template <int D, bool F8>
 __device__ __forceinline__ bool mma_role(Shared<D, F8>& S, const TilesLaunch& L, int chunk) {
-  constexpr int kStages = Shared<D, F8>::kStages;
+  using Sh = Shared<D, F8>;
+  constexpr int PAIR = kPair<D>, kStages = Sh::kStages;
   constexpr uint32_t kF16 = F8 ? (1u << 7) | (1u << 10) : 0u;  // format fields: 1 bf16, 0 f16
-  constexpr uint32_t kIdescQk = umma_idesc_bf16(kTile, kTile) ^ kF16;
-  constexpr uint32_t kIdescPv = (umma_idesc_bf16(kTile, D) ^ kF16) | kTransposeB;
-  constexpr uint32_t kSlab = kTile * 128;
+  constexpr uint32_t kIdescQk = umma_idesc_bf16(kTile * PAIR, kTile) ^ kF16;
+  constexpr uint32_t kIdescPv = (umma_idesc_bf16(kTile * PAIR, D) ^ kF16) | kTransposeB;
   const uint32_t tmem = S.tmem;
   // first words of the descriptors; kept opaque, so that each step's is one
   // addition and not a register of its own through the loop
-  uint32_t q_lo = desc_lo(smem_u32(S.q[0]), 16), k_lo = desc_lo(smem_u32(S.k[0]), 16),
-           v_lo = desc_lo(smem_u32(S.v[0]), kSlab);
-  constexpr uint32_t kTileLo = Shared<D, F8>::kTileBytes >> 4;
+  uint32_t q_lo = desc_lo(smem_u32(S.q[0])), k_lo = desc_lo(smem_u32(S.k[0])), v_lo = desc_lo(smem_u32(S.v[0]));
   auto qk = [&](int x, int st) {
     asm volatile("" : "+r"(q_lo), "+r"(k_lo));
-    const uint32_t a = q_lo + x * kTileLo, b = k_lo + st * kTileLo;
+    const uint32_t a = q_lo + x * (Sh::kQBytes >> 4), b = k_lo + st * (Sh::kKBytes >> 4);
 #pragma unroll
-    for (int s = 0; s < D / 16; ++s) {
-      const uint32_t off = ((s / 4) * kSlab + (s % 4) * 32) >> 4;
-      umma_ss(tmem + kColS + 128 * x, a + off, b + off, kIdescQk, s > 0);
-    }
-    umma_commit(&S.s_ready[x]);
+    for (int s = 0; s < D / 16; ++s)
+      umma_ss<PAIR>(tmem + kColS + 128 * x, a + (((s / 4) * kTile * 128 + (s % 4) * 32) >> 4),
+                    b + (((s / 4) * Sh::kKeys * 128 + (s % 4) * 32) >> 4), kIdescQk, s > 0);
+    commit_all<PAIR>(&S.s_ready[x]);
   };
   auto pv = [&](int x, int st, int half, bool first) {
     asm volatile("" : "+r"(v_lo));
-    const uint32_t b = v_lo + st * kTileLo;
+    const uint32_t b = v_lo + st * (Sh::kVBytes >> 4);
 #pragma unroll
     for (int s = 4 * half; s < 4 * half + 4; ++s)
-      umma_ts(tmem + kColO + 128 * x, tmem + kColS + 128 * x + 8 * s, b + ((s * 2048) >> 4), kIdescPv,
-              !(first && s == 0));
+      umma_ts<PAIR>(tmem + kColO + 128 * x, tmem + kColS + 128 * x + 8 * s, b + ((s * 2048) >> 4), kIdescPv,
+                    !(first && s == 0));
   };
   if (!mbar_wait(F8 ? &S.q_ready : &S.q_full, 0)) return false;
   int done = 0, p_done[2] = {0, 0};
@@ -716,7 +870,7 @@ __device__ __forceinline__ bool mma_role(Shared<D, F8>& S, const TilesLaunch& L,
 #pragma unroll
     for (int x = 0; x < 2; ++x)
       if (ps.act[x]) qk(x, done % kStages);
-    umma_commit(&S.k_empty[done % kStages]);
+    commit_all<PAIR>(&S.k_empty[done % kStages]);
     for (int i = 0; i < n; ++i, ++done) {
       const int st = done % kStages, nst = (done + 1) % kStages;
       const bool more = i + 1 < n;
@@ -732,16 +886,16 @@ __device__ __forceinline__ bool mma_role(Shared<D, F8>& S, const TilesLaunch& L,
           pv(x, st, half, i == 0);
         }
         ++p_done[x];
-        if (x == 1 || !ps.act[1]) umma_commit(&S.v_empty[st]);
+        if (x == 1 || !ps.act[1]) commit_all<PAIR>(&S.v_empty[st]);
         if (more) {
           if (!k_there && !mbar_wait(&S.k_full[nst], ((done + 1) / kStages) & 1)) return false;
           k_there = true;
           tc_fence_after();
           qk(x, nst);
         } else
-          umma_commit(&S.o_done[x]);
+          commit_all<PAIR>(&S.o_done[x]);
       }
-      if (more) umma_commit(&S.k_empty[nst]);
+      if (more) commit_all<PAIR>(&S.k_empty[nst]);
     }
   }
   return true;
@@ -751,7 +905,7 @@ __device__ __forceinline__ bool mma_role(Shared<D, F8>& S, const TilesLaunch& L,
 template <int D>
 __device__ __forceinline__ bool prep_role(Shared<D, false>& S, const TilesLaunch& L, int chunk) {
   const AttnLaunch& p = L.a;
-  constexpr int kStages = Roles<false>::kStages, kPrepWarps = Roles<false>::kPrepWarps;
+  constexpr int PAIR = kPair<D>, kStages = Shared<D, false>::kStages, kPrepWarps = Roles<false>::kPrepWarps;
   const int tid = threadIdx.x - Roles<false>::kPrepWarp * 32;
   int done = 0;
   for (int seg = 0; seg < S.segs; ++seg) {
@@ -772,12 +926,10 @@ __device__ __forceinline__ bool prep_role(Shared<D, false>& S, const TilesLaunch
           bool bad = false;
           if (!zero) {
 #pragma unroll
-            for (int c = 0; c < D / 64; ++c)
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const uint4 x = *reinterpret_cast<const uint4*>(at + c * kTile * 128 + e * 16);
-                bad = bad || nonfinite2(x.x) || nonfinite2(x.y) || nonfinite2(x.z) || nonfinite2(x.w);
-              }
+            for (int e = 0; e < 2; ++e) {
+              const uint4 x = *reinterpret_cast<const uint4*>(at + e * 16);
+              bad = bad || nonfinite2(x.x) || nonfinite2(x.y) || nonfinite2(x.z) || nonfinite2(x.w);
+            }
           }
           const uint32_t b = __ballot_sync(0xffffffffu, bad);
           if ((b >> (threadIdx.x & 28)) & 0xfu) {
@@ -786,84 +938,94 @@ __device__ __forceinline__ bool prep_role(Shared<D, false>& S, const TilesLaunch
           }
           if (zero) {
 #pragma unroll
-            for (int c = 0; c < D / 64; ++c)
-#pragma unroll
-              for (int e = 0; e < 2; ++e)
-                *reinterpret_cast<uint4*>(at + c * kTile * 128 + e * 16) = make_uint4(0, 0, 0, 0);
+            for (int e = 0; e < 2; ++e) *reinterpret_cast<uint4*>(at + e * 16) = make_uint4(0, 0, 0, 0);
           }
         }
         fence_proxy_async_smem();  // the MMA reads these stores through the async proxy
       }
       __syncwarp();
-      if ((threadIdx.x & 31) == 0) mbar_arrive(&S.v_safe[st]);
+      if ((threadIdx.x & 31) == 0) arrive_first<PAIR>(&S.v_safe[st]);
     }
   }
   return true;
 }
 
-// e4m3: codes of the ring to halves in the MMA's layout (128-byte swizzled
-// rows of 64 dims), K and V in turn. Lanes of one key row read its 16-byte
-// pieces; a piece becomes two 16-byte chunks, written in an order that keeps
-// the eight lanes of a store on different banks.
+// e4m3: 16-code pieces of a raw tile (rows of ROW codes) to halves in the MMA's
+// layout: 128-byte swizzled rows of 64 dims, slabs of ROWS rows. The lanes of
+// one row read its pieces; a piece becomes two 16-byte chunks, written in an
+// order that keeps the eight lanes of a store on different banks. CHECK: rows
+// from `dead` on and rows with a NaN become 0; returns whether there was a NaN.
+template <int ROWS, int ROW>
+__device__ __forceinline__ bool codes_to_halves(const uint4 (&x)[4], unsigned char* out, int tid, bool check, int dead) {
+  constexpr int kPieces = ROW / 16, kStep = 128;
+  static_assert(ROWS * kPieces == 4 * kStep, "four pieces per thread");
+  const int piece = tid % kPieces;
+  bool met = false;
+  out += (piece / 4) * ROWS * 128;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int key = (j * kStep + tid) / kPieces;
+    uint4 c = x[j];
+    if (check) {
+      const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+      bool nan = false;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t y = (w[e] & 0x7f7f7f7fu) ^ 0x7f7f7f7fu;  // a zero byte: NaN
+        nan = nan || (((y - 0x01010101u) & ~y & 0x80808080u) != 0u);
+      }
+      bool zero = key >= dead;
+      const uint32_t b = __ballot_sync(0xffffffffu, nan && !zero);
+      if ((b >> ((tid & 31) / kPieces * kPieces)) & ((1u << kPieces) - 1u)) zero = met = true;
+      if (zero) c = make_uint4(0, 0, 0, 0);
+    }
+    uint4 a, b;
+    e4m3x4_f16x4(c.x, a.x, a.y);
+    e4m3x4_f16x4(c.y, a.z, a.w);
+    e4m3x4_f16x4(c.z, b.x, b.y);
+    e4m3x4_f16x4(c.w, b.z, b.w);
+    const int odd = kPieces == 8 ? piece >> 2 : 0;  // dims above 64 write their second chunk first
+    const int c0 = 2 * (piece & 3) + odd;
+    *reinterpret_cast<uint4*>(out + key * 128 + ((c0 ^ (key & 7)) << 4)) = odd ? b : a;
+    *reinterpret_cast<uint4*>(out + key * 128 + (((c0 ^ 1) ^ (key & 7)) << 4)) = odd ? a : b;
+  }
+  return met;
+}
+
 template <int D>
 __device__ __forceinline__ bool prep_role(Shared<D, true>& S, const TilesLaunch& L, int chunk) {
+  using Sh = Shared<D, true>;
+  constexpr int PAIR = kPair<D>, kRaw = Sh::kRaw, kStages = Sh::kStages;
+  static_assert(Sh::kKeys * D == 4 * 128 * 16 && kTile * Sh::kDims == 4 * 128 * 16, "four pieces per thread");
   const AttnLaunch& p = L.a;
-  constexpr int kRaw = Roles<true>::kRaw, kThreadsHere = Roles<true>::kPrepWarps * 32;
-  constexpr int kPieces = D / 16;  // 16-code pieces of a key row
   const int tid = threadIdx.x - Roles<true>::kPrepWarp * 32;
-  const int piece = tid % kPieces;
   int done = 0;
   for (int seg = 0; seg < S.segs; ++seg) {
     const Pass ps = get_pass(S, L, seg, chunk);
     for (int i = ps.i0; i < ps.i1; ++i, ++done) {
-      const int t0 = ps.tile0(i);
+      const int t0 = ps.tile0(i), st = done % kStages;
       const bool check = ps.partial(t0, p);
 #pragma unroll
       for (int kv = 0; kv < 2; ++kv) {
-        const int idx = 2 * done + kv, st = idx % kRaw;
-        bool ok = mbar_wait(&S.raw_full[st], (idx / kRaw) & 1);
-        uint4 x[kTile * kPieces / kThreadsHere];
+        const int idx = 2 * done + kv, rs = idx % kRaw;
+        bool ok = mbar_wait(&S.raw_full[rs], (idx / kRaw) & 1);
+        uint4 x[4];
         if (ok) {
 #pragma unroll
-          for (int j = 0; j < kTile * kPieces / kThreadsHere; ++j)
-            x[j] = *reinterpret_cast<const uint4*>(S.raw[st] + (j * kThreadsHere + tid) * 16);
-          ok = mbar_wait(kv ? &S.v_empty[0] : &S.k_empty[0], (done & 1) ^ 1);
+          for (int j = 0; j < 4; ++j) x[j] = *reinterpret_cast<const uint4*>(S.raw[rs] + (j * 128 + tid) * 16);
+          ok = mbar_wait(kv ? &S.v_empty[st] : &S.k_empty[st], ((done / kStages) & 1) ^ 1);
         }
         if (!__all_sync(0xffffffffu, ok)) return false;
-        if ((threadIdx.x & 31) == 0) mbar_arrive(&S.raw_empty[st]);  // every lane has its pieces
-        unsigned char* out = (kv ? S.v[0] : S.k[0]) + (piece / 4) * kTile * 128;
-#pragma unroll
-        for (int j = 0; j < kTile * kPieces / kThreadsHere; ++j) {
-          const int key = (j * kThreadsHere + tid) / kPieces;
-          if (kv && check) {
-            const uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
-            bool nan = false;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const uint32_t y = (w[e] & 0x7f7f7f7fu) ^ 0x7f7f7f7fu;  // a zero byte: NaN
-              nan = nan || (((y - 0x01010101u) & ~y & 0x80808080u) != 0u);
-            }
-            bool zero = t0 + key >= ps.most;
-            const uint32_t b = __ballot_sync(0xffffffffu, nan && !zero);
-            if ((b >> ((threadIdx.x & 31) / kPieces * kPieces)) & ((1u << kPieces) - 1u)) {
-              zero = true;
-              *reinterpret_cast<volatile int*>(&S.nonfinite) = seg + 1;
-            }
-            if (zero) x[j] = make_uint4(0, 0, 0, 0);
-          }
-          uint4 a, b;
-          e4m3x4_f16x4(x[j].x, a.x, a.y);
-          e4m3x4_f16x4(x[j].y, a.z, a.w);
-          e4m3x4_f16x4(x[j].z, b.x, b.y);
-          e4m3x4_f16x4(x[j].w, b.z, b.w);
-          const int odd = D == 128 ? piece >> 2 : 0;  // dims above 64 write their second chunk first
-          const int c0 = 2 * (piece & 3) + odd;
-          *reinterpret_cast<uint4*>(out + key * 128 + ((c0 ^ (key & 7)) << 4)) = odd ? b : a;
-          *reinterpret_cast<uint4*>(out + key * 128 + (((c0 ^ 1) ^ (key & 7)) << 4)) = odd ? a : b;
+        if ((threadIdx.x & 31) == 0) mbar_arrive(&S.raw_empty[rs]);  // every lane has its pieces
+        if (kv) {
+          if (codes_to_halves<kTile, Sh::kDims>(x, S.v[st], tid, check, ps.most - t0))
+            *reinterpret_cast<volatile int*>(&S.nonfinite) = seg + 1;
+        } else {
+          codes_to_halves<Sh::kKeys, D>(x, S.k[st], tid, false, 0);
         }
         fence_proxy_async_smem();  // the MMA reads these stores through the async proxy
         __syncwarp();
-        if ((threadIdx.x & 31) == 0) mbar_arrive(kv ? &S.v_safe[0] : &S.k_full[0]);
+        if ((threadIdx.x & 31) == 0) arrive_first<PAIR>(kv ? &S.v_safe[st] : &S.k_full[st]);
       }
     }
   }
@@ -876,27 +1038,29 @@ __global__ void __launch_bounds__(Roles<F8>::kThreads, 1)
                       const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
   extern __shared__ unsigned char raw[];
   using Sh = Shared<D, F8>;
+  constexpr int PAIR = kPair<D>, kRows = kMaxRows<D>;
   Sh& S = *reinterpret_cast<Sh*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const AttnLaunch& p = L.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  int u = blockIdx.x;
+  const int rank = PAIR == 2 ? static_cast<int>(cta_rank()) : 0;
+  int u = blockIdx.x / PAIR;
   const int chunk = u % p.chunks;
   u /= p.chunks;
   const int kvh = u % p.c.heads;
   // the last rows first: with causal lengths they have the most keys
-  const int rows_here = 2 * L.rows_per_tile;
+  const int rows_here = 2 * PAIR * L.rows_per_tile;
   const int row0 = (L.row_tiles - 1 - u / p.c.heads) * rows_here;
 
   // ---- set-up: barriers, TMEM, the rows' lengths and the runs of one request
   if (tid == 0) {
     mbar_init(&S.q_full, 1);
-    mbar_init(&S.q_ready, kSoftmaxWarps * 32);
+    mbar_init(&S.q_ready, kSoftmaxWarps * PAIR);
     for (int i = 0; i < Sh::kStages; ++i) {
-      mbar_init(&S.k_full[i], F8 ? Roles<F8>::kPrepWarps : 1);
+      mbar_init(&S.k_full[i], F8 ? Roles<F8>::kPrepWarps * PAIR : 1);
       mbar_init(&S.k_empty[i], 1);
       mbar_init(&S.v_full[i], 1);
       mbar_init(&S.v_empty[i], 1);
-      mbar_init(&S.v_safe[i], Roles<F8>::kPrepWarps);
+      mbar_init(&S.v_safe[i], Roles<F8>::kPrepWarps * PAIR);
     }
     for (int i = 0; i < Sh::kRaw; ++i) {
       mbar_init(&S.raw_full[i], 1);
@@ -904,26 +1068,24 @@ __global__ void __launch_bounds__(Roles<F8>::kThreads, 1)
     }
     for (int x = 0; x < 2; ++x) {
       mbar_init(&S.s_ready[x], 1);
-      mbar_init(&S.p_ready[x][0], 128);
-      mbar_init(&S.p_ready[x][1], 128);
+      mbar_init(&S.p_ready[x][0], 4 * PAIR);
+      mbar_init(&S.p_ready[x][1], 4 * PAIR);
       mbar_init(&S.o_done[x], 1);
     }
     S.nonfinite = 0;
     fence_mbar_init();
   }
-  if (warp == kMmaWarp) {
-    tmem_alloc(&S.tmem, kTmemCols);
-    tmem_relinquish();
-  }
+  if (warp == kMmaWarp) tmem_take<PAIR>(&S.tmem);
   if (warp == kTmaWarp && lane == 0) {
     prefetch_tmap(&qmap);
     prefetch_tmap(&kmap);
     prefetch_tmap(&vmap);
   }
-  int n = 0, b = -1;
-  if (tid < kMaxRows) {
-    const int row = row0 + tid;
-    if (tid < rows_here && row < p.rows) {
+  // both CTAs of a pair look at all its rows
+  for (int i = tid; i < kRows; i += Roles<F8>::kThreads) {
+    int n = 0, b = -1;
+    const int row = row0 + i;
+    if (i < rows_here && row < p.rows) {
       n = p.seq_lens[row];
       b = p.row_to_batch[row];
       if (n < 0 || n > p.max_len || b < 0 || b >= p.bt_rows ||
@@ -933,30 +1095,35 @@ __global__ void __launch_bounds__(Roles<F8>::kThreads, 1)
         b = -1;
       }
     }
-    S.row_n[tid] = n;
-    S.row_b[tid] = b;
-    S.seg_most[tid] = 0;
-    S.seg_least[tid] = S.seg_low[tid] = INT_MAX;
+    S.row_n[i] = n;
+    S.row_b[i] = b;
+    S.seg_most[i] = 0;
+    S.seg_least[i] = S.seg_low[i] = INT_MAX;
   }
   __syncthreads();
-  bool start = false;
-  uint32_t starts = 0;
-  if (tid < kMaxRows) {
-    start = tid < rows_here && (tid == 0 || S.row_b[tid - 1] != b);
-    starts = __ballot_sync(0xffffffffu, start);
-    if (lane == 0) S.warp_starts[warp] = __popc(starts);
+  // runs of one request, 32 rows to a warp
+  constexpr int kGroups = kRows / 32;
+  for (int w = warp; w < kGroups; w += Roles<F8>::kThreads / 32) {
+    const int i = 32 * w + lane;
+    const uint32_t starts =
+        __ballot_sync(0xffffffffu, i < rows_here && (i == 0 || S.row_b[i - 1] != S.row_b[i]));
+    if (lane == 0) S.warp_starts[w] = __popc(starts);
   }
   __syncthreads();
-  if (tid < kMaxRows) {
+  for (int w = warp; w < kGroups; w += Roles<F8>::kThreads / 32) {
+    const int i = 32 * w + lane;
+    const bool start = i < rows_here && (i == 0 || S.row_b[i - 1] != S.row_b[i]);
+    const uint32_t starts = __ballot_sync(0xffffffffu, start);
     int id = -1;
-    for (int w = 0; w < warp; ++w) id += S.warp_starts[w];
+    for (int v = 0; v < w; ++v) id += S.warp_starts[v];
     id += __popc(starts & ((2u << lane) - 1u));
-    if (start) S.seg_start[id] = tid;
-    if (tid == rows_here - 1) {
+    if (start) S.seg_start[id] = i;
+    if (i == rows_here - 1) {
       S.segs = id + 1;
       S.seg_start[id + 1] = rows_here;
     }
-    if (tid < rows_here && n > 0) {
+    const int n = S.row_n[i];
+    if (i < rows_here && n > 0) {
       atomicMax(&S.seg_most[id], n);
       atomicMin(&S.seg_least[id], n);
       atomicMin(&S.seg_low[id], p.window > 0 ? max(0, n - p.window) : 0);
@@ -964,10 +1131,11 @@ __global__ void __launch_bounds__(Roles<F8>::kThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
+  if (PAIR == 2) cluster_sync();  // the other CTA's barriers are set up
   tc_fence_after();
 
   bool ok = true;
-  // the softmax warps hold a row of S (128 registers); the others give up what
+  // the softmax warps hold (half of) a row of S; the others give up what
   // they take beyond the launch's share: 2 * 200 + 104 = 3 * 168 (12 warps),
   // 2 * 160 + 88 + 104 = 4 * 128 (16 warps)
   if (warp < kSoftmaxWarps) {
@@ -975,16 +1143,16 @@ __global__ void __launch_bounds__(Roles<F8>::kThreads, 1)
       asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
     else
       asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
-    ok = softmax_role<D, F8>(S, L, warp >> 2, kvh, chunk, row0);
+    ok = softmax_role<D, F8>(S, L, warp >> 2, kvh, chunk, row0, rank);
   } else if (warp < 12) {
     if (F8)
       asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     else
       asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
     if (warp == kTmaWarp) {
-      ok = tma_role<D, F8>(S, L, &qmap, &kmap, &vmap, kvh, chunk, row0);
+      ok = tma_role<D, F8>(S, L, &qmap, &kmap, &vmap, kvh, chunk, row0, rank);
     } else if (warp == kMmaWarp) {
-      if (lane == 0) ok = mma_role<D, F8>(S, L, chunk);
+      if (lane == 0 && rank == 0) ok = mma_role<D, F8>(S, L, chunk);
     } else if (!F8) {
       ok = prep_role<D>(S, L, chunk);
     }
@@ -996,27 +1164,30 @@ __global__ void __launch_bounds__(Roles<F8>::kThreads, 1)
   __syncwarp();
   tc_fence_before();
   __syncthreads();
+  // no CTA of a pair ends while the other may still read or signal it
+  if (PAIR == 2) cluster_sync();
   if (warp == kMmaWarp) {
     tc_fence_after();
-    tmem_dealloc(S.tmem, kTmemCols);
+    tmem_give<PAIR>(S.tmem);
   }
   if (p.chunks > 1) pdl_trigger();
 }
 
-// 4-D map of a cache: (dim, token, head, block), boxes of one block's tokens.
-bool cache_map(CUtensorMap* map, const void* base, const CacheView& c, const long long* st) {
+// 4-D map of a cache: (dim, token, head, block), boxes of `dims` dims of up to
+// `keys` tokens of a block. bf16: in the MMA's 128-byte swizzled layout; codes:
+// plain rows for the prep warps.
+bool cache_map(CUtensorMap* map, const void* base, const CacheView& c, const long long* st, int dims, int keys) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return false;
   const cuuint32_t bs = 1u << c.bs_log2;
-  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(c.dim), bs, static_cast<cuuint64_t>(c.heads),
+  const cuuint64_t size[4] = {static_cast<cuuint64_t>(c.dim), bs, static_cast<cuuint64_t>(c.heads),
                               static_cast<cuuint64_t>(c.num_blocks)};
   const cuuint64_t strides[3] = {static_cast<cuuint64_t>(st[2]), static_cast<cuuint64_t>(st[1]),
                                  static_cast<cuuint64_t>(st[0])};
-  // bf16: 64-dim slabs in the MMA's layout; codes: plain rows for the prep warps
-  const cuuint32_t box[4] = {c.f8 ? static_cast<cuuint32_t>(c.dim) : 64, bs, 1, 1};
+  const cuuint32_t box[4] = {static_cast<cuuint32_t>(dims), std::min(bs, static_cast<cuuint32_t>(keys)), 1, 1};
   const cuuint32_t one[4] = {1, 1, 1, 1};
   return fn(map, c.f8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base),
-            dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            size, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
             c.f8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -1038,14 +1209,17 @@ bool query_map(CUtensorMap* map, const AttnLaunch& p, int rows_per_tile) {
 
 template <int D, bool F8>
 cudaError_t launch_tiles_t(const AttnLaunch& p, cudaStream_t stream) {
+  using Sh = Shared<D, F8>;
+  constexpr int PAIR = kPair<D>;
   TilesLaunch L{p, kTile / p.group, 0};
-  L.row_tiles = (p.rows + 2 * L.rows_per_tile - 1) / (2 * L.rows_per_tile);
+  const int rows_here = 2 * PAIR * L.rows_per_tile;
+  L.row_tiles = (p.rows + rows_here - 1) / rows_here;
   CUtensorMap qmap, kmap, vmap;
-  if (!query_map(&qmap, p, L.rows_per_tile) || !cache_map(&kmap, p.c.k, p.c, p.c.kst) ||
-      !cache_map(&vmap, p.c.v, p.c, p.c.vst))
+  if (!query_map(&qmap, p, L.rows_per_tile) || !cache_map(&kmap, p.c.k, p.c, p.c.kst, F8 ? D : 64, Sh::kKeys) ||
+      !cache_map(&vmap, p.c.v, p.c, p.c.vst, Sh::kDims, kTile))
     return cudaErrorInvalidValue;
-  static_assert(sizeof(Shared<D, F8>) + 1024 <= 227 * 1024, "shared memory of a CTA");
-  constexpr size_t smem = sizeof(Shared<D, F8>) + 1024;
+  constexpr size_t smem = sizeof(Sh) + 1024;
+  static_assert(smem <= 227 * 1024, "shared memory of a CTA");
   static bool attr_done[64];
   int dev = 0;
   cudaGetDevice(&dev);
@@ -1055,10 +1229,19 @@ cudaError_t launch_tiles_t(const AttnLaunch& p, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     if (dev < 64) attr_done[dev] = true;
   }
-  const long long grid = static_cast<long long>(L.row_tiles) * p.c.heads * p.chunks;
+  const long long grid = static_cast<long long>(L.row_tiles) * p.c.heads * p.chunks * PAIR;
   if (grid > INT_MAX) return cudaErrorInvalidConfiguration;
-  attn_tiles_kernel<D, F8><<<static_cast<unsigned>(grid), Roles<F8>::kThreads, smem, stream>>>(L, qmap, kmap, vmap);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(Roles<F8>::kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim = {PAIR, 1, 1};
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, attn_tiles_kernel<D, F8>, L, qmap, kmap, vmap);
 }
 
 }  // namespace
@@ -1066,8 +1249,10 @@ cudaError_t launch_tiles_t(const AttnLaunch& p, cudaStream_t stream) {
 bool attn_tiles_apply(int group, float scale_log2) { return group <= kTile && scale_log2 > 0.f; }
 
 AttnPlan attn_tiles_plan(long long rows, int q_heads, int heads, int dim, long long max_keys, int num_sms) {
-  const int per = kTile / (q_heads / heads);
-  const long long units = (rows + 2 * per - 1) / (2 * per) * heads;
+  const int pair = dim == 128 ? kPair<128> : kPair<64>;
+  const int per = 2 * pair * (kTile / (q_heads / heads));
+  const long long units = (rows + per - 1) / per * heads;
+  num_sms /= pair;
   const long long tiles = std::max<long long>(1, (max_keys + kTile - 1) / kTile);
   // cost in tile steps: waves of CTAs, each its share of the tiles and about
   // four steps of start and end, and the partial results' traffic
