@@ -388,9 +388,8 @@ cudaError_t launch_append_kv(const AppendLaunch& p, cudaStream_t stream) {
   const int rows_per_cta = p.rows <= 512 ? 1 : 4;
   const int row_ctas = (p.q || !p.c.f8) ? (p.rows + rows_per_cta - 1) / rows_per_cta : 0;
   // decode rows are units of their own, one per warp; packed rows make units
-  // of up to a block, so a wider window wastes fewer CTAs on rows that only
-  // continue one
-  const int window = p.row_to_batch ? 32 : kWarps;
+  // of up to a block, so a window of a block leaves few CTAs without a unit
+  const int window = p.row_to_batch ? std::max(32, 1 << p.c.bs_log2) : kWarps;
   const long long block_ctas = p.c.f8 ? (static_cast<long long>(p.rows) + window - 1) / window * p.c.heads * 2 : 0;
   const long long grid = row_ctas + block_ctas;
   if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;

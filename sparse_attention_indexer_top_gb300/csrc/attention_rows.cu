@@ -15,8 +15,14 @@
 // through a private ring of 16-byte asynchronous copies (a lane computes its
 // key's address from the block table or the slot list, so pages of any size
 // and gathered slots are the same loop), and no CTA-wide barrier runs in the
-// loop. More than 16 heads per kv head: MT warps form a team that loads each
-// key once and shares it, one 16-head tile per warp.
+// loop.
+//
+// Up to 8 heads per kv head (FEW): the products are S^T = K Q^T and O^T =
+// V^T P^T, with the heads as the MMA's 8-wide side, so that no half of a tile is
+// padding; P goes from the accumulator layout to the operand's by one 8 x 8
+// transpose for 8 keys. Up to 16 heads: S = Q K^T, O = P V with the heads as the
+// 16-wide side. More: MT warps form a team that loads each key once and
+// shares it, one 16-head tile per warp.
 #include "sai_internal.h"
 #include "sai_ptx.cuh"
 
@@ -67,6 +73,12 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// Transpose of an 8 x 8 matrix of 16-bit values, row lane/4, columns 2(lane%4) + {0, 1} per lane.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -96,10 +108,14 @@ __device__ __forceinline__ float ex2(float x) {
 __device__ __forceinline__ float bf16_lo(uint32_t x) { return __uint_as_float(x << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t x) { return __uint_as_float(x & 0xffff0000u); }
 
-// Ring depth of each warp's (team's) 16-key (16 * MT keys) stages: as deep as
-// leaves two (bf16) or three (e4m3) CTAs per SM.
+// Ring depth of each warp's (team's) 16-key (16 * MT keys) stages. A group's
+// work is a chain of dependent steps, so more warps beat deeper rings: at dim
+// 128, 4096 rows on 512 slots take 427 us with two bf16 stages (three CTAs per
+// SM), 527 with three (two CTAs), 863 with four; e4m3 324 us with three stages,
+// 366 with four, 489 with six; 64 decode rows of 4096-32768 keys 712, 697, 842
+// and 411, 405, 519 us.
 template <int D, bool F8>
-constexpr int kDepth = F8 ? (D == 128 ? 4 : 6) : (D == 128 ? 3 : 5);
+constexpr int kDepth = F8 ? (D == 128 ? 3 : 4) : (D == 128 ? 2 : 3);
 
 // What a row sees: keys j in [0, count), key j being token j (j < low) or
 // shift + j of the request, or slot j.
@@ -144,7 +160,7 @@ __device__ __forceinline__ float join_factor(float2 ml, float base) {
 
 // OWN: each team has a unit (row, kv head, head group) of its own; else the
 // teams of a CTA share one unit's keys and join at the end.
-template <int D, bool F8, int MT, bool OWN>
+template <int D, bool F8, int MT, bool OWN, bool FEW>
 __global__ void __launch_bounds__(kThreads) attn_rows_kernel(const AttnLaunch p) {
   constexpr int E = F8 ? 1 : 2;
   constexpr int RB = D * E;         // bytes of a key row
@@ -155,13 +171,15 @@ __global__ void __launch_bounds__(kThreads) attn_rows_kernel(const AttnLaunch p)
   constexpr int KB = SK * RB;       // bytes of a stage's keys (and of its values)
   constexpr int STAGE = 2 * KB + SK * 8 + MT * 4 + (16 - MT * 4 % 16) % 16;
   constexpr int NS = D / 16;        // k16 steps of q.k, and 16-dim column groups of O
+  constexpr int HT = FEW ? 8 : 16;  // heads of a tile
+  static_assert(!FEW || MT == 1, "one tile of few heads");
 
   extern __shared__ __align__(128) unsigned char smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int team = warp / MT, mt = warp % MT;
   const int g = lane >> 2, t = lane & 3;
 
-  const int hg_count = (p.group + 16 * MT - 1) / (16 * MT);
+  const int hg_count = (p.group + HT * MT - 1) / (HT * MT);
   int chunk = 0, hg, kvh, row;
   if (OWN) {
     // kv head by kv head, so that the rows at work share one head's keys in L2
@@ -194,9 +212,9 @@ __global__ void __launch_bounds__(kThreads) attn_rows_kernel(const AttnLaunch p)
   }
 
   // ---- the 16 heads of this warp as A fragments; rows g and g + 8 per lane
-  const int head_in_group = hg * 16 * MT + mt * 16;
+  const int head_in_group = hg * HT * MT + mt * HT;
   const int head0 = kvh * p.group + head_in_group;
-  const bool v0 = head_in_group + g < p.group, v1 = head_in_group + g + 8 < p.group;
+  const bool v0 = head_in_group + g < p.group, v1 = !FEW && head_in_group + g + 8 < p.group;
   const uint16_t* q0 = p.q + static_cast<long long>(row) * p.q_row + static_cast<long long>(head0 + g) * D;
   const uint16_t* q1 = q0 + 8 * D;
   uint32_t qa[NS][4];
@@ -246,6 +264,10 @@ __global__ void __launch_bounds__(kThreads) attn_rows_kernel(const AttnLaunch p)
     const float f0 = factor(a0, &i0), f1 = factor(a1, &i1);
     sc0 *= i0;
     sc1 *= i1;
+    if (FEW) {  // the lane's scores are of heads 2t and 2t + 1
+      sc1 = __shfl_sync(0xffffffffu, sc0, 8 * t + 4);
+      sc0 = __shfl_sync(0xffffffffu, sc0, 8 * t);
+    }
 #pragma unroll
     for (int s = 0; s < NS; ++s) {
       qa[s][0] = pack_f16(bf16_lo(qa[s][0]) * f0, bf16_hi(qa[s][0]) * f0);
@@ -326,11 +348,12 @@ __global__ void __launch_bounds__(kThreads) attn_rows_kernel(const AttnLaunch p)
       named_bar(1 + team, 32 * MT);
   };
 
-  float o[NS][2][4];
+  constexpr int NO = FEW ? 1 : 2;  // accumulator tiles per 16 dims
+  float o[NS][NO][4];
 #pragma unroll
   for (int s = 0; s < NS; ++s)
 #pragma unroll
-    for (int e = 0; e < 2; ++e) o[s][e][0] = o[s][e][1] = o[s][e][2] = o[s][e][3] = 0.f;
+    for (int e = 0; e < NO; ++e) o[s][e][0] = o[s][e][1] = o[s][e][2] = o[s][e][3] = 0.f;
   float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
 
   {
@@ -354,6 +377,116 @@ __global__ void __launch_bounds__(kThreads) attn_rows_kernel(const AttnLaunch p)
         const uint32_t live = *reinterpret_cast<const uint32_t*>(stp + 2 * KB + SK * 8 + kg * 4);
         if (live == 0) continue;
         const uint32_t kb = st + kg * 16 * RB, vb = kb + KB;
+        if constexpr (FEW) {
+          // scores of 16 keys x 8 heads: the lane has keys g and g + 8 of
+          // heads 2t and 2t + 1
+          float c[4] = {0.f, 0.f, 0.f, 0.f}, c2[4] = {0.f, 0.f, 0.f, 0.f};  // two chains of products
+          const int krow = (lane & 7) + ((lane >> 3) & 1) * 8, khalf = lane >> 4;
+          if (!F8) {
+#pragma unroll
+            for (int s2 = 0; s2 < NS; ++s2) {
+              uint32_t r[4];
+              ldsm4(kb + krow * RB + (((2 * s2 + khalf) ^ (krow & 7)) << 4), r);
+              mma16816<false>(s2 & 1 ? c2 : c, r, qa[s2][0], qa[s2][2]);
+            }
+          } else {
+#pragma unroll
+            for (int s2 = 0; s2 < NS; s2 += 2) {
+              uint32_t r[4];
+              const int ch = s2 + khalf;
+              ldsm4(kb + krow * RB + ((CPR >= 8 ? (ch ^ (krow & 7)) : (ch ^ ((krow >> 1) & 3))) << 4), r);
+              const uint32_t a0[4] = {e4m3x2_f16x2(r[0]), e4m3x2_f16x2(r[1]), e4m3x2_f16x2_hi(r[0]),
+                                      e4m3x2_f16x2_hi(r[1])};
+              const uint32_t a1[4] = {e4m3x2_f16x2(r[2]), e4m3x2_f16x2(r[3]), e4m3x2_f16x2_hi(r[2]),
+                                      e4m3x2_f16x2_hi(r[3])};
+              mma16816<true>(c, a0, qa[s2][0], qa[s2][2]);
+              mma16816<true>(c2, a1, qa[s2 + 1][0], qa[s2 + 1][2]);
+            }
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) c[e] += c2[e];
+          float vs[2], ev[2];
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            const int key = g + 8 * n;
+            const bool on = (live >> key) & 1;
+            float k0 = sc0, k1 = sc1;
+            vs[n] = 1.f;
+            ev[n] = 0.f;
+            if (F8) {
+              const float* sp = reinterpret_cast<const float*>(stp + 2 * KB) + kg * 16 + key;
+              k0 *= sp[0];
+              k1 *= sp[0];
+              vs[n] = sp[SK];
+              ev[n] = static_cast<float>(max(kMinExp, static_cast<int>((__float_as_uint(vs[n]) >> 23) & 255) - 127));
+            }
+            c[2 * n] = on ? c[2 * n] * k0 : -INFINITY;
+            c[2 * n + 1] = on ? c[2 * n + 1] * k1 : -INFINITY;
+          }
+          float x0 = fmaxf(c[0] + ev[0], c[2] + ev[1]), x1 = fmaxf(c[1] + ev[0], c[3] + ev[1]);
+          if (__any_sync(0xffffffffu, x0 > m0 + 8.f || x1 > m1 + 8.f)) {
+#pragma unroll
+            for (int f = 4; f < 32; f <<= 1) {
+              x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, f));
+              x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, f));
+            }
+            const bool up0 = x0 > m0 + 8.f, up1 = x1 > m1 + 8.f;
+            const float f0 = up0 ? (m0 == -INFINITY ? 0.f : ex2(m0 - x0)) : 1.f;
+            const float f1 = up1 ? (m1 == -INFINITY ? 0.f : ex2(m1 - x1)) : 1.f;
+            if (up0) m0 = x0;
+            if (up1) m1 = x1;
+            l0 *= f0;
+            l1 *= f1;
+#pragma unroll
+            for (int s2 = 0; s2 < NS; ++s2) {
+              o[s2][0][0] *= f0;
+              o[s2][0][1] *= f1;
+              o[s2][0][2] *= f0;
+              o[s2][0][3] *= f1;
+            }
+          }
+          const float b0 = m0 == -INFINITY ? 0.f : m0, b1 = m1 == -INFINITY ? 0.f : m1;
+          uint32_t pb[2];
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            float w0 = ex2(c[2 * n] - b0), w1 = ex2(c[2 * n + 1] - b1);
+            l0 += w0;
+            l1 += w1;
+            if (F8) {
+              w0 *= vs[n];
+              w1 *= vs[n];
+            }
+            pb[n] = transpose8x8(F8 ? pack_f16(w0, w1) : pack_bf16(w0, w1));
+          }
+          if (!F8) {
+            const int vrow = (lane & 7) + (lane >> 4) * 8, vhalf = (lane >> 3) & 1;
+#pragma unroll
+            for (int s2 = 0; s2 < NS; ++s2) {
+              uint32_t r[4];
+              ldsm4_t(vb + vrow * RB + (((2 * s2 + vhalf) ^ (vrow & 7)) << 4), r);
+              mma16816<false>(o[s2][0], r, pb[0], pb[1]);
+            }
+          } else {
+            // transposed 16-bit pairs hold two dims of keys 2t and 2t + 1; a
+            // byte permute makes them two keys of one dim each: even dims of
+            // the 16-byte chunk are the tile's rows 0-7, odd dims rows 8-15
+            const int vrow = lane & 15, vhalf = lane >> 4;
+#pragma unroll
+            for (int s2 = 0; s2 < NS; s2 += 2) {
+              uint32_t r[4];
+              const int ch = s2 + vhalf;
+              ldsm4_t(vb + vrow * RB + ((CPR >= 8 ? (ch ^ (vrow & 7)) : (ch ^ ((vrow >> 1) & 3))) << 4), r);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) r[i] = __byte_perm(r[i], 0u, 0x3120);
+              const uint32_t a0[4] = {e4m3x2_f16x2(r[0]), e4m3x2_f16x2_hi(r[0]), e4m3x2_f16x2(r[1]),
+                                      e4m3x2_f16x2_hi(r[1])};
+              const uint32_t a1[4] = {e4m3x2_f16x2(r[2]), e4m3x2_f16x2_hi(r[2]), e4m3x2_f16x2(r[3]),
+                                      e4m3x2_f16x2_hi(r[3])};
+              mma16816<true>(o[s2][0], a0, pb[0], pb[1]);
+              mma16816<true>(o[s2 + 1][0], a1, pb[0], pb[1]);
+            }
+          }
+        } else {
         // scores of 16 heads x 16 keys
         float c[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
         const int krow = (lane & 7) + ((lane >> 4) & 1) * 8, khalf = (lane >> 3) & 1;
@@ -401,14 +534,15 @@ __global__ void __launch_bounds__(kThreads) attn_rows_kernel(const AttnLaunch p)
             x0 = fmaxf(x0, c[n][e] + ev);
             x1 = fmaxf(x1, c[n][e + 2] + ev);
           }
-        x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 1));
-        x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 1));
-        x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 2));
-        x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 2));
         // the maximum moves only when it is passed by more than 2^8 (weights
         // up to 256 are as exact as weights up to 1), so O is rarely rescaled
-        const bool up0 = x0 > m0 + 8.f, up1 = x1 > m1 + 8.f;
-        if (__any_sync(0xffffffffu, up0 || up1)) {
+        if (__any_sync(0xffffffffu, x0 > m0 + 8.f || x1 > m1 + 8.f)) {
+#pragma unroll
+          for (int f = 1; f < 4; f <<= 1) {
+            x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, f));
+            x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, f));
+          }
+          const bool up0 = x0 > m0 + 8.f, up1 = x1 > m1 + 8.f;
           const float f0 = up0 ? (m0 == -INFINITY ? 0.f : ex2(m0 - x0)) : 1.f;
           const float f1 = up1 ? (m1 == -INFINITY ? 0.f : ex2(m1 - x1)) : 1.f;
           if (up0) m0 = x0;
@@ -418,7 +552,7 @@ __global__ void __launch_bounds__(kThreads) attn_rows_kernel(const AttnLaunch p)
 #pragma unroll
           for (int s2 = 0; s2 < NS; ++s2)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
+            for (int e = 0; e < NO; ++e) {
               o[s2][e][0] *= f0;
               o[s2][e][1] *= f0;
               o[s2][e][2] *= f1;
@@ -460,7 +594,7 @@ __global__ void __launch_bounds__(kThreads) attn_rows_kernel(const AttnLaunch p)
             uint32_t r[4];
             ldsm4_t(vb + vrow * RB + (((2 * s2 + vhalf) ^ (vrow & 7)) << 4), r);
             mma16816<false>(o[s2][0], pa, r[0], r[1]);
-            mma16816<false>(o[s2][1], pa, r[2], r[3]);
+            mma16816<false>(o[s2][NO - 1], pa, r[2], r[3]);
           }
         } else {
           // transposed 16-bit pairs hold two dims of keys 2t and 2t + 1; a
@@ -474,20 +608,22 @@ __global__ void __launch_bounds__(kThreads) attn_rows_kernel(const AttnLaunch p)
 #pragma unroll
             for (int i = 0; i < 4; ++i) r[i] = __byte_perm(r[i], 0u, 0x3120);
             mma16816<true>(o[s2][0], pa, e4m3x2_f16x2(r[0]), e4m3x2_f16x2(r[1]));
-            mma16816<true>(o[s2][1], pa, e4m3x2_f16x2_hi(r[0]), e4m3x2_f16x2_hi(r[1]));
+            mma16816<true>(o[s2][NO - 1], pa, e4m3x2_f16x2_hi(r[0]), e4m3x2_f16x2_hi(r[1]));
             mma16816<true>(o[s2 + 1][0], pa, e4m3x2_f16x2(r[2]), e4m3x2_f16x2(r[3]));
-            mma16816<true>(o[s2 + 1][1], pa, e4m3x2_f16x2_hi(r[2]), e4m3x2_f16x2_hi(r[3]));
+            mma16816<true>(o[s2 + 1][NO - 1], pa, e4m3x2_f16x2_hi(r[2]), e4m3x2_f16x2_hi(r[3]));
           }
+        }
         }
       }
     }
   }
   cp_wait<0>();
   if (bad_slot) atomicOr(p.status, kDevBadPage);
-  l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
-  l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
-  l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
-  l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
+#pragma unroll
+  for (int f = FEW ? 4 : 1; f < (FEW ? 32 : 4); f <<= 1) {
+    l0 += __shfl_xor_sync(0xffffffffu, l0, f);
+    l1 += __shfl_xor_sync(0xffffffffu, l1, f);
+  }
 
   // ---- join the teams' results (same head tile mt, different keys); with
   // OWN the same way through the team's own ring, for whole-line stores
@@ -500,49 +636,67 @@ __global__ void __launch_bounds__(kThreads) attn_rows_kernel(const AttnLaunch p)
   };
   part_sync();  // the ring is done with; its memory holds the partial results
   constexpr int OS = D + 4;  // floats between rows
-  float* po = reinterpret_cast<float*>(OWN ? ring : smem);          // [JOIN * MT][16][OS]
-  float2* pml = reinterpret_cast<float2*>(po + JOIN * MT * 16 * OS);  // [JOIN * MT][16]
+  float* po = reinterpret_cast<float*>(OWN ? ring : smem);            // [JOIN * MT][HT][OS]
+  float2* pml = reinterpret_cast<float2*>(po + JOIN * MT * HT * OS);  // [JOIN * MT][HT]
   {
     const int slot = OWN ? mt : warp;
-    float* w = po + slot * 16 * OS;
+    float* w = po + slot * HT * OS;
+    if constexpr (FEW) {
+      float *w0 = w + 2 * t * OS, *w1 = w0 + OS;
 #pragma unroll
-    for (int s = 0; s < NS; ++s) {
-      if (!F8) {
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int d = 16 * s + 8 * e + 2 * t;
-          *reinterpret_cast<float2*>(w + g * OS + d) = make_float2(o[s][e][0], o[s][e][1]);
-          *reinterpret_cast<float2*>(w + (g + 8) * OS + d) = make_float2(o[s][e][2], o[s][e][3]);
-        }
-      } else {
-        const int d = 16 * s + 4 * t;
-        *reinterpret_cast<float4*>(w + g * OS + d) = make_float4(o[s][0][0], o[s][1][0], o[s][0][1], o[s][1][1]);
-        *reinterpret_cast<float4*>(w + (g + 8) * OS + d) = make_float4(o[s][0][2], o[s][1][2], o[s][0][3], o[s][1][3]);
+      for (int s = 0; s < NS; ++s) {
+        const int d = 16 * s + (F8 ? 2 * g : g), d2 = d + (F8 ? 1 : 8);
+        w0[d] = o[s][0][0];
+        w1[d] = o[s][0][1];
+        w0[d2] = o[s][0][2];
+        w1[d2] = o[s][0][3];
       }
-    }
-    if (t == 0) {
-      pml[slot * 16 + g] = make_float2(m0, l0);
-      pml[slot * 16 + g + 8] = make_float2(m1, l1);
+      if (g == 0) {
+        pml[slot * HT + 2 * t] = make_float2(m0, l0);
+        pml[slot * HT + 2 * t + 1] = make_float2(m1, l1);
+      }
+    } else {
+#pragma unroll
+      for (int s = 0; s < NS; ++s) {
+        if (!F8) {
+#pragma unroll
+          for (int e = 0; e < NO; ++e) {
+            const int d = 16 * s + 8 * e + 2 * t;
+            *reinterpret_cast<float2*>(w + g * OS + d) = make_float2(o[s][e][0], o[s][e][1]);
+            *reinterpret_cast<float2*>(w + (g + 8) * OS + d) = make_float2(o[s][e][2], o[s][e][3]);
+          }
+        } else {
+          const int d = 16 * s + 4 * t;
+          *reinterpret_cast<float4*>(w + g * OS + d) =
+              make_float4(o[s][0][0], o[s][NO - 1][0], o[s][0][1], o[s][NO - 1][1]);
+          *reinterpret_cast<float4*>(w + (g + 8) * OS + d) =
+              make_float4(o[s][0][2], o[s][NO - 1][2], o[s][0][3], o[s][NO - 1][3]);
+        }
+      }
+      if (t == 0) {
+        pml[slot * HT + g] = make_float2(m0, l0);
+        pml[slot * HT + g + 8] = make_float2(m1, l1);
+      }
     }
   }
   part_sync();
   constexpr int LPR = D / 4;  // lanes of four dims to a head row
-  for (int i = OWN ? mt * 32 + lane : threadIdx.x; i < min(16 * MT, p.group - hg * 16 * MT) * LPR;
+  for (int i = OWN ? mt * 32 + lane : threadIdx.x; i < min(HT * MT, p.group - hg * HT * MT) * LPR;
        i += OWN ? 32 * MT : kThreads) {
     const int hr = i / LPR, d = (i % LPR) * 4;
-    const int tile = hr / 16, r = hr % 16;
-    const int hin = hg * 16 * MT + hr;
+    const int tile = hr / HT, r = hr % HT;
+    const int hin = hg * HT * MT + hr;
     float m = -INFINITY;
 #pragma unroll
-    for (int k = 0; k < JOIN; ++k) m = fmaxf(m, pml[(k * MT + tile) * 16 + r].x);
+    for (int k = 0; k < JOIN; ++k) m = fmaxf(m, pml[(k * MT + tile) * HT + r].x);
     const float base = m == -INFINITY ? 0.f : m;
     float l = 0.f;
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int k = 0; k < JOIN; ++k) {
-      const float2 ml = pml[(k * MT + tile) * 16 + r];
+      const float2 ml = pml[(k * MT + tile) * HT + r];
       const float f = join_factor(ml, base);
-      const float4 x = *reinterpret_cast<const float4*>(po + ((k * MT + tile) * 16 + r) * OS + d);
+      const float4 x = *reinterpret_cast<const float4*>(po + ((k * MT + tile) * HT + r) * OS + d);
       l += f * ml.y;
       a.x += f * x.x;
       a.y += f * x.y;
@@ -617,35 +771,37 @@ constexpr size_t rows_smem() {
   return ring > join ? ring : join;
 }
 
-template <int D, bool F8, int MT, bool OWN>
+template <int D, bool F8, int MT, bool OWN, bool FEW>
 cudaError_t launch_rows_t(const AttnLaunch& p, cudaStream_t stream) {
   constexpr size_t smem = rows_smem<D, F8, MT>();
   static bool attr_done[64];
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev >= 64 || !attr_done[dev]) {
-    cudaError_t e = cudaFuncSetAttribute(attn_rows_kernel<D, F8, MT, OWN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    cudaError_t e = cudaFuncSetAttribute(attn_rows_kernel<D, F8, MT, OWN, FEW>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          static_cast<int>(smem));
     if (e != cudaSuccess) return e;
     if (dev < 64) attr_done[dev] = true;
   }
-  const long long groups = (p.group + 16 * MT - 1) / (16 * MT);
+  constexpr int heads = (FEW ? 8 : 16) * MT;
+  const long long groups = (p.group + heads - 1) / heads;
   long long grid = static_cast<long long>(p.rows) * p.c.heads * groups * p.chunks;
   if (OWN) grid = (grid * MT + kWarps - 1) / kWarps;
-  attn_rows_kernel<D, F8, MT, OWN><<<static_cast<unsigned>(grid), kThreads, smem, stream>>>(p);
+  attn_rows_kernel<D, F8, MT, OWN, FEW><<<static_cast<unsigned>(grid), kThreads, smem, stream>>>(p);
   return cudaGetLastError();
 }
 
-template <int D, bool F8, int MT>
+template <int D, bool F8, int MT, bool FEW>
 cudaError_t launch_rows_m(const AttnLaunch& p, cudaStream_t stream) {
-  return p.own ? launch_rows_t<D, F8, MT, true>(p, stream) : launch_rows_t<D, F8, MT, false>(p, stream);
+  return p.own ? launch_rows_t<D, F8, MT, true, FEW>(p, stream) : launch_rows_t<D, F8, MT, false, FEW>(p, stream);
 }
 
 template <int D, bool F8>
 cudaError_t launch_rows_d(const AttnLaunch& p, cudaStream_t stream) {
-  if (p.group <= 16) return launch_rows_m<D, F8, 1>(p, stream);
-  if (p.group <= 32) return launch_rows_m<D, F8, 2>(p, stream);
-  return launch_rows_m<D, F8, 4>(p, stream);
+  if (p.group <= 8) return launch_rows_m<D, F8, 1, true>(p, stream);
+  if (p.group <= 16) return launch_rows_m<D, F8, 1, false>(p, stream);
+  if (p.group <= 32) return launch_rows_m<D, F8, 2, false>(p, stream);
+  return launch_rows_m<D, F8, 4, false>(p, stream);
 }
 
 }  // namespace
