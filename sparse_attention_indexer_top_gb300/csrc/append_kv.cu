@@ -136,64 +136,67 @@ __device__ __forceinline__ void rotate(float (&a)[8], float (&b)[8], const Angle
 }
 
 // ------------------------------------------------------------- row CTAs
-// `rows` neighbouring rows: their query heads, and with a bf16 cache their
-// keys and values. A thread stays with one row and one place in the heads, so
-// it loads its angles once; four heads' loads are in flight at a time.
-__device__ void row_cta(const AppendLaunch& p, int row0, int rows) {
-  const int lph = p.c.dim / 16;  // lanes to a head
-  const int slots = kThreads / lph / rows;  // heads of a row at once
-  const int l = threadIdx.x % lph, slot = threadIdx.x / lph;
-  const int row = row0 + slot / slots;
-  if (row >= p.rows || slot >= slots * rows) return;
-  const RowPlace r = row_place(p, row, l == 0 && slot % slots == 0);
-  const Chunks ch = chunks_of(l, p.rot, p.c.dim);
-  const bool turn = ch.rotated && r.pos >= 0;
-  Angles ang;
-  if (turn) load_angles(p, r.pos, ch, ang);
-  const int kv = p.c.f8 ? 0 : p.c.heads;
-  const int off = r.pos & ((1 << p.c.bs_log2) - 1);
-  const int all = p.q_heads + 2 * kv;
+// n heads of one row, `src_step` values and `dst_step` bytes apart, four of
+// them in flight.
+__device__ __forceinline__ void move_heads(const uint16_t* src, int src_step, char* dst, long long dst_step, int n,
+                                           const Chunks& ch, bool live, bool turn, const Angles& ang, int interleaved) {
   constexpr int kAhead = 4;
-  for (int h0 = slot % slots; h0 < all; h0 += kAhead * slots) {
+  for (; n > 0; n -= kAhead) {
     uint4 xa[kAhead], xb[kAhead];
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
-      const int h = h0 + j * slots;
       xa[j] = xb[j] = make_uint4(0, 0, 0, 0);
-      if (h < all && r.pos >= 0) {
-        const uint16_t* src = h < p.q_heads        ? p.q + row * p.q_row + static_cast<long long>(h) * p.c.dim
-                              : h < p.q_heads + kv ? p.k + row * p.k_row + static_cast<long long>(h - p.q_heads) * p.c.dim
-                                                   : p.v + row * p.v_row +
-                                                         static_cast<long long>(h - p.q_heads - kv) * p.c.dim;
-        xa[j] = __ldg(reinterpret_cast<const uint4*>(src) + ch.a);
-        xb[j] = __ldg(reinterpret_cast<const uint4*>(src) + ch.b);
+      if (j < n && live) {
+        xa[j] = __ldg(reinterpret_cast<const uint4*>(src + j * src_step) + ch.a);
+        xb[j] = __ldg(reinterpret_cast<const uint4*>(src + j * src_step) + ch.b);
       }
     }
+    src += kAhead * src_step;
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
-      const int h = h0 + j * slots;
-      if (h >= all) break;
-      const bool is_q = h < p.q_heads, is_v = h >= p.q_heads + kv;
-      if (!is_q && r.pos < 0) continue;
-      if (turn && !is_v) {
+      if (j >= n) break;
+      if (turn) {
         float a[8], b[8];
         unpack8(xa[j], a);
         unpack8(xb[j], b);
-        rotate(a, b, ang, p.interleaved);
+        rotate(a, b, ang, interleaved);
         xa[j] = pack8(a);
         xb[j] = pack8(b);
       }
-      char* dst;
-      if (is_q) {
-        dst = reinterpret_cast<char*>(p.out_q + (static_cast<long long>(row) * p.q_heads + h) * p.c.dim);
-      } else {
-        const long long* st = is_v ? p.c.vst : p.c.kst;
-        dst = (is_v ? p.c.v : p.c.k) + r.blk * st[0] + (h - p.q_heads - (is_v ? kv : 0)) * st[1] + off * st[2];
-      }
       reinterpret_cast<uint4*>(dst)[ch.a] = xa[j];
       reinterpret_cast<uint4*>(dst)[ch.b] = xb[j];
+      dst += dst_step;
     }
   }
+}
+
+// `rows` neighbouring rows: their query heads, and with a bf16 cache their
+// keys and values. A thread stays with one row and one place in the heads, so
+// it loads its angles once.
+__device__ __forceinline__ void row_cta(const AppendLaunch& p, int row0, int rows) {
+  const int dim = p.c.dim, lph = dim / 16;  // lanes to a head
+  const int slots = kThreads / lph / rows;  // heads of a row at once
+  const int l = threadIdx.x % lph, slot = threadIdx.x / lph;
+  const int row = row0 + slot / slots, first = slot % slots;
+  if (row >= p.rows || slot >= slots * rows) return;
+  const RowPlace r = row_place(p, row, l == 0 && first == 0);
+  const Chunks ch = chunks_of(l, p.rot, dim);
+  const bool live = r.pos >= 0, turn = ch.rotated && live;
+  Angles ang;
+  if (turn) load_angles(p, r.pos, ch, ang);
+  const int step = slots * dim;
+  if (p.q) {
+    char* dst = reinterpret_cast<char*>(p.out_q + (static_cast<long long>(row) * p.q_heads + first) * dim);
+    move_heads(p.q + row * p.q_row + first * dim, step, dst, 2 * step, (p.q_heads - first + slots - 1) / slots, ch, live,
+               turn, ang, p.interleaved);
+  }
+  if (p.c.f8 || !live) return;
+  const int n = (p.c.heads - first + slots - 1) / slots;
+  const long long off = r.pos & ((1 << p.c.bs_log2) - 1);
+  move_heads(p.k + row * p.k_row + first * dim, step, p.c.k + r.blk * p.c.kst[0] + first * p.c.kst[1] + off * p.c.kst[2],
+             slots * p.c.kst[1], n, ch, true, turn, ang, p.interleaved);
+  move_heads(p.v + row * p.v_row + first * dim, step, p.c.v + r.blk * p.c.vst[0] + first * p.c.vst[1] + off * p.c.vst[2],
+             slots * p.c.vst[1], n, ch, true, false, ang, p.interleaved);
 }
 
 // ------------------------------------------------------------- block CTAs
@@ -216,13 +219,23 @@ __device__ __forceinline__ float needed_scale(float amax) {
   return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
 }
 
-// Values of token `row`, head h, lane l's 16 dims; rotated when they are keys.
+// The lane's 16 dims of token `row`, head h, as they came.
+struct Raw {
+  uint4 a, b;
+};
 template <bool KEYS>
-__device__ __forceinline__ void load_values(const AppendLaunch& p, int row, int pos, int h, const Chunks& ch,
-                                            float (&a)[8], float (&b)[8]) {
-  const uint16_t* src = (KEYS ? p.k + row * p.k_row : p.v + row * p.v_row) + static_cast<long long>(h) * p.c.dim;
-  unpack8(__ldg(reinterpret_cast<const uint4*>(src) + ch.a), a);
-  unpack8(__ldg(reinterpret_cast<const uint4*>(src) + ch.b), b);
+__device__ __forceinline__ Raw load_raw(const AppendLaunch& p, int row, int h, const Chunks& ch) {
+  const uint4* src = reinterpret_cast<const uint4*>((KEYS ? p.k + row * p.k_row : p.v + row * p.v_row) +
+                                                    static_cast<long long>(h) * p.c.dim);
+  return Raw{__ldg(src + ch.a), __ldg(src + ch.b)};
+}
+// ... and as they are stored: keys rotated. Done once for the scale and once
+// for the codes: the raw values are half the registers of the rotated ones.
+template <bool KEYS>
+__device__ __forceinline__ void values_of(const AppendLaunch& p, const Raw& x, int pos, const Chunks& ch, float (&a)[8],
+                                          float (&b)[8]) {
+  unpack8(x.a, a);
+  unpack8(x.b, b);
   if (KEYS && ch.rotated) {
     Angles g;
     load_angles(p, pos, ch, g);
@@ -262,6 +275,7 @@ __device__ void block_cta(const AppendLaunch& p, int r0, int window, int h) {
   __shared__ uint32_t s_more[kWarps];  // bit j: row r0 + j goes on with the unit of the row before it
   __shared__ uint32_t s_live[kWarps];  // bit j: row r0 + j is appended
   __shared__ float s_amax[kWarps];
+  __shared__ int s_pos[kThreads], s_blk[kThreads];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int dim = p.c.dim, lph = dim / 16;
   const int bs = 1 << p.c.bs_log2;
@@ -279,6 +293,8 @@ __device__ void block_cta(const AppendLaunch& p, int r0, int window, int h) {
       const int b = p.row_to_batch ? p.row_to_batch[row - 1] : row - 1;
       more = n == r.pos && b == r.batch;  // the row before is the token before (a live row: same block)
     }
+    s_pos[tid] = r.pos;
+    s_blk[tid] = r.blk;
     const uint32_t live = __ballot_sync(0xffffffffu, r.pos >= 0);
     const uint32_t go = __ballot_sync(0xffffffffu, more);
     if (lane == 0) {
@@ -303,16 +319,14 @@ __device__ void block_cta(const AppendLaunch& p, int r0, int window, int h) {
   const int l = lane % lph;
   const Chunks ch = chunks_of(l, KEYS ? p.rot : 0, dim);
   int small = 0;
-  for (int j = 0; j < window; ++j) {
-    if (!((s_live[j >> 5] >> (j & 31)) & 1) || ((s_more[j >> 5] >> (j & 31)) & 1)) continue;
+  // the unit that begins at row r0 + j
+  auto unit = [&](int j) {
     const int len = unit_len(j);
     const bool by_warp = len <= kSmallUnit;
-    if (by_warp && (small++ % kWarps) != warp) continue;
+    if (by_warp && (small++ % kWarps) != warp) return;
     const int row = r0 + j;
-    const int pos = p.seq_lens[row] - 1;
-    const int b = p.row_to_batch ? p.row_to_batch[row] : row;
+    const int pos = s_pos[j], blk = s_blk[j];
     const int off = pos & (bs - 1);
-    const int blk = p.block_table[b * p.bt_stride + (pos >> p.c.bs_log2)];
     char* base = cache + blk * st[0];
     float* scale = scales + static_cast<long long>(blk) * p.c.heads + h;
     const float old = off ? *scale : 0.f;
@@ -322,7 +336,7 @@ __device__ void block_cta(const AppendLaunch& p, int r0, int window, int h) {
       const bool on = tok < len && tok < tpw;
       float a[8], bb[8], m = 0.f;
       if (on) {
-        load_values<KEYS>(p, row + tok, pos + tok, h, ch, a, bb);
+        values_of<KEYS>(p, load_raw<KEYS>(p, row + tok, h, ch), pos + tok, ch, a, bb);
         m = amax16(a, bb, 0.f);
       }
 #pragma unroll
@@ -334,13 +348,18 @@ __device__ void block_cta(const AppendLaunch& p, int r0, int window, int h) {
       if (lane == 0) *scale = s;
     } else {
       const int tok0 = tid / lph, tstep = kThreads / lph;
-      float a[TPT][8], bb[TPT][8], m = 0.f;
+      Raw x[TPT];
+      float m = 0.f;
+#pragma unroll
+      for (int i = 0; i < TPT; ++i)
+        if (tok0 + i * tstep < len) x[i] = load_raw<KEYS>(p, row + tok0 + i * tstep, h, ch);
 #pragma unroll
       for (int i = 0; i < TPT; ++i) {
         const int tok = tok0 + i * tstep;
         if (tok < len) {
-          load_values<KEYS>(p, row + tok, pos + tok, h, ch, a[i], bb[i]);
-          m = amax16(a[i], bb[i], m);
+          float a[8], bb[8];
+          values_of<KEYS>(p, x[i], pos + tok, ch, a, bb);
+          m = amax16(a, bb, m);
         }
       }
 #pragma unroll
@@ -354,17 +373,29 @@ __device__ void block_cta(const AppendLaunch& p, int r0, int window, int h) {
 #pragma unroll
       for (int i = 0; i < TPT; ++i) {
         const int tok = tok0 + i * tstep;
-        if (tok < len) store_codes(base + (off + tok) * st[2], ch, a[i], bb[i], inv);
+        if (tok < len) {
+          float a[8], bb[8];
+          // opaque, or the compiler keeps the rotated values of the first time
+          asm volatile("" : "+r"(x[i].a.x), "+r"(x[i].a.y), "+r"(x[i].a.z), "+r"(x[i].a.w), "+r"(x[i].b.x),
+                       "+r"(x[i].b.y), "+r"(x[i].b.z), "+r"(x[i].b.w));
+          values_of<KEYS>(p, x[i], pos + tok, ch, a, bb);
+          store_codes(base + (off + tok) * st[2], ch, a, bb, inv);
+        }
       }
       if (off && s != old) rescale_cells(base, st[2], off, dim, old / s, tid, kThreads);
       __syncthreads();  // s_amax and the old scale have been read
       if (tid == 0) *scale = s;
     }
+  };
+  for (int w = 0; w < window; w += 32) {
+    uint32_t begins = s_live[w >> 5] & ~s_more[w >> 5];
+    if (window - w < 32) begins &= (1u << (window - w)) - 1u;
+    for (; begins; begins &= begins - 1) unit(w + __ffs(begins) - 1);
   }
 }
 
 template <int TPT>
-__global__ void __launch_bounds__(kThreads) append_kv_kernel(const AppendLaunch p, int rows_per_cta,
+__global__ void __launch_bounds__(kThreads, 3) append_kv_kernel(const AppendLaunch p, int rows_per_cta,
                                                               int block_ctas, int window) {
   // the block CTAs first: they are the longer ones
   if (static_cast<int>(blockIdx.x) >= block_ctas) {
