@@ -580,15 +580,19 @@ __device__ __forceinline__ bool softmax_role(Shared<D, F8>& S, const TilesLaunch
       const bool whole = t0 + kTile <= ln.n && (t0 >= ln.first || t0 + kTile <= ln.sinks);
       const bool masked = !__all_sync(0xffffffffu, whole) || bad;
       if (bad && lane == 0) atomicOr(p.status, kDevBadPage);
-      // scores of columns [c0, c0 + 32) that the row does not see become -inf
+      // scores of columns [c0, c0 + 32) that the row does not see become -inf:
+      // one bit a column, so that an element costs a test and a select
       auto mask = [&](uint32_t* s, int c0) {
-        const int hi = ln.n - t0 - c0, lo = ln.first - t0 - c0, sk = ln.sinks - t0 - c0;
-        const uint32_t dead = bad >> (c0 / 16);
+        auto below = [&](int x) {  // the bits under column x of the tile
+          x -= t0 + c0;
+          return x <= 0 ? 0u : x >= 32 ? ~0u : (1u << x) - 1u;
+        };
+        uint32_t see = below(ln.n) & (~below(ln.first) | below(ln.sinks));
+        if ((bad >> (c0 / 16)) & 1) see &= 0xffff0000u;
+        if ((bad >> (c0 / 16)) & 2) see &= 0x0000ffffu;
 #pragma unroll
-        for (int c = 0; c < 32; ++c) {
-          const bool see = c < hi && (c >= lo || c < sk) && !((dead >> (c / 16)) & 1);
-          if (!see) s[c] = 0xff800000u;
-        }
+        for (int c = 0; c < 32; ++c)
+          if (!(see & (1u << c))) s[c] = 0xff800000u;
       };
       // largest exponent of 32 columns
       auto largest = [&](const uint32_t* s, int c0, float top) {
