@@ -84,24 +84,25 @@ long long most_keys(int32_t max_seq_len, int32_t window, int32_t sinks) {
   return std::min<long long>(max_seq_len, static_cast<long long>(window) + sinks);
 }
 
-// Splits rows over key chunks and launches the row or the tile kernel.
-int run_attention(sai::AttnLaunch& p, bool tiles, long long max_keys, void* workspace, size_t workspace_bytes, int sms,
-                  sai_stream_t stream) {
-  const sai::AttnPlan plan =
-      tiles ? sai::attn_tiles_plan(p.rows, p.q_heads, p.c.heads, p.c.dim, max_keys, sms)
-            : sai::attn_rows_plan(p.rows, p.q_heads, p.c.heads, p.c.dim, p.c.f8, max_keys, sms);
-  if (plan.workspace_bytes && (!workspace || workspace_bytes < plan.workspace_bytes || !aligned(workspace, 16)))
-    return SAI_ERR_WORKSPACE;
+bool space(const void* workspace, size_t bytes, size_t need) {
+  return need == 0 || (workspace && bytes >= need && aligned(workspace, 16));
+}
+
+// Splits rows over key chunks and launches the row kernel.
+int run_rows(sai::AttnLaunch& p, long long max_keys, void* workspace, size_t workspace_bytes, int sms,
+             sai_stream_t stream) {
+  const sai::AttnPlan plan = sai::attn_rows_plan(p.rows, p.q_heads, p.c.heads, p.c.dim, p.c.f8, max_keys, sms);
+  if (!space(workspace, workspace_bytes, plan.workspace_bytes)) return SAI_ERR_WORKSPACE;
   p.chunks = plan.chunks;
   p.own = plan.own;
-  if (plan.chunks > 1) {
+  p.clustered = plan.clustered;
+  if (plan.workspace_bytes) {
     p.part_o = static_cast<float*>(workspace);
     p.part_ml = reinterpret_cast<float2*>(p.part_o + static_cast<size_t>(p.rows) * p.q_heads * plan.chunks * p.c.dim);
   }
   const long long units = static_cast<long long>(p.rows) * p.c.heads * ((p.group + 15) / 16) * plan.chunks;
   if (units > INT_MAX || static_cast<long long>(p.rows) * p.q_heads > INT_MAX) return SAI_ERR_SHAPE;
-  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  return cuda_status(tiles ? sai::launch_attn_tiles(p, s) : sai::launch_attn_rows(p, s));
+  return cuda_status(sai::launch_attn_rows(p, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 }  // namespace
@@ -162,7 +163,7 @@ size_t sai_paged_attention_workspace(int64_t rows, int32_t q_heads, int32_t head
   size_t bytes = sai::attn_rows_plan(rows, q_heads, heads, dim, f8, keys, sms).workspace_bytes;
   // enough for either kernel: the tile kernel leaves calls with sm_scale <= 0 to the row kernel
   if (packed && sai::attn_tiles_apply(q_heads / heads, 1.f))
-    bytes = std::max(bytes, sai::attn_tiles_plan(rows, q_heads, heads, dim, keys, sms).workspace_bytes);
+    bytes = std::max(bytes, sai::attn_tiles_workspace(rows, q_heads, heads, dim, keys, sms));
   return bytes;
 }
 
@@ -197,8 +198,13 @@ int sai_paged_attention(const uint16_t* q, int64_t q_row_stride, int32_t q_heads
   p.scale_log2 = sm_scale * 1.44269504088896340736f;
   p.out = out;
   p.lse = out_lse;
-  const bool tiles = packed && sai::attn_tiles_apply(p.group, p.scale_log2);
-  return run_attention(p, tiles, most_keys(max_seq_len, window, sinks), workspace, workspace_bytes, sms, stream);
+  const long long keys = most_keys(max_seq_len, window, sinks);
+  if (packed && sai::attn_tiles_apply(p.group, p.scale_log2)) {
+    const size_t need = sai::attn_tiles_workspace(rows, q_heads, p.c.heads, p.c.dim, keys, sms);
+    if (!space(workspace, workspace_bytes, need)) return SAI_ERR_WORKSPACE;
+    return cuda_status(sai::launch_attn_tiles(p, keys, workspace, sms, reinterpret_cast<cudaStream_t>(stream)));
+  }
+  return run_rows(p, keys, workspace, workspace_bytes, sms, stream);
 }
 
 size_t sai_sparse_attention_workspace(int64_t rows, int32_t q_heads, int32_t heads, int32_t dim, int32_t dtype,
@@ -236,7 +242,7 @@ int sai_sparse_attention(const uint16_t* q, int64_t q_row_stride, int32_t q_head
   p.scale_log2 = sm_scale * 1.44269504088896340736f;
   p.out = out;
   p.lse = out_lse;
-  return run_attention(p, false, k, workspace, workspace_bytes, sms, stream);
+  return run_rows(p, k, workspace, workspace_bytes, sms, stream);
 }
 
 }  // extern "C"

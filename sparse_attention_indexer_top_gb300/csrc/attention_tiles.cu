@@ -26,6 +26,12 @@
 // pair needs 96 and half the copies. The first CTA's MMA thread issues for
 // both; the second CTA's softmax and prep warps report to its barriers.
 //
+// Work: a unit is a kv head and the rows of one CTA (pair). With many units
+// each CTA (pair) takes one; with few, the CTAs stay and the units' key tiles,
+// end to end, are dealt out in equal shares, so that the last wave is full and
+// a few long units fill the GPU: a unit cut by a share's border leaves two or
+// more partial results (maximum, sum, O) that a second kernel joins.
+//
 // Roles (bf16 cache, 12 warps): 0-3 softmax of tile A, 4-7 softmax of tile B,
 // 8 TMA, 9 MMA, 10-11 "prep", which makes the value tile safe to multiply: a
 // weight of 0 times a NaN or infinity that a row must not see would still be
@@ -70,6 +76,7 @@ struct Roles {
   static constexpr int kPrepWarps = F8 ? 4 : 2;
   static constexpr int kThreads = (kPrepWarp + kPrepWarps) * 32;
 };
+constexpr uint32_t kSetUpBar = 1;  // named barrier of all threads between pieces
 constexpr float kLn2 = 0.69314718055994530942f;
 
 // TMEM columns: S (and P over it) of tiles A and B, then their O.
@@ -79,6 +86,26 @@ struct TilesLaunch {
   AttnLaunch a;
   int rows_per_tile;  // floor(128 / group): rows of one CTA's part of an MMA tile
   int row_tiles;      // CTAs (pairs) along the rows
+  int dealt;          // units' tiles dealt out over the grid (else one unit per CTA or pair)
+  int4* borders;      // dealt: the first step of each share after the first: kv head, row tile, step of the unit, unit's
+                      // steps; entry 0: number of shares, steps of a kv head
+};
+
+constexpr int kMaxDealt = 1024;  // most row tiles when dealt out
+constexpr int kUnitWeight = 3;   // a unit's start and end, in tile steps
+constexpr int kLeastShare = 8;   // tile steps that are worth a CTA (pair) of their own
+
+// Shares: share i holds the steps [i * total / n, (i + 1) * total / n).
+__device__ __forceinline__ long long share_start(long long i, long long total, int n) { return i * total / n; }
+__device__ __forceinline__ int share_of(long long step, long long total, int n) {
+  return static_cast<int>(((step + 1) * n - 1) / total);
+}
+
+// What a CTA (pair) does at a time: a unit's tiles from `from` to `to` of `of`.
+struct Piece {
+  int kvh, row0;
+  int from, to, of;
+  int slot;  // place of its partial results, -1: the piece is the whole unit
 };
 
 template <int D, bool F8>
@@ -104,15 +131,20 @@ struct Shared {
   uint64_t raw_full[kRaw ? kRaw : 1], raw_empty[kRaw ? kRaw : 1];
   uint64_t s_ready[2], p_ready[2][2], o_done[2];  // p_ready: first and second half of the keys
   uint32_t tmem;
-  int nonfinite;  // number of the last pass (from 1) that met a non-finite value row
+  int nonfinite;  // number of the piece's last pass (from 1) that met a non-finite value row
+  int stop;       // a wait gave up: no further piece
   int segs;
+  Piece piece;             // at work on
+  long long step, begin, end;  // dealt: next step, and the share
+  int more;                // a piece follows
+  int deal[kMaxDealt + 2];  // dealt: the row tiles' weights, summed up, and the number of shares
   int warp_starts[16];
   int row_n[kMaxRows<D>], row_b[kMaxRows<D>];
   int seg_start[kMaxRows<D> + 1], seg_most[kMaxRows<D>], seg_least[kMaxRows<D>], seg_low[kMaxRows<D>];
   float4 scales[F8 ? kSoftmaxWarps : 1][8];  // per softmax warp: k scale, log2 v scale, 1 / v scale of 16 keys
 };
 
-// One request's rows of the CTA (pair) and the tiles that its chunk walks.
+// One request's rows of the CTA (pair) and the tiles that the piece walks.
 struct Pass {
   int s, e;        // rows [s, e) of the pair
   int batch;
@@ -120,7 +152,7 @@ struct Pass {
   int low;         // least first key of a row's window (0: no window)
   int first_tiles; // tiles that hold the first `sinks` tokens before the window's tiles
   int low_tile;
-  int i0, i1;      // tile indices of this chunk
+  int i0, i1;      // tile indices of this piece
   bool act[2];     // MMA tile has rows of the pass
   __device__ __forceinline__ int tile0(int i) const {
     return (i < first_tiles ? i : i - first_tiles + low_tile) * kTile;
@@ -134,8 +166,9 @@ struct Pass {
 };
 
 template <int D, bool F8>
-__device__ __forceinline__ Pass get_pass(const Shared<D, F8>& S, const TilesLaunch& L, int seg, int chunk) {
+__device__ __forceinline__ Pass get_pass(const Shared<D, F8>& S, const TilesLaunch& L, int seg) {
   const AttnLaunch& p = L.a;
+  const Piece& pc = S.piece;
   Pass r;
   r.s = S.seg_start[seg];
   r.e = S.seg_start[seg + 1];
@@ -153,8 +186,8 @@ __device__ __forceinline__ Pass get_pass(const Shared<D, F8>& S, const TilesLaun
     if (r.low > 0) r.first_tiles = min((min(p.sinks, r.low) + kTile - 1) / kTile, r.low_tile);
     tiles = r.first_tiles + (r.most + kTile - 1) / kTile - r.low_tile;
   }
-  r.i0 = static_cast<int>(static_cast<long long>(tiles) * chunk / p.chunks);
-  r.i1 = static_cast<int>(static_cast<long long>(tiles) * (chunk + 1) / p.chunks);
+  r.i0 = static_cast<int>(static_cast<long long>(tiles) * pc.from / pc.of);
+  r.i1 = static_cast<int>(static_cast<long long>(tiles) * pc.to / pc.of);
   return r;
 }
 
@@ -442,14 +475,15 @@ __device__ __noinline__ void add_nonfinite(const AttnLaunch& p, const Pass& ps, 
   }
 }
 
-// 32 columns of the thread's row, from column c0; an unseen row's O may hold anything.
+// 32 columns of the thread's row, from column c0; an unseen row's O may hold
+// anything. `part`: place of the row's partial results, -1: they are final.
 template <int D>
-__device__ __forceinline__ void write_columns(const AttnLaunch& p, const Lane& ln, int chunk, float l, int c0,
+__device__ __forceinline__ void write_columns(const AttnLaunch& p, const Lane& ln, long long part, float l, int c0,
                                               const float (&o)[32]) {
   if (!ln.live) return;
   const bool none = l == 0.f;
-  if (p.chunks > 1) {
-    float4* dst = reinterpret_cast<float4*>(p.part_o + (ln.head * p.chunks + chunk) * D + c0);
+  if (part >= 0) {
+    float4* dst = reinterpret_cast<float4*>(p.part_o + part * D + c0);
 #pragma unroll
     for (int d = 0; d < 8; ++d)
       dst[d] = none ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(o[4 * d], o[4 * d + 1], o[4 * d + 2], o[4 * d + 3]);
@@ -467,10 +501,10 @@ __device__ __forceinline__ void write_columns(const AttnLaunch& p, const Lane& l
     dst[d] = none ? make_uint4(0, 0, 0, 0) : x;
   }
 }
-__device__ __forceinline__ void write_sums(const AttnLaunch& p, const Lane& ln, int chunk, float m, float l) {
+__device__ __forceinline__ void write_sums(const AttnLaunch& p, const Lane& ln, long long part, float m, float l) {
   if (!ln.live) return;
-  if (p.chunks > 1)
-    p.part_ml[ln.head * p.chunks + chunk] = make_float2(m, l);
+  if (part >= 0)
+    p.part_ml[part] = make_float2(m, l);
   else if (p.lse)
     p.lse[ln.head] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
@@ -502,9 +536,15 @@ __device__ __forceinline__ float query_to_f16(unsigned char* tile, int r) {
   return __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
 }
 
+// What a role has behind it, over the pieces: the phases of its barriers.
+struct Progress {
+  int pieces = 0, tiles = 0, passes = 0;
+  int weights[2] = {0, 0};  // MMA: tiles' weights taken
+};
+
 template <int D, bool F8>
-__device__ __forceinline__ bool softmax_role(Shared<D, F8>& S, const TilesLaunch& L, int x, int kvh, int chunk,
-                                             int row0, int rank) {
+__device__ __forceinline__ bool softmax_role(Shared<D, F8>& S, const TilesLaunch& L, int x, int rank, Progress& at) {
+  const Piece& pc = S.piece;
   constexpr int PAIR = kPair<D>;
   const AttnLaunch& p = L.a;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, quad = warp & 3;
@@ -514,10 +554,9 @@ __device__ __forceinline__ bool softmax_role(Shared<D, F8>& S, const TilesLaunch
   const uint32_t to = S.tmem + lanes + kColO + 128 * x;
   const int local = (x * PAIR + rank) * L.rows_per_tile + r / p.group;
   const bool in_tile = r < L.rows_per_tile * p.group;
-  int tiles_done = 0, passes_done = 0;
   float scale = p.scale_log2;
   if (F8) {
-    const bool ok = mbar_wait(&S.q_full, 0);
+    const bool ok = mbar_wait(&S.q_full, at.pieces & 1);
     if (!__all_sync(0xffffffffu, ok)) return false;
     scale *= query_to_f16<D>(S.q[x], r);
     fence_proxy_async_smem();
@@ -526,21 +565,22 @@ __device__ __forceinline__ bool softmax_role(Shared<D, F8>& S, const TilesLaunch
   }
 
   for (int seg = 0; seg < S.segs; ++seg) {
-    const Pass ps = get_pass(S, L, seg, chunk);
+    const Pass ps = get_pass(S, L, seg);
     if (!ps.act[x]) continue;
     Lane ln;
-    ln.row = row0 + local;
+    ln.row = pc.row0 + local;
     ln.live = in_tile && local >= ps.s && local < ps.e && ln.row < p.rows;
     ln.n = ln.live ? S.row_n[local] : 0;
     ln.first = p.window > 0 ? max(0, ln.n - p.window) : 0;
     ln.sinks = min(p.sinks, ln.first);
-    ln.head = static_cast<long long>(ln.row) * p.q_heads + kvh * p.group + r % p.group;
+    ln.head = static_cast<long long>(ln.row) * p.q_heads + pc.kvh * p.group + r % p.group;
+    const long long part = pc.slot < 0 ? -1 : (static_cast<long long>(pc.slot) * 2 * PAIR * L.rows_per_tile + local) * p.group + r % p.group;
     float m = -INFINITY, l = 0.f;
     if (ps.i0 == ps.i1) {
       const float o[32] = {};
 #pragma unroll 1
-      for (int c = 0; c < D; c += 32) write_columns<D>(p, ln, chunk, l, c, o);
-      write_sums(p, ln, chunk, m, l);
+      for (int c = 0; c < D; c += 32) write_columns<D>(p, ln, part, l, c, o);
+      write_sums(p, ln, part, m, l);
       continue;
     }
     // lanes 0-7: block of the tile's 16-key group (-1: none, -2: bad), read
@@ -554,7 +594,7 @@ __device__ __forceinline__ bool softmax_role(Shared<D, F8>& S, const TilesLaunch
     };
     auto scales_of = [&](int blk) -> float2 {
       if (!F8 || blk < 0) return make_float2(1.f, 1.f);
-      const long long at = static_cast<long long>(blk) * p.c.heads + kvh;
+      const long long at = static_cast<long long>(blk) * p.c.heads + pc.kvh;
       return make_float2(p.c.ks[at], p.c.vs[at]);
     };
     int blk1 = block_of(ps.i0), blk2 = block_of(ps.i0 + 1);
@@ -572,9 +612,9 @@ __device__ __forceinline__ bool softmax_role(Shared<D, F8>& S, const TilesLaunch
       }
       blk1 = blk2;
       blk2 = block_of(i + 2);
-      const bool ok = mbar_wait(&S.s_ready[x], tiles_done & 1);
+      const bool ok = mbar_wait(&S.s_ready[x], at.tiles & 1);
       if (!__all_sync(0xffffffffu, ok)) return false;
-      ++tiles_done;
+      ++at.tiles;
       tc_fence_after();
       const int t0 = ps.tile0(i);
       const bool whole = t0 + kTile <= ln.n && (t0 >= ln.first || t0 + kTile <= ln.sinks);
@@ -719,9 +759,9 @@ __device__ __forceinline__ bool softmax_role(Shared<D, F8>& S, const TilesLaunch
       }
       hand_over(1);
     }
-    const bool ok = mbar_wait(&S.o_done[x], passes_done & 1);
+    const bool ok = mbar_wait(&S.o_done[x], at.passes & 1);
     if (!__all_sync(0xffffffffu, ok)) return false;
-    ++passes_done;
+    ++at.passes;
     tc_fence_after();
     bool extra = *reinterpret_cast<volatile int*>(&S.nonfinite) == seg + 1;
     if (PAIR == 2) {
@@ -737,11 +777,11 @@ __device__ __forceinline__ bool softmax_role(Shared<D, F8>& S, const TilesLaunch
       float o[32];
 #pragma unroll
       for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(u[e]);
-      if (extra) add_nonfinite<D, F8>(p, get_pass(S, L, seg, chunk), kvh, ln, m, c, o);
-      write_columns<D>(p, ln, chunk, l, c, o);
+      if (extra) add_nonfinite<D, F8>(p, get_pass(S, L, seg), pc.kvh, ln, m, c, o);
+      write_columns<D>(p, ln, part, l, c, o);
     }
     tc_fence_before();
-    write_sums(p, ln, chunk, m, l);
+    write_sums(p, ln, part, m, l);
   }
   return true;
 }
@@ -749,8 +789,8 @@ __device__ __forceinline__ bool softmax_role(Shared<D, F8>& S, const TilesLaunch
 // ---------------------------------------------------------------------- TMA
 template <int D, bool F8>
 __device__ __forceinline__ bool tma_role(Shared<D, F8>& S, const TilesLaunch& L, const CUtensorMap* qmap,
-                                         const CUtensorMap* kmap, const CUtensorMap* vmap, int kvh, int chunk,
-                                         int row0, int rank) {
+                                         const CUtensorMap* kmap, const CUtensorMap* vmap, int rank, Progress& progress) {
+  const Piece& pc = S.piece;
   using Sh = Shared<D, F8>;
   constexpr int PAIR = kPair<D>, kStages = Sh::kStages, kRaw = F8 ? Sh::kRaw : 1;
   const AttnLaunch& p = L.a;
@@ -765,14 +805,14 @@ __device__ __forceinline__ bool tma_role(Shared<D, F8>& S, const TilesLaunch& L,
       mbar_arrive_expect_tx(&S.q_full, PAIR * bytes);
     for (int x = 0; x < 2; ++x)
       for (int c = 0; c < Sh::kSlabs; ++c)
-        tma_3d<PAIR>(S.q[x] + c * kTile * 128, qmap, 64 * c, kvh * p.group, row0 + (x * PAIR + rank) * L.rows_per_tile,
-                     bar);
+        tma_3d<PAIR>(S.q[x] + c * kTile * 128, qmap, 64 * c, pc.kvh * p.group,
+                     pc.row0 + (x * PAIR + rank) * L.rows_per_tile, bar);
   }
   const int bs = 1 << p.c.bs_log2;
   const int k_box = min(bs, Sh::kKeys);  // keys of one K copy; a V copy takes a block
-  int done = 0;
+  int& done = progress.tiles;
   for (int seg = 0; seg < S.segs; ++seg) {
-    const Pass ps = get_pass(S, L, seg, chunk);
+    const Pass ps = get_pass(S, L, seg);
     // block of the lane's copy, copies being `box` keys each; -1: none. A bad
     // block is read as the one past the end, which the copy fills with zeros.
     auto block_of = [&](int i, int box) -> int {
@@ -820,13 +860,13 @@ __device__ __forceinline__ bool tma_role(Shared<D, F8>& S, const TilesLaunch& L,
           const uint32_t bar = shared ? first_cta<PAIR>(full) : smem_u32(full);
           const int tok = lane * box & (bs - 1);
           if (kv)
-            tma_4d<PAIR>(dst, vmap, Sh::kDims * rank, 0, kvh, blk[kv], bar);
+            tma_4d<PAIR>(dst, vmap, Sh::kDims * rank, 0, pc.kvh, blk[kv], bar);
           else if (F8)
-            tma_4d<PAIR>(dst, kmap, 0, tok, kvh, blk[kv], bar);
+            tma_4d<PAIR>(dst, kmap, 0, tok, pc.kvh, blk[kv], bar);
           else
 #pragma unroll
             for (int c = 0; c < Sh::kSlabs; ++c)
-              tma_4d<PAIR>(dst + c * Sh::kKeys * 128, kmap, 64 * c, tok, kvh, blk[kv], bar);
+              tma_4d<PAIR>(dst + c * Sh::kKeys * 128, kmap, 64 * c, tok, pc.kvh, blk[kv], bar);
         }
       }
     }
@@ -836,7 +876,7 @@ __device__ __forceinline__ bool tma_role(Shared<D, F8>& S, const TilesLaunch& L,
 
 // ---------------------------------------------------------------------- MMA
 template <int D, bool F8>
-__device__ __forceinline__ bool mma_role(Shared<D, F8>& S, const TilesLaunch& L, int chunk) {
+__device__ __forceinline__ bool mma_role(Shared<D, F8>& S, const TilesLaunch& L, Progress& progress) {
   using Sh = Shared<D, F8>;
   constexpr int PAIR = kPair<D>, kStages = Sh::kStages;
   constexpr uint32_t kF16 = F8 ? (1u << 7) | (1u << 10) : 0u;  // format fields: 1 bf16, 0 f16
@@ -863,10 +903,11 @@ __device__ __forceinline__ bool mma_role(Shared<D, F8>& S, const TilesLaunch& L,
       umma_ts<PAIR>(tmem + kColO + 128 * x, tmem + kColS + 128 * x + 8 * s, b + ((s * 2048) >> 4), kIdescPv,
                     !(first && s == 0));
   };
-  if (!mbar_wait(F8 ? &S.q_ready : &S.q_full, 0)) return false;
-  int done = 0, p_done[2] = {0, 0};
+  if (!mbar_wait(F8 ? &S.q_ready : &S.q_full, progress.pieces & 1)) return false;
+  int& done = progress.tiles;
+  int(&p_done)[2] = progress.weights;
   for (int seg = 0; seg < S.segs; ++seg) {
-    const Pass ps = get_pass(S, L, seg, chunk);
+    const Pass ps = get_pass(S, L, seg);
     const int n = ps.i1 - ps.i0;
     if (n == 0) continue;
     if (!mbar_wait(&S.k_full[done % kStages], (done / kStages) & 1)) return false;
@@ -907,13 +948,13 @@ __device__ __forceinline__ bool mma_role(Shared<D, F8>& S, const TilesLaunch& L,
 
 // --------------------------------------------------------------------- prep
 template <int D>
-__device__ __forceinline__ bool prep_role(Shared<D, false>& S, const TilesLaunch& L, int chunk) {
+__device__ __forceinline__ bool prep_role(Shared<D, false>& S, const TilesLaunch& L, Progress& progress) {
   const AttnLaunch& p = L.a;
   constexpr int PAIR = kPair<D>, kStages = Shared<D, false>::kStages, kPrepWarps = Roles<false>::kPrepWarps;
   const int tid = threadIdx.x - Roles<false>::kPrepWarp * 32;
-  int done = 0;
+  int& done = progress.tiles;
   for (int seg = 0; seg < S.segs; ++seg) {
-    const Pass ps = get_pass(S, L, seg, chunk);
+    const Pass ps = get_pass(S, L, seg);
     for (int i = ps.i0; i < ps.i1; ++i, ++done) {
       const int st = done % kStages;
       const bool ok = mbar_wait(&S.v_full[st], (done / kStages) & 1);
@@ -997,15 +1038,15 @@ __device__ __forceinline__ bool codes_to_halves(const uint4 (&x)[4], unsigned ch
 }
 
 template <int D>
-__device__ __forceinline__ bool prep_role(Shared<D, true>& S, const TilesLaunch& L, int chunk) {
+__device__ __forceinline__ bool prep_role(Shared<D, true>& S, const TilesLaunch& L, Progress& progress) {
   using Sh = Shared<D, true>;
   constexpr int PAIR = kPair<D>, kRaw = Sh::kRaw, kStages = Sh::kStages;
   static_assert(Sh::kKeys * D == 4 * 128 * 16 && kTile * Sh::kDims == 4 * 128 * 16, "four pieces per thread");
   const AttnLaunch& p = L.a;
   const int tid = threadIdx.x - Roles<true>::kPrepWarp * 32;
-  int done = 0;
+  int& done = progress.tiles;
   for (int seg = 0; seg < S.segs; ++seg) {
-    const Pass ps = get_pass(S, L, seg, chunk);
+    const Pass ps = get_pass(S, L, seg);
     for (int i = ps.i0; i < ps.i1; ++i, ++done) {
       const int t0 = ps.tile0(i), st = done % kStages;
       const bool check = ps.partial(t0, p);
@@ -1036,26 +1077,150 @@ __device__ __forceinline__ bool prep_role(Shared<D, true>& S, const TilesLaunch&
   return true;
 }
 
+// The row tiles' weights, summed up, in S.deal (every CTA computes the same);
+// the number of shares behind them.
+template <int D, bool F8>
+__device__ __forceinline__ void deal_units(Shared<D, F8>& S, const TilesLaunch& L, int most_shares) {
+  const AttnLaunch& p = L.a;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rows_here = 2 * kPair<D> * L.rows_per_tile;
+  for (int t = warp; t < L.row_tiles; t += Roles<F8>::kThreads / 32) {
+    int most = 0, low = INT_MAX;
+    for (int i = lane; i < rows_here && t * rows_here + i < p.rows; i += 32) {
+      const int n = p.seq_lens[t * rows_here + i];
+      if (n > 0 && n <= p.max_len) {
+        most = max(most, n);
+        low = min(low, p.window > 0 ? max(0, n - p.window) : 0);
+      }
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+      most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
+      low = min(low, __shfl_xor_sync(0xffffffffu, low, o));
+    }
+    if (lane == 0) S.deal[t + 1] = kUnitWeight + (most > 0 ? (most + kTile - 1) / kTile - low / kTile : 0);
+  }
+  __syncthreads();
+  if (warp == 0) {
+    int sum = 0;
+    for (int t0 = 0; t0 < L.row_tiles; t0 += 32) {
+      const int t = t0 + lane;
+      int x = t < L.row_tiles ? S.deal[t + 1] : 0;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      if (t < L.row_tiles) S.deal[t + 1] = sum + x;
+      sum += __shfl_sync(0xffffffffu, x, 31);
+    }
+    if (lane == 0) {
+      S.deal[0] = 0;
+      const long long total = static_cast<long long>(sum) * p.c.heads;
+      const int shares = static_cast<int>(max(1LL, min(static_cast<long long>(most_shares), total / kLeastShare)));
+      S.deal[L.row_tiles + 1] = shares;
+      if (blockIdx.x == 0) L.borders[0] = make_int4(shares, sum, 0, 0);
+    }
+  }
+  __syncthreads();
+}
+
+// The piece that holds this CTA's (pair's) step `step` of its share [.., end);
+// moves `step` to the next piece.
+template <int D, bool F8>
+__device__ __forceinline__ Piece next_piece(const Shared<D, F8>& S, const TilesLaunch& L, int share, long long& step,
+                                            long long begin, long long end) {
+  const int sum = S.deal[L.row_tiles];
+  Piece pc;
+  pc.kvh = static_cast<int>(step / sum);
+  const int in_head = static_cast<int>(step - static_cast<long long>(pc.kvh) * sum);
+  int lo = 0, hi = L.row_tiles - 1;  // the row tile with deal[t] <= in_head < deal[t + 1]
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (S.deal[mid] <= in_head)
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  const long long a = static_cast<long long>(pc.kvh) * sum + S.deal[lo];
+  pc.of = S.deal[lo + 1] - S.deal[lo];
+  pc.row0 = lo * 2 * kPair<D> * L.rows_per_tile;
+  pc.from = static_cast<int>(step - a);
+  pc.to = static_cast<int>(min(static_cast<long long>(pc.of), end - a));
+  pc.slot = pc.from == 0 && pc.to == pc.of ? -1 : 2 * share + (a <= begin ? 0 : 1);
+  step = a + pc.to;
+  return pc;
+}
+
+// The rows of the piece: lengths, and the runs of one request. Both CTAs of a
+// pair look at all its rows. Every thread calls it; ends with a barrier.
+template <int D, bool F8>
+__device__ __forceinline__ void set_up_rows(Shared<D, F8>& S, const TilesLaunch& L) {
+  const Piece& pc = S.piece;
+  constexpr int kThreads = Roles<F8>::kThreads, kRows = kMaxRows<D>, kGroups = kRows / 32;
+  const AttnLaunch& p = L.a;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rows_here = 2 * kPair<D> * L.rows_per_tile;
+  if (tid == 0) S.nonfinite = 0;
+  for (int i = tid; i < kRows; i += kThreads) {
+    int n = 0, b = -1;
+    const int row = pc.row0 + i;
+    if (i < rows_here && row < p.rows) {
+      n = p.seq_lens[row];
+      b = p.row_to_batch[row];
+      if (n < 0 || n > p.max_len || b < 0 || b >= p.bt_rows ||
+          ((static_cast<long long>(n) - 1) >> p.c.bs_log2) >= p.bt_stride) {
+        atomicOr(p.status, kDevBadRowMeta);
+        n = 0;
+        b = -1;
+      }
+    }
+    S.row_n[i] = n;
+    S.row_b[i] = b;
+    S.seg_most[i] = 0;
+    S.seg_least[i] = S.seg_low[i] = INT_MAX;
+  }
+  named_bar(kSetUpBar, kThreads);
+  for (int w = warp; w < kGroups; w += kThreads / 32) {
+    const int i = 32 * w + lane;
+    const uint32_t starts = __ballot_sync(0xffffffffu, i < rows_here && (i == 0 || S.row_b[i - 1] != S.row_b[i]));
+    if (lane == 0) S.warp_starts[w] = __popc(starts);
+  }
+  named_bar(kSetUpBar, kThreads);
+  for (int w = warp; w < kGroups; w += kThreads / 32) {
+    const int i = 32 * w + lane;
+    const bool start = i < rows_here && (i == 0 || S.row_b[i - 1] != S.row_b[i]);
+    const uint32_t starts = __ballot_sync(0xffffffffu, start);
+    int id = -1;
+    for (int v = 0; v < w; ++v) id += S.warp_starts[v];
+    id += __popc(starts & ((2u << lane) - 1u));
+    if (start) S.seg_start[id] = i;
+    if (i == rows_here - 1) {
+      S.segs = id + 1;
+      S.seg_start[id + 1] = rows_here;
+    }
+    const int n = S.row_n[i];
+    if (i < rows_here && n > 0) {
+      atomicMax(&S.seg_most[id], n);
+      atomicMin(&S.seg_least[id], n);
+      atomicMin(&S.seg_low[id], p.window > 0 ? max(0, n - p.window) : 0);
+    }
+  }
+  named_bar(kSetUpBar, kThreads);
+}
+
 template <int D, bool F8>
 __global__ void __launch_bounds__(Roles<F8>::kThreads, 1)
     attn_tiles_kernel(const __grid_constant__ TilesLaunch L, const __grid_constant__ CUtensorMap qmap,
                       const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
   extern __shared__ unsigned char raw[];
   using Sh = Shared<D, F8>;
-  constexpr int PAIR = kPair<D>, kRows = kMaxRows<D>;
+  constexpr int PAIR = kPair<D>;
   Sh& S = *reinterpret_cast<Sh*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const AttnLaunch& p = L.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank = PAIR == 2 ? static_cast<int>(cta_rank()) : 0;
-  int u = blockIdx.x / PAIR;
-  const int chunk = u % p.chunks;
-  u /= p.chunks;
-  const int kvh = u % p.c.heads;
-  // the last rows first: with causal lengths they have the most keys
-  const int rows_here = 2 * PAIR * L.rows_per_tile;
-  const int row0 = (L.row_tiles - 1 - u / p.c.heads) * rows_here;
 
-  // ---- set-up: barriers, TMEM, the rows' lengths and the runs of one request
   if (tid == 0) {
     mbar_init(&S.q_full, 1);
     mbar_init(&S.q_ready, kSoftmaxWarps * PAIR);
@@ -1076,7 +1241,7 @@ __global__ void __launch_bounds__(Roles<F8>::kThreads, 1)
       mbar_init(&S.p_ready[x][1], 4 * PAIR);
       mbar_init(&S.o_done[x], 1);
     }
-    S.nonfinite = 0;
+    S.stop = 0;
     fence_mbar_init();
   }
   if (warp == kMmaWarp) tmem_take<PAIR>(&S.tmem);
@@ -1085,52 +1250,25 @@ __global__ void __launch_bounds__(Roles<F8>::kThreads, 1)
     prefetch_tmap(&kmap);
     prefetch_tmap(&vmap);
   }
-  // both CTAs of a pair look at all its rows
-  for (int i = tid; i < kRows; i += Roles<F8>::kThreads) {
-    int n = 0, b = -1;
-    const int row = row0 + i;
-    if (i < rows_here && row < p.rows) {
-      n = p.seq_lens[row];
-      b = p.row_to_batch[row];
-      if (n < 0 || n > p.max_len || b < 0 || b >= p.bt_rows ||
-          ((static_cast<long long>(n) - 1) >> p.c.bs_log2) >= p.bt_stride) {
-        atomicOr(p.status, kDevBadRowMeta);
-        n = 0;
-        b = -1;
+  const int group = blockIdx.x / PAIR;  // CTA, or pair
+  if (L.dealt) deal_units(S, L, gridDim.x / PAIR);
+  if (tid == 0) {
+    S.more = 1;
+    if (!L.dealt) {
+      // the last rows first: with causal lengths they have the most keys
+      S.piece = Piece{group % p.c.heads, (L.row_tiles - 1 - group / p.c.heads) * 2 * PAIR * L.rows_per_tile, 0, 1, 1, -1};
+    } else {
+      const int shares = S.deal[L.row_tiles + 1];
+      const long long total = static_cast<long long>(S.deal[L.row_tiles]) * p.c.heads;
+      S.more = group < shares;
+      S.step = S.begin = share_start(group, total, shares);
+      S.end = share_start(group + 1, total, shares);
+      if (group < shares) {
+        S.piece = next_piece(S, L, group, S.step, S.begin, S.end);
+        const Piece& pc = S.piece;
+        if (rank == 0 && group > 0)
+          L.borders[group] = make_int4(pc.kvh, pc.row0 / (2 * PAIR * L.rows_per_tile), pc.from, pc.of);
       }
-    }
-    S.row_n[i] = n;
-    S.row_b[i] = b;
-    S.seg_most[i] = 0;
-    S.seg_least[i] = S.seg_low[i] = INT_MAX;
-  }
-  __syncthreads();
-  // runs of one request, 32 rows to a warp
-  constexpr int kGroups = kRows / 32;
-  for (int w = warp; w < kGroups; w += Roles<F8>::kThreads / 32) {
-    const int i = 32 * w + lane;
-    const uint32_t starts =
-        __ballot_sync(0xffffffffu, i < rows_here && (i == 0 || S.row_b[i - 1] != S.row_b[i]));
-    if (lane == 0) S.warp_starts[w] = __popc(starts);
-  }
-  __syncthreads();
-  for (int w = warp; w < kGroups; w += Roles<F8>::kThreads / 32) {
-    const int i = 32 * w + lane;
-    const bool start = i < rows_here && (i == 0 || S.row_b[i - 1] != S.row_b[i]);
-    const uint32_t starts = __ballot_sync(0xffffffffu, start);
-    int id = -1;
-    for (int v = 0; v < w; ++v) id += S.warp_starts[v];
-    id += __popc(starts & ((2u << lane) - 1u));
-    if (start) S.seg_start[id] = i;
-    if (i == rows_here - 1) {
-      S.segs = id + 1;
-      S.seg_start[id + 1] = rows_here;
-    }
-    const int n = S.row_n[i];
-    if (i < rows_here && n > 0) {
-      atomicMax(&S.seg_most[id], n);
-      atomicMin(&S.seg_least[id], n);
-      atomicMin(&S.seg_low[id], p.window > 0 ? max(0, n - p.window) : 0);
     }
   }
   tc_fence_before();
@@ -1138,7 +1276,34 @@ __global__ void __launch_bounds__(Roles<F8>::kThreads, 1)
   if (PAIR == 2) cluster_sync();  // the other CTA's barriers are set up
   tc_fence_after();
 
-  bool ok = true;
+  // Piece by piece; `role` is one role's work on one.
+  auto pieces = [&](auto role) {
+    Progress at;
+    while (S.more) {
+      set_up_rows(S, L);
+      const bool ok = role(at);
+      ++at.pieces;
+      if (!ok) {
+        // both CTAs of a pair stop after this piece
+        atomicOr(p.status, kDevWaitTimeout);
+        S.stop = 1;
+        if (PAIR == 2)
+          asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(peer_addr(&S.stop, rank ^ 1)), "r"(1) : "memory");
+      }
+      __syncwarp();
+      tc_fence_before();
+      named_bar(kSetUpBar, Roles<F8>::kThreads);
+      // neither CTA goes on, or ends, while the other may still read or signal it
+      if (PAIR == 2) cluster_sync();
+      tc_fence_after();
+      if (!L.dealt) break;
+      if (tid == 0) {
+        S.more = S.step < S.end && !S.stop;
+        if (S.more) S.piece = next_piece(S, L, group, S.step, S.begin, S.end);
+      }
+      named_bar(kSetUpBar, Roles<F8>::kThreads);
+    }
+  };
   // the softmax warps hold (half of) a row of S; the others give up what
   // they take beyond the launch's share: 2 * 200 + 104 = 3 * 168 (12 warps),
   // 2 * 160 + 88 + 104 = 4 * 128 (16 warps)
@@ -1147,34 +1312,72 @@ __global__ void __launch_bounds__(Roles<F8>::kThreads, 1)
       asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
     else
       asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
-    ok = softmax_role<D, F8>(S, L, warp >> 2, kvh, chunk, row0, rank);
+    pieces([&](Progress& at) { return softmax_role<D, F8>(S, L, warp >> 2, rank, at); });
   } else if (warp < 12) {
     if (F8)
       asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     else
       asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
-    if (warp == kTmaWarp) {
-      ok = tma_role<D, F8>(S, L, &qmap, &kmap, &vmap, kvh, chunk, row0, rank);
-    } else if (warp == kMmaWarp) {
-      if (lane == 0 && rank == 0) ok = mma_role<D, F8>(S, L, chunk);
-    } else if (!F8) {
-      ok = prep_role<D>(S, L, chunk);
-    }
+    pieces([&](Progress& at) {
+      if (warp == kTmaWarp) return tma_role<D, F8>(S, L, &qmap, &kmap, &vmap, rank, at);
+      if (warp == kMmaWarp) return lane != 0 || rank != 0 || mma_role<D, F8>(S, L, at);
+      if constexpr (!F8) return prep_role<D>(S, L, at);
+      return true;
+    });
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
-    ok = prep_role<D>(S, L, chunk);
+    if constexpr (F8) pieces([&](Progress& at) { return prep_role<D>(S, L, at); });
   }
-  if (!ok) atomicOr(p.status, kDevWaitTimeout);
-  __syncwarp();
-  tc_fence_before();
   __syncthreads();
-  // no CTA of a pair ends while the other may still read or signal it
-  if (PAIR == 2) cluster_sync();
   if (warp == kMmaWarp) {
     tc_fence_after();
     tmem_give<PAIR>(S.tmem);
   }
-  if (p.chunks > 1) pdl_trigger();
+  if (L.dealt) pdl_trigger();
+}
+
+// Joins the units that were cut: block (j, i) does rows and heads 4j to 4j + 3,
+// one warp each, of the unit that share i + 1 begins inside of, if that is
+// the unit's first cut.
+template <int D>
+__global__ void __launch_bounds__(128) attn_tiles_join_kernel(const __grid_constant__ TilesLaunch L) {
+  const AttnLaunch& p = L.a;
+  const int rows_here = 2 * kPair<D> * L.rows_per_tile, lane = threadIdx.x & 31;
+  const int first = blockIdx.y;
+  const int item = blockIdx.x * 4 + (threadIdx.x >> 5);
+  pdl_wait();
+  const int4 head4 = L.borders[0], cut = L.borders[first + 1];
+  const int shares = head4.x, sum = head4.y, kvh = cut.x;
+  if (first + 1 >= shares || cut.z == 0 || item >= rows_here * p.group) return;
+  const long long total = static_cast<long long>(sum) * p.c.heads;
+  const long long a = share_start(first + 1, total, shares) - cut.z, b = a + cut.w;  // the unit's steps
+  if (a < share_start(first, total, shares)) return;  // an earlier share cut it first
+  const int last = share_of(b - 1, total, shares);
+  const int row = cut.y * rows_here + item / p.group;
+  if (row >= p.rows) return;
+  auto slot = [&](int share) { return 2 * share + (a <= share_start(share, total, shares) ? 0 : 1); };
+  constexpr int V = D / 32;
+  float m = -INFINITY, l = 0.f, o[V];
+#pragma unroll
+  for (int j = 0; j < V; ++j) o[j] = 0.f;
+  const long long items = static_cast<long long>(rows_here) * p.group;
+  for (int i = first; i <= last; ++i) m = fmaxf(m, p.part_ml[slot(i) * items + item].x);
+  const float base = m == -INFINITY ? 0.f : m;
+#pragma unroll 2
+  for (int i = first; i <= last; ++i) {
+    const long long at = slot(i) * items + item;
+    const float2 x = p.part_ml[at];
+    const float f = x.y != x.y ? x.y : (x.x == -INFINITY ? 0.f : ex2(x.x - base));
+    l += f * x.y;
+#pragma unroll
+    for (int j = 0; j < V; ++j) o[j] += f * p.part_o[at * D + lane * V + j];
+  }
+  const long long head = static_cast<long long>(row) * p.q_heads + kvh * p.group + item % p.group;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + head * D + lane * V);
+#pragma unroll
+  for (int j = 0; j < V; j += 2) dst[j / 2] = pack_bf16(o[j] * inv, o[j + 1] * inv);
+  if (lane == 0 && p.lse) p.lse[head] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
 // 4-D map of a cache: (dim, token, head, block), boxes of `dims` dims of up to
@@ -1211,13 +1414,45 @@ bool query_map(CUtensorMap* map, const AttnLaunch& p, int rows_per_tile) {
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Row tiles of a call, CTAs (pairs) of the GPU, and whether the units' tiles
+// are dealt out. In tile steps, whole units take (waves of units) x (most tiles
+// + 4 for a unit's start and end); dealt out they take their even share, a
+// second start and end, and about 14 steps for the deal, the partial
+// results and the join. 2048 rows on 32768 keys, 32 / 4 heads (128 units, 76
+// pairs, 256 tiles): 0.80 ms dealt out, 0.89 whole; 512 rows on 4512 keys,
+// 64 / 8 heads (64 units, 36 tiles): 106 us and 78. From three waves on, units
+// of unlike lengths fill the gaps by themselves: 1849 rows of four requests
+// (232 units) 0.56 ms dealt out, 0.49 whole.
+struct Work {
+  int rows_here, row_tiles, shares;
+  bool dealt;
+};
+Work work_of(long long rows, int group, int heads, int dim, long long max_keys, int num_sms) {
+  const int pair = dim == 128 ? kPair<128> : kPair<64>;
+  Work w;
+  w.rows_here = 2 * pair * (kTile / group);
+  w.row_tiles = static_cast<int>((rows + w.rows_here - 1) / w.rows_here);
+  w.shares = num_sms / pair;
+  const long long units = static_cast<long long>(w.row_tiles) * heads;
+  const long long tiles = (max_keys + kTile - 1) / kTile, waves = (units + w.shares - 1) / w.shares;
+  w.dealt = w.row_tiles <= kMaxDealt && waves <= 3 &&
+            units * (tiles + kUnitWeight) / w.shares + 18 < waves * (tiles + 4) * 92 / 100;
+  return w;
+}
+size_t border_bytes(const Work& w) { return (static_cast<size_t>(w.shares) * sizeof(int4) + 255) & ~static_cast<size_t>(255); }
+
 template <int D, bool F8>
-cudaError_t launch_tiles_t(const AttnLaunch& p, cudaStream_t stream) {
+cudaError_t launch_tiles_t(const AttnLaunch& p, const Work& w, void* workspace, cudaStream_t stream) {
   using Sh = Shared<D, F8>;
   constexpr int PAIR = kPair<D>;
-  TilesLaunch L{p, kTile / p.group, 0};
-  const int rows_here = 2 * PAIR * L.rows_per_tile;
-  L.row_tiles = (p.rows + rows_here - 1) / rows_here;
+  TilesLaunch L{p, kTile / p.group, w.row_tiles, w.dealt ? 1 : 0, nullptr};
+  if (w.dealt) {
+    char* at = static_cast<char*>(workspace);
+    const size_t items = static_cast<size_t>(2) * w.shares * w.rows_here * p.group;
+    L.borders = reinterpret_cast<int4*>(at);
+    L.a.part_o = reinterpret_cast<float*>(at + border_bytes(w));
+    L.a.part_ml = reinterpret_cast<float2*>(L.a.part_o + items * D);
+  }
   CUtensorMap qmap, kmap, vmap;
   if (!query_map(&qmap, p, L.rows_per_tile) || !cache_map(&kmap, p.c.k, p.c, p.c.kst, F8 ? D : 64, Sh::kKeys) ||
       !cache_map(&vmap, p.c.v, p.c, p.c.vst, Sh::kDims, kTile))
@@ -1233,7 +1468,7 @@ cudaError_t launch_tiles_t(const AttnLaunch& p, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     if (dev < 64) attr_done[dev] = true;
   }
-  const long long grid = static_cast<long long>(L.row_tiles) * p.c.heads * p.chunks * PAIR;
+  const long long grid = (w.dealt ? w.shares : static_cast<long long>(L.row_tiles) * p.c.heads) * PAIR;
   if (grid > INT_MAX) return cudaErrorInvalidConfiguration;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(grid));
@@ -1245,45 +1480,36 @@ cudaError_t launch_tiles_t(const AttnLaunch& p, cudaStream_t stream) {
   at[0].val.clusterDim = {PAIR, 1, 1};
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attn_tiles_kernel<D, F8>, L, qmap, kmap, vmap);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, attn_tiles_kernel<D, F8>, L, qmap, kmap, vmap);
+  if (e != cudaSuccess || !w.dealt || w.shares < 2) return e;
+  cudaLaunchConfig_t join{};
+  join.gridDim = dim3((w.rows_here * p.group + 3) / 4, w.shares - 1);
+  join.blockDim = dim3(128);
+  join.stream = stream;
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  join.attrs = at;
+  join.numAttrs = 1;
+  return cudaLaunchKernelEx(&join, attn_tiles_join_kernel<D>, L);
 }
 
 }  // namespace
 
 bool attn_tiles_apply(int group, float scale_log2) { return group <= kTile && scale_log2 > 0.f; }
 
-AttnPlan attn_tiles_plan(long long rows, int q_heads, int heads, int dim, long long max_keys, int num_sms) {
-  const int pair = dim == 128 ? kPair<128> : kPair<64>;
-  const int per = 2 * pair * (kTile / (q_heads / heads));
-  const long long units = (rows + per - 1) / per * heads;
-  num_sms /= pair;
-  const long long tiles = std::max<long long>(1, (max_keys + kTile - 1) / kTile);
-  // cost in tile steps: waves of CTAs, each its share of the tiles and about
-  // four steps of start and end, and the partial results' traffic
-  AttnPlan pl{1, 0, false};
-  double best = 1e300;
-  for (long long c = 1; c <= std::min<long long>(tiles, 32); ++c) {
-    const double waves = static_cast<double>((units * c + num_sms - 1) / num_sms);
-    double cost = waves * (static_cast<double>(tiles) / c + 4);
-    if (c > 1) cost += 6 + static_cast<double>(rows) * q_heads * c * dim * 8 / 3e6;
-    if (cost < best * 0.98) {
-      best = cost;
-      pl.chunks = static_cast<int>(c);
-    }
-  }
-  if (pl.chunks > 1)
-    pl.workspace_bytes = static_cast<size_t>(rows) * q_heads * pl.chunks * (static_cast<size_t>(dim) * 4 + 8);
-  return pl;
+size_t attn_tiles_workspace(long long rows, int q_heads, int heads, int dim, long long max_keys, int num_sms) {
+  const int group = q_heads / heads;
+  const Work w = work_of(rows, group, heads, dim, max_keys, num_sms);
+  if (!w.dealt) return 0;
+  return border_bytes(w) + static_cast<size_t>(2) * w.shares * w.rows_here * group * (static_cast<size_t>(dim) * 4 + 8);
 }
 
-cudaError_t launch_attn_tiles(const AttnLaunch& p, cudaStream_t stream) {
-  cudaError_t e;
+cudaError_t launch_attn_tiles(const AttnLaunch& p, long long max_keys, void* workspace, int num_sms,
+                              cudaStream_t stream) {
+  const Work w = work_of(p.rows, p.group, p.c.heads, p.c.dim, max_keys, num_sms);
   if (p.c.dim == 128)
-    e = p.c.f8 ? launch_tiles_t<128, true>(p, stream) : launch_tiles_t<128, false>(p, stream);
-  else
-    e = p.c.f8 ? launch_tiles_t<64, true>(p, stream) : launch_tiles_t<64, false>(p, stream);
-  if (e != cudaSuccess || p.chunks == 1) return e;
-  return launch_attn_join(p, true, stream);
+    return p.c.f8 ? launch_tiles_t<128, true>(p, w, workspace, stream) : launch_tiles_t<128, false>(p, w, workspace, stream);
+  return p.c.f8 ? launch_tiles_t<64, true>(p, w, workspace, stream) : launch_tiles_t<64, false>(p, w, workspace, stream);
 }
 
 }  // namespace sai

@@ -177,26 +177,25 @@ struct AttnLaunch {
   float scale_log2;  // sm_scale * log2(e)
   uint16_t* out;
   float* lse;
-  int chunks;      // key chunks per row; > 1: partial results
-  bool own;        // row kernel: see AttnPlan
-  float* part_o;   // [rows, q_heads, chunks, dim]
-  float2* part_ml; // [rows, q_heads, chunks]: running maximum (log2 units) and sum
+  int chunks;      // row kernel: key chunks per row; > 1: partial results
+  bool own, clustered;  // row kernel: see AttnPlan
+  float* part_o;   // row kernel: [rows, q_heads, chunks, dim]; tile kernel: [slots, rows and heads of a unit, dim]
+  float2* part_ml; // without dim: running maximum (log2 units) and sum
   int* status;
 };
 // Chunks per row of the row kernel, and its partial results' bytes.
 struct AttnPlan {
   int chunks;
   size_t workspace_bytes;
-  bool own;  // row kernel: a unit for each team of warps instead of each CTA
+  bool own;        // a unit for each team of warps instead of each CTA
+  bool clustered;  // a unit's chunks are a cluster and need no workspace
 };
 AttnPlan attn_rows_plan(long long rows, int q_heads, int heads, int dim, bool f8, long long max_keys, int num_sms);
 cudaError_t launch_attn_rows(const AttnLaunch& p, cudaStream_t stream);
-// Joins the chunks' partial results; all_chunks: every chunk has written one
-// for every row (else those that hold keys of the row).
-cudaError_t launch_attn_join(const AttnLaunch& p, bool all_chunks, cudaStream_t stream);
-// The tile kernel of packed rows: whether it takes a call, its chunks, and its launch.
+// The tile kernel of packed rows: whether it takes a call, its workspace, its launch.
 bool attn_tiles_apply(int group, float scale_log2);
-AttnPlan attn_tiles_plan(long long rows, int q_heads, int heads, int dim, long long max_keys, int num_sms);
-cudaError_t launch_attn_tiles(const AttnLaunch& p, cudaStream_t stream);
+size_t attn_tiles_workspace(long long rows, int q_heads, int heads, int dim, long long max_keys, int num_sms);
+cudaError_t launch_attn_tiles(const AttnLaunch& p, long long max_keys, void* workspace, int num_sms,
+                              cudaStream_t stream);
 
 }  // namespace sai

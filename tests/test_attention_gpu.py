@@ -406,3 +406,33 @@ def test_refusals():
     odd = torch.zeros((4, 2, 24, 128), dtype=torch.bfloat16, device=DEV)
     with pytest.raises(sai.SaiError, match="unsupported"):
         paged(cache=sai.KVCache(odd, odd))
+
+
+DEALT = [
+    # long keys and few units: the tile kernel deals its tiles out over the SMs and joins the units that are cut
+    [(70, 6000)],
+    [(3, 9000), (200, 230), (40, 7001)],
+    [(300, 5200)],
+]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("dim,hkv,group,bs", [(128, 1, 8, 128), (64, 2, 4, 32), (128, 2, 3, 16)])
+@pytest.mark.parametrize("reqs", DEALT)
+def test_packed_rows_dealt_out(dtype, dim, hkv, group, bs, reqs):
+    _packed(dtype, dim, hkv, group, bs, reqs, 0, 0)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+def test_packed_rows_dealt_out_by_a_far_bound(dtype):
+    """A bound far above the lengths, rows of length 0 and windows: shares without tiles, units without keys."""
+    totals = [700, 40]
+    c = Case(57, totals, dtype=dtype, bs=32)
+    lens = [0] * 30 + list(range(600, 701)) + [0, 40, 0]
+    r2b = [0] * 131 + [1] * 3
+    q, q64 = c.queries(len(lens), 8)
+    for window, sinks in ((0, 0), (200, 9)):
+        out, lse = sai.paged_attention(q, c.cache, c.t_table, _lens(lens), max_seq_len=50000, row_to_batch=_lens(r2b),
+                                       packed=True, window=window, sinks=sinks, want_lse=True)
+        _check(c, q64, [(b, A.seen(n, window, sinks)) for b, n in zip(r2b, lens)], out, lse, 128 ** -0.5)
+    assert sai.device_status() == 0
