@@ -890,15 +890,18 @@ AttnPlan attn_rows_plan(long long rows, int q_heads, int heads, int dim, bool f8
   const long long units = rows * heads * (group <= 64 ? 1 : (group + 63) / 64);
   // Chunks of at least 128 keys until a wave of CTAs (three per SM) is full:
   // one row of 700 keys takes 6.2 us with six chunks, 7.4 with three, 8.8 with
-  // eleven. Past that only long rows are cut, in chunks of at least 2048 keys,
-  // up to four waves, so that rows of unlike lengths even out: 64 rows of
+  // eleven. Past that only long rows are cut, in chunks of at least 512 keys, up
+  // to four waves, so that rows of unlike lengths even out: 64 rows of
   // 4096-32768 keys, e4m3, 410 us with four chunks a row, 460 with two.
   auto up = [](long long a, long long b) { return (a + b - 1) / b; };
   const long long wave = 3LL * num_sms;
   const long long fill = std::min(up(wave, std::max(1LL, units)), up(max_keys, 128));
-  const long long even = std::min(up(4 * wave, std::max(1LL, units)), up(max_keys, 2048));
+  const long long even = std::min(up(4 * wave, std::max(1LL, units)), up(max_keys, 512));
   const long long chunks = std::max(1LL, std::min(64LL, std::max(fill, even)));
-  AttnPlan pl{static_cast<int>(chunks), 0, false, chunks > 1 && chunks <= 8};
+  // a cluster only within the first wave: beyond it, waiting for as many free
+  // places at once costs more than the second kernel (37 windowed rows: 67 us
+  // clustered, 59 joined)
+  AttnPlan pl{static_cast<int>(chunks), 0, false, chunks > 1 && chunks <= 8 && units * chunks <= wave};
   // enough units for every team to have its own: no joining
   const int teams = group <= 16 ? 4 : group <= 32 ? 2 : 1;
   pl.own = chunks == 1 && units >= 4LL * num_sms * teams;

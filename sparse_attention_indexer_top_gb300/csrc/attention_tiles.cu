@@ -32,22 +32,24 @@
 // a few long units fill the GPU: a unit cut by a share's border leaves two or
 // more partial results (maximum, sum, O) that a second kernel joins.
 //
-// Roles (bf16 cache, 12 warps): 0-3 softmax of tile A, 4-7 softmax of tile B,
-// 8 TMA, 9 MMA, 10-11 "prep", which makes the value tile safe to multiply: a
-// weight of 0 times a NaN or infinity that a row must not see would still be
-// NaN, so in tiles that some row sees only in part, rows of V past the
-// request's end become 0, and rows with a non-finite value too; if such a row
-// of V is seen by some query row, its share is added at the end from
-// global memory.
+// Roles (12 warps): 0-3 softmax of tile A, 4-7 softmax of tile B, 8 TMA, 9
+// MMA, 10-11 "prep", which makes the value tile safe to multiply: a weight of 0
+// times a NaN or infinity that a row must not see would still be NaN, so in
+// tiles that some row sees only in part, rows of V past the request's end become
+// 0, and rows with a non-finite value too; if such a row of V is seen by some
+// query row, its share is added at the end from global memory.
 //
-// e4m3 cache (16 warps): the products run in f16, which holds e4m3 codes
-// exactly; 12-15 are the prep warps and turn the codes of each K and V tile
-// into halves in the MMA's layout (one conversion for two tiles of rows). The
-// queries are brought to [2^14, 2^15) by a power of two for each (row, head)
-// and stored as halves. The block scales stay out of the tiles: a key scale is
-// part of the softmax's multiplier, and with w_t = 2^(s_t - m) * vscale_t, taken
-// as one exponent s_t + log2(vscale_t) - m with m the maximum of s + log2
-// vscale, weights are at most 2^8 whatever the scales; l adds w_t / vscale_t.
+// e4m3 cache: the products run in f16, which holds e4m3 codes exactly. The prep
+// warps turn the codes of each K and V tile into halves in the MMA's layout, one
+// conversion for all the tiles of rows; with 2^E the power of two of the
+// tile's largest block scale, a block of scale 2^e f, 1 <= f < 2, is multiplied
+// by 2^(e - E) (exact down to e - E = -12), and the softmax applies 2^E: a key
+// tile's in its multiplier, a value tile's in the exponent, w_t = 2^(s_t + Ev -
+// m) with m the maximum of s + Ev, so that weights are at most 2^8 whatever the
+// scales; l adds w_t / 2^Ev. What is left of a scale, f or a power below 2^-12,
+// goes to the softmax too, 16 keys at a time: nothing when scales are
+// powers of two, as append_kv makes them. The queries are brought to [2^14,
+// 2^15) by a power of two for each (row, head) and stored as halves.
 #include <cuda.h>
 #include <cuda_fp16.h>
 
@@ -70,12 +72,9 @@ constexpr int kMaxRows = 2 * kTile * kPair<D>;        // query rows of a pair (g
 constexpr int kSoftmaxWarps = 8;
 constexpr int kTmaWarp = 8;
 constexpr int kMmaWarp = 9;
-template <bool F8>
-struct Roles {
-  static constexpr int kPrepWarp = F8 ? 12 : 10;
-  static constexpr int kPrepWarps = F8 ? 4 : 2;
-  static constexpr int kThreads = (kPrepWarp + kPrepWarps) * 32;
-};
+constexpr int kPrepWarp = 10;
+constexpr int kPrepWarps = 2;
+constexpr int kThreads = (kPrepWarp + kPrepWarps) * 32;
 constexpr uint32_t kSetUpBar = 1;  // named barrier of all threads between pieces
 constexpr float kLn2 = 0.69314718055994530942f;
 
@@ -125,8 +124,8 @@ struct Shared {
   unsigned char k[kStages][kKBytes];
   unsigned char v[kStages][kVBytes];
   unsigned char raw[kRaw ? kRaw : 1][kRaw ? kKeys * D : 16];
-  // In the first CTA of a pair, for both (the MMA waits there): q_ready, k_full,
-  // v_safe, p_ready. In each CTA for itself: the others.
+  // In the first CTA of a pair, for both (the MMA waits there): q_full (bf16),
+  // q_ready, k_full, v_safe, p_ready. In each CTA for itself: the others.
   uint64_t q_full, q_ready, k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages], v_safe[kStages];
   uint64_t raw_full[kRaw ? kRaw : 1], raw_empty[kRaw ? kRaw : 1];
   uint64_t s_ready[2], p_ready[2][2], o_done[2];  // p_ready: first and second half of the keys
@@ -141,7 +140,7 @@ struct Shared {
   int warp_starts[16];
   int row_n[kMaxRows<D>], row_b[kMaxRows<D>];
   int seg_start[kMaxRows<D> + 1], seg_most[kMaxRows<D>], seg_least[kMaxRows<D>], seg_low[kMaxRows<D>];
-  float4 scales[F8 ? kSoftmaxWarps : 1][8];  // per softmax warp: k scale, log2 v scale, 1 / v scale of 16 keys
+  float2 factors[F8 ? kSoftmaxWarps : 1][8];  // per softmax warp: what the tiles leave of the k and v scales of 16 keys
 };
 
 // One request's rows of the CTA (pair) and the tiles that the piece walks.
@@ -386,18 +385,21 @@ __device__ __forceinline__ bool nonfinite2(uint32_t x) {
   return (x & 0x7f80u) == 0x7f80u || (x & 0x7f800000u) == 0x7f800000u;
 }
 
-// log2 of a block scale: the exponent exactly, so powers of two are exact
-// (scales below 2^-100 count as 2^-100).
-__device__ __forceinline__ float log2_scale(float s) {
-  s = fmaxf(s, 7.888609052210118e-31f);
-  const uint32_t u = __float_as_uint(s);
-  return static_cast<float>(static_cast<int>(u >> 23) - 127) + log2f(__uint_as_float((u & 0x7fffffu) | 0x3f800000u));
+// Exponent of a block scale (scales outside 2^-100 .. 2^100 leave the rest to
+// their factor), and 2^e.
+__device__ __forceinline__ int exponent_of(float scale) {
+  return max(-100, min(100, static_cast<int>((__float_as_uint(scale) >> 23) & 255u) - 127));
 }
-// Two e4m3 codes of each 16-bit half to halves, exactly.
-__device__ __forceinline__ void e4m3x4_f16x4(uint32_t c, uint32_t& a, uint32_t& b) {
-  asm("{\n\t.reg .b16 x, y;\n\tmov.b32 {x, y}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, x;\n\tcvt.rn.f16x2.e4m3x2 %1, y;\n\t}"
-      : "=r"(a), "=r"(b)
-      : "r"(c));
+__device__ __forceinline__ float power_of(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
+constexpr int kNoScale = -1000;   // exponent of a group without a block
+constexpr int kLeastShift = -12;  // e - E that is still exact in f16
+
+// Two e4m3 codes of each 16-bit half to halves, times a power of two (two halves).
+__device__ __forceinline__ void e4m3x4_f16x4(uint32_t c, uint32_t power, uint32_t& a, uint32_t& b) {
+  asm("{\n\t.reg .b16 x, y;\n\tmov.b32 {x, y}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, x;\n\tcvt.rn.f16x2.e4m3x2 %1, y;\n\t"
+      "mul.rn.f16x2 %0, %0, %3;\n\tmul.rn.f16x2 %1, %1, %3;\n\t}"
+      : "=&r"(a), "=&r"(b)
+      : "r"(c), "r"(power));
 }
 __device__ __forceinline__ uint32_t pack_f16(float a, float b) {
   uint32_t r;
@@ -458,13 +460,13 @@ __device__ __noinline__ void add_nonfinite(const AttnLaunch& p, const Pass& ps, 
         const float2 b = values2<F8>(k, d);
         s = fmaf(bf16_lo(a), b.x, fmaf(bf16_hi(a), b.y, s));
       }
-      float e = s * p.scale_log2, vl = 0.f;
+      float e = s * p.scale_log2, vscale = 1.f;
       if (F8) {
         const long long at = static_cast<long long>(blk) * p.c.heads + kvh;
         e *= p.c.ks[at];
-        vl = log2_scale(p.c.vs[at]);
+        vscale = p.c.vs[at];
       }
-      const float w = ex2(e + vl - (m == -INFINITY ? 0.f : m));
+      const float w = ex2(e - (m == -INFINITY ? 0.f : m)) * vscale;
 #pragma unroll
       for (int d = 0; d < 16; ++d) {
         const float2 x = values2<F8>(v, c0 / 2 + d);
@@ -536,6 +538,81 @@ __device__ __forceinline__ float query_to_f16(unsigned char* tile, int r) {
   return __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
 }
 
+// Scores of 32 columns that the row does not see become -inf: columns from n
+// on, and those below `first` that are not below `sinks`; bits 0 and 1 of `bad`
+// take out 16 each. One bit a column, so that an element costs a test and a
+// select.
+__device__ __forceinline__ void mask32(uint32_t* s, int n, int first, int sinks, uint32_t bad) {
+  auto below = [](int x) { return x <= 0 ? 0u : x >= 32 ? ~0u : (1u << x) - 1u; };
+  uint32_t see = below(n) & (~below(first) | below(sinks));
+  if (bad & 1) see &= 0xffff0000u;
+  if (bad & 2) see &= 0x0000ffffu;
+#pragma unroll
+  for (int c = 0; c < 32; ++c)
+    if (!(see & (1u << c))) s[c] = 0xff800000u;
+}
+
+// Multiplies the thread's row of O by f.
+template <int D>
+__device__ __forceinline__ void rescale_o(uint32_t to, float f) {
+#pragma unroll 1
+  for (int c = 0; c < D; c += 32) {
+    uint32_t u[32];
+    tmem_ld32(to + c, u);
+    tmem_ld_wait32(u);
+#pragma unroll
+    for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(__uint_as_float(u[e]) * f);
+    tmem_st16(to + c, u);
+    tmem_st16(to + c + 16, u + 16);
+  }
+}
+
+// A tile of an e4m3 cache whose scales are not all in the tile's powers:
+// factors[g] are left over of 16 keys' scales. Out of line, and S is read twice
+// 32 columns at a time: beside the plain code it slowed that by half.
+template <int D>
+__device__ __noinline__ float2 rough_tile(uint32_t ts, uint32_t to, float2 ml, float mul, float ev, float un_ev,
+                                          const float2* factors, int3 sees, uint32_t bad, bool have_o) {
+  uint32_t s[32];
+  float top = -INFINITY;
+#pragma unroll 1
+  for (int c0 = 0; c0 < kTile; c0 += 32) {
+    tmem_ld32(ts + c0, s);
+    tmem_ld_wait32(s);
+    mask32(s, sees.x - c0, sees.y - c0, sees.z - c0, bad >> (c0 / 16));
+#pragma unroll
+    for (int c = 0; c < 32; ++c) top = fmaxf(top, __uint_as_float(s[c]) * factors[(c0 + c) / 16].x);
+  }
+  top = fmaf(top, mul, ev);
+  const bool up = top > ml.x + 8.f;
+  if (__any_sync(0xffffffffu, up)) {
+    const float f = up ? (ml.x == -INFINITY ? 0.f : ex2(ml.x - top)) : 1.f;
+    if (up) ml.x = top;
+    ml.y *= f;
+    if (have_o) rescale_o<D>(to, f);
+  }
+  const float off = ev - (ml.x == -INFINITY ? 0.f : ml.x);
+  float sum = 0.f;
+#pragma unroll 1
+  for (int c0 = 0; c0 < kTile; c0 += 32) {  // weights of chunk c go over scores of chunk c / 2
+    tmem_ld32(ts + c0, s);
+    tmem_ld_wait32(s);
+    mask32(s, sees.x - c0, sees.y - c0, sees.z - c0, bad >> (c0 / 16));
+#pragma unroll
+    for (int c = 0; c < 32; c += 2) {
+      const float2 f = factors[(c0 + c) / 16];
+      const float a = ex2(fmaf(__uint_as_float(s[c]), mul * f.x, off));
+      const float b = ex2(fmaf(__uint_as_float(s[c + 1]), mul * f.x, off));
+      sum += a + b;
+      s[c / 2] = pack_f16(a * f.y, b * f.y);
+    }
+    tmem_st16(ts + c0 / 2, s);
+  }
+  tmem_st_wait();
+  ml.y = fmaf(sum, un_ev, ml.y);
+  return ml;
+}
+
 // What a role has behind it, over the pieces: the phases of its barriers.
 struct Progress {
   int pieces = 0, tiles = 0, passes = 0;
@@ -601,13 +678,24 @@ __device__ __forceinline__ bool softmax_role(Shared<D, F8>& S, const TilesLaunch
     float2 sc1 = scales_of(blk1);
     for (int i = ps.i0; i < ps.i1; ++i) {
       const uint32_t bad = __ballot_sync(0xffffffffu, blk1 == -2);
-      const float4* gs = S.scales[F8 ? warp : 0];
+      // the tile's multiplier and exponent; rough: scales are not all of it
+      float mul = scale, ev = 0.f, un_ev = 1.f;
+      bool rough = false;
+      const float2* factors = S.factors[F8 ? warp : 0];
       if (F8) {
-        __syncwarp();  // the last tile's have been read
-        if (lane < 8)
-          S.scales[warp][lane] =
-              make_float4(sc1.x, log2_scale(sc1.y), 1.f / fmaxf(sc1.y, 7.888609052210118e-31f), 0.f);
-        __syncwarp();
+        const int ek = blk1 >= 0 ? exponent_of(sc1.x) : kNoScale, e2 = blk1 >= 0 ? exponent_of(sc1.y) : kNoScale;
+        const int tk = max(-100, __reduce_max_sync(0xffffffffu, ek)), tv = max(-100, __reduce_max_sync(0xffffffffu, e2));
+        mul = scale * power_of(tk);
+        ev = static_cast<float>(tv);
+        un_ev = power_of(-tv);
+        const float2 f = blk1 >= 0 ? make_float2(sc1.x * power_of(-max(ek, tk + kLeastShift)),
+                                                 sc1.y * power_of(-max(e2, tv + kLeastShift)))
+                                   : make_float2(1.f, 1.f);
+        rough = __any_sync(0xffffffffu, f.x != 1.f || f.y != 1.f);
+        if (rough) {
+          if (lane < 8) S.factors[warp][lane] = f;
+          __syncwarp();
+        }
         sc1 = scales_of(blk2);
       }
       blk1 = blk2;
@@ -620,20 +708,7 @@ __device__ __forceinline__ bool softmax_role(Shared<D, F8>& S, const TilesLaunch
       const bool whole = t0 + kTile <= ln.n && (t0 >= ln.first || t0 + kTile <= ln.sinks);
       const bool masked = !__all_sync(0xffffffffu, whole) || bad;
       if (bad && lane == 0) atomicOr(p.status, kDevBadPage);
-      // scores of columns [c0, c0 + 32) that the row does not see become -inf:
-      // one bit a column, so that an element costs a test and a select
-      auto mask = [&](uint32_t* s, int c0) {
-        auto below = [&](int x) {  // the bits under column x of the tile
-          x -= t0 + c0;
-          return x <= 0 ? 0u : x >= 32 ? ~0u : (1u << x) - 1u;
-        };
-        uint32_t see = below(ln.n) & (~below(ln.first) | below(ln.sinks));
-        if ((bad >> (c0 / 16)) & 1) see &= 0xffff0000u;
-        if ((bad >> (c0 / 16)) & 2) see &= 0x0000ffffu;
-#pragma unroll
-        for (int c = 0; c < 32; ++c)
-          if (!(see & (1u << c))) s[c] = 0xff800000u;
-      };
+      auto mask = [&](uint32_t* s, int c0) { mask32(s, ln.n - t0 - c0, ln.first - t0 - c0, ln.sinks - t0 - c0, bad >> (c0 / 16)); };
       // largest exponent of 32 columns
       auto largest = [&](const uint32_t* s, int c0, float top) {
 #pragma unroll
@@ -645,48 +720,36 @@ __device__ __forceinline__ bool softmax_role(Shared<D, F8>& S, const TilesLaunch
           a = max3(a, at(10), at(11));
           b = max3(b, at(12), at(13));
           a = max3(a, at(14), at(15));
-          if (F8) {
-            const float4 k = gs[c0 / 16 + g];
-            top = fmaxf(top, fmaf(fmaxf(a, b), scale * k.x, k.y));
-          } else {
-            top = max3(top, a, b);
-          }
+          top = max3(top, a, b);
         }
         return top;
       };
-      // bf16: the row of S stays in registers. e4m3 (more warps, fewer
-      // registers each): its first half does; the other columns are read for
-      // the maximum and read again for their weights.
-      constexpr int kHeld = F8 ? 64 : 128;
-      uint32_t s[kHeld], u[32];
-#pragma unroll
-      for (int c = 0; c < kHeld; c += 32) tmem_ld32(ts + c, s + c);
-      float top = -INFINITY;
-      if (F8) {
-        tmem_ld32(ts + 64, u);
-        tmem_ld_wait32(u);
-#pragma unroll
-        for (int c = 0; c < kHeld; c += 32) tmem_ld_wait32(s + c);
-        if (masked) mask(u, 64);
-        top = largest(u, 64, top);
-        tmem_ld32(ts + 96, u);
-      } else {
-#pragma unroll
-        for (int c = 0; c < kHeld; c += 32) tmem_ld_wait32(s + c);
+      if (F8 && rough) {
+        const float2 ml = rough_tile<D>(ts, to, make_float2(m, l), mul, ev, un_ev, factors,
+                                        make_int3(ln.n - t0, ln.first - t0, ln.sinks - t0), bad, i > ps.i0);
+        m = ml.x;
+        l = ml.y;
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          arrive_first<PAIR>(&S.p_ready[x][0]);
+          arrive_first<PAIR>(&S.p_ready[x][1]);
+        }
+        continue;
       }
+      uint32_t s[kTile];
+#pragma unroll
+      for (int c = 0; c < kTile; c += 32) tmem_ld32(ts + c, s + c);
+#pragma unroll
+      for (int c = 0; c < kTile; c += 32) tmem_ld_wait32(s + c);
       if (masked) {
 #pragma unroll
-        for (int c = 0; c < kHeld; c += 32) mask(s + c, c);
+        for (int c = 0; c < kTile; c += 32) mask(s + c, c);
       }
+      float top = -INFINITY;
 #pragma unroll
-      for (int c = 0; c < kHeld; c += 32) top = largest(s + c, c, top);
-      if (F8) {
-        tmem_ld_wait32(u);
-        if (masked) mask(u, 96);
-        top = largest(u, 96, top);
-      } else {
-        top *= scale;
-      }
+      for (int c = 0; c < kTile; c += 32) top = largest(s + c, c, top);
+      top = fmaf(top, mul, ev);
       // the maximum moves only when it is passed by more than 2^8: weights up
       // to 256 are as exact in 16 bits as weights up to 1, and O is rarely
       // rescaled
@@ -695,44 +758,27 @@ __device__ __forceinline__ bool softmax_role(Shared<D, F8>& S, const TilesLaunch
         const float f = up ? (m == -INFINITY ? 0.f : ex2(m - top)) : 1.f;
         if (up) m = top;
         l *= f;
-        if (i > ps.i0) {
-#pragma unroll 1
-          for (int c = 0; c < D; c += 32) {
-            tmem_ld32(to + c, u);
-            tmem_ld_wait32(u);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(__uint_as_float(u[e]) * f);
-            tmem_st16(to + c, u);
-            tmem_st16(to + c + 16, u + 16);
-          }
-        }
+        if (i > ps.i0) rescale_o<D>(to, f);
       }
       const float base = m == -INFINITY ? 0.f : m;
-      // weights of 32 columns, 16 bits each (relative error 2^-9, f16 2^-12;
-      // under the output's own), over the scores' TMEM columns
+      // weights of 32 columns in 16 bits (relative error 2^-9, f16 2^-12; under
+      // the output's own), over the scores' TMEM columns
+      float tile_l = 0.f;
       auto weights = [&](uint32_t* s, int c0) {
         uint64_t sum[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
-        uint64_t scale2 = pair(scale, scale), base2 = pair(-base, -base);
-        float a, b, inv = 1.f;
+        const float off = ev - base;
+        float a, b;
+        const uint64_t mul2 = pair(mul, mul), off2 = pair(off, off);
 #pragma unroll
         for (int c = 0; c < 32; c += 2) {
-          if (F8 && c % 16 == 0) {
-            const float4 k = gs[(c0 + c) / 16];
-            scale2 = pair(scale * k.x, scale * k.x);
-            base2 = pair(k.y - base, k.y - base);
-            inv = k.z;
-          }
-          unpair(fma2(pair(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), scale2, base2), a, b);
+          unpair(fma2(pair(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), mul2, off2), a, b);
           a = ex2(a);
           b = ex2(b);
           sum[(c >> 1) & 1] = add2(sum[(c >> 1) & 1], pair(a, b));
           s[c / 2] = F8 ? pack_f16(a, b) : pack_bf16(a, b);
-          if (c % 16 == 14 && (F8 || c == 30)) {
-            unpair(add2(sum[0], sum[1]), a, b);
-            l = F8 ? fmaf(a + b, inv, l) : l + (a + b);
-            sum[0] = sum[1] = pair(0.f, 0.f);
-          }
         }
+        unpair(add2(sum[0], sum[1]), a, b);
+        tile_l += a + b;
         tmem_st16(ts + c0 / 2, s);
       };
       auto hand_over = [&](int half) {
@@ -741,23 +787,13 @@ __device__ __forceinline__ bool softmax_role(Shared<D, F8>& S, const TilesLaunch
         __syncwarp();
         if (lane == 0) arrive_first<PAIR>(&S.p_ready[x][half]);
       };
-      if (F8) tmem_ld32(ts + 64, u);
       weights(s, 0);
       weights(s + 32, 32);
       hand_over(0);
-      if (F8) {
-        tmem_ld_wait32(u);
-        tmem_ld32(ts + 96, s);
-        if (masked) mask(u, 64);
-        weights(u, 64);
-        tmem_ld_wait32(s);
-        if (masked) mask(s, 96);
-        weights(s, 96);
-      } else {
-        weights(s + kHeld / 2, 64);
-        weights(s + kHeld - 32, 96);
-      }
+      weights(s + 64, 64);
+      weights(s + 96, 96);
       hand_over(1);
+      l = fmaf(tile_l, un_ev, l);
     }
     const bool ok = mbar_wait(&S.o_done[x], at.passes & 1);
     if (!__all_sync(0xffffffffu, ok)) return false;
@@ -948,10 +984,10 @@ __device__ __forceinline__ bool mma_role(Shared<D, F8>& S, const TilesLaunch& L,
 
 // --------------------------------------------------------------------- prep
 template <int D>
-__device__ __forceinline__ bool prep_role(Shared<D, false>& S, const TilesLaunch& L, Progress& progress) {
+__device__ __forceinline__ bool prep_role(Shared<D, false>& S, const TilesLaunch& L, int, Progress& progress) {
   const AttnLaunch& p = L.a;
-  constexpr int PAIR = kPair<D>, kStages = Shared<D, false>::kStages, kPrepWarps = Roles<false>::kPrepWarps;
-  const int tid = threadIdx.x - Roles<false>::kPrepWarp * 32;
+  constexpr int PAIR = kPair<D>, kStages = Shared<D, false>::kStages;
+  const int tid = threadIdx.x - kPrepWarp * 32;
   int& done = progress.tiles;
   for (int seg = 0; seg < S.segs; ++seg) {
     const Pass ps = get_pass(S, L, seg);
@@ -995,22 +1031,32 @@ __device__ __forceinline__ bool prep_role(Shared<D, false>& S, const TilesLaunch
   return true;
 }
 
-// e4m3: 16-code pieces of a raw tile (rows of ROW codes) to halves in the MMA's
-// layout: 128-byte swizzled rows of 64 dims, slabs of ROWS rows. The lanes of
-// one row read its pieces; a piece becomes two 16-byte chunks, written in an
-// order that keeps the eight lanes of a store on different banks. CHECK: rows
-// from `dead` on and rows with a NaN become 0; returns whether there was a NaN.
+// e4m3: 16-code pieces of a raw tile (ROWS rows of ROW codes) to halves in the
+// MMA's layout: 128-byte swizzled rows of 64 dims, slabs of ROWS rows. The
+// lanes of one row read its pieces; a piece becomes two 16-byte chunks, written
+// in an order that keeps the eight lanes of a store on different banks. Lane
+// `lane0` + g of the warp has the power of two of the rows 16g to 16g + 15.
+// `check`: rows from `dead` on and rows with a NaN become 0; returns whether
+// there was a NaN.
 template <int ROWS, int ROW>
-__device__ __forceinline__ bool codes_to_halves(const uint4 (&x)[4], unsigned char* out, int tid, bool check, int dead) {
-  constexpr int kPieces = ROW / 16, kStep = 128;
-  static_assert(ROWS * kPieces == 4 * kStep, "four pieces per thread");
+__device__ __forceinline__ bool codes_to_halves(const uint4* raw, unsigned char* out, int tid, uint32_t power, int lane0,
+                                                bool check, int dead) {
+  constexpr int kPieces = ROW / 16, kStep = kPrepWarps * 32;
+  static_assert(ROWS * kPieces == 8 * kStep, "eight pieces per thread");
   const int piece = tid % kPieces;
   bool met = false;
   out += (piece / 4) * ROWS * 128;
+#pragma unroll 1
+  for (int j0 = 0; j0 < 8; j0 += 4) {
+  uint4 x[4];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
+  for (int j = 0; j < 4; ++j) x[j] = raw[(j0 + j) * kStep + tid];
+#pragma unroll
+  for (int jj = 0; jj < 4; ++jj) {
+    const int j = j0 + jj;
     const int key = (j * kStep + tid) / kPieces;
-    uint4 c = x[j];
+    const uint32_t f = __shfl_sync(0xffffffffu, power, lane0 + j * (kStep / kPieces) / 16);
+    uint4 c = x[jj];
     if (check) {
       const uint32_t w[4] = {c.x, c.y, c.z, c.w};
       bool nan = false;
@@ -1025,52 +1071,74 @@ __device__ __forceinline__ bool codes_to_halves(const uint4 (&x)[4], unsigned ch
       if (zero) c = make_uint4(0, 0, 0, 0);
     }
     uint4 a, b;
-    e4m3x4_f16x4(c.x, a.x, a.y);
-    e4m3x4_f16x4(c.y, a.z, a.w);
-    e4m3x4_f16x4(c.z, b.x, b.y);
-    e4m3x4_f16x4(c.w, b.z, b.w);
+    e4m3x4_f16x4(c.x, f, a.x, a.y);
+    e4m3x4_f16x4(c.y, f, a.z, a.w);
+    e4m3x4_f16x4(c.z, f, b.x, b.y);
+    e4m3x4_f16x4(c.w, f, b.z, b.w);
     const int odd = kPieces == 8 ? piece >> 2 : 0;  // dims above 64 write their second chunk first
     const int c0 = 2 * (piece & 3) + odd;
     *reinterpret_cast<uint4*>(out + key * 128 + ((c0 ^ (key & 7)) << 4)) = odd ? b : a;
     *reinterpret_cast<uint4*>(out + key * 128 + (((c0 ^ 1) ^ (key & 7)) << 4)) = odd ? a : b;
   }
+  }
   return met;
 }
 
 template <int D>
-__device__ __forceinline__ bool prep_role(Shared<D, true>& S, const TilesLaunch& L, Progress& progress) {
+__device__ __forceinline__ bool prep_role(Shared<D, true>& S, const TilesLaunch& L, int rank, Progress& progress) {
   using Sh = Shared<D, true>;
   constexpr int PAIR = kPair<D>, kRaw = Sh::kRaw, kStages = Sh::kStages;
-  static_assert(Sh::kKeys * D == 4 * 128 * 16 && kTile * Sh::kDims == 4 * 128 * 16, "four pieces per thread");
   const AttnLaunch& p = L.a;
-  const int tid = threadIdx.x - Roles<true>::kPrepWarp * 32;
+  const int tid = threadIdx.x - kPrepWarp * 32, lane = threadIdx.x & 31;
+  const int kvh = S.piece.kvh;
   int& done = progress.tiles;
   for (int seg = 0; seg < S.segs; ++seg) {
     const Pass ps = get_pass(S, L, seg);
+    // lanes 0-7: block of the tile's 16-key group, read two tiles ahead, and its
+    // scales, read one ahead
+    auto block_of = [&](int i) -> int {
+      if (i >= ps.i1 || lane >= 8) return -1;
+      const int t = ps.tile0(i) + 16 * lane;
+      if (t >= ps.most) return -1;
+      return p.block_table[ps.batch * p.bt_stride + (t >> p.c.bs_log2)];
+    };
+    auto exponents_of = [&](int blk) -> int2 {
+      if (blk < 0 || blk >= p.c.num_blocks) return make_int2(kNoScale, kNoScale);
+      const long long at = static_cast<long long>(blk) * p.c.heads + kvh;
+      return make_int2(exponent_of(p.c.ks[at]), exponent_of(p.c.vs[at]));
+    };
+    int blk1 = block_of(ps.i0 + 1);
+    int2 ex = exponents_of(block_of(ps.i0));
+    // 2^(e - E) as two halves, of this lane's 16 keys
+    auto shift_of = [&](int e) -> uint32_t {
+      const int d = max(kLeastShift, e - max(-100, __reduce_max_sync(0xffffffffu, e)));
+      return static_cast<uint32_t>(15 + d) << 10 | static_cast<uint32_t>(15 + d) << 26;
+    };
     for (int i = ps.i0; i < ps.i1; ++i, ++done) {
+      const uint32_t k_power = shift_of(ex.x), v_power = shift_of(ex.y);
+      ex = exponents_of(blk1);
+      blk1 = block_of(i + 2);
       const int t0 = ps.tile0(i), st = done % kStages;
       const bool check = ps.partial(t0, p);
 #pragma unroll
       for (int kv = 0; kv < 2; ++kv) {
         const int idx = 2 * done + kv, rs = idx % kRaw;
         bool ok = mbar_wait(&S.raw_full[rs], (idx / kRaw) & 1);
-        uint4 x[4];
-        if (ok) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) x[j] = *reinterpret_cast<const uint4*>(S.raw[rs] + (j * 128 + tid) * 16);
-          ok = mbar_wait(kv ? &S.v_empty[st] : &S.k_empty[st], ((done / kStages) & 1) ^ 1);
-        }
+        ok = ok && mbar_wait(kv ? &S.v_empty[st] : &S.k_empty[st], ((done / kStages) & 1) ^ 1);
         if (!__all_sync(0xffffffffu, ok)) return false;
-        if ((threadIdx.x & 31) == 0) mbar_arrive(&S.raw_empty[rs]);  // every lane has its pieces
+        const uint4* raw = reinterpret_cast<const uint4*>(S.raw[rs]);
         if (kv) {
-          if (codes_to_halves<kTile, Sh::kDims>(x, S.v[st], tid, check, ps.most - t0))
+          if (codes_to_halves<kTile, Sh::kDims>(raw, S.v[st], tid, v_power, 0, check, ps.most - t0))
             *reinterpret_cast<volatile int*>(&S.nonfinite) = seg + 1;
         } else {
-          codes_to_halves<Sh::kKeys, D>(x, S.k[st], tid, false, 0);
+          codes_to_halves<Sh::kKeys, D>(raw, S.k[st], tid, k_power, rank * (Sh::kKeys / 16), false, 0);
         }
         fence_proxy_async_smem();  // the MMA reads these stores through the async proxy
         __syncwarp();
-        if ((threadIdx.x & 31) == 0) arrive_first<PAIR>(kv ? &S.v_safe[st] : &S.k_full[st]);
+        if (lane == 0) {
+          mbar_arrive(&S.raw_empty[rs]);
+          arrive_first<PAIR>(kv ? &S.v_safe[st] : &S.k_full[st]);
+        }
       }
     }
   }
@@ -1084,7 +1152,7 @@ __device__ __forceinline__ void deal_units(Shared<D, F8>& S, const TilesLaunch& 
   const AttnLaunch& p = L.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rows_here = 2 * kPair<D> * L.rows_per_tile;
-  for (int t = warp; t < L.row_tiles; t += Roles<F8>::kThreads / 32) {
+  for (int t = warp; t < L.row_tiles; t += kThreads / 32) {
     int most = 0, low = INT_MAX;
     for (int i = lane; i < rows_here && t * rows_here + i < p.rows; i += 32) {
       const int n = p.seq_lens[t * rows_here + i];
@@ -1157,7 +1225,7 @@ __device__ __forceinline__ Piece next_piece(const Shared<D, F8>& S, const TilesL
 template <int D, bool F8>
 __device__ __forceinline__ void set_up_rows(Shared<D, F8>& S, const TilesLaunch& L) {
   const Piece& pc = S.piece;
-  constexpr int kThreads = Roles<F8>::kThreads, kRows = kMaxRows<D>, kGroups = kRows / 32;
+  constexpr int kRows = kMaxRows<D>, kGroups = kRows / 32;
   const AttnLaunch& p = L.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rows_here = 2 * kPair<D> * L.rows_per_tile;
@@ -1210,7 +1278,7 @@ __device__ __forceinline__ void set_up_rows(Shared<D, F8>& S, const TilesLaunch&
 }
 
 template <int D, bool F8>
-__global__ void __launch_bounds__(Roles<F8>::kThreads, 1)
+__global__ void __launch_bounds__(kThreads, 1)
     attn_tiles_kernel(const __grid_constant__ TilesLaunch L, const __grid_constant__ CUtensorMap qmap,
                       const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
   extern __shared__ unsigned char raw[];
@@ -1225,15 +1293,15 @@ __global__ void __launch_bounds__(Roles<F8>::kThreads, 1)
     mbar_init(&S.q_full, 1);
     mbar_init(&S.q_ready, kSoftmaxWarps * PAIR);
     for (int i = 0; i < Sh::kStages; ++i) {
-      mbar_init(&S.k_full[i], F8 ? Roles<F8>::kPrepWarps * PAIR : 1);
+      mbar_init(&S.k_full[i], F8 ? kPrepWarps * PAIR : 1);
       mbar_init(&S.k_empty[i], 1);
       mbar_init(&S.v_full[i], 1);
       mbar_init(&S.v_empty[i], 1);
-      mbar_init(&S.v_safe[i], Roles<F8>::kPrepWarps * PAIR);
+      mbar_init(&S.v_safe[i], kPrepWarps * PAIR);
     }
     for (int i = 0; i < Sh::kRaw; ++i) {
       mbar_init(&S.raw_full[i], 1);
-      mbar_init(&S.raw_empty[i], Roles<F8>::kPrepWarps);
+      mbar_init(&S.raw_empty[i], kPrepWarps);
     }
     for (int x = 0; x < 2; ++x) {
       mbar_init(&S.s_ready[x], 1);
@@ -1292,7 +1360,7 @@ __global__ void __launch_bounds__(Roles<F8>::kThreads, 1)
       }
       __syncwarp();
       tc_fence_before();
-      named_bar(kSetUpBar, Roles<F8>::kThreads);
+      named_bar(kSetUpBar, kThreads);
       // neither CTA goes on, or ends, while the other may still read or signal it
       if (PAIR == 2) cluster_sync();
       tc_fence_after();
@@ -1301,32 +1369,21 @@ __global__ void __launch_bounds__(Roles<F8>::kThreads, 1)
         S.more = S.step < S.end && !S.stop;
         if (S.more) S.piece = next_piece(S, L, group, S.step, S.begin, S.end);
       }
-      named_bar(kSetUpBar, Roles<F8>::kThreads);
+      named_bar(kSetUpBar, kThreads);
     }
   };
-  // the softmax warps hold (half of) a row of S; the others give up what
-  // they take beyond the launch's share: 2 * 200 + 104 = 3 * 168 (12 warps),
-  // 2 * 160 + 88 + 104 = 4 * 128 (16 warps)
+  // the softmax warps hold a row of S (128 registers); the others give up what
+  // they take beyond the launch's share: 2 * 200 + 104 = 3 * 168
   if (warp < kSoftmaxWarps) {
-    if (F8)
-      asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
-    else
-      asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
     pieces([&](Progress& at) { return softmax_role<D, F8>(S, L, warp >> 2, rank, at); });
-  } else if (warp < 12) {
-    if (F8)
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-    else
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
     pieces([&](Progress& at) {
       if (warp == kTmaWarp) return tma_role<D, F8>(S, L, &qmap, &kmap, &vmap, rank, at);
       if (warp == kMmaWarp) return lane != 0 || rank != 0 || mma_role<D, F8>(S, L, at);
-      if constexpr (!F8) return prep_role<D>(S, L, at);
-      return true;
+      return prep_role<D>(S, L, rank, at);
     });
-  } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
-    if constexpr (F8) pieces([&](Progress& at) { return prep_role<D>(S, L, at); });
   }
   __syncthreads();
   if (warp == kMmaWarp) {
@@ -1472,7 +1529,7 @@ cudaError_t launch_tiles_t(const AttnLaunch& p, const Work& w, void* workspace, 
   if (grid > INT_MAX) return cudaErrorInvalidConfiguration;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(grid));
-  cfg.blockDim = dim3(Roles<F8>::kThreads);
+  cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute at[1];

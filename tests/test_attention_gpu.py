@@ -27,7 +27,8 @@ def _bits(x, dtype):
 class Case:
     """A paged cache with `total` tokens for each request, NaN in every cell that holds none."""
 
-    def __init__(self, seed, totals, *, dtype, hkv=2, dim=128, bs=128, nhd=False, blocks=None, vscales=(-8, -5)):
+    def __init__(self, seed, totals, *, dtype, hkv=2, dim=128, bs=128, nhd=False, blocks=None, vscales=(-8, -5),
+                 any_scales=False):
         rng = np.random.default_rng(seed)
         self.rng, self.bs, self.hkv, self.dim, self.dtype = rng, bs, hkv, dim, dtype
         per = [max(1, -(-t // bs)) for t in totals]
@@ -52,6 +53,9 @@ class Case:
         if dtype == "e4m3":
             self.ks, self.vs = (torch.exp2(torch.from_numpy(rng.integers(*r, (nb, hkv))).float()).to(DEV)
                                 for r in ((-8, -5), vscales))
+            if any_scales:
+                for x in (self.ks, self.vs):
+                    x.mul_(torch.from_numpy(rng.uniform(1, 2, (nb, hkv))).float().to(DEV))
         self.kv = []
         for b, t in enumerate(totals):
             vals = []
@@ -436,3 +440,25 @@ def test_packed_rows_dealt_out_by_a_far_bound(dtype):
                                        packed=True, window=window, sinks=sinks, want_lse=True)
         _check(c, q64, [(b, A.seen(n, window, sinks)) for b, n in zip(r2b, lens)], out, lse, 128 ** -0.5)
     assert sai.device_status() == 0
+
+
+@pytest.mark.parametrize("packed", [False, True])
+@pytest.mark.parametrize("dim,group,bs", [(128, 4, 16), (64, 8, 128), (128, 20, 64)])
+def test_scales_that_are_no_powers_of_two(packed, dim, group, bs):
+    reqs = [(90, 400), (1, 150), (64, 64)]
+    c = Case(58, [t for _, t in reqs], dtype="e4m3", dim=dim, bs=bs, any_scales=True)
+    lens = [t - n + j + 1 for n, t in reqs for j in range(n)]
+    r2b = [b for b, (n, _) in enumerate(reqs) for _ in range(n)]
+    q, q64 = c.queries(len(lens), 2 * group)
+    out, lse = sai.paged_attention(q, c.cache, c.t_table, _lens(lens), max_seq_len=400, row_to_batch=_lens(r2b),
+                                   packed=packed, want_lse=True)
+    _check(c, q64, [(b, np.arange(n)) for b, n in zip(r2b, lens)], out, lse, dim ** -0.5)
+
+
+def test_packed_block_scales_far_apart():
+    lens = list(range(201, 301))
+    c = Case(59, [300], dtype="e4m3", bs=16, vscales=(-40, 30))
+    q, q64 = c.queries(100, 8)
+    out, lse = sai.paged_attention(q, c.cache, c.t_table, _lens(lens), max_seq_len=300, row_to_batch=_lens([0] * 100),
+                                   packed=True, want_lse=True)
+    _check(c, q64, [(0, np.arange(n)) for n in lens], out, lse, 128 ** -0.5)
