@@ -118,12 +118,13 @@ struct Shared {
   static constexpr int kKBytes = kSlabs * kKeys * 128, kVBytes = kTile * 128;
   // K and V tiles of the MMA; of e4m3 fewer, fed from a ring of code tiles
   // that K and V take in turn
-  static constexpr int kStages = F8 ? 2 : D == 128 ? 4 : 3;
+  static constexpr int kStages = F8 ? 2 : 3;
   static constexpr int kRaw = F8 ? 8 : 0;
   unsigned char q[2][kQBytes];
   unsigned char k[kStages][kKBytes];
   unsigned char v[kStages][kVBytes];
   unsigned char raw[kRaw ? kRaw : 1][kRaw ? kKeys * D : 16];
+  unsigned char stage[kSoftmaxWarps][32 * 64];  // rows on their way out
   // In the first CTA of a pair, for both (the MMA waits there): q_full (bf16),
   // q_ready, k_full, v_safe, p_ready. In each CTA for itself: the others.
   uint64_t q_full, q_ready, k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages], v_safe[kStages];
@@ -477,31 +478,57 @@ __device__ __noinline__ void add_nonfinite(const AttnLaunch& p, const Pass& ps, 
   }
 }
 
+// Writes 64 bytes of each of the warp's 32 rows (`mine` of the lane's own, to
+// `dst`, null: not written). A lane's row is a line of its own in memory, so
+// the rows go through 2 KB of shared memory and four lanes write one
+// row's 64 bytes: a quarter of the store's passes (an epilogue of 10,400 cycles
+// without).
+__device__ __forceinline__ void write_rows64(unsigned char* stage, const uint4 (&mine)[4], char* dst) {
+  const int lane = threadIdx.x & 31;
+  __syncwarp();  // the last 64 bytes have been read
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
+    *reinterpret_cast<uint4*>(stage + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4)) = mine[c];
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int row = 8 * i + lane / 4, c = lane % 4;
+    const uint4 x = *reinterpret_cast<const uint4*>(stage + row * 64 + ((c ^ ((row >> 1) & 3)) << 4));
+    char* to = reinterpret_cast<char*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(dst), row));
+    if (to) *reinterpret_cast<uint4*>(to + 16 * c) = x;
+  }
+}
+
 // 32 columns of the thread's row, from column c0; an unseen row's O may hold
 // anything. `part`: place of the row's partial results, -1: they are final.
 template <int D>
 __device__ __forceinline__ void write_columns(const AttnLaunch& p, const Lane& ln, long long part, float l, int c0,
-                                              const float (&o)[32]) {
-  if (!ln.live) return;
+                                              const float (&o)[32], unsigned char* stage) {
   const bool none = l == 0.f;
+  uint4 x[4];
   if (part >= 0) {
-    float4* dst = reinterpret_cast<float4*>(p.part_o + part * D + c0);
+    char* dst = ln.live ? reinterpret_cast<char*>(p.part_o + part * D + c0) : nullptr;
 #pragma unroll
-    for (int d = 0; d < 8; ++d)
-      dst[d] = none ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(o[4 * d], o[4 * d + 1], o[4 * d + 2], o[4 * d + 3]);
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int d = 0; d < 4; ++d) {
+        const float* v = o + 16 * h + 4 * d;
+        x[d] = none ? make_uint4(0, 0, 0, 0)
+                    : make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+      }
+      write_rows64(stage, x, dst ? dst + 64 * h : nullptr);
+    }
     return;
   }
   const float inv = none ? 0.f : 1.f / l;
-  uint4* dst = reinterpret_cast<uint4*>(p.out + ln.head * D + c0);
 #pragma unroll
   for (int d = 0; d < 4; ++d) {
-    uint4 x;
-    x.x = pack_bf16(o[8 * d] * inv, o[8 * d + 1] * inv);
-    x.y = pack_bf16(o[8 * d + 2] * inv, o[8 * d + 3] * inv);
-    x.z = pack_bf16(o[8 * d + 4] * inv, o[8 * d + 5] * inv);
-    x.w = pack_bf16(o[8 * d + 6] * inv, o[8 * d + 7] * inv);
-    dst[d] = none ? make_uint4(0, 0, 0, 0) : x;
+    const float* v = o + 8 * d;
+    x[d] = none ? make_uint4(0, 0, 0, 0)
+                : make_uint4(pack_bf16(v[0] * inv, v[1] * inv), pack_bf16(v[2] * inv, v[3] * inv),
+                             pack_bf16(v[4] * inv, v[5] * inv), pack_bf16(v[6] * inv, v[7] * inv));
   }
+  write_rows64(stage, x, ln.live ? reinterpret_cast<char*>(p.out + ln.head * D + c0) : nullptr);
 }
 __device__ __forceinline__ void write_sums(const AttnLaunch& p, const Lane& ln, long long part, float m, float l) {
   if (!ln.live) return;
@@ -651,12 +678,13 @@ __device__ __forceinline__ bool softmax_role(Shared<D, F8>& S, const TilesLaunch
     ln.first = p.window > 0 ? max(0, ln.n - p.window) : 0;
     ln.sinks = min(p.sinks, ln.first);
     ln.head = static_cast<long long>(ln.row) * p.q_heads + pc.kvh * p.group + r % p.group;
+    // -1: final
     const long long part = pc.slot < 0 ? -1 : (static_cast<long long>(pc.slot) * 2 * PAIR * L.rows_per_tile + local) * p.group + r % p.group;
     float m = -INFINITY, l = 0.f;
     if (ps.i0 == ps.i1) {
       const float o[32] = {};
 #pragma unroll 1
-      for (int c = 0; c < D; c += 32) write_columns<D>(p, ln, part, l, c, o);
+      for (int c = 0; c < D; c += 32) write_columns<D>(p, ln, part, l, c, o, S.stage[warp]);
       write_sums(p, ln, part, m, l);
       continue;
     }
@@ -814,7 +842,7 @@ __device__ __forceinline__ bool softmax_role(Shared<D, F8>& S, const TilesLaunch
 #pragma unroll
       for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(u[e]);
       if (extra) add_nonfinite<D, F8>(p, get_pass(S, L, seg), pc.kvh, ln, m, c, o);
-      write_columns<D>(p, ln, part, l, c, o);
+      write_columns<D>(p, ln, part, l, c, o, S.stage[warp]);
     }
     tc_fence_before();
     write_sums(p, ln, part, m, l);
