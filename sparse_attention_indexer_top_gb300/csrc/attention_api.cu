@@ -30,9 +30,11 @@ int check_cache(const sai_kv_cache* c, sai::CacheView* out) {
   if (!c->k || !c->v || (f8 && (!c->k_scale || !c->v_scale))) return SAI_ERR_NULL;
   const int elem = f8 ? 1 : 2;
   for (int i = 0; i < 3; ++i) {
-    out->kst[i] = c->k_stride[i] * elem;
-    out->vst[i] = c->v_stride[i] * elem;
+    // the stride of an axis of one means nothing; the tensor maps want a valid one
+    const bool one = i == 0 ? c->num_blocks == 1 : i == 1 && c->heads == 1;
     if (c->k_stride[i] < 0 || c->v_stride[i] < 0) return SAI_ERR_SHAPE;
+    out->kst[i] = one ? 16 : c->k_stride[i] * elem;
+    out->vst[i] = one ? 16 : c->v_stride[i] * elem;
     if (out->kst[i] % 16 || out->vst[i] % 16) return SAI_ERR_ALIGN;
   }
   if (!aligned(c->k, 16) || !aligned(c->v, 16) || (f8 && (!aligned(c->k_scale, 4) || !aligned(c->v_scale, 4))))
