@@ -841,7 +841,14 @@ __device__ __forceinline__ bool softmax_role(Shared<D, F8>& S, const TilesLaunch
       float o[32];
 #pragma unroll
       for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(u[e]);
-      if (extra) add_nonfinite<D, F8>(p, get_pass(S, L, seg), pc.kvh, ln, m, c, o);
+      if (extra) {
+        float t[32];  // o itself stays in registers: only what is passed by address lives in memory
+#pragma unroll
+        for (int e = 0; e < 32; ++e) t[e] = o[e];
+        add_nonfinite<D, F8>(p, get_pass(S, L, seg), pc.kvh, ln, m, c, t);
+#pragma unroll
+        for (int e = 0; e < 32; ++e) o[e] = t[e];
+      }
       write_columns<D>(p, ln, part, l, c, o, S.stage[warp]);
     }
     tc_fence_before();
