@@ -261,6 +261,12 @@ __device__ __forceinline__ void commit_all(uint64_t* bar) {
   else
     umma_commit(bar);
 }
+// True in one thread of the (converged) warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
 template <int PAIR>
 __device__ __forceinline__ void tmem_take(uint32_t* result) {
   if (PAIR == 2) {
@@ -954,11 +960,17 @@ __device__ __forceinline__ bool mma_role(Shared<D, F8>& S, const TilesLaunch& L,
   constexpr uint32_t kIdescQk = umma_idesc_bf16(kTile * PAIR, kTile) ^ kF16;
   constexpr uint32_t kIdescPv = (umma_idesc_bf16(kTile * PAIR, D) ^ kF16) | kTransposeB;
   const uint32_t tmem = S.tmem;
-  // first words of the descriptors; kept opaque, so that each step's is one
-  // addition and not a register of its own through the loop
-  uint32_t q_lo = desc_lo(smem_u32(S.q[0])), k_lo = desc_lo(smem_u32(S.k[0])), v_lo = desc_lo(smem_u32(S.v[0]));
+  // The whole warp walks the loop, so that descriptors stay in uniform
+  // registers, and one thread issues.
+  const uint32_t q_lo = desc_lo(smem_u32(S.q[0])), k_lo = desc_lo(smem_u32(S.k[0])), v_lo = desc_lo(smem_u32(S.v[0]));
+  const bool lead = elect_one();
+  // A wait that gives up does not leave the loop, which would split the warp:
+  // the rest runs through without waiting, on whatever is in the buffers, and the
+  // piece is reported.
+  bool lost = false;
+  auto wait = [&](uint64_t* bar, uint32_t parity) { lost = lost || !mbar_wait(bar, parity); };
   auto qk = [&](int x, int st) {
-    asm volatile("" : "+r"(q_lo), "+r"(k_lo));
+    if (!lead) return;
     const uint32_t a = q_lo + x * (Sh::kQBytes >> 4), b = k_lo + st * (Sh::kKBytes >> 4);
 #pragma unroll
     for (int s = 0; s < D / 16; ++s)
@@ -967,54 +979,55 @@ __device__ __forceinline__ bool mma_role(Shared<D, F8>& S, const TilesLaunch& L,
     commit_all<PAIR>(&S.s_ready[x]);
   };
   auto pv = [&](int x, int st, int half, bool first) {
-    asm volatile("" : "+r"(v_lo));
+    if (!lead) return;
     const uint32_t b = v_lo + st * (Sh::kVBytes >> 4);
 #pragma unroll
     for (int s = 4 * half; s < 4 * half + 4; ++s)
       umma_ts<PAIR>(tmem + kColO + 128 * x, tmem + kColS + 128 * x + 8 * s, b + ((s * 2048) >> 4), kIdescPv,
                     !(first && s == 0));
   };
-  if (!mbar_wait(F8 ? &S.q_ready : &S.q_full, progress.pieces & 1)) return false;
+  wait(F8 ? &S.q_ready : &S.q_full, progress.pieces & 1);
   int& done = progress.tiles;
   int(&p_done)[2] = progress.weights;
   for (int seg = 0; seg < S.segs; ++seg) {
     const Pass ps = get_pass(S, L, seg);
     const int n = ps.i1 - ps.i0;
     if (n == 0) continue;
-    if (!mbar_wait(&S.k_full[done % kStages], (done / kStages) & 1)) return false;
+    wait(&S.k_full[done % kStages], (done / kStages) & 1);
     tc_fence_after();
 #pragma unroll
     for (int x = 0; x < 2; ++x)
       if (ps.act[x]) qk(x, done % kStages);
-    commit_all<PAIR>(&S.k_empty[done % kStages]);
+    if (lead) commit_all<PAIR>(&S.k_empty[done % kStages]);
     for (int i = 0; i < n; ++i, ++done) {
       const int st = done % kStages, nst = (done + 1) % kStages;
       const bool more = i + 1 < n;
       bool k_there = false;
-      if (!mbar_wait(&S.v_safe[st], (done / kStages) & 1)) return false;
+      wait(&S.v_safe[st], (done / kStages) & 1);
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         if (!ps.act[x]) continue;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-          if (!mbar_wait(&S.p_ready[x][half], p_done[x] & 1)) return false;
+          wait(&S.p_ready[x][half], p_done[x] & 1);
           tc_fence_after();
           pv(x, st, half, i == 0);
         }
         ++p_done[x];
-        if (x == 1 || !ps.act[1]) commit_all<PAIR>(&S.v_empty[st]);
+        if (lead && (x == 1 || !ps.act[1])) commit_all<PAIR>(&S.v_empty[st]);
         if (more) {
-          if (!k_there && !mbar_wait(&S.k_full[nst], ((done + 1) / kStages) & 1)) return false;
+          if (!k_there) wait(&S.k_full[nst], ((done + 1) / kStages) & 1);
           k_there = true;
           tc_fence_after();
           qk(x, nst);
-        } else
+        } else if (lead) {
           commit_all<PAIR>(&S.o_done[x]);
+        }
       }
-      if (more) commit_all<PAIR>(&S.k_empty[nst]);
+      if (lead && more) commit_all<PAIR>(&S.k_empty[nst]);
     }
   }
-  return true;
+  return !lost;
 }
 
 // --------------------------------------------------------------------- prep
@@ -1416,7 +1429,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
     pieces([&](Progress& at) {
       if (warp == kTmaWarp) return tma_role<D, F8>(S, L, &qmap, &kmap, &vmap, rank, at);
-      if (warp == kMmaWarp) return lane != 0 || rank != 0 || mma_role<D, F8>(S, L, at);
+      if (warp == kMmaWarp) return rank != 0 || mma_role<D, F8>(S, L, at);
       return prep_role<D>(S, L, rank, at);
     });
   }
