@@ -665,9 +665,9 @@ __device__ __forceinline__ bool softmax_role(Shared<D, F8>& S, const TilesLaunch
   const int local = (x * PAIR + rank) * L.rows_per_tile + r / p.group;
   const bool in_tile = r < L.rows_per_tile * p.group;
   float scale = p.scale_log2;
+  bool lost = false;  // as in the MMA role: no way out of the loop
   if (F8) {
-    const bool ok = mbar_wait(&S.q_full, at.pieces & 1);
-    if (!__all_sync(0xffffffffu, ok)) return false;
+    lost = !mbar_wait(&S.q_full, at.pieces & 1);
     scale *= query_to_f16<D>(S.q[x], r);
     fence_proxy_async_smem();
     __syncwarp();
@@ -734,8 +734,8 @@ __device__ __forceinline__ bool softmax_role(Shared<D, F8>& S, const TilesLaunch
       }
       blk1 = blk2;
       blk2 = block_of(i + 2);
-      const bool ok = mbar_wait(&S.s_ready[x], at.tiles & 1);
-      if (!__all_sync(0xffffffffu, ok)) return false;
+      lost = lost || !mbar_wait(&S.s_ready[x], at.tiles & 1);
+      __syncwarp();
       ++at.tiles;
       tc_fence_after();
       const int t0 = ps.tile0(i);
@@ -829,8 +829,8 @@ __device__ __forceinline__ bool softmax_role(Shared<D, F8>& S, const TilesLaunch
       hand_over(1);
       l = fmaf(tile_l, un_ev, l);
     }
-    const bool ok = mbar_wait(&S.o_done[x], at.passes & 1);
-    if (!__all_sync(0xffffffffu, ok)) return false;
+    lost = lost || !mbar_wait(&S.o_done[x], at.passes & 1);
+    __syncwarp();
     ++at.passes;
     tc_fence_after();
     bool extra = *reinterpret_cast<volatile int*>(&S.nonfinite) == seg + 1;
@@ -860,7 +860,7 @@ __device__ __forceinline__ bool softmax_role(Shared<D, F8>& S, const TilesLaunch
     tc_fence_before();
     write_sums(p, ln, part, m, l);
   }
-  return true;
+  return !lost;
 }
 
 // ---------------------------------------------------------------------- TMA
@@ -1027,6 +1027,11 @@ __device__ __forceinline__ bool mma_role(Shared<D, F8>& S, const TilesLaunch& L,
       if (lead && more) commit_all<PAIR>(&S.k_empty[nst]);
     }
   }
+  if (lost) {  // let the products in flight end before their memory goes
+    const unsigned long long t = global_timer_ns();
+    while (global_timer_ns() - t < 200000ull) {
+    }
+  }
   return !lost;
 }
 
@@ -1037,12 +1042,13 @@ __device__ __forceinline__ bool prep_role(Shared<D, false>& S, const TilesLaunch
   constexpr int PAIR = kPair<D>, kStages = Shared<D, false>::kStages;
   const int tid = threadIdx.x - kPrepWarp * 32;
   int& done = progress.tiles;
+  bool lost = false;
   for (int seg = 0; seg < S.segs; ++seg) {
     const Pass ps = get_pass(S, L, seg);
     for (int i = ps.i0; i < ps.i1; ++i, ++done) {
       const int st = done % kStages;
-      const bool ok = mbar_wait(&S.v_full[st], (done / kStages) & 1);
-      if (!__all_sync(0xffffffffu, ok)) return false;
+      lost = lost || !mbar_wait(&S.v_full[st], (done / kStages) & 1);
+      __syncwarp();
       const int t0 = ps.tile0(i);
       if (ps.partial(t0, p)) {
         // 16 keys at a time, four lanes to a key row (swizzling keeps a row's
@@ -1076,7 +1082,7 @@ __device__ __forceinline__ bool prep_role(Shared<D, false>& S, const TilesLaunch
       if ((threadIdx.x & 31) == 0) arrive_first<PAIR>(&S.v_safe[st]);
     }
   }
-  return true;
+  return !lost;
 }
 
 // e4m3: 16-code pieces of a raw tile (ROWS rows of ROW codes) to halves in the
@@ -1140,6 +1146,7 @@ __device__ __forceinline__ bool prep_role(Shared<D, true>& S, const TilesLaunch&
   const int tid = threadIdx.x - kPrepWarp * 32, lane = threadIdx.x & 31;
   const int kvh = S.piece.kvh;
   int& done = progress.tiles;
+  bool lost = false;
   for (int seg = 0; seg < S.segs; ++seg) {
     const Pass ps = get_pass(S, L, seg);
     // lanes 0-7: block of the tile's 16-key group, read two tiles ahead, and its
@@ -1171,9 +1178,9 @@ __device__ __forceinline__ bool prep_role(Shared<D, true>& S, const TilesLaunch&
 #pragma unroll
       for (int kv = 0; kv < 2; ++kv) {
         const int idx = 2 * done + kv, rs = idx % kRaw;
-        bool ok = mbar_wait(&S.raw_full[rs], (idx / kRaw) & 1);
-        ok = ok && mbar_wait(kv ? &S.v_empty[st] : &S.k_empty[st], ((done / kStages) & 1) ^ 1);
-        if (!__all_sync(0xffffffffu, ok)) return false;
+        lost = lost || !mbar_wait(&S.raw_full[rs], (idx / kRaw) & 1);
+        lost = lost || !mbar_wait(kv ? &S.v_empty[st] : &S.k_empty[st], ((done / kStages) & 1) ^ 1);
+        __syncwarp();
         const uint4* raw = reinterpret_cast<const uint4*>(S.raw[rs]);
         if (kv) {
           if (codes_to_halves<kTile, Sh::kDims>(raw, S.v[st], tid, v_power, 0, check, ps.most - t0))
@@ -1190,7 +1197,7 @@ __device__ __forceinline__ bool prep_role(Shared<D, true>& S, const TilesLaunch&
       }
     }
   }
-  return true;
+  return !lost;
 }
 
 // The row tiles' weights, summed up, in S.deal (every CTA computes the same);
