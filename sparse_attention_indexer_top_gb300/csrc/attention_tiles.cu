@@ -401,12 +401,14 @@ __device__ __forceinline__ float power_of(int e) { return __uint_as_float(static
 constexpr int kNoScale = -1000;   // exponent of a group without a block
 constexpr int kLeastShift = -12;  // e - E that is still exact in f16
 
-// Two e4m3 codes of each 16-bit half to halves, times a power of two (two halves).
-__device__ __forceinline__ void e4m3x4_f16x4(uint32_t c, uint32_t power, uint32_t& a, uint32_t& b) {
-  asm("{\n\t.reg .b16 x, y;\n\tmov.b32 {x, y}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, x;\n\tcvt.rn.f16x2.e4m3x2 %1, y;\n\t"
-      "mul.rn.f16x2 %0, %0, %3;\n\tmul.rn.f16x2 %1, %1, %3;\n\t}"
-      : "=&r"(a), "=&r"(b)
-      : "r"(c), "r"(power));
+// Four e4m3 codes to halves, exactly.
+__device__ __forceinline__ void e4m3x4_f16x4(uint32_t c, uint32_t& a, uint32_t& b) {
+  asm("{\n\t.reg .b16 x, y;\n\tmov.b32 {x, y}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, x;\n\tcvt.rn.f16x2.e4m3x2 %1, y;\n\t}"
+      : "=r"(a), "=r"(b)
+      : "r"(c));
+}
+__device__ __forceinline__ void mul_f16x2(uint32_t& a, uint32_t power) {
+  asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(a) : "r"(power));
 }
 __device__ __forceinline__ uint32_t pack_f16(float a, float b) {
   uint32_t r;
@@ -1089,51 +1091,63 @@ __device__ __forceinline__ bool prep_role(Shared<D, false>& S, const TilesLaunch
 // MMA's layout: 128-byte swizzled rows of 64 dims, slabs of ROWS rows. The
 // lanes of one row read its pieces; a piece becomes two 16-byte chunks, written
 // in an order that keeps the eight lanes of a store on different banks. Lane
-// `lane0` + g of the warp has the power of two of the rows 16g to 16g + 15.
-// `check`: rows from `dead` on and rows with a NaN become 0; returns whether
-// there was a NaN.
-template <int ROWS, int ROW>
-__device__ __forceinline__ bool codes_to_halves(const uint4* raw, unsigned char* out, int tid, uint32_t power, int lane0,
-                                                bool check, int dead) {
-  constexpr int kPieces = ROW / 16, kStep = kPrepWarps * 32;
-  static_assert(ROWS * kPieces == 8 * kStep, "eight pieces per thread");
-  const int piece = tid % kPieces;
+// `lane0` + g of the warp has the power of two of the rows 16g to 16g + 15
+// (SHIFT; without, all of them are 1). `check`: rows from `dead` on and rows with
+// a NaN become 0; returns whether there was a NaN.
+template <int ROWS, int ROW, bool SHIFT>
+__device__ __forceinline__ bool codes_to_halves(const uint4* raw, unsigned char* out, uint32_t tid, uint32_t power,
+                                                int lane0, bool check, int dead) {
+  constexpr uint32_t kPieces = ROW / 16, kStep = kPrepWarps * 32, kRowStep = kStep / kPieces;
+  static_assert(ROWS * kPieces == 8 * kStep && kRowStep % 8 == 0, "eight pieces per thread, alike in swizzle");
+  const uint32_t piece = tid % kPieces, row0 = tid / kPieces;
+  const uint32_t odd = kPieces == 8 ? piece >> 2 : 0;  // dims above 64 write their second chunk first
+  const uint32_t c0 = 2 * (piece & 3) + odd;
+  unsigned char* first = out + (piece / 4) * ROWS * 128 + row0 * 128 + ((c0 ^ (row0 & 7)) << 4);
+  unsigned char* second = out + (piece / 4) * ROWS * 128 + row0 * 128 + (((c0 ^ 1) ^ (row0 & 7)) << 4);
   bool met = false;
-  out += (piece / 4) * ROWS * 128;
 #pragma unroll 1
-  for (int j0 = 0; j0 < 8; j0 += 4) {
-  uint4 x[4];
+  for (uint32_t j0 = 0; j0 < 8; j0 += 4) {
+    uint4 x[4];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) x[j] = raw[(j0 + j) * kStep + tid];
+    for (uint32_t j = 0; j < 4; ++j) x[j] = raw[j * kStep + tid];
+    raw += 4 * kStep;
 #pragma unroll
-  for (int jj = 0; jj < 4; ++jj) {
-    const int j = j0 + jj;
-    const int key = (j * kStep + tid) / kPieces;
-    const uint32_t f = __shfl_sync(0xffffffffu, power, lane0 + j * (kStep / kPieces) / 16);
-    uint4 c = x[jj];
-    if (check) {
-      const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-      bool nan = false;
+    for (uint32_t j = 0; j < 4; ++j) {
+      uint4 c = x[j];
+      if (check) {
+        const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+        bool nan = false;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const uint32_t y = (w[e] & 0x7f7f7f7fu) ^ 0x7f7f7f7fu;  // a zero byte: NaN
-        nan = nan || (((y - 0x01010101u) & ~y & 0x80808080u) != 0u);
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t y = (w[e] & 0x7f7f7f7fu) ^ 0x7f7f7f7fu;  // a zero byte: NaN
+          nan = nan || (((y - 0x01010101u) & ~y & 0x80808080u) != 0u);
+        }
+        bool zero = static_cast<int>((j0 + j) * kRowStep + row0) >= dead;
+        const uint32_t b = __ballot_sync(0xffffffffu, nan && !zero);
+        if ((b >> ((tid & 31) / kPieces * kPieces)) & ((1u << kPieces) - 1u)) zero = met = true;
+        if (zero) c = make_uint4(0, 0, 0, 0);
       }
-      bool zero = key >= dead;
-      const uint32_t b = __ballot_sync(0xffffffffu, nan && !zero);
-      if ((b >> ((tid & 31) / kPieces * kPieces)) & ((1u << kPieces) - 1u)) zero = met = true;
-      if (zero) c = make_uint4(0, 0, 0, 0);
+      uint4 a, b;
+      e4m3x4_f16x4(c.x, a.x, a.y);
+      e4m3x4_f16x4(c.y, a.z, a.w);
+      e4m3x4_f16x4(c.z, b.x, b.y);
+      e4m3x4_f16x4(c.w, b.z, b.w);
+      if (SHIFT) {
+        const uint32_t f = __shfl_sync(0xffffffffu, power, lane0 + (j0 + j) * kRowStep / 16);
+        mul_f16x2(a.x, f);
+        mul_f16x2(a.y, f);
+        mul_f16x2(a.z, f);
+        mul_f16x2(a.w, f);
+        mul_f16x2(b.x, f);
+        mul_f16x2(b.y, f);
+        mul_f16x2(b.z, f);
+        mul_f16x2(b.w, f);
+      }
+      *reinterpret_cast<uint4*>(first + j * kRowStep * 128) = odd ? b : a;
+      *reinterpret_cast<uint4*>(second + j * kRowStep * 128) = odd ? a : b;
     }
-    uint4 a, b;
-    e4m3x4_f16x4(c.x, f, a.x, a.y);
-    e4m3x4_f16x4(c.y, f, a.z, a.w);
-    e4m3x4_f16x4(c.z, f, b.x, b.y);
-    e4m3x4_f16x4(c.w, f, b.z, b.w);
-    const int odd = kPieces == 8 ? piece >> 2 : 0;  // dims above 64 write their second chunk first
-    const int c0 = 2 * (piece & 3) + odd;
-    *reinterpret_cast<uint4*>(out + key * 128 + ((c0 ^ (key & 7)) << 4)) = odd ? b : a;
-    *reinterpret_cast<uint4*>(out + key * 128 + (((c0 ^ 1) ^ (key & 7)) << 4)) = odd ? a : b;
-  }
+    first += 4 * kRowStep * 128;
+    second += 4 * kRowStep * 128;
   }
   return met;
 }
@@ -1164,9 +1178,10 @@ __device__ __forceinline__ bool prep_role(Shared<D, true>& S, const TilesLaunch&
     };
     int blk1 = block_of(ps.i0 + 1);
     int2 ex = exponents_of(block_of(ps.i0));
-    // 2^(e - E) as two halves, of this lane's 16 keys
+    // 2^(e - E) as two halves, of this lane's 16 keys (a group without a block: 1)
     auto shift_of = [&](int e) -> uint32_t {
-      const int d = max(kLeastShift, e - max(-100, __reduce_max_sync(0xffffffffu, e)));
+      const int top = max(-100, __reduce_max_sync(0xffffffffu, e));
+      const int d = e == kNoScale ? 0 : max(kLeastShift, e - top);
       return static_cast<uint32_t>(15 + d) << 10 | static_cast<uint32_t>(15 + d) << 26;
     };
     for (int i = ps.i0; i < ps.i1; ++i, ++done) {
@@ -1182,11 +1197,16 @@ __device__ __forceinline__ bool prep_role(Shared<D, true>& S, const TilesLaunch&
         lost = lost || !mbar_wait(kv ? &S.v_empty[st] : &S.k_empty[st], ((done / kStages) & 1) ^ 1);
         __syncwarp();
         const uint4* raw = reinterpret_cast<const uint4*>(S.raw[rs]);
+        constexpr uint32_t kOne = 0x3c003c00u;
         if (kv) {
-          if (codes_to_halves<kTile, Sh::kDims>(raw, S.v[st], tid, v_power, 0, check, ps.most - t0))
-            *reinterpret_cast<volatile int*>(&S.nonfinite) = seg + 1;
+          const bool met = __any_sync(0xffffffffu, v_power != kOne)
+                               ? codes_to_halves<kTile, Sh::kDims, true>(raw, S.v[st], tid, v_power, 0, check, ps.most - t0)
+                               : codes_to_halves<kTile, Sh::kDims, false>(raw, S.v[st], tid, 0, 0, check, ps.most - t0);
+          if (met) *reinterpret_cast<volatile int*>(&S.nonfinite) = seg + 1;
+        } else if (__any_sync(0xffffffffu, k_power != kOne)) {
+          codes_to_halves<Sh::kKeys, D, true>(raw, S.k[st], tid, k_power, rank * (Sh::kKeys / 16), false, 0);
         } else {
-          codes_to_halves<Sh::kKeys, D>(raw, S.k[st], tid, k_power, rank * (Sh::kKeys / 16), false, 0);
+          codes_to_halves<Sh::kKeys, D, false>(raw, S.k[st], tid, 0, 0, false, 0);
         }
         fence_proxy_async_smem();  // the MMA reads these stores through the async proxy
         __syncwarp();
