@@ -384,6 +384,7 @@ int sai_topk_transform_noalloc(const float* scores, int64_t rows, int64_t score_
  */
 #define SAI_CACHE_BF16 0
 #define SAI_CACHE_E4M3 1
+#define SAI_PACKED_TILES 2
 
 typedef struct {
   void* k;
@@ -454,8 +455,11 @@ int sai_append_kv(const sai_kv_cache* cache, const uint16_t* k, int64_t k_row_st
  * max_seq_len host-side bound of seq_lens (longer rows are bad rows).
  * packed      0: each row by itself (decode; its keys are split over CTAs).
  *             1: neighbouring rows mostly share a request and have
- *             neighbouring lengths (prefill): they are taken as tiles, which
- *             needs row_to_batch. Any rows give right results either way.
+ *             neighbouring lengths (prefill): they are taken as tiles where
+ *             the sizes make that faster, which needs row_to_batch.
+ *             SAI_PACKED_TILES: as tiles whatever the sizes (not with more
+ *             than 128 query heads to a kv head or sm_scale <= 0).
+ *             Any rows give right results in every case.
  * out         bf16 [rows, q_heads, dim]; out_lse fp32 [rows, q_heads] or NULL.
  * workspace   sai_paged_attention_workspace(...) bytes (same arguments, same
  *             device), 16-byte aligned; NULL when that is 0. Calls that share

@@ -16,6 +16,7 @@ import torch
 
 from ._lib import SaiError, binding, check, load, status_string  # noqa: F401
 from .attention import (  # noqa: F401
+    PACKED_TILES,
     KVCache,
     append_kv,
     paged_attention,

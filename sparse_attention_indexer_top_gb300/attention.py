@@ -21,6 +21,7 @@ import torch
 from ._lib import KVCacheDesc, binding, load
 
 _BF16, _E4M3 = 0, 1
+PACKED_TILES = 2
 
 
 class KVCache:
@@ -96,7 +97,7 @@ def append_kv(cache: KVCache, k: torch.Tensor, v: torch.Tensor, block_table: tor
 
 
 def paged_attention_workspace(rows: int, q_heads: int, cache: KVCache, *, max_seq_len: int, window: int = 0,
-                              sinks: int = 0, packed: bool = False) -> int:
+                              sinks: int = 0, packed: int = False) -> int:
     """Workspace bytes of ``paged_attention`` for these sizes."""
     return int(load().sai_paged_attention_workspace(rows, q_heads, cache.heads, cache.dim, cache.dtype, max_seq_len,
                                                     window, sinks, int(packed)))
@@ -108,7 +109,7 @@ def sparse_attention_workspace(rows: int, q_heads: int, cache: KVCache, k: int) 
 
 
 def paged_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, seq_lens: torch.Tensor, *,
-                    max_seq_len: int, row_to_batch: Optional[torch.Tensor] = None, packed: bool = False,
+                    max_seq_len: int, row_to_batch: Optional[torch.Tensor] = None, packed: int = False,
                     window: int = 0, sinks: int = 0, sm_scale: Optional[float] = None,
                     out: Optional[torch.Tensor] = None, want_lse: bool = False,
                     out_lse: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None, stream=None):
@@ -117,7 +118,8 @@ def paged_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, 
     ``q`` is bf16 ``[rows, q_heads, dim]`` (any row stride; ``q_heads`` a
     multiple of the cache's heads). With ``window`` a row sees its last
     ``window`` keys and the request's first ``sinks``. ``packed`` (prefill,
-    needs ``row_to_batch``) takes neighbouring rows as tiles. ``sm_scale``
+    needs ``row_to_batch``) takes neighbouring rows as tiles where their sizes
+    make that faster, ``packed=PACKED_TILES`` whatever they are. ``sm_scale``
     defaults to ``dim ** -0.5``. Returns ``out`` (bf16, like ``q``), or ``(out,
     lse)`` with ``want_lse`` or ``out_lse`` (fp32 ``[rows, q_heads]``). A row
     that sees no key gives zeros and -inf.

@@ -90,6 +90,13 @@ bool space(const void* workspace, size_t bytes, size_t need) {
   return need == 0 || (workspace && bytes >= need && aligned(workspace, 16));
 }
 
+// Whether a call's rows are taken as tiles: packed 1 by sizes, 2 wherever they can be.
+bool as_tiles(int32_t packed, int64_t rows, int32_t q_heads, int32_t heads, int32_t dim, bool f8, long long keys, int sms,
+              float scale_log2) {
+  if (!packed || !sai::attn_tiles_apply(q_heads / heads, scale_log2)) return false;
+  return packed == SAI_PACKED_TILES || sai::attn_tiles_pay(rows, q_heads, heads, dim, f8, keys, sms);
+}
+
 // Splits rows over key chunks and launches the row kernel.
 int run_rows(sai::AttnLaunch& p, long long max_keys, void* workspace, size_t workspace_bytes, int sms,
              sai_stream_t stream) {
@@ -164,7 +171,7 @@ size_t sai_paged_attention_workspace(int64_t rows, int32_t q_heads, int32_t head
   const long long keys = most_keys(max_seq_len, window, sinks);
   size_t bytes = sai::attn_rows_plan(rows, q_heads, heads, dim, f8, keys, sms).workspace_bytes;
   // enough for either kernel: the tile kernel leaves calls with sm_scale <= 0 to the row kernel
-  if (packed && sai::attn_tiles_apply(q_heads / heads, 1.f))
+  if (as_tiles(packed, rows, q_heads, heads, dim, f8, keys, sms, 1.f))
     bytes = std::max(bytes, sai::attn_tiles_workspace(rows, q_heads, heads, dim, keys, sms));
   return bytes;
 }
@@ -181,6 +188,7 @@ int sai_paged_attention(const uint16_t* q, int64_t q_row_stride, int32_t q_heads
   if ((e = check_attention(q, q_row_stride, q_heads, p.c, rows, sm_scale, out, out_lse)) != SAI_OK) return e;
   if (rows == 0) return SAI_OK;
   if ((e = check_table(block_table, bt_rows, bt_stride, row_to_batch, seq_lens, rows)) != SAI_OK) return e;
+  if (packed < 0 || packed > SAI_PACKED_TILES) return SAI_ERR_UNSUPPORTED;
   if (packed && !row_to_batch) return SAI_ERR_NULL;
   int dev, sms;
   if (!device_setup(&dev, &p.status, &sms)) return SAI_ERR_CUDA;
@@ -201,7 +209,7 @@ int sai_paged_attention(const uint16_t* q, int64_t q_row_stride, int32_t q_heads
   p.out = out;
   p.lse = out_lse;
   const long long keys = most_keys(max_seq_len, window, sinks);
-  if (packed && sai::attn_tiles_apply(p.group, p.scale_log2)) {
+  if (as_tiles(packed, rows, q_heads, p.c.heads, p.c.dim, p.c.f8, keys, sms, p.scale_log2)) {
     const size_t need = sai::attn_tiles_workspace(rows, q_heads, p.c.heads, p.c.dim, keys, sms);
     if (!space(workspace, workspace_bytes, need)) return SAI_ERR_WORKSPACE;
     return cuda_status(sai::launch_attn_tiles(p, keys, workspace, sms, reinterpret_cast<cudaStream_t>(stream)));

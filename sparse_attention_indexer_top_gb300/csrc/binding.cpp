@@ -222,7 +222,7 @@ PyObject* paged_attention(PyObject* const* a) {
   const int32_t* lens = row_index(a[4], "seq_lens", rows, c.device);
   const int32_t most = int32_of(a[5], "max_seq_len"), window = int32_of(a[8], "window"), sinks = int32_of(a[9], "sinks");
   const int32_t* r2b = a[6] == Py_None ? nullptr : row_index(a[6], "row_to_batch", rows, c.device);
-  const int packed = PyObject_IsTrue(a[7]) == 1;
+  const int32_t packed = int32_of(a[7], "packed");  // False, True, PACKED_TILES
   if (packed && !r2b) refuse("packed rows need row_to_batch");
   const double scale = scale_of(a[10], c);
   const at::Tensor out = output(a[11], "out", {rows, q.heads, c.d->dim}, at::kBFloat16, c);

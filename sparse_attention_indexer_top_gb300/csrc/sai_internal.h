@@ -192,8 +192,10 @@ struct AttnPlan {
 };
 AttnPlan attn_rows_plan(long long rows, int q_heads, int heads, int dim, bool f8, long long max_keys, int num_sms);
 cudaError_t launch_attn_rows(const AttnLaunch& p, cudaStream_t stream);
-// The tile kernel of packed rows: whether it takes a call, its workspace, its launch.
+// The tile kernel of packed rows: whether it takes a call, whether it beats the
+// row kernel on these sizes, its workspace, its launch.
 bool attn_tiles_apply(int group, float scale_log2);
+bool attn_tiles_pay(long long rows, int q_heads, int heads, int dim, bool f8, long long max_keys, int num_sms);
 size_t attn_tiles_workspace(long long rows, int q_heads, int heads, int dim, long long max_keys, int num_sms);
 cudaError_t launch_attn_tiles(const AttnLaunch& p, long long max_keys, void* workspace, int num_sms,
                               cudaStream_t stream);

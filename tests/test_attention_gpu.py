@@ -182,11 +182,11 @@ def _packed(dtype, dim, hkv, group, bs, reqs, window, sinks):
     r2b = [b for b, (n, _) in enumerate(reqs) for _ in range(n)]
     q, q64 = c.queries(len(lens), hkv * group)
     kw = dict(max_seq_len=max(lens), row_to_batch=_lens(r2b), window=window, sinks=sinks, want_lse=True)
-    out, lse = sai.paged_attention(q, c.cache, c.t_table, _lens(lens), packed=True, **kw)
     cells = [(b, A.seen(n, window, sinks)) for b, n in zip(r2b, lens)]
-    _check(c, q64, cells, out, lse, dim ** -0.5)
-    out, lse = sai.paged_attention(q, c.cache, c.t_table, _lens(lens), **kw)
-    _check(c, q64, cells, out, lse, dim ** -0.5)
+    # as tiles, as the sizes have it, and row by row
+    for packed in (sai.PACKED_TILES, True, False):
+        out, lse = sai.paged_attention(q, c.cache, c.t_table, _lens(lens), packed=packed, **kw)
+        _check(c, q64, cells, out, lse, dim ** -0.5)
     assert sai.device_status() == 0
 
 
@@ -198,7 +198,7 @@ def test_packed_rows_in_any_order_with_padding_rows(dtype):
     r2b = [int(x) for x in c.rng.integers(0, 3, 150)]
     lens = [int(c.rng.integers(0, totals[b] + 1)) if i % 7 else 0 for i, b in enumerate(r2b)]
     q, q64 = c.queries(150, 8)
-    for packed in (True, False):
+    for packed in (True, False, sai.PACKED_TILES):
         out, lse = sai.paged_attention(q, c.cache, c.t_table, _lens(lens), max_seq_len=513, row_to_batch=_lens(r2b),
                                        packed=packed, want_lse=True)
         _check(c, q64, [(b, np.arange(n)) for b, n in zip(r2b, lens)], out, lse, 128 ** -0.5)
@@ -223,7 +223,7 @@ def test_unseen_nonfinite_cells_do_not_matter(dtype, bad):
         c.v[blk, :, at % 64] = val
     lens = list(range(1, n + 1))
     q, q64 = c.queries(n, 8)
-    for packed in (True, False):
+    for packed in (True, False, sai.PACKED_TILES):
         for window, sinks in ((0, 0), (30, 4)):
             out, lse = sai.paged_attention(q, c.cache, c.t_table, _lens(lens), max_seq_len=n,
                                            row_to_batch=_lens([0] * n), packed=packed, window=window, sinks=sinks,
@@ -236,7 +236,7 @@ def test_unseen_nonfinite_cells_do_not_matter(dtype, bad):
                 assert torch.isnan(out[torch.from_numpy(sees).to(DEV)]).all()
 
 
-@pytest.mark.parametrize("packed", [False, True])
+@pytest.mark.parametrize("packed", [False, True, 2])
 def test_layouts_strides_and_streams(packed):
     """Tokens before heads in the cache, k and v in one array, queries as a slice of a fused projection, and a call on
     another stream than torch's current one."""
@@ -281,13 +281,13 @@ def test_offsets_past_32_bits(dtype):
         table = torch.where(c.t_table >= 0, c.t_table + (blocks - small), -1).to(torch.int32)
     q, q64 = c.queries(2, 8)
     cells = [(b, np.arange(n)) for b, n in enumerate(lens)]
-    for packed in (False, True):
+    for packed in (False, True, sai.PACKED_TILES):
         out, lse = sai.paged_attention(q, cache, table, _lens(lens), max_seq_len=200, row_to_batch=_lens([0, 1]),
                                        packed=packed, want_lse=True)
         _check(c, q64, cells, out, lse, 128 ** -0.5)
 
 
-@pytest.mark.parametrize("packed", [False, True])
+@pytest.mark.parametrize("packed", [False, True, 2])
 def test_bad_rows_are_emptied_and_flagged(packed):
     c = Case(100, [300, 200], dtype="bf16", bs=64)
     q, q64 = c.queries(5, 8)
@@ -437,12 +437,12 @@ def test_packed_rows_dealt_out_by_a_far_bound(dtype):
     q, q64 = c.queries(len(lens), 8)
     for window, sinks in ((0, 0), (200, 9)):
         out, lse = sai.paged_attention(q, c.cache, c.t_table, _lens(lens), max_seq_len=50000, row_to_batch=_lens(r2b),
-                                       packed=True, window=window, sinks=sinks, want_lse=True)
+                                       packed=sai.PACKED_TILES, window=window, sinks=sinks, want_lse=True)
         _check(c, q64, [(b, A.seen(n, window, sinks)) for b, n in zip(r2b, lens)], out, lse, 128 ** -0.5)
     assert sai.device_status() == 0
 
 
-@pytest.mark.parametrize("packed", [False, True])
+@pytest.mark.parametrize("packed", [False, True, 2])
 @pytest.mark.parametrize("dim,group,bs", [(128, 4, 16), (64, 8, 128), (128, 20, 64)])
 def test_scales_that_are_no_powers_of_two(packed, dim, group, bs):
     reqs = [(90, 400), (1, 150), (64, 64)]
@@ -460,5 +460,5 @@ def test_packed_block_scales_far_apart():
     c = Case(59, [300], dtype="e4m3", bs=16, vscales=(-40, 30))
     q, q64 = c.queries(100, 8)
     out, lse = sai.paged_attention(q, c.cache, c.t_table, _lens(lens), max_seq_len=300, row_to_batch=_lens([0] * 100),
-                                   packed=True, want_lse=True)
+                                   packed=sai.PACKED_TILES, want_lse=True)
     _check(c, q64, [(0, np.arange(n)) for n in lens], out, lse, 128 ** -0.5)

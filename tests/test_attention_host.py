@@ -77,6 +77,8 @@ def test_paged_attention_arguments(lib):
     assert _paged(lib, d, bt=None) == -1
     assert _paged(lib, d, bt_rows=3) == -2
     assert _paged(lib, d, packed=1) == -1  # tiles need row_to_batch
+    assert _paged(lib, d, packed=2) == -1
+    assert _paged(lib, d, packed=3) == -3
     assert _paged(lib, d, lse=P + 2) == -7
     assert _paged(lib, d, rows=0, q=None, out=None, bt=None, lens=None) == 0
 
