@@ -1551,10 +1551,11 @@ bool query_map(CUtensorMap* map, const AttnLaunch& p, int rows_per_tile) {
 // + 4 for a unit's start and end); dealt out they take their even share, a
 // second start and end, and about 14 steps for the deal, the partial
 // results and the join. 2048 rows on 32768 keys, 32 / 4 heads (128 units, 76
-// pairs, 256 tiles): 0.80 ms dealt out, 0.89 whole; 512 rows on 4512 keys,
-// 64 / 8 heads (64 units, 36 tiles): 106 us and 78. From three waves on, units
-// of unlike lengths fill the gaps by themselves: 1849 rows of four requests
-// (232 units) 0.56 ms dealt out, 0.49 whole.
+// pairs, 256 tiles): 0.63 ms dealt out, 0.68 whole; 512 rows on 4512 keys,
+// 64 / 8 heads (64 units, 36 tiles): 87 us and 62; 512 rows on 16512 keys,
+// 8 / 1 heads (8 units): 60 us and 182. From three waves on, units of unlike
+// lengths fill the gaps by themselves: 1849 rows of four requests (232 units)
+// 0.45 ms dealt out, 0.40 whole.
 struct Work {
   int rows_here, row_tiles, shares;
   bool dealt;
