@@ -131,7 +131,9 @@ struct Shared {
   uint64_t raw_full[kRaw ? kRaw : 1], raw_empty[kRaw ? kRaw : 1];
   uint64_t s_ready[2], p_ready[2][2], o_done[2];  // p_ready: first and second half of the keys
   uint32_t tmem;
-  int nonfinite;  // number of the piece's last pass (from 1) that met a non-finite value row
+  // A pass of the piece met a non-finite value row. One mark for all passes: prep runs ahead of the softmax, over a
+  // pass's end too, and add_nonfinite looks for its own pass's rows.
+  int nonfinite;
   int stop;       // a wait gave up: no further piece
   int segs;
   Piece piece;             // at work on
@@ -835,11 +837,11 @@ __device__ __forceinline__ bool softmax_role(Shared<D, F8>& S, const TilesLaunch
     __syncwarp();
     ++at.passes;
     tc_fence_after();
-    bool extra = *reinterpret_cast<volatile int*>(&S.nonfinite) == seg + 1;
+    bool extra = *reinterpret_cast<volatile int*>(&S.nonfinite) != 0;
     if (PAIR == 2) {
       int other;
       asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(other) : "r"(peer_addr(&S.nonfinite, rank ^ 1)) : "memory");
-      extra = extra || other == seg + 1;
+      extra = extra || other != 0;
     }
 #pragma unroll 1
     for (int c = 0; c < D; c += 32) {
@@ -1071,7 +1073,7 @@ __device__ __forceinline__ bool prep_role(Shared<D, false>& S, const TilesLaunch
           const uint32_t b = __ballot_sync(0xffffffffu, bad);
           if ((b >> (threadIdx.x & 28)) & 0xfu) {
             zero = true;
-            *reinterpret_cast<volatile int*>(&S.nonfinite) = seg + 1;
+            *reinterpret_cast<volatile int*>(&S.nonfinite) = 1;
           }
           if (zero) {
 #pragma unroll
@@ -1202,7 +1204,7 @@ __device__ __forceinline__ bool prep_role(Shared<D, true>& S, const TilesLaunch&
           const bool met = __any_sync(0xffffffffu, v_power != kOne)
                                ? codes_to_halves<kTile, Sh::kDims, true>(raw, S.v[st], tid, v_power, 0, check, ps.most - t0)
                                : codes_to_halves<kTile, Sh::kDims, false>(raw, S.v[st], tid, 0, 0, check, ps.most - t0);
-          if (met) *reinterpret_cast<volatile int*>(&S.nonfinite) = seg + 1;
+          if (met) *reinterpret_cast<volatile int*>(&S.nonfinite) = 1;
         } else if (__any_sync(0xffffffffu, k_power != kOne)) {
           codes_to_halves<Sh::kKeys, D, true>(raw, S.k[st], tid, k_power, rank * (Sh::kKeys / 16), false, 0);
         } else {
