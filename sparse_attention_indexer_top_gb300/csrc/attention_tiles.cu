@@ -611,14 +611,20 @@ template <int D>
 __device__ __noinline__ float2 rough_tile(uint32_t ts, uint32_t to, float2 ml, float mul, float ev, float un_ev,
                                           const float2* factors, int3 sees, uint32_t bad, bool have_o) {
   uint32_t s[32];
+  // masked after the scaling: a scale may be 0, and 0 * -inf is NaN
+  auto scaled = [&](int c0) {
+#pragma unroll
+    for (int c = 0; c < 32; ++c) s[c] = __float_as_uint(__uint_as_float(s[c]) * factors[(c0 + c) / 16].x);
+    mask32(s, sees.x - c0, sees.y - c0, sees.z - c0, bad >> (c0 / 16));
+  };
   float top = -INFINITY;
 #pragma unroll 1
   for (int c0 = 0; c0 < kTile; c0 += 32) {
     tmem_ld32(ts + c0, s);
     tmem_ld_wait32(s);
-    mask32(s, sees.x - c0, sees.y - c0, sees.z - c0, bad >> (c0 / 16));
+    scaled(c0);
 #pragma unroll
-    for (int c = 0; c < 32; ++c) top = fmaxf(top, __uint_as_float(s[c]) * factors[(c0 + c) / 16].x);
+    for (int c = 0; c < 32; ++c) top = fmaxf(top, __uint_as_float(s[c]));
   }
   top = fmaf(top, mul, ev);
   const bool up = top > ml.x + 8.f;
@@ -634,14 +640,14 @@ __device__ __noinline__ float2 rough_tile(uint32_t ts, uint32_t to, float2 ml, f
   for (int c0 = 0; c0 < kTile; c0 += 32) {  // weights of chunk c go over scores of chunk c / 2
     tmem_ld32(ts + c0, s);
     tmem_ld_wait32(s);
-    mask32(s, sees.x - c0, sees.y - c0, sees.z - c0, bad >> (c0 / 16));
+    scaled(c0);
 #pragma unroll
     for (int c = 0; c < 32; c += 2) {
-      const float2 f = factors[(c0 + c) / 16];
-      const float a = ex2(fmaf(__uint_as_float(s[c]), mul * f.x, off));
-      const float b = ex2(fmaf(__uint_as_float(s[c + 1]), mul * f.x, off));
+      const float f = factors[(c0 + c) / 16].y;
+      const float a = ex2(fmaf(__uint_as_float(s[c]), mul, off));
+      const float b = ex2(fmaf(__uint_as_float(s[c + 1]), mul, off));
       sum += a + b;
-      s[c / 2] = pack_f16(a * f.y, b * f.y);
+      s[c / 2] = pack_f16(a * f, b * f);
     }
     tmem_st16(ts + c0 / 2, s);
   }

@@ -81,3 +81,28 @@ def test_seen_nonfinite_values(dtype, dim, group, bs, window, sinks, reqs, marks
         out, lse = sai.paged_attention(q, c.cache, c.t_table, _lens(lens), max_seq_len=max(lens), window=window,
                                        sinks=sinks, row_to_batch=_lens(r2b), packed=packed, want_lse=True)
         _check_any(c, q64, cells, out, lse, dim ** -0.5)
+
+
+# --- block scales of 0
+
+@pytest.mark.parametrize("packed", [False, True, 2])
+@pytest.mark.parametrize("dim,group,bs", [(128, 4, 16), (64, 8, 128), (128, 20, 64)])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (70, 9)])
+@pytest.mark.parametrize("share", [0.5, 1.0])
+def test_zero_scales(packed, dim, group, bs, window, sinks, share):
+    """Blocks with a scale of 0 hold zeros. A log-sum-exp may be off by the spacing of the running maximum, which
+    carries the value scale's exponent (at most 64 and a few): three roundings of numbers below 128, 3 * 2^-18."""
+    reqs = [(90, 400), (1, 150), (64, 64)]
+    c = Case(210 + dim, [t for _, t in reqs], dtype="e4m3", hkv=2, dim=dim, bs=bs)
+    for x, which in ((c.ks, 0), (c.vs, 1)):
+        zero = torch.from_numpy(c.rng.random(tuple(x.shape)) < share).to(DEV)
+        x.masked_fill_(zero, 0.0)
+        for b, (_, t) in enumerate(reqs):
+            for j in range(0, t, bs):
+                c.kv[b][which][j:j + bs, zero[int(c.table[b, j // bs])].cpu().numpy()] = 0.0
+    lens, r2b = _rows(reqs)
+    lens[3] = lens[100] = 0
+    q, q64 = c.queries(len(lens), 2 * group)
+    out, lse = sai.paged_attention(q, c.cache, c.t_table, _lens(lens), max_seq_len=400, row_to_batch=_lens(r2b),
+                                   packed=packed, window=window, sinks=sinks, want_lse=True)
+    _check_any(c, q64, [(b, A.seen(n, window, sinks)) for b, n in zip(r2b, lens)], out, lse, dim ** -0.5, 3 * 2.0 ** -18)
