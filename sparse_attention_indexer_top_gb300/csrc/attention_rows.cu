@@ -37,6 +37,16 @@ constexpr int kThreads = kWarps * 32;
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr int kMinExp = -64;  // scales below 2^-64 count as 2^-64 in the running maximum
 
+// The running maximum m moves only when it is passed by more than 2^8, so that
+// O is rarely rescaled. Weights in bf16 are as exact up to 2^8 as up to 1.
+// Weights times value scales in f16 (e4m3) use its range: m is set 2^6 below the
+// maximum, they reach 2^15, and one below 2^-14 is off by 2^-25 at most, 2^-31
+// of the largest.
+template <bool F8>
+constexpr float kLift = F8 ? 6.f : 0.f;
+template <bool F8>
+constexpr float kPassed = kLift<F8> + 8.f;
+
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
   asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
@@ -458,13 +468,15 @@ __global__ void __launch_bounds__(kThreads) attn_rows_kernel(const AttnLaunch p)
             c[2 * n + 1] = on ? c[2 * n + 1] * k1 : -INFINITY;
           }
           float x0 = fmaxf(c[0] + ev[0], c[2] + ev[1]), x1 = fmaxf(c[1] + ev[0], c[3] + ev[1]);
-          if (__any_sync(0xffffffffu, x0 > m0 + 8.f || x1 > m1 + 8.f)) {
+          if (__any_sync(0xffffffffu, x0 > m0 + kPassed<F8> || x1 > m1 + kPassed<F8>)) {
 #pragma unroll
             for (int f = 4; f < 32; f <<= 1) {
               x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, f));
               x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, f));
             }
-            const bool up0 = x0 > m0 + 8.f, up1 = x1 > m1 + 8.f;
+            const bool up0 = x0 > m0 + kPassed<F8>, up1 = x1 > m1 + kPassed<F8>;
+            x0 -= kLift<F8>;
+            x1 -= kLift<F8>;
             const float f0 = up0 ? (m0 == -INFINITY ? 0.f : ex2(m0 - x0)) : 1.f;
             const float f1 = up1 ? (m1 == -INFINITY ? 0.f : ex2(m1 - x1)) : 1.f;
             if (up0) m0 = x0;
@@ -546,8 +558,8 @@ __global__ void __launch_bounds__(kThreads) attn_rows_kernel(const AttnLaunch p)
         }
         // the lane's keys are 2t, 2t + 1, 8 + 2t, 9 + 2t. With block scales,
         // the running maximum is that of s_t + exponent(v scale): the weights
-        // that multiply v codes are then at most 2 (times 2^8, below) whatever
-        // the scales, and fit f16; l adds the same weights without the scale.
+        // that multiply v codes then fit f16 whatever the scales; l adds the
+        // same weights without the scale.
         float x0 = -INFINITY, x1 = -INFINITY;
         float vs[2][2];
 #pragma unroll
@@ -568,15 +580,15 @@ __global__ void __launch_bounds__(kThreads) attn_rows_kernel(const AttnLaunch p)
             x0 = fmaxf(x0, c[n][e] + ev);
             x1 = fmaxf(x1, c[n][e + 2] + ev);
           }
-        // the maximum moves only when it is passed by more than 2^8 (weights
-        // up to 256 are as exact as weights up to 1), so O is rarely rescaled
-        if (__any_sync(0xffffffffu, x0 > m0 + 8.f || x1 > m1 + 8.f)) {
+        if (__any_sync(0xffffffffu, x0 > m0 + kPassed<F8> || x1 > m1 + kPassed<F8>)) {
 #pragma unroll
           for (int f = 1; f < 4; f <<= 1) {
             x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, f));
             x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, f));
           }
-          const bool up0 = x0 > m0 + 8.f, up1 = x1 > m1 + 8.f;
+          const bool up0 = x0 > m0 + kPassed<F8>, up1 = x1 > m1 + kPassed<F8>;
+          x0 -= kLift<F8>;
+          x1 -= kLift<F8>;
           const float f0 = up0 ? (m0 == -INFINITY ? 0.f : ex2(m0 - x0)) : 1.f;
           const float f1 = up1 ? (m1 == -INFINITY ? 0.f : ex2(m1 - x1)) : 1.f;
           if (up0) m0 = x0;
@@ -608,7 +620,8 @@ __global__ void __launch_bounds__(kThreads) attn_rows_kernel(const AttnLaunch p)
             }
           }
         // the weights as bf16 (f16 with e4m3 values): the MMA's other operand
-        // is the cache's type; relative error 2^-9 (2^-12), under the output's
+        // is the cache's type; relative error 2^-9 (2^-12 and the absolute term
+        // of kLift), under the output's
         uint32_t pa[4];
         if (F8) {
           pa[0] = pack_f16(c[0][0], c[0][1]);

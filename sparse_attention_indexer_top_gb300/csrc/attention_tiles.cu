@@ -45,8 +45,8 @@
 // tile's largest block scale, a block of scale 2^e f, 1 <= f < 2, is multiplied
 // by 2^(e - E) (exact down to e - E = -12), and the softmax applies 2^E: a key
 // tile's in its multiplier, a value tile's in the exponent, w_t = 2^(s_t + Ev -
-// m) with m the maximum of s + Ev, so that weights are at most 2^8 whatever the
-// scales; l adds w_t / 2^Ev. What is left of a scale, f or a power below 2^-12,
+// m) with m up to 2^14 below the maximum of s + Ev, so that weights fit f16 whatever
+// the scales; l adds w_t / 2^Ev. What is left of a scale, f or a power below 2^-12,
 // goes to the softmax too, 16 keys at a time: nothing when scales are
 // powers of two, as append_kv makes them. The queries are brought to [2^14,
 // 2^15) by a power of two for each (row, head) and stored as halves.
@@ -77,6 +77,16 @@ constexpr int kPrepWarps = 2;
 constexpr int kThreads = (kPrepWarp + kPrepWarps) * 32;
 constexpr uint32_t kSetUpBar = 1;  // named barrier of all threads between pieces
 constexpr float kLn2 = 0.69314718055994530942f;
+
+// The running maximum m of a row moves only when it is passed by more than
+// 2^8, so that O is rarely rescaled. Weights in bf16 are as exact up to 2^8 as
+// up to 1. Weights in f16 (e4m3) use its range: m is set 2^6 below the maximum,
+// weights reach 2^14 (below 2^15 with what is left of a scale), and one below
+// 2^-14 is off by 2^-25 at most, 2^-31 of the largest.
+template <bool F8>
+constexpr float kLift = F8 ? 6.f : 0.f;
+template <bool F8>
+constexpr float kPassed = kLift<F8> + 8.f;
 
 // TMEM columns: S (and P over it) of tiles A and B, then their O.
 constexpr uint32_t kColS = 0, kColO = 256, kTmemCols = 512;
@@ -394,10 +404,12 @@ __device__ __forceinline__ bool nonfinite2(uint32_t x) {
   return (x & 0x7f80u) == 0x7f80u || (x & 0x7f800000u) == 0x7f800000u;
 }
 
-// Exponent of a block scale (scales outside 2^-100 .. 2^100 leave the rest to
-// their factor), and 2^e.
+// Exponent of a block scale (scales outside 2^-64 .. 2^100, 0 among them, leave
+// the rest to their factor; l holds weights over the value scale's power, which
+// fits fp32 down to 2^-64 for any number of keys), and 2^e.
+constexpr int kLeastExp = -64;
 __device__ __forceinline__ int exponent_of(float scale) {
-  return max(-100, min(100, static_cast<int>((__float_as_uint(scale) >> 23) & 255u) - 127));
+  return max(kLeastExp, min(100, static_cast<int>((__float_as_uint(scale) >> 23) & 255u) - 127));
 }
 __device__ __forceinline__ float power_of(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
 constexpr int kNoScale = -1000;   // exponent of a group without a block
@@ -627,10 +639,11 @@ __device__ __noinline__ float2 rough_tile(uint32_t ts, uint32_t to, float2 ml, f
     for (int c = 0; c < 32; ++c) top = fmaxf(top, __uint_as_float(s[c]));
   }
   top = fmaf(top, mul, ev);
-  const bool up = top > ml.x + 8.f;
+  const bool up = top > ml.x + kPassed<true>;
   if (__any_sync(0xffffffffu, up)) {
-    const float f = up ? (ml.x == -INFINITY ? 0.f : ex2(ml.x - top)) : 1.f;
-    if (up) ml.x = top;
+    const float to_m = top - kLift<true>;
+    const float f = up ? (ml.x == -INFINITY ? 0.f : ex2(ml.x - to_m)) : 1.f;
+    if (up) ml.x = to_m;
     ml.y *= f;
     if (have_o) rescale_o<D>(to, f);
   }
@@ -728,7 +741,7 @@ __device__ __forceinline__ bool softmax_role(Shared<D, F8>& S, const TilesLaunch
       const float2* factors = S.factors[F8 ? warp : 0];
       if (F8) {
         const int ek = blk1 >= 0 ? exponent_of(sc1.x) : kNoScale, e2 = blk1 >= 0 ? exponent_of(sc1.y) : kNoScale;
-        const int tk = max(-100, __reduce_max_sync(0xffffffffu, ek)), tv = max(-100, __reduce_max_sync(0xffffffffu, e2));
+        const int tk = max(kLeastExp, __reduce_max_sync(0xffffffffu, ek)), tv = max(kLeastExp, __reduce_max_sync(0xffffffffu, e2));
         mul = scale * power_of(tk);
         ev = static_cast<float>(tv);
         un_ev = power_of(-tv);
@@ -794,19 +807,18 @@ __device__ __forceinline__ bool softmax_role(Shared<D, F8>& S, const TilesLaunch
 #pragma unroll
       for (int c = 0; c < kTile; c += 32) top = largest(s + c, c, top);
       top = fmaf(top, mul, ev);
-      // the maximum moves only when it is passed by more than 2^8: weights up
-      // to 256 are as exact in 16 bits as weights up to 1, and O is rarely
-      // rescaled
-      const bool up = top > m + 8.f;
+      const bool up = top > m + kPassed<F8>;
       if (__any_sync(0xffffffffu, up)) {
+        top -= kLift<F8>;
         const float f = up ? (m == -INFINITY ? 0.f : ex2(m - top)) : 1.f;
         if (up) m = top;
         l *= f;
         if (i > ps.i0) rescale_o<D>(to, f);
       }
       const float base = m == -INFINITY ? 0.f : m;
-      // weights of 32 columns in 16 bits (relative error 2^-9, f16 2^-12; under
-      // the output's own), over the scores' TMEM columns
+      // weights of 32 columns in 16 bits (relative error 2^-9, under the output's
+      // own; f16 2^-12 and the absolute term of kLift), over the scores' TMEM
+      // columns
       float tile_l = 0.f;
       auto weights = [&](uint32_t* s, int c0) {
         uint64_t sum[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
@@ -1188,7 +1200,7 @@ __device__ __forceinline__ bool prep_role(Shared<D, true>& S, const TilesLaunch&
     int2 ex = exponents_of(block_of(ps.i0));
     // 2^(e - E) as two halves, of this lane's 16 keys (a group without a block: 1)
     auto shift_of = [&](int e) -> uint32_t {
-      const int top = max(-100, __reduce_max_sync(0xffffffffu, e));
+      const int top = max(kLeastExp, __reduce_max_sync(0xffffffffu, e));
       const int d = e == kNoScale ? 0 : max(kLeastShift, e - top);
       return static_cast<uint32_t>(15 + d) << 10 | static_cast<uint32_t>(15 + d) << 26;
     };

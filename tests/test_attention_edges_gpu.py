@@ -106,3 +106,42 @@ def test_zero_scales(packed, dim, group, bs, window, sinks, share):
     out, lse = sai.paged_attention(q, c.cache, c.t_table, _lens(lens), max_seq_len=400, row_to_batch=_lens(r2b),
                                    packed=packed, window=window, sinks=sinks, want_lse=True)
     _check_any(c, q64, [(b, A.seen(n, window, sinks)) for b, n in zip(r2b, lens)], out, lse, dim ** -0.5, 3 * 2.0 ** -18)
+
+
+# --- small weights beside blocks with large scales
+
+@pytest.mark.parametrize("rows,packed", [(1, False), (2500, False), (200, 2)])
+@pytest.mark.parametrize("group", [4, 16, 20])
+def test_small_weights_beside_a_large_scale(rows, packed, group):
+    """Two kinds of runs in turn (128 tokens for tiles, 64 for single rows' warps): a key of weight 1 in a block of value scale 2^10 whose codes are 0 but in dim
+    0, and keys of weights about 2^-16 with value scale 1, which alone fill the other dims.
+
+    The weights of an e4m3 cache go to f16 below a maximum of score plus scale exponent, at least 2^6 there: each is
+    off by at most 2^-25 * 2^-6 of 2^(16 + 10) beside its relative 2^-12. With sum e_t the softmax's denominator, that
+    is 2^-31 * 2^26 * sum |v_t| / sum e_t for an element, and the bounds' own terms.
+    """
+    n, dim = 2048, 128
+    c = Case(220, [n], dtype="e4m3", hkv=1, dim=dim, bs=16)
+    kind = (np.arange(n) // (128 if packed else 64)) % 2  # 0: large scale
+    kc, vc = np.zeros((n, dim)), np.zeros((n, dim))
+    kc[:, 0] = np.where(kind == 0, np.where(np.arange(n) % 16 == 0, 16.0, -240.0), c.rng.choice([0.0, 0.25, -0.5, 0.75], n))
+    vc[kind == 1] = np.exp2(c.rng.integers(-2, 6, (n // 2, dim)))
+    vc[kind == 0, 0] = 1.0
+    ks, vs = np.ones(n), np.where(kind == 0, 2.0 ** 10, 1.0)
+    for x, codes, s, scale in ((c.k, kc, c.ks, ks), (c.v, vc, c.vs, vs)):
+        t = torch.from_numpy(codes).to(torch.float8_e4m3fn).view(torch.uint8).to(DEV).view(-1, 16, dim)
+        blk = torch.from_numpy(c.table[0]).long().to(DEV)
+        x.view(torch.uint8)[blk, 0] = t
+        s[blk, 0] = torch.from_numpy(scale[::16]).float().to(DEV)
+    q = torch.zeros((rows, group, dim), dtype=torch.bfloat16, device=DEV)
+    q[:, :, 0] = 1.0
+    sm = float(np.log(2.0))
+    ref, rl, mag = A.attend(q[0].double().cpu().numpy(), kc[:, None], (vc * vs[:, None])[:, None], sm)
+    total = np.exp2(kc[:, 0]).sum()
+    out, lse = sai.paged_attention(q, c.cache, c.t_table, _lens([n] * rows), max_seq_len=n, row_to_batch=_lens([0] * rows),
+                                   packed=packed, sm_scale=sm, want_lse=True)
+    tol = 2.0 ** -8 * ref + 2.0 ** -8 * mag + 2.0 ** -5 * (vc * vs[:, None]).sum(0) / total * (np.arange(dim) > 0)
+    assert (tol[:, 1:] < 0.5 * ref[:, 1:]).all()  # zeros there would be found out
+    err = np.abs(out.double().cpu().numpy() - ref[None])
+    assert (err <= tol[None]).all()
+    assert (np.abs(lse.double().cpu().numpy() - rl[None]) <= 2.0 ** -15).all()
