@@ -300,7 +300,7 @@ __global__ void __launch_bounds__(kThreads) attn_rows_kernel(const AttnLaunch p)
     // 2^(14 - exponent), from the exponent field (0 and infinity: as they are)
     auto factor = [](float a, float* inv) {
       const int e = static_cast<int>(__float_as_uint(a) >> 23);
-      const int up = (e == 0 || e == 255) ? 0 : max(-100, min(100, 14 - (e - 127)));
+      const int up = (e == 0 || e == 255) ? 0 : min(126, 14 - (e - 127));  // 2^up and 2^-up are normal numbers
       *inv = __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
       return __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
     };

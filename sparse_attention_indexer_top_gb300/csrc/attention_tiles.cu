@@ -575,7 +575,7 @@ __device__ __forceinline__ float query_to_f16(unsigned char* tile, int r) {
     for (int e = 0; e < 4; ++e) amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(w[e])), fabsf(bf16_hi(w[e]))));
   }
   const int e = static_cast<int>(__float_as_uint(amax) >> 23);
-  const int up = (e == 0 || e == 255) ? 0 : max(-100, min(100, 14 - (e - 127)));
+  const int up = (e == 0 || e == 255) ? 0 : min(126, 14 - (e - 127));  // 2^up and 2^-up are normal numbers
   const float f = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
 #pragma unroll
   for (int c = 0; c < D / 8; ++c) {

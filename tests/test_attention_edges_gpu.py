@@ -145,3 +145,23 @@ def test_small_weights_beside_a_large_scale(rows, packed, group):
     err = np.abs(out.double().cpu().numpy() - ref[None])
     assert (err <= tol[None]).all()
     assert (np.abs(lse.double().cpu().numpy() - rl[None]) <= 2.0 ** -15).all()
+
+
+# --- queries of any size
+
+@pytest.mark.parametrize("packed", [False, 2])
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("group", [4, 16, 20])
+@pytest.mark.parametrize("power", [-120, -95, 95, 112, 120])
+def test_query_sizes(packed, dtype, group, power):
+    """Queries times 2^power with sm_scale over it: the same scores."""
+    reqs = [(70, 300), (20, 20)]
+    c = Case(230, [t for _, t in reqs], dtype=dtype, hkv=1, bs=64)
+    lens, r2b = _rows(reqs)
+    q, _ = c.queries(len(lens), group)
+    scaled = q * 2.0 ** power
+    q64 = scaled.double().cpu().numpy() * 2.0 ** -power  # the least ones have lost bits
+    out, lse = sai.paged_attention(scaled, c.cache, c.t_table, _lens(lens), max_seq_len=300,
+                                   row_to_batch=_lens(r2b), packed=packed, sm_scale=2.0 ** -power * 128 ** -0.5,
+                                   want_lse=True)
+    _check(c, q64, [(b, np.arange(n)) for b, n in zip(r2b, lens)], out, lse, 128 ** -0.5)
