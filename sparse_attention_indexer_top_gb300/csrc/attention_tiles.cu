@@ -742,7 +742,7 @@ __device__ __forceinline__ bool softmax_role(Shared<D, F8>& S, const TilesLaunch
       if (F8) {
         const int ek = blk1 >= 0 ? exponent_of(sc1.x) : kNoScale, e2 = blk1 >= 0 ? exponent_of(sc1.y) : kNoScale;
         const int tk = max(kLeastExp, __reduce_max_sync(0xffffffffu, ek)), tv = max(kLeastExp, __reduce_max_sync(0xffffffffu, e2));
-        mul = scale * power_of(tk);
+        mul = fmaxf(scale * power_of(tk), 1.17549435e-38f);  // not 0: masked scores are -inf
         ev = static_cast<float>(tv);
         un_ev = power_of(-tv);
         const float2 f = blk1 >= 0 ? make_float2(sc1.x * power_of(-max(ek, tk + kLeastShift)),

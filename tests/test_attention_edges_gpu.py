@@ -165,3 +165,16 @@ def test_query_sizes(packed, dtype, group, power):
                                    row_to_batch=_lens(r2b), packed=packed, sm_scale=2.0 ** -power * 128 ** -0.5,
                                    want_lse=True)
     _check(c, q64, [(b, np.arange(n)) for b, n in zip(r2b, lens)], out, lse, 128 ** -0.5)
+
+
+@pytest.mark.parametrize("packed", [False, 2])
+@pytest.mark.parametrize("group", [4, 20])
+def test_tiny_queries_and_key_scales(packed, group):
+    """Scores that are 0 in fp32: every seen key has the same weight."""
+    n = 200
+    c = Case(231, [n], dtype="e4m3", hkv=1, bs=32)
+    c.ks.fill_(2.0 ** -64)
+    q, _ = c.queries(n, group)
+    out, lse = sai.paged_attention(q * 2.0 ** -90, c.cache, c.t_table, _lens(range(1, n + 1)), max_seq_len=n,
+                                   row_to_batch=_lens([0] * n), packed=packed, want_lse=True)
+    _check(c, np.zeros((n, group, 128)), [(0, np.arange(i + 1)) for i in range(n)], out, lse, 1.0)
