@@ -379,7 +379,11 @@ int sai_topk_transform_noalloc(const float* scores, int64_t rows, int64_t score_
  *             order and k and v may share one array. 16-byte aligned, every
  *             stride a multiple of 16 bytes.
  * k_scale,    fp32 [num_blocks, heads], contiguous: value = code * scale, one
- * v_scale     scale for each block of tokens and kv head. e4m3 only.
+ * v_scale     scale for each block of tokens and kv head, 0 included. e4m3
+ *             only. The attention sums are exact to their rounding while the
+ *             value scales that a row sees are within 2^100 of each other
+ *             (those below 2^-64 count as 2^-64); beyond that, weights of keys
+ *             with small scales may be lost from the sums.
  * block_size  16, 32, 64 or 128; dim 64 or 128.
  */
 #define SAI_CACHE_BF16 0

@@ -404,12 +404,13 @@ __device__ __forceinline__ bool nonfinite2(uint32_t x) {
   return (x & 0x7f80u) == 0x7f80u || (x & 0x7f800000u) == 0x7f800000u;
 }
 
-// Exponent of a block scale (scales outside 2^-64 .. 2^100, 0 among them, leave
+// Exponent of a block scale (scales outside 2^-64 .. 2^120, 0 among them, leave
 // the rest to their factor; l holds weights over the value scale's power, which
-// fits fp32 down to 2^-64 for any number of keys), and 2^e.
+// fits fp32 down to 2^-64 for any number of keys; 2^120 is the scale of the
+// largest bf16 values), and 2^e.
 constexpr int kLeastExp = -64;
 __device__ __forceinline__ int exponent_of(float scale) {
-  return max(kLeastExp, min(100, static_cast<int>((__float_as_uint(scale) >> 23) & 255u) - 127));
+  return max(kLeastExp, min(120, static_cast<int>((__float_as_uint(scale) >> 23) & 255u) - 127));
 }
 __device__ __forceinline__ float power_of(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
 constexpr int kNoScale = -1000;   // exponent of a group without a block

@@ -178,3 +178,18 @@ def test_tiny_queries_and_key_scales(packed, group):
     out, lse = sai.paged_attention(q * 2.0 ** -90, c.cache, c.t_table, _lens(range(1, n + 1)), max_seq_len=n,
                                    row_to_batch=_lens([0] * n), packed=packed, want_lse=True)
     _check(c, np.zeros((n, group, 128)), [(0, np.arange(i + 1)) for i in range(n)], out, lse, 1.0)
+
+
+@pytest.mark.parametrize("packed", [False, 2])
+@pytest.mark.parametrize("group", [4, 20])
+@pytest.mark.parametrize("scales", [(105, 119), (-70, -60), (-62, 36)])
+def test_value_scales_of_any_size(packed, group, scales):
+    """Up to what append_kv makes of the largest bf16 values. A log-sum-exp may be off by the spacing of the running
+    maximum, which carries the value scale's exponent: three roundings of numbers below 128, 3 * 2^-18."""
+    reqs = [(70, 300), (20, 20)]
+    c = Case(232, [t for _, t in reqs], dtype="e4m3", hkv=1, bs=32, vscales=scales)
+    lens, r2b = _rows(reqs)
+    q, q64 = c.queries(len(lens), group)
+    out, lse = sai.paged_attention(q, c.cache, c.t_table, _lens(lens), max_seq_len=300, row_to_batch=_lens(r2b),
+                                   packed=packed, want_lse=True)
+    _check_any(c, q64, [(b, np.arange(n)) for b, n in zip(r2b, lens)], out, lse, 128 ** -0.5, 3 * 2.0 ** -18)
