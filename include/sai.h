@@ -451,8 +451,8 @@ int sai_append_kv(const sai_kv_cache* cache, const uint16_t* k, int64_t k_row_st
  * a / (q_heads / heads):
  *   out[i, a] = sum_t e_t v_t / sum_t e_t,  e_t = exp(sm_scale * q[i, a].k_t)
  *   out_lse[i, a] = log sum_t e_t
- * with fp32 sums. A row that sees no key, and a bad row (status bit 1), gets
- * zeros and -inf. What an unseen cell holds, NaN included, does not matter.
+ * with fp32 sums. A row that sees no key (or only keys of score -inf), and a
+ * bad row (status bit 1), gets zeros and -inf. What an unseen cell holds, NaN included, does not matter.
  * Keys on a block id outside [0, num_blocks) are not seen and set bit 4.
  *
  * q           bf16 [rows, q_heads, dim], row stride in elements as above.

@@ -162,13 +162,15 @@ __device__ __forceinline__ int chunk_keys(int count, int chunks) {
   return ((count + chunks - 1) / chunks + 63) & ~63;
 }
 
-// Four dims of a finished row.
+// Four dims of a finished row; a sum of 0 gives zeros whatever the values are
+// (0 times a NaN or infinite value has made the accumulator NaN).
 template <int D>
 __device__ __forceinline__ void write_row4(const AttnLaunch& p, long long head, int d, float m, float l, float4 a) {
-  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const bool none = l == 0.f;
+  const float inv = 1.f / l;
   *reinterpret_cast<uint2*>(p.out + head * D + d) =
-      make_uint2(pack_bf16(a.x * inv, a.y * inv), pack_bf16(a.z * inv, a.w * inv));
-  if (d == 0 && p.lse) p.lse[head] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+      none ? make_uint2(0u, 0u) : make_uint2(pack_bf16(a.x * inv, a.y * inv), pack_bf16(a.z * inv, a.w * inv));
+  if (d == 0 && p.lse) p.lse[head] = none ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
 // Weight of a partial result (maximum, sum) when joined under the maximum

@@ -193,3 +193,20 @@ def test_value_scales_of_any_size(packed, group, scales):
     out, lse = sai.paged_attention(q, c.cache, c.t_table, _lens(lens), max_seq_len=300, row_to_batch=_lens(r2b),
                                    packed=packed, want_lse=True)
     _check_any(c, q64, [(b, np.arange(n)) for b, n in zip(r2b, lens)], out, lse, 128 ** -0.5, 3 * 2.0 ** -18)
+
+
+# --- rows all of whose scores are -inf
+
+@pytest.mark.parametrize("packed", [False, 2])
+@pytest.mark.parametrize("group,n", [(4, 40), (16, 300), (20, 40), (4, 9000)])
+def test_all_scores_minus_infinity(packed, group, n):
+    """A row whose sum is 0 gives zeros and -inf, whatever its values are."""
+    c = Case(240, [n], dtype="bf16", hkv=1, bs=64)
+    q, _ = c.queries(30, group)
+    q[:, :, 0] = 1.0
+    c.k[:, :, :, 0] = -INF
+    c.k[:, :, :, 1:] = 0.0
+    _spoil(c, [(0, 5, 3, NAN), (0, n - 35, 70, INF)])
+    out, lse = sai.paged_attention(q, c.cache, c.t_table, _lens(range(n - 29, n + 1)), max_seq_len=n,
+                                   row_to_batch=_lens([0] * 30), packed=packed, want_lse=True)
+    assert (out == 0).all() and torch.isneginf(lse).all()
