@@ -429,11 +429,12 @@ typedef struct {
  * q, out_q    bf16 [rows, q_heads, dim] like k, and the rotated queries
  *             (contiguous; zeros for padding rows), or both NULL.
  * cos_sin     fp32 [max_pos, rot_dim], 16-byte aligned, or NULL with
- *             rot_dim = 0: no rotation. rot_dim is a multiple of 16 up to dim.
+ *             rot_dim = 0: no rotation, and max_pos is a bound of the positions
+ *             alone (0: none). rot_dim is a multiple of 16 up to dim.
  * The rows of one request that meet in one block are neighbours in the order
  * of their positions, without gaps (a decode row by itself, or a packed
  * chunk). A row with a length below 0 or above bt_stride*block_size or
- * (with cos_sin) max_pos, or with a request outside [0, bt_rows), sets status
+ * max_pos, or with a request outside [0, bt_rows), sets status
  * bit 1 and is skipped; a block id outside [0, num_blocks) sets bit 4 and its
  * rows are skipped.
  */

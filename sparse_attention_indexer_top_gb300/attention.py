@@ -5,10 +5,11 @@ keys and queries and writes keys and values into it, ``sparse_attention``
 attends over the slots that ``index_score_topk`` or ``topk_transform`` picked,
 and ``paged_attention`` over all keys of a row or a sliding window of them.
 Rows, ``seq_lens``, ``row_to_batch`` and ``block_table`` mean what they mean
-for ``index_score_topk``. As everywhere in this package, the computation runs
-in libsai.so; the checks and the allocations of the calls are in the compiled
-module ``_binding`` (csrc/binding.cpp), because a decode step makes them once a
-layer.
+for ``index_score_topk``; the table may be columns of a wider one, and a length
+past its columns makes a bad row. As everywhere in this package, the
+computation runs in libsai.so; the checks and the allocations of the calls are
+in the compiled module ``_binding`` (csrc/binding.cpp), because a decode step
+makes them once a layer.
 """
 
 from __future__ import annotations

@@ -37,7 +37,7 @@ __device__ __forceinline__ RowPlace row_place(const AppendLaunch& p, int row, bo
   const int b = p.row_to_batch ? p.row_to_batch[row] : row;
   if (n == 0) return r;
   const int pos = n - 1;
-  if (n < 0 || b < 0 || b >= p.bt_rows || (pos >> p.c.bs_log2) >= p.bt_stride || (p.rot && pos >= p.max_pos)) {
+  if (n < 0 || b < 0 || b >= p.bt_rows || (pos >> p.c.bs_log2) >= p.bt_stride || pos >= p.max_pos) {
     if (flag) atomicOr(p.status, kDevBadRowMeta);
     return r;
   }

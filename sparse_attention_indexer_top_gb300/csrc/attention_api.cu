@@ -149,7 +149,7 @@ int sai_append_kv(const sai_kv_cache* cache, const uint16_t* k, int64_t k_row_st
   p.q_row = q_row_stride;
   p.q_heads = q ? q_heads : 0;
   p.cos_sin = cos_sin;
-  p.max_pos = max_pos;
+  p.max_pos = cos_sin || max_pos > 0 ? max_pos : INT64_MAX;
   p.rot = rot_dim;
   p.interleaved = interleaved != 0;
   p.block_table = block_table;

@@ -13,6 +13,7 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
 #include <cmath>
 #include <stdexcept>
 #include <string>
@@ -96,12 +97,18 @@ Rows rows_of(PyObject* o, const char* name, int64_t rows, int64_t heads, const C
 
 struct Table {
   const int32_t* p;
-  int64_t rows, cols;
+  int64_t rows, stride;
+  int64_t cells;  // tokens that a row of it names, if rows are more than that apart; else no bound of its own
 };
-Table table_of(PyObject* o, int device) {
-  const at::Tensor& t = need(o, "block_table", at::kInt, 2, device);
-  if (!t.is_contiguous()) refuse("block_table must be contiguous");
-  return Table{static_cast<const int32_t*>(t.data_ptr()), t.size(0), t.size(1)};
+// int32 [requests, blocks], perhaps columns of a wider table: the library
+// bounds lengths by the stride, so the bound by columns is passed beside it.
+Table table_of(PyObject* o, const Cache& c) {
+  const at::Tensor& t = need(o, "block_table", at::kInt, 2, c.device);
+  const int64_t rows = t.size(0), cols = t.size(1), stride = rows > 1 && cols > 0 ? t.stride(0) : cols;
+  if ((cols > 1 && t.stride(1) != 1) || stride < cols)
+    refuse("block_table needs unit column stride and rows that do not overlap");
+  return Table{static_cast<const int32_t*>(t.data_ptr()), rows, stride,
+               stride > cols ? cols * c.d->block_size : INT64_MAX};
 }
 
 Cache cache_of(PyObject* ref, PyObject* device) {
@@ -164,16 +171,16 @@ PyObject* append_kv(PyObject* const* a) {
   if (!kt || kt->dim() != 3) refuse("k must have 3 dims");
   const int64_t rows = kt->size(0);
   const Rows k = rows_of(a[2], "k", rows, c.d->heads, c), v = rows_of(a[3], "v", rows, c.d->heads, c);
-  const Table bt = table_of(a[4], c.device);
+  const Table bt = table_of(a[4], c);
   const int32_t* lens = row_index(a[5], "seq_lens", rows, c.device);
   const int32_t* r2b = a[9] == Py_None ? nullptr : row_index(a[9], "row_to_batch", rows, c.device);
   const float* cs = nullptr;
-  int64_t max_pos = 0, rot = 0;
+  int64_t max_pos = bt.cells, rot = 0;
   if (a[6] != Py_None) {
     const at::Tensor& t = need(a[6], "cos_sin", at::kFloat, 2, c.device);
     if (!t.is_contiguous()) refuse("cos_sin must be contiguous");
     cs = static_cast<const float*>(t.data_ptr());
-    max_pos = t.size(0);
+    max_pos = std::min(max_pos, t.size(0));
     rot = std::min<int64_t>(t.size(1), INT32_MAX);
   }
   Rows q{nullptr, 0, 0};
@@ -186,7 +193,7 @@ PyObject* append_kv(PyObject* const* a) {
   }
   check(sai_append_kv(c.d, k.p, k.stride, v.p, v.stride, q.p, q.stride, q.heads,
                       out.defined() ? static_cast<uint16_t*>(out.data_ptr()) : nullptr, cs, max_pos,
-                      static_cast<int32_t>(rot), PyObject_IsTrue(a[10]) == 1, bt.p, bt.rows, bt.cols, r2b, lens, rows,
+                      static_cast<int32_t>(rot), PyObject_IsTrue(a[10]) == 1, bt.p, bt.rows, bt.stride, r2b, lens, rows,
                       stream_of(c)),
         "sai_append_kv");
   if (!out.defined()) Py_RETURN_NONE;
@@ -218,9 +225,9 @@ PyObject* paged_attention(PyObject* const* a) {
   if (!qt || qt->dim() != 3) refuse("q must have 3 dims");
   const int64_t rows = qt->size(0);
   const Rows q = rows_of(a[2], "q", rows, 0, c);
-  const Table bt = table_of(a[3], c.device);
+  const Table bt = table_of(a[3], c);
   const int32_t* lens = row_index(a[4], "seq_lens", rows, c.device);
-  const int32_t most = int32_of(a[5], "max_seq_len"), window = int32_of(a[8], "window"), sinks = int32_of(a[9], "sinks");
+  const int32_t most = static_cast<int32_t>(std::min<int64_t>(int32_of(a[5], "max_seq_len"), bt.cells)), window = int32_of(a[8], "window"), sinks = int32_of(a[9], "sinks");
   const int32_t* r2b = a[6] == Py_None ? nullptr : row_index(a[6], "row_to_batch", rows, c.device);
   const int32_t packed = int32_of(a[7], "packed");  // False, True, PACKED_TILES
   if (packed && !r2b) refuse("packed rows need row_to_batch");
@@ -231,7 +238,7 @@ PyObject* paged_attention(PyObject* const* a) {
   const Space w = workspace_of(a[14], a[14] == Py_None ? sai_paged_attention_workspace(rows, q.heads, c.d->heads, c.d->dim,
                                                                                        c.d->dtype, most, window, sinks, packed)
                                                        : 0, c);
-  check(sai_paged_attention(q.p, q.stride, q.heads, c.d, bt.p, bt.rows, bt.cols, r2b, lens, rows, most, window, sinks,
+  check(sai_paged_attention(q.p, q.stride, q.heads, c.d, bt.p, bt.rows, bt.stride, r2b, lens, rows, most, window, sinks,
                             static_cast<float>(scale), packed, static_cast<uint16_t*>(out.data_ptr()),
                             lse.defined() ? static_cast<float*>(lse.data_ptr()) : nullptr, w.p, w.bytes, stream_of(c)),
         "sai_paged_attention");

@@ -210,3 +210,58 @@ def test_all_scores_minus_infinity(packed, group, n):
     out, lse = sai.paged_attention(q, c.cache, c.t_table, _lens(range(n - 29, n + 1)), max_seq_len=n,
                                    row_to_batch=_lens([0] * 30), packed=packed, want_lse=True)
     assert (out == 0).all() and torch.isneginf(lse).all()
+
+
+# --- block tables that are slices of wider ones
+
+@pytest.mark.parametrize("packed", [False, 2])
+def test_sliced_block_table(packed):
+    """Columns of a wide table, as index_score_topk takes them; what lies beside the slice is never used."""
+    reqs = [(70, 300), (20, 20), (1, 256)]
+    c = Case(250, [t for _, t in reqs], dtype="bf16", bs=64)
+    lens, r2b = _rows(reqs)
+    q, q64 = c.queries(len(lens), 8)
+    rows, cols = c.table.shape
+    wide = torch.zeros((rows, cols + 7), dtype=torch.int32, device=DEV)
+    wide[:, 3:3 + cols] = c.t_table
+    part = wide[:, 3:3 + cols]
+    cells = [(b, np.arange(n)) for b, n in zip(r2b, lens)]
+    kw = dict(max_seq_len=1000, row_to_batch=_lens(r2b), packed=packed, want_lse=True)
+    sai.device_status()
+    out, lse = sai.paged_attention(q, c.cache, part, _lens(lens), **kw)
+    _check(c, q64, cells, out, lse, 128 ** -0.5)
+    assert sai.device_status() == 0
+    # a length that passes the slice, but not the wide table: a bad row
+    lens[0] = cols * 64 + 1
+    out, lse = sai.paged_attention(q, c.cache, part, _lens(lens), **kw)
+    _check(c, q64, [(0, np.arange(0))] + cells[1:], out, lse, 128 ** -0.5)
+    assert sai.device_status() == 1
+    # one request: the stride of an axis of one means nothing
+    sai.paged_attention(q[:1], c.cache, wide[:1, 3:3 + cols], _lens([300]), **dict(kw, row_to_batch=_lens([0])))
+    assert sai.device_status() == 0
+    for bad in (c.t_table.t().contiguous().t(), c.t_table[:1].expand(rows, cols)):
+        with pytest.raises(ValueError, match="block_table"):
+            sai.paged_attention(q, c.cache, bad, _lens(lens), **kw)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("rot", [0, 64])
+def test_append_through_a_sliced_block_table(dtype, rot):
+    lens = [64, 33, 1]
+    a, b = (Case(251, [64, 33, 1], dtype=dtype, dim=64, bs=32) for _ in range(2))
+    rows, cols = a.table.shape
+    wide = torch.zeros((rows, cols + 5), dtype=torch.int32, device=DEV)
+    wide[:, 2:2 + cols] = a.t_table
+    k, v = (torch.randn((rows, 2, 64), device=DEV).to(torch.bfloat16) for _ in range(2))
+    cs = torch.rand((500, rot), device=DEV) if rot else None
+    bits = lambda c: [x.contiguous().view(torch.uint8).clone() for x in (c.k, c.v)]
+    sai.device_status()
+    sai.append_kv(a.cache, k, v, a.t_table, _lens(lens), cs)
+    sai.append_kv(b.cache, k, v, wide[:, 2:2 + cols], _lens(lens), cs)
+    assert sai.device_status() == 0
+    assert all(torch.equal(x, y) for x, y in zip(bits(a), bits(b)))
+    # past the slice, but not past the wide table: skipped and flagged
+    before = bits(b)
+    sai.append_kv(b.cache, k, v, wide[:, 2:2 + cols], _lens([cols * 32 + 1, 0, 0]), cs)
+    assert sai.device_status() == 1
+    assert all(torch.equal(x, y) for x, y in zip(before, bits(b)))
