@@ -50,6 +50,12 @@ int32_t int32_of(PyObject* o, const char* name) {
   return static_cast<int32_t>(v);
 }
 
+bool truth(PyObject* o) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) throw Raised{};
+  return v == 1;
+}
+
 const at::Tensor* tensor(PyObject* o, const char* name) {
   if (o == Py_None) return nullptr;
   if (!THPVariable_Check(o)) refuse(std::string(name) + " must be a tensor");
@@ -183,6 +189,7 @@ PyObject* append_kv(PyObject* const* a) {
     max_pos = std::min(max_pos, t.size(0));
     rot = std::min<int64_t>(t.size(1), INT32_MAX);
   }
+  const bool interleaved = truth(a[10]);
   Rows q{nullptr, 0, 0};
   at::Tensor out;
   if (a[7] != Py_None) {
@@ -193,7 +200,7 @@ PyObject* append_kv(PyObject* const* a) {
   }
   check(sai_append_kv(c.d, k.p, k.stride, v.p, v.stride, q.p, q.stride, q.heads,
                       out.defined() ? static_cast<uint16_t*>(out.data_ptr()) : nullptr, cs, max_pos,
-                      static_cast<int32_t>(rot), PyObject_IsTrue(a[10]) == 1, bt.p, bt.rows, bt.stride, r2b, lens, rows,
+                      static_cast<int32_t>(rot), interleaved, bt.p, bt.rows, bt.stride, r2b, lens, rows,
                       stream_of(c)),
         "sai_append_kv");
   if (!out.defined()) Py_RETURN_NONE;
@@ -234,7 +241,7 @@ PyObject* paged_attention(PyObject* const* a) {
   const double scale = scale_of(a[10], c);
   const at::Tensor out = output(a[11], "out", {rows, q.heads, c.d->dim}, at::kBFloat16, c);
   at::Tensor lse;
-  if (a[13] != Py_None || PyObject_IsTrue(a[12]) == 1) lse = output(a[13], "out_lse", {rows, q.heads}, at::kFloat, c);
+  if (truth(a[12]) || a[13] != Py_None) lse = output(a[13], "out_lse", {rows, q.heads}, at::kFloat, c);
   const Space w = workspace_of(a[14], a[14] == Py_None ? sai_paged_attention_workspace(rows, q.heads, c.d->heads, c.d->dim,
                                                                                        c.d->dtype, most, window, sinks, packed)
                                                        : 0, c);
@@ -260,7 +267,7 @@ PyObject* sparse_attention(PyObject* const* a) {
   const double scale = scale_of(a[4], c);
   const at::Tensor out = output(a[5], "out", {rows, q.heads, c.d->dim}, at::kBFloat16, c);
   at::Tensor lse;
-  if (a[7] != Py_None || PyObject_IsTrue(a[6]) == 1) lse = output(a[7], "out_lse", {rows, q.heads}, at::kFloat, c);
+  if (truth(a[6]) || a[7] != Py_None) lse = output(a[7], "out_lse", {rows, q.heads}, at::kFloat, c);
   const int32_t k32 = static_cast<int32_t>(k);
   const Space w = workspace_of(
       a[8], a[8] == Py_None ? sai_sparse_attention_workspace(rows, q.heads, c.d->heads, c.d->dim, c.d->dtype, k32) : 0, c);

@@ -265,3 +265,18 @@ def test_append_through_a_sliced_block_table(dtype, rot):
     sai.append_kv(b.cache, k, v, wide[:, 2:2 + cols], _lens([cols * 32 + 1, 0, 0]), cs)
     assert sai.device_status() == 1
     assert all(torch.equal(x, y) for x, y in zip(before, bits(b)))
+
+
+# --- arguments without a truth value
+
+def test_flags_without_a_truth_value():
+    c = Case(260, [10], dtype="bf16", dim=64, bs=16)
+    x = torch.ones((1, 2, 64), dtype=torch.bfloat16, device=DEV)
+    before = c.k.view(torch.uint8).clone()
+    with pytest.raises(RuntimeError, match="ambiguous"):
+        sai.append_kv(c.cache, x, x, c.t_table, _lens([10]), interleaved=torch.ones(2))
+    assert torch.equal(before, c.k.view(torch.uint8))
+    with pytest.raises(RuntimeError, match="ambiguous"):
+        sai.paged_attention(x, c.cache, c.t_table, _lens([10]), max_seq_len=10, want_lse=torch.ones(2))
+    with pytest.raises(RuntimeError, match="ambiguous"):
+        sai.sparse_attention(x, c.cache, _lens([[0]]), want_lse=torch.ones(2))
