@@ -186,8 +186,8 @@ PyObject* append_kv(PyObject* const* a) {
     const at::Tensor& t = need(a[6], "cos_sin", at::kFloat, 2, c.device);
     if (!t.is_contiguous()) refuse("cos_sin must be contiguous");
     cs = static_cast<const float*>(t.data_ptr());
-    max_pos = std::min(max_pos, t.size(0));
     rot = std::min<int64_t>(t.size(1), INT32_MAX);
+    if (rot) max_pos = std::min(max_pos, t.size(0));  // angles of no dims bound nothing
   }
   const bool interleaved = truth(a[10]);
   Rows q{nullptr, 0, 0};

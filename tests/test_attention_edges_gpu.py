@@ -267,6 +267,17 @@ def test_append_through_a_sliced_block_table(dtype, rot):
     assert all(torch.equal(x, y) for x, y in zip(before, bits(b)))
 
 
+def test_append_with_angles_of_no_dims():
+    """They bound no position."""
+    c = Case(252, [33], dtype="bf16", dim=64, bs=32)
+    x = torch.randn((1, 2, 64), device=DEV).to(torch.bfloat16)
+    sai.device_status()
+    sai.append_kv(c.cache, x, x, c.t_table, _lens([33]), torch.empty((2, 0), device=DEV))
+    assert sai.device_status() == 0
+    assert torch.equal(c.k[int(c.table[0, 1]), :, 0], x[0])
+
+
+
 # --- arguments without a truth value
 
 def test_flags_without_a_truth_value():
