@@ -457,7 +457,8 @@ int sai_append_kv(const sai_kv_cache* cache, const uint16_t* k, int64_t k_row_st
  * Keys on a block id outside [0, num_blocks) are not seen and set bit 4.
  *
  * q           bf16 [rows, q_heads, dim], row stride in elements as above.
- * max_seq_len host-side bound of seq_lens (longer rows are bad rows).
+ * max_seq_len host-side bound of seq_lens (longer rows are bad rows, and rows
+ *             above 2^31 - 8192 keys).
  * packed      0: each row by itself (decode; its keys are split over CTAs).
  *             1: neighbouring rows mostly share a request and have
  *             neighbouring lengths (prefill): they are taken as tiles where

@@ -81,6 +81,10 @@ int check_attention(const uint16_t* q, int64_t q_row_stride, int32_t q_heads, co
   return SAI_OK;
 }
 
+// Longest row of paged_attention: the kernels step past a row's end by up to 64
+// chunks of 64 keys in 32 bits.
+constexpr int kMostLen = INT_MAX - 8191;
+
 long long most_keys(int32_t max_seq_len, int32_t window, int32_t sinks) {
   if (window <= 0) return max_seq_len;
   return std::min<long long>(max_seq_len, static_cast<long long>(window) + sinks);
@@ -201,7 +205,7 @@ int sai_paged_attention(const uint16_t* q, int64_t q_row_stride, int32_t q_heads
   p.bt_stride = bt_stride;
   p.row_to_batch = row_to_batch;
   p.seq_lens = seq_lens;
-  p.max_len = max_seq_len;
+  p.max_len = std::min(max_seq_len, kMostLen);
   p.window = window;
   p.sinks = sinks;
   p.rows = static_cast<int>(rows);

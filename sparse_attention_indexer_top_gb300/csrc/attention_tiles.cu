@@ -1262,7 +1262,8 @@ __device__ __forceinline__ void deal_units(Shared<D, F8>& S, const TilesLaunch& 
       most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
       low = min(low, __shfl_xor_sync(0xffffffffu, low, o));
     }
-    if (lane == 0) S.deal[t + 1] = kUnitWeight + (most > 0 ? (most + kTile - 1) / kTile - low / kTile : 0);
+    // at most 2^20, so that kMaxDealt of them fit 32 bits (a step is then several tiles)
+    if (lane == 0) S.deal[t + 1] = kUnitWeight + (most > 0 ? min((most + kTile - 1) / kTile - low / kTile, 1 << 20) : 0);
   }
   __syncthreads();
   if (warp == 0) {

@@ -278,6 +278,25 @@ def test_append_with_angles_of_no_dims():
 
 
 
+@pytest.mark.parametrize("packed", [False, 2])
+@pytest.mark.parametrize("window", [0, 1000])
+def test_lengths_near_2_to_31(packed, window):
+    """A table of 2^24 blocks to a request: lengths whose rounded ends would pass 32 bits are bad rows, the others right."""
+    c = Case(253, [300], dtype="bf16", hkv=1, bs=128)
+    table = torch.full((1, 1 << 24), int(c.table[0, 0]), dtype=torch.int32, device=DEV)
+    table[:, :c.table.shape[1]] = c.t_table
+    top = 2 ** 31 - 1
+    lens = [300, top, top - 100, 2 ** 31 - 8191, 17]
+    q, q64 = c.queries(len(lens), 8)
+    sai.device_status()
+    out, lse = sai.paged_attention(q, c.cache, table, _lens(lens), max_seq_len=top, row_to_batch=_lens([0] * 5),
+                                   packed=packed, window=window, want_lse=True)
+    assert sai.device_status() == 1
+    cells = [(0, A.seen(n, window, 0)) if n <= 300 else (0, np.arange(0)) for n in lens]
+    _check(c, q64, cells, out, lse, 128 ** -0.5)
+
+
+
 # --- arguments without a truth value
 
 def test_flags_without_a_truth_value():
