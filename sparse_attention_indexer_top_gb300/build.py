@@ -5,7 +5,8 @@ Each ``csrc/*.cu`` translation unit is compiled in parallel to an object
 file, then linked into ``libsai.so`` next to this file. Objects live in
 ``_build/`` (git-ignored). A unit is rebuilt when it or any header is newer
 than its object. ``csrc/binding.cpp`` becomes ``_binding.so``, against the
-installed torch; it is also rebuilt when torch's version has changed.
+installed torch; a stamp beside its object names the torch and the Python it
+was linked for, and it is linked again when either is another.
 """
 
 from __future__ import annotations
@@ -43,10 +44,12 @@ def _newest_header() -> float:
 
 
 def _binding_job(hdr: float):
-    """Command that compiles binding.cpp to an object, its object, and whether it is out of date."""
+    """Command that compiles binding.cpp to an object, its object, the linker's arguments, whether the object is out of
+    date, and the name of the torch and the Python that it is for."""
     import torch
 
-    src, obj = os.path.join(CSRC, "binding.cpp"), os.path.join(BUILD, f"binding-torch-{torch.__version__}.o")
+    abi = f"torch-{torch.__version__}-{sys.implementation.cache_tag}"
+    src, obj = os.path.join(CSRC, "binding.cpp"), os.path.join(BUILD, f"binding-{abi}.o")
     top = os.path.dirname(torch.__file__)
     inc = [os.path.join(top, "include"), sysconfig.get_paths()["include"],
            os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include"), "/usr/local/cuda/include"]
@@ -55,7 +58,15 @@ def _binding_job(hdr: float):
     link = ["-L" + os.path.join(top, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10", "-L" + HERE,
             "-l:libsai.so", "-Wl,-rpath,$ORIGIN"]
     stale = not os.path.exists(obj) or os.path.getmtime(obj) < max(os.path.getmtime(src), hdr)
-    return cmd, obj, link, stale
+    return cmd, obj, link, stale, abi
+
+
+def _read(path: str) -> str:
+    try:
+        with open(path) as f:
+            return f.read()
+    except OSError:
+        return ""
 
 
 def build(verbose: bool = False, force: bool = False) -> str:
@@ -72,8 +83,8 @@ def build(verbose: bool = False, force: bool = False) -> str:
         if force or not os.path.exists(o) or os.path.getmtime(o) < max(os.path.getmtime(s), hdr):
             jobs.append([nvcc, *ARCH, *FLAGS, "-c", s, "-o", o])
 
-    cmd, bobj, link, stale = _binding_job(hdr)
-    if stale:
+    cmd, bobj, link, stale, abi = _binding_job(hdr)
+    if force or stale:
         jobs.append(cmd)
 
     def run(cmd):
@@ -89,10 +100,14 @@ def build(verbose: bool = False, force: bool = False) -> str:
         tmp = LIB + ".tmp"
         run([nvcc, *ARCH, "-shared", "-o", tmp, *objs])
         os.replace(tmp, LIB)
-    if not os.path.exists(BINDING) or os.path.getmtime(BINDING) < max(os.path.getmtime(bobj), os.path.getmtime(LIB)):
+    stamp = os.path.join(BUILD, "binding.stamp")
+    if (not os.path.exists(BINDING) or _read(stamp) != abi
+            or os.path.getmtime(BINDING) < max(os.path.getmtime(bobj), os.path.getmtime(LIB))):
         tmp = BINDING + ".tmp"
         run(["g++", "-shared", "-o", tmp, bobj, *link])
         os.replace(tmp, BINDING)
+        with open(stamp, "w") as f:
+            f.write(abi)
     return LIB
 
 
