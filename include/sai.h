@@ -421,7 +421,8 @@ typedef struct {
  * that the call puts into this block and head; s = need when the call writes
  * the block's first cell, else max(old scale, need), and then the codes of the
  * cells before the call's first one are rounded to the new scale (exact
- * but for values that become subnormal). Infinities saturate, NaN stays NaN.
+ * but for values that become subnormal). An old scale that is no power of two
+ * and stays is applied as x * (1 / s) in fp32. Infinities saturate, NaN stays NaN.
  *
  * k, v        bf16 [rows, heads, dim]; heads and dims contiguous, the stride
  *             between rows given in elements (a slice of a fused projection).
@@ -466,7 +467,8 @@ int sai_append_kv(const sai_kv_cache* cache, const uint16_t* k, int64_t k_row_st
  *             SAI_PACKED_TILES: as tiles whatever the sizes (not with more
  *             than 128 query heads to a kv head or sm_scale <= 0).
  *             Any rows give right results in every case.
- * out         bf16 [rows, q_heads, dim]; out_lse fp32 [rows, q_heads] or NULL.
+ * out         bf16 [rows, q_heads, dim], not overlapping q; out_lse fp32
+ *             [rows, q_heads] or NULL.
  * workspace   sai_paged_attention_workspace(...) bytes (same arguments, same
  *             device), 16-byte aligned; NULL when that is 0. Calls that share
  *             a workspace must not overlap on the GPU.
