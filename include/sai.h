@@ -62,8 +62,8 @@ const char* sai_last_error(void);
  * Read (and optionally clear) the device status word of the current device
  * after synchronizing `stream`. *out_bits receives the OR of the bits set by
  * kernels since the last clear: 1 = bad row metadata, 2 = an internal
- * pipeline wait gave up, 4 = a block id out of range. Returns
- * SAI_ERR_DEVICE_CHECK if any bit was set, else SAI_OK.
+ * pipeline wait gave up, 4 = a block id out of range, 8 = a request got no
+ * pages (sai_resize_pages). Returns SAI_ERR_DEVICE_CHECK if any bit was set, else SAI_OK.
  */
 int sai_device_status(int* out_bits, int clear, sai_stream_t stream);
 
@@ -494,6 +494,116 @@ int sai_sparse_attention(const uint16_t* q, int64_t q_row_stride, int32_t q_head
                          const int32_t* slots, int64_t slots_stride, int32_t k, int64_t rows, float sm_scale,
                          uint16_t* out, float* out_lse, void* workspace, size_t workspace_bytes,
                          sai_stream_t stream);
+
+/*
+ * Pages of the caches: copying, forking, growing and ending requests, compacting.
+ *
+ * A pool of num_blocks pages (the blocks of the caches) is shared by all layers:
+ * page p is block p of every array of the pool. refs[p] (int32) counts the
+ * requests whose table names page p, and whoever else holds it (a prompt store);
+ * 0 or below: free. Request r holds the first ceil(seq_lens[r] / block_size)
+ * entries of row r of block_table ([requests, width], rows bt_stride elements
+ * apart), here one row and one length for each request, not for each query row.
+ * The calls below read tables, lengths and counts on the device, decide there
+ * and write new ones; nothing comes back to the host. Which page is taken
+ * depends on the counts alone (the lowest free pages, in the order of requests),
+ * so equal states give equal tables.
+ *
+ * sai_page_array describes one array of the pool: page p is count[0] x count[1]
+ * rows of row_bytes contiguous bytes, stride[] apart, at base + p * page_stride
+ * (all in bytes, multiples of 4). cells names the axis (0 or 1) that counts the
+ * page's tokens, so that a partly filled page may be copied in part; -1: it is
+ * copied whole. sai_cache_page_arrays writes the arrays of a cache (k, v, and
+ * for e4m3 k_scale, v_scale) to out[4] and returns how many they are, or an
+ * error below 0. Pages of one array must not overlap.
+ */
+typedef struct {
+  void* base;
+  int64_t page_stride;
+  int64_t stride[2];
+  int32_t count[2];
+  int32_t row_bytes;
+  int32_t cells;
+} sai_page_array;
+
+int sai_cache_page_arrays(const sai_kv_cache* cache, sai_page_array* out);
+
+/*
+ * sai_copy_pages -- page dst[i] becomes a copy of page src[i] in every array,
+ * i < pairs. A pair with an id below 0 or with src[i] = dst[i] is left out, one
+ * with an id at or above num_blocks too, and sets status bit 4. A page may be a
+ * source more than once; a page that is the target of two pairs, or a source and
+ * a target, ends up with a mixture. arrays is a HOST array of descriptors.
+ */
+int sai_copy_pages(const sai_page_array* arrays, int32_t num_arrays, int64_t num_blocks, const int32_t* src,
+                   const int32_t* dst, int64_t pairs, sai_stream_t stream);
+
+/*
+ * sai_fork_pages -- request i of the new batch, i < children, continues request
+ * parents[i] of the old one (-1: none), sharing all its pages:
+ *   out_table[i, :] = block_table[parents[i], :] (-1: every entry -1)
+ *   out_lens[i] = seq_lens[parents[i]] (-1: 0)
+ *   out_refs[p] = refs[p] + sum over the old requests that hold p of
+ *                 (number of their children - 1)
+ * so that old requests without a child are freed. No page is copied: a shared
+ * last page is, by sai_resize_pages, when one of its requests grows.
+ * A parent outside [-1, requests) sets status bit 1 and counts as -1; an old
+ * request with a length outside [0, width * block_size] sets bit 1 and counts as
+ * one of length 0 without children. A held id outside [0, num_blocks) sets bit 4
+ * and is not counted. out_refs may be refs; out_table and out_lens are memory of
+ * their own.
+ */
+int sai_fork_pages(const int32_t* block_table, int64_t requests, int64_t width, int64_t bt_stride,
+                   const int32_t* seq_lens, int32_t block_size, const int32_t* refs, int64_t num_blocks,
+                   const int32_t* parents, int64_t children, int32_t* out_table, int64_t out_stride, int32_t* out_lens,
+                   int32_t* out_refs, sai_stream_t stream);
+
+/*
+ * sai_resize_pages -- every request r gets the pages that new_lens[r] tokens
+ * need (to be called before sai_append_kv), or gives back those that it does
+ * not need any more (0: all of them).
+ *
+ * Growing: with a last page that is partly filled and has refs above 1, the
+ * request first gets a page of its own with a copy of the filled cells (arrays
+ * without a cells axis: of the whole page), unless it is the last of as
+ * many growing requests as refs counts, all with this last page: that one keeps
+ * it. Then come the pages for the new tokens. New pages are free ones, lowest id
+ * first, request by request, the copy before the others; their refs become 1.
+ * Shrinking: entries from ceil(new_lens / block_size) on become -1 and their refs
+ * one less. Pages that the call frees are not given out by it.
+ *
+ * A request is served when the pages wanted by it and by all before it are
+ * there (and always when it wants none); one that is not keeps table, length
+ * and pages, and sets status bit 8. out_lens[r] is new_lens[r] where served,
+ * else seq_lens[r]. A length outside [0, width * block_size] sets bit 1, a last
+ * page outside [0, num_blocks) bit 4: the request is left as it is. out_table,
+ * out_lens and out_refs may be the inputs themselves (not partly overlap them).
+ * workspace: sai_resize_pages_workspace(...) bytes, 16-byte aligned; calls that
+ * share it must not overlap on the GPU.
+ */
+size_t sai_resize_pages_workspace(int64_t num_blocks, int64_t requests);
+int sai_resize_pages(const sai_page_array* arrays, int32_t num_arrays, int64_t num_blocks, int32_t block_size,
+                     const int32_t* block_table, int64_t requests, int64_t width, int64_t bt_stride,
+                     const int32_t* seq_lens, const int32_t* new_lens, const int32_t* refs, int32_t* out_table,
+                     int64_t out_stride, int32_t* out_lens, int32_t* out_refs, void* workspace, size_t workspace_bytes,
+                     sai_stream_t stream);
+
+/*
+ * sai_compact_pages -- brings the H pages with refs above 0 to the ids [0, H):
+ * those at H and above move, in ascending order, to the free ids below H, in
+ * ascending order; the others stay. out_moves[p] is page p's new id (-1: free),
+ * for whatever else names pages; out_refs moves along; the entries that requests
+ * hold are renamed in out_table (the others stay as they are). A length outside
+ * [0, width * block_size] sets status bit 1 and its row stays; a held id outside
+ * [0, num_blocks) sets bit 4 and stays; one of a free page sets bit 4 and becomes
+ * -1. out_table and out_refs may be the inputs. workspace as above.
+ */
+size_t sai_compact_pages_workspace(int64_t num_blocks);
+int sai_compact_pages(const sai_page_array* arrays, int32_t num_arrays, int64_t num_blocks, int32_t block_size,
+                      const int32_t* block_table, int64_t requests, int64_t width, int64_t bt_stride,
+                      const int32_t* seq_lens, const int32_t* refs, int32_t* out_table, int64_t out_stride,
+                      int32_t* out_refs, int32_t* out_moves, void* workspace, size_t workspace_bytes,
+                      sai_stream_t stream);
 
 #ifdef __cplusplus
 }

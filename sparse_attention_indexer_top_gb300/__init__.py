@@ -24,6 +24,15 @@ from .attention import (  # noqa: F401
     sparse_attention,
     sparse_attention_workspace,
 )
+from .pages import (  # noqa: F401
+    PageSet,
+    compact_pages,
+    compact_pages_workspace,
+    copy_pages,
+    fork_pages,
+    resize_pages,
+    resize_pages_workspace,
+)
 
 TOPK = 512
 

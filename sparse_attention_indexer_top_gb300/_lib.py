@@ -25,6 +25,13 @@ class KVCacheDesc(ctypes.Structure):
                 ("dim", _c_i32), ("dtype", _c_i32)]
 
 
+class PageArrayDesc(ctypes.Structure):
+    """sai_page_array of include/sai.h."""
+
+    _fields_ = [("base", _vp), ("page_stride", _c_i64), ("stride", _c_i64 * 2), ("count", _c_i32 * 2),
+                ("row_bytes", _c_i32), ("cells", _c_i32)]
+
+
 # name -> (restype, argtypes); mirrors include/sai.h
 SIGNATURES = {
     "sai_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -68,6 +75,16 @@ SIGNATURES = {
     "sai_sparse_attention_workspace": (_c_size, [_c_i64, _c_i32, _c_i32, _c_i32, _c_i32, _c_i32]),
     "sai_sparse_attention": (ctypes.c_int, [_vp, _c_i64, _c_i32, _vp, _vp, _c_i64, _c_i32, _c_i64, _f32, _vp, _vp,
                                             _vp, _c_size, _vp]),
+    "sai_cache_page_arrays": (ctypes.c_int, [_vp, _vp]),
+    "sai_copy_pages": (ctypes.c_int, [_vp, _c_i32, _c_i64, _vp, _vp, _c_i64, _vp]),
+    "sai_fork_pages": (ctypes.c_int, [_vp, _c_i64, _c_i64, _c_i64, _vp, _c_i32, _vp, _c_i64, _vp, _c_i64, _vp, _c_i64,
+                                      _vp, _vp, _vp]),
+    "sai_resize_pages_workspace": (_c_size, [_c_i64, _c_i64]),
+    "sai_resize_pages": (ctypes.c_int, [_vp, _c_i32, _c_i64, _c_i32, _vp, _c_i64, _c_i64, _c_i64, _vp, _vp, _vp, _vp,
+                                        _c_i64, _vp, _vp, _vp, _c_size, _vp]),
+    "sai_compact_pages_workspace": (_c_size, [_c_i64]),
+    "sai_compact_pages": (ctypes.c_int, [_vp, _c_i32, _c_i64, _c_i32, _vp, _c_i64, _c_i64, _c_i64, _vp, _vp, _vp,
+                                         _c_i64, _vp, _vp, _vp, _c_size, _vp]),
 }
 
 _lib = None

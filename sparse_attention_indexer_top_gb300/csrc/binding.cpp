@@ -1,10 +1,10 @@
-// Python binding of the cache and attention entry points: argument checks,
+// Python binding of the cache, attention and page entry points: argument checks,
 // allocation and the call in one step. A decode step makes these calls once a
 // layer with kernels of a few microseconds, and the same checks made in Python
 // took three to four times as long as the launch.
 //
-// Argument rules and messages are those that attention.py documents; every
-// function runs on torch's current stream of the cache's device.
+// Argument rules and messages are those that attention.py and pages.py document;
+// every function runs on torch's current stream of the cache's (table's) device.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
@@ -279,6 +279,132 @@ PyObject* sparse_attention(PyObject* const* a) {
   return attention_result(out, lse);
 }
 
+// ---- pages: the descriptors of a PageSet object, kept by the Python object
+struct Pages {
+  const sai_page_array* arrays;
+  int32_t n;
+  int64_t blocks;
+  int32_t block_size;
+  Cache c;  // the device
+};
+// (arrays, number, num_blocks, block_size, device)
+Pages pages_of(PyObject* const* a) {
+  Pages p{static_cast<const sai_page_array*>(PyLong_AsVoidPtr(a[0])), int32_of(a[1], "arrays"), integer(a[2]),
+          int32_of(a[3], "block_size"), Cache{nullptr, int32_of(a[4], "device")}};
+  if (PyErr_Occurred()) throw Raised{};
+  return p;
+}
+void current(const Cache& c, const char* what) {
+  const int now = c10::cuda::current_device();
+  if (now != c.device)
+    refuse("the current device is cuda:" + std::to_string(now) + ", " + what + " on cuda:" + std::to_string(c.device));
+}
+
+// int32 [n], contiguous.
+const at::Tensor& ints(PyObject* o, const char* name, const Cache& c) {
+  const at::Tensor& t = need(o, name, at::kInt, 1, c.device);
+  if (!t.is_contiguous()) refuse(std::string(name) + " must be contiguous");
+  return t;
+}
+const int32_t* counts(PyObject* o, int64_t blocks, const Cache& c) { return row_index(o, "refs", blocks, c.device); }
+int32_t* data32(const at::Tensor& t) { return static_cast<int32_t*>(t.data_ptr()); }
+
+struct Plane {
+  at::Tensor t;
+  int64_t rows, width, stride;
+};
+// int32 [rows, width], perhaps columns of a wider table.
+Plane plane_of(const at::Tensor& t, const char* name) {
+  const int64_t rows = t.size(0), cols = t.size(1), stride = rows > 1 ? t.stride(0) : cols;
+  if ((cols > 1 && t.stride(1) != 1) || stride < cols)
+    refuse(std::string(name) + " needs unit column stride and rows that do not overlap");
+  return Plane{t, rows, cols, stride};
+}
+Plane plane(PyObject* o, const char* name, const Cache& c) { return plane_of(need(o, name, at::kInt, 2, c.device), name); }
+Plane out_plane(PyObject* o, int64_t rows, int64_t width, const Cache& c) {
+  if (o == Py_None) return Plane{fresh({rows, width}, at::kInt, c), rows, width, width};
+  const Plane p = plane(o, "out_table", c);
+  if (p.rows != rows || p.width != width)
+    refuse("out_table must be [" + std::to_string(rows) + ", " + std::to_string(width) + "]");
+  return p;
+}
+
+PyObject* results(const at::Tensor& a, const at::Tensor& b, const at::Tensor& c) {
+  PyObject *x = THPVariable_Wrap(a), *y = x ? THPVariable_Wrap(b) : nullptr, *z = y ? THPVariable_Wrap(c) : nullptr;
+  PyObject* r = z ? PyTuple_Pack(3, x, y, z) : nullptr;
+  Py_XDECREF(x);
+  Py_XDECREF(y);
+  Py_XDECREF(z);
+  return r;
+}
+
+// (pages..., src, dst)
+PyObject* copy_pages(PyObject* const* a) {
+  const Pages p = pages_of(a);
+  current(p.c, "the pages are");
+  const at::Tensor &src = ints(a[5], "src", p.c), &dst = ints(a[6], "dst", p.c);
+  if (src.size(0) != dst.size(0)) refuse("src and dst must be of one length");
+  check(sai_copy_pages(p.arrays, p.n, p.blocks, data32(src), data32(dst), src.size(0), stream_of(p.c)), "sai_copy_pages");
+  Py_RETURN_NONE;
+}
+
+// (block_table, seq_lens, refs, parents, block_size, out_table, out_lens, out_refs)
+PyObject* fork_pages(PyObject* const* a) {
+  const at::Tensor* t = tensor(a[0], "block_table");
+  if (!t || !t->is_cuda()) refuse("block_table must be on a CUDA device");
+  const Cache c{nullptr, static_cast<int>(t->get_device())};
+  current(c, "the table is");
+  const Plane table = plane(a[0], "block_table", c);
+  const int32_t* lens = row_index(a[1], "seq_lens", table.rows, c.device);
+  const at::Tensor &refs = ints(a[2], "refs", c), &parents = ints(a[3], "parents", c);
+  const int64_t children = parents.size(0);
+  const Plane out = out_plane(a[5], children, table.width, c);
+  const at::Tensor out_lens = output(a[6], "out_lens", {children}, at::kInt, c);
+  const at::Tensor out_refs = output(a[7], "out_refs", {refs.size(0)}, at::kInt, c);
+  check(sai_fork_pages(data32(table.t), table.rows, table.width, table.stride, lens, int32_of(a[4], "block_size"),
+                       data32(refs), refs.size(0), data32(parents), children, data32(out.t), out.stride, data32(out_lens),
+                       data32(out_refs), stream_of(c)),
+        "sai_fork_pages");
+  return results(out.t, out_lens, out_refs);
+}
+
+// (pages..., block_table, seq_lens, new_lens, refs, out_table, out_lens, out_refs, workspace)
+PyObject* resize_pages(PyObject* const* a) {
+  const Pages p = pages_of(a);
+  current(p.c, "the pages are");
+  const Plane table = plane(a[5], "block_table", p.c);
+  const int32_t* lens = row_index(a[6], "seq_lens", table.rows, p.c.device);
+  const int32_t* to = row_index(a[7], "new_lens", table.rows, p.c.device);
+  const int32_t* refs = counts(a[8], p.blocks, p.c);
+  const Plane out = out_plane(a[9], table.rows, table.width, p.c);
+  const at::Tensor out_lens = output(a[10], "out_lens", {table.rows}, at::kInt, p.c);
+  const at::Tensor out_refs = output(a[11], "out_refs", {p.blocks}, at::kInt, p.c);
+  const Space w = workspace_of(a[12], a[12] == Py_None ? sai_resize_pages_workspace(p.blocks, table.rows) : 0, p.c);
+  check(sai_resize_pages(p.arrays, p.n, p.blocks, p.block_size, data32(table.t), table.rows, table.width, table.stride,
+                         lens, to, refs, data32(out.t), out.stride, data32(out_lens), data32(out_refs), w.p, w.bytes,
+                         stream_of(p.c)),
+        "sai_resize_pages");
+  return results(out.t, out_lens, out_refs);
+}
+
+// (pages..., block_table, seq_lens, refs, out_table, out_refs, out_moves, workspace)
+PyObject* compact_pages(PyObject* const* a) {
+  const Pages p = pages_of(a);
+  current(p.c, "the pages are");
+  const Plane table = plane(a[5], "block_table", p.c);
+  const int32_t* lens = row_index(a[6], "seq_lens", table.rows, p.c.device);
+  const int32_t* refs = counts(a[7], p.blocks, p.c);
+  const Plane out = out_plane(a[8], table.rows, table.width, p.c);
+  const at::Tensor out_refs = output(a[9], "out_refs", {p.blocks}, at::kInt, p.c);
+  const at::Tensor moves = output(a[10], "out_moves", {p.blocks}, at::kInt, p.c);
+  const Space w = workspace_of(a[11], a[11] == Py_None ? sai_compact_pages_workspace(p.blocks) : 0, p.c);
+  check(sai_compact_pages(p.arrays, p.n, p.blocks, p.block_size, data32(table.t), table.rows, table.width, table.stride,
+                          lens, refs, data32(out.t), out.stride, data32(out_refs), data32(moves), w.p, w.bytes,
+                          stream_of(p.c)),
+        "sai_compact_pages");
+  return results(out.t, out_refs, moves);
+}
+
 // Runs one of the above; C++ exceptions become Python errors.
 template <PyObject* (*F)(PyObject* const*), int N>
 PyObject* guarded(PyObject*, PyObject* const* args, Py_ssize_t n) {
@@ -313,6 +439,12 @@ PyMethodDef methods[] = {
     {"paged_attention", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(&guarded<paged_attention, 15>)), METH_FASTCALL,
      nullptr},
     {"sparse_attention", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(&guarded<sparse_attention, 9>)), METH_FASTCALL,
+     nullptr},
+    {"copy_pages", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(&guarded<copy_pages, 7>)), METH_FASTCALL, nullptr},
+    {"fork_pages", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(&guarded<fork_pages, 8>)), METH_FASTCALL, nullptr},
+    {"resize_pages", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(&guarded<resize_pages, 13>)), METH_FASTCALL,
+     nullptr},
+    {"compact_pages", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(&guarded<compact_pages, 12>)), METH_FASTCALL,
      nullptr},
     {nullptr, nullptr, 0, nullptr}};
 

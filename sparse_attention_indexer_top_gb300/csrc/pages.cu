@@ -1,0 +1,509 @@
+// Pages of a pool: copies, forks, growing and ending requests, compacting.
+//
+// All of it is moving bytes: a copied page is read and written once, tables and
+// counts likewise, and what is decided in between is small. So the copies are
+// one kernel over 16-byte units, spread over all SMs whatever the number of
+// pages, and the decisions are prefix sums over the pool's counts (which pages
+// are free) and over the requests (how many each wants), which make the answer
+// independent of the order in which CTAs run. A call is a chain of two or three
+// kernels; each is launched while the one before ends, and waits for it.
+#include "sai_internal.h"
+#include "sai_ptx.cuh"
+
+#include <algorithm>
+#include <climits>
+
+namespace sai {
+namespace {
+
+// ------------------------------------------------------------------ copies
+constexpr int kCopyThreads = 256;
+constexpr int kCopyUnits = 4;  // of a thread, in flight at once
+constexpr uint32_t kPiece = kCopyThreads * kCopyUnits;
+
+__device__ __forceinline__ uint32_t divided(uint32_t u, uint32_t m, uint32_t sh) {
+  return static_cast<uint32_t>((static_cast<unsigned long long>(u) * m) >> (24 + sh));
+}
+
+template <typename V>
+__device__ __forceinline__ void copy_piece(const PageArray& a, long long src, long long dst, uint32_t u0, uint32_t cells) {
+  V x[kCopyUnits];
+  long long at[kCopyUnits];
+#pragma unroll
+  for (int i = 0; i < kCopyUnits; ++i) {
+    const uint32_t u = u0 + i * kCopyThreads + threadIdx.x;
+    const uint32_t row = divided(u, a.m_row, a.sh_row), o = u - row * a.row_units;
+    const uint32_t outer = divided(row, a.m_inner, a.sh_inner), inner = row - outer * a.inner;
+    const bool in = a.cells < 0 || (a.cells == 0 ? outer < cells : a.cells == 1 ? inner < cells : o < cells * a.cell_units);
+    at[i] = u < a.units && in ? outer * a.s0 + inner * a.s1 + static_cast<long long>(o) * sizeof(V) : -1;
+    if (at[i] >= 0) x[i] = *reinterpret_cast<const V*>(a.base + src * a.page_stride + at[i]);
+  }
+#pragma unroll
+  for (int i = 0; i < kCopyUnits; ++i)
+    if (at[i] >= 0) *reinterpret_cast<V*>(a.base + dst * a.page_stride + at[i]) = x[i];
+}
+
+__global__ void __launch_bounds__(kCopyThreads) page_copy_kernel(const __grid_constant__ PageCopy c) {
+  pdl_wait();
+  const long long pairs = c.count ? *c.count : c.pairs;
+  const uint32_t pieces = c.first[c.arrays];
+  const uint32_t step_pair = gridDim.x / pieces, step_piece = gridDim.x % pieces;
+  long long pair = blockIdx.x / pieces;
+  uint32_t piece = blockIdx.x % pieces;
+  while (pair < pairs) {
+    const int src = c.src[pair], dst = c.dst[pair];
+    if (src >= 0 && dst >= 0 && src != dst) {
+      if (src < c.num_blocks && dst < c.num_blocks) {
+        int lo = 0, hi = c.arrays - 1;  // the array with first[i] <= piece < first[i + 1]
+        while (lo < hi) {
+          const int mid = (lo + hi + 1) >> 1;
+          if (c.first[mid] <= piece)
+            lo = mid;
+          else
+            hi = mid - 1;
+        }
+        const uint32_t u0 = (piece - c.first[lo]) * kPiece;
+        const uint32_t cells = c.cells ? static_cast<uint32_t>(c.cells[pair]) : 1u << 16;
+        if (c.a[lo].wide)
+          copy_piece<uint4>(c.a[lo], src, dst, u0, cells);
+        else
+          copy_piece<uint32_t>(c.a[lo], src, dst, u0, cells);
+      } else if (piece == 0 && threadIdx.x == 0) {
+        atomicOr(c.status, kDevBadPage);
+      }
+    }
+    pair += step_pair;
+    piece += step_piece;
+    if (piece >= pieces) {
+      piece -= pieces;
+      ++pair;
+    }
+  }
+}
+
+// ------------------------------------------------------- sums over a CTA
+// Exclusive prefix sum of x over the CTA and the total; every thread calls it.
+template <int THREADS, typename T>
+__device__ __forceinline__ T block_scan(T x, T* total) {
+  __shared__ T sums[THREADS / 32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  T y = x;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const T z = __shfl_up_sync(0xffffffffu, y, o);
+    if (lane >= o) y += z;
+  }
+  if (lane == 31) sums[warp] = y;
+  __syncthreads();
+  T before = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < THREADS / 32; ++w) {
+    before += w < warp ? sums[w] : 0;
+    all += sums[w];
+  }
+  __syncthreads();  // sums may be written again
+  *total = all;
+  return before + y - x;
+}
+
+__device__ __forceinline__ long long pages_of(int len, int bs) { return (static_cast<long long>(len) + bs - 1) / bs; }
+__device__ __forceinline__ bool good_len(int len, const PageTable& t) {
+  return len >= 0 && len <= t.width * t.block_size;
+}
+
+// ------------------------------------------------------------ free pages
+constexpr int kScanThreads = 512;
+constexpr int kScanPages = 16;  // of a thread
+constexpr long long kChunk = kScanThreads * kScanPages;
+constexpr int kMostChunks = 512;
+
+// One chunk: the free pages' list and number, the held pages' bits, a copy of
+// the counts.
+__device__ __forceinline__ void scan_chunk(const PoolScan& s, int chunk) {
+  const long long c0 = chunk * s.chunk;
+  int found = 0;
+  for (long long base = c0; base < min(c0 + s.chunk, s.num_blocks); base += kChunk) {
+    const long long p0 = base + threadIdx.x * kScanPages;
+    int r[kScanPages];
+    uint32_t free = 0;
+    const bool whole = p0 + kScanPages <= s.num_blocks;
+    if (whole && (reinterpret_cast<uintptr_t>(s.refs) & 15) == 0) {
+#pragma unroll
+      for (int i = 0; i < kScanPages / 4; ++i)
+        *reinterpret_cast<int4*>(r + 4 * i) = *reinterpret_cast<const int4*>(s.refs + p0 + 4 * i);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kScanPages; ++i) r[i] = p0 + i < s.num_blocks ? s.refs[p0 + i] : 1;
+    }
+#pragma unroll
+    for (int i = 0; i < kScanPages; ++i) free |= (r[i] <= 0 ? 1u : 0u) << i;
+    if (s.out_refs != s.refs) {
+      if (whole && (reinterpret_cast<uintptr_t>(s.out_refs) & 15) == 0) {
+#pragma unroll
+        for (int i = 0; i < kScanPages / 4; ++i)
+          *reinterpret_cast<int4*>(s.out_refs + p0 + 4 * i) = *reinterpret_cast<const int4*>(r + 4 * i);
+      } else {
+#pragma unroll
+        for (int i = 0; i < kScanPages; ++i)
+          if (p0 + i < s.num_blocks) s.out_refs[p0 + i] = r[i];
+      }
+    }
+    if (s.held) {
+      // pages past the end count as held in `free`, but have no bit
+      const long long left = s.num_blocks - p0;
+      const uint32_t here = left >= kScanPages ? 0xffffu : left <= 0 ? 0u : (1u << left) - 1u;
+      const uint32_t mine = ~free & here, other = __shfl_down_sync(0xffffffffu, mine, 1);
+      if ((threadIdx.x & 1) == 0 && left > 0) s.held[p0 / 32] = mine | other << 16;
+    }
+    int total;
+    int at = found + block_scan<kScanThreads>(__popc(free), &total);
+    while (free) {
+      s.free_list[c0 + at++] = static_cast<int>(p0) + __ffs(free) - 1;
+      free &= free - 1;
+    }
+    found += total;
+  }
+  if (threadIdx.x == 0) s.counts[chunk] = found;
+}
+
+// Free pages before each chunk, in shared memory, and their number.
+template <int THREADS>
+__device__ __forceinline__ int free_before(const PoolScan& s, int (&before)[kMostChunks]) {
+  int sum = 0;
+  for (int c0 = 0; c0 < s.chunks; c0 += THREADS) {
+    const int c = c0 + threadIdx.x;
+    int total;
+    const int x = block_scan<THREADS>(c < s.chunks ? s.counts[c] : 0, &total);
+    if (c < s.chunks) before[c] = sum + x;
+    sum += total;
+  }
+  __syncthreads();
+  return sum;
+}
+// The k-th free page.
+__device__ __forceinline__ int free_page(const PoolScan& s, const int (&before)[kMostChunks], int k) {
+  int lo = 0, hi = s.chunks - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (before[mid] <= k)
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  return s.free_list[lo * s.chunk + k - before[lo]];
+}
+
+// ------------------------------------------------------------------ forks
+constexpr int kForkThreads = 128;
+
+// Children's rows and lengths, and the counts before the change.
+__global__ void __launch_bounds__(kForkThreads) fork_rows_kernel(const ForkLaunch p) {
+  if (p.out_refs != p.refs)
+    for (long long i = blockIdx.x * static_cast<long long>(kForkThreads) + threadIdx.x; i < p.num_blocks;
+         i += static_cast<long long>(gridDim.x) * kForkThreads)
+      p.out_refs[i] = p.refs[i];
+  pdl_trigger();
+  for (long long i = blockIdx.x; i < p.children; i += gridDim.x) {
+    long long r = p.parents[i];
+    const bool bad = r < -1 || r >= p.t.requests;
+    const int len = bad || r < 0 ? 0 : p.t.lens[r];
+    if (bad && threadIdx.x == 0) atomicOr(p.status, kDevBadRowMeta);
+    if (bad || !good_len(len, p.t)) r = -1;
+    for (long long c = threadIdx.x; c < p.t.width; c += kForkThreads)
+      p.t.out[i * p.t.out_stride + c] = r < 0 ? -1 : p.t.table[r * p.t.stride + c];
+    if (threadIdx.x == 0) p.out_lens[i] = r < 0 ? 0 : len;
+  }
+}
+
+// Each old request's pages are held once for each child.
+__global__ void __launch_bounds__(kForkThreads) fork_refs_kernel(const ForkLaunch p) {
+  pdl_wait();
+  for (long long r = blockIdx.x; r < p.t.requests; r += gridDim.x) {
+    const int len = p.t.lens[r];
+    if (!good_len(len, p.t)) {
+      if (threadIdx.x == 0) atomicOr(p.status, kDevBadRowMeta);
+      continue;
+    }
+    int mine = 0, children;
+    for (long long i = threadIdx.x; i < p.children; i += kForkThreads) mine += p.parents[i] == r;
+    block_scan<kForkThreads>(mine, &children);
+    const int pages = static_cast<int>(pages_of(len, p.t.block_size));
+    bool bad = false;
+    for (int c = threadIdx.x; c < pages; c += kForkThreads) {
+      const int page = p.t.table[r * p.t.stride + c];
+      if (page < 0 || page >= p.num_blocks)
+        bad = true;
+      else if (children != 1)
+        atomicAdd(p.out_refs + page, children - 1);
+    }
+    if (bad) atomicOr(p.status, kDevBadPage);
+  }
+}
+
+// ------------------------------------------------- growing and shrinking
+enum : int { kGood = 1, kCopies = 2, kKeeps = 4 };
+
+// What each request wants, and which free pages (by number) are for it. One CTA.
+__device__ __forceinline__ void plan_requests(const ResizeLaunch& p) {
+  const PageTable& t = p.t;
+  constexpr int kTile = 2048;
+  __shared__ int others[kTile];
+  if (threadIdx.x == 0) *p.count = 0;
+  int any = 0;
+  for (long long r0 = 0; r0 < t.requests; r0 += kScanThreads) {
+    const long long r = r0 + threadIdx.x;
+    int shared = -1;
+    if (r < t.requests) {
+      const int len = t.lens[r], want = p.new_lens[r];
+      int state = 0, need = 0, last = -1;
+      if (!good_len(len, t) || !good_len(want, t)) {
+        atomicOr(p.status, kDevBadRowMeta);
+      } else {
+        state = kGood;
+        need = static_cast<int>(max(0LL, pages_of(want, t.block_size) - pages_of(len, t.block_size)));
+        if (want > len && len % t.block_size) {
+          last = t.table[r * t.stride + len / t.block_size];
+          if (last < 0 || last >= p.s.num_blocks) {
+            atomicOr(p.status, kDevBadPage);
+            state = need = 0;
+          } else if (p.s.refs[last] > 1) {
+            state |= kCopies;
+            shared = last;
+          }
+        }
+      }
+      p.plan[r] = make_int4(0, need, state, last);
+      p.last_shared[r] = shared;
+    }
+    any |= __syncthreads_or(shared >= 0);
+  }
+  long long upto = 0;
+  for (long long r0 = 0; r0 < t.requests; r0 += kScanThreads) {
+    const long long r = r0 + threadIdx.x;
+    int4 x = r < t.requests ? p.plan[r] : make_int4(0, 0, 0, 0);
+    if (any) {
+      const int mine = r < t.requests ? p.last_shared[r] : -1;
+      int same = 0;
+      bool later = false;
+      for (long long k0 = 0; k0 < t.requests; k0 += kTile) {
+        const int n = static_cast<int>(min(static_cast<long long>(kTile), t.requests - k0));
+        __syncthreads();
+        for (int k = threadIdx.x; k < n; k += kScanThreads) others[k] = p.last_shared[k0 + k];
+        __syncthreads();
+        if (mine >= 0)
+          for (int k = 0; k < n; ++k)
+            if (others[k] == mine) {
+              ++same;
+              later = later || k0 + k > r;
+            }
+      }
+      if (mine >= 0) {
+        // the last of all its holders keeps the page: those before it leave it, or it is not served either
+        if (!later && same == p.s.refs[mine])
+          x.z = (x.z & ~kCopies) | kKeeps;
+        else
+          ++x.y;
+      }
+    }
+    long long total;
+    const long long before = block_scan<kScanThreads>(static_cast<long long>(x.y), &total);
+    x.x = static_cast<int>(min(upto + before, 1LL << 30));  // past every pool's end
+    if (r < t.requests) p.plan[r] = x;
+    upto += total;
+  }
+}
+
+__global__ void __launch_bounds__(kScanThreads) resize_plan_kernel(const ResizeLaunch p) {
+  pdl_trigger();
+  if (blockIdx.x == 0)
+    plan_requests(p);
+  else
+    scan_chunk(p.s, blockIdx.x - 1);
+}
+
+constexpr int kApplyThreads = 128;
+
+__global__ void __launch_bounds__(kApplyThreads) resize_apply_kernel(const ResizeLaunch p) {
+  __shared__ int before[kMostChunks];
+  const PageTable& t = p.t;
+  pdl_wait();
+  pdl_trigger();
+  const int free = free_before<kApplyThreads>(p.s, before);
+  for (long long r = blockIdx.x; r < t.requests; r += gridDim.x) {
+    const int4 x = p.plan[r];
+    const int len = t.lens[r], want = p.new_lens[r], bs = t.block_size;
+    const bool wants = x.y > 0 || (x.z & kKeeps);
+    const bool served = (x.z & kGood) && (!wants || static_cast<long long>(x.x) + x.y <= free);
+    const int have = static_cast<int>(pages_of(len, bs)), to = static_cast<int>(pages_of(want, bs));
+    const int copies = (x.z & kCopies) ? 1 : 0;
+    bool bad = false;
+    for (long long c = threadIdx.x; c < t.width; c += kApplyThreads) {
+      const int old = t.table[r * t.stride + c];
+      int page = old;
+      if (served) {
+        if (copies && c == have - 1) {
+          page = free_page(p.s, before, x.x);
+          const int k = atomicAdd(p.count, 1);
+          p.src[k] = old;
+          p.dst[k] = page;
+          p.cells[k] = len % bs;
+          atomicAdd(p.s.out_refs + old, -1);
+        } else if (c >= have && c < to) {
+          page = free_page(p.s, before, x.x + copies + static_cast<int>(c) - have);
+        } else if (c >= to && c < have) {
+          page = -1;
+          if (old < 0 || old >= p.s.num_blocks)
+            bad = true;
+          else
+            atomicAdd(p.s.out_refs + old, -1);
+        }
+        if (page != old && page >= 0) p.s.out_refs[page] = 1;
+      }
+      if (page != old || t.out != t.table) t.out[r * t.out_stride + c] = page;
+    }
+    if (bad) atomicOr(p.status, kDevBadPage);
+    __syncthreads();  // out_lens may be the lengths that the other threads read
+    if (threadIdx.x == 0) {
+      p.out_lens[r] = served ? want : len;
+      if ((x.z & kGood) && !served) atomicOr(p.status, kDevNoPages);
+    }
+  }
+}
+
+// ------------------------------------------------------------- compacting
+__global__ void __launch_bounds__(kScanThreads) compact_scan_kernel(const PoolScan s) {
+  pdl_trigger();
+  scan_chunk(s, blockIdx.x);
+}
+
+// Every held page's new id; the counts move, and the copies are written down.
+__global__ void __launch_bounds__(kScanThreads) compact_moves_kernel(const CompactLaunch p) {
+  __shared__ int before[kMostChunks];
+  __shared__ int below;
+  const PoolScan& s = p.s;
+  pdl_wait();
+  pdl_trigger();
+  const int free = free_before<kScanThreads>(s, before);
+  const int held = static_cast<int>(s.num_blocks) - free;
+  if (threadIdx.x == 0) below = 0;
+  __syncthreads();
+  // free pages below `held` = pages that move
+  const int last = held == s.num_blocks ? -1 : static_cast<int>(held / s.chunk);
+  if (last >= 0) {
+    int n = 0;
+    for (long long w = last * s.chunk / 32 + threadIdx.x; w * 32 < held; w += kScanThreads) {
+      const long long here = held - w * 32;
+      n += __popc(~s.held[w] & (here >= 32 ? ~0u : (1u << here) - 1u));
+    }
+    n = __reduce_add_sync(0xffffffffu, n);
+    if ((threadIdx.x & 31) == 0 && n) atomicAdd(&below, n);
+  }
+  __syncthreads();
+  const int moving = last < 0 ? 0 : before[last] + below;
+  if (blockIdx.x == 0 && threadIdx.x == 0) *p.count = moving;
+  const long long c0 = blockIdx.x * s.chunk;
+  int rank = static_cast<int>(c0) - before[blockIdx.x];  // held pages before the chunk
+  for (long long base = c0; base < min(c0 + s.chunk, s.num_blocks); base += kChunk) {
+    const long long p0 = base + threadIdx.x * kScanPages;
+    const uint32_t bits = p0 < s.num_blocks ? (s.held[p0 / 32] >> (p0 & 16)) & 0xffffu : 0u;
+    int total;
+    int at = rank + block_scan<kScanThreads>(__popc(bits), &total);
+    for (int i = 0; i < kScanPages && p0 + i < s.num_blocks; ++i) {
+      const int page = static_cast<int>(p0) + i;
+      int to = -1;
+      if ((bits >> i) & 1) {
+        to = page;
+        if (page >= held) {
+          const int j = at - (held - moving);  // number among the pages that move
+          to = free_page(s, before, j);
+          p.src[j] = page;
+          p.dst[j] = to;
+          s.out_refs[to] = s.refs[page];
+          s.out_refs[page] = 0;
+        }
+        ++at;
+      }
+      p.moves[page] = to;
+    }
+    rank += total;
+  }
+}
+
+__global__ void __launch_bounds__(kForkThreads) compact_rename_kernel(const CompactLaunch p) {
+  const PageTable& t = p.t;
+  pdl_wait();
+  pdl_trigger();
+  for (long long r = blockIdx.x; r < t.requests; r += gridDim.x) {
+    const int len = t.lens[r];
+    const bool good = good_len(len, t);
+    if (!good && threadIdx.x == 0) atomicOr(p.status, kDevBadRowMeta);
+    const long long pages = good ? pages_of(len, t.block_size) : 0;
+    bool bad = false;
+    for (long long c = threadIdx.x; c < t.width; c += kForkThreads) {
+      const int old = t.table[r * t.stride + c];
+      int page = old;
+      if (c < pages) {
+        if (old >= 0 && old < p.s.num_blocks)
+          page = p.moves[old];
+        else
+          bad = true;
+        bad = bad || page < 0;
+      }
+      if (page != old || t.out != t.table) t.out[r * t.out_stride + c] = page;
+    }
+    if (bad) atomicOr(p.status, kDevBadPage);
+  }
+}
+
+template <typename... P>
+cudaError_t launch(void (*kernel)(P...), long long grid, int threads, bool dependent, cudaStream_t stream, const P&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(threads);
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = dependent ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+}  // namespace
+
+void pool_chunks(long long num_blocks, PoolScan* s) {
+  s->num_blocks = num_blocks;
+  s->chunk = kChunk;
+  while ((num_blocks + s->chunk - 1) / s->chunk > kMostChunks) s->chunk *= 2;
+  s->chunks = static_cast<int>((num_blocks + s->chunk - 1) / s->chunk);
+}
+
+cudaError_t launch_page_copy(const PageCopy& c, bool dependent, int num_sms, cudaStream_t stream) {
+  const long long grid = std::min<long long>(8LL * num_sms, c.pairs * c.first[c.arrays]);
+  return launch(page_copy_kernel, grid, kCopyThreads, dependent, stream, c);
+}
+
+cudaError_t launch_fork(const ForkLaunch& p, int num_sms, cudaStream_t stream) {
+  const long long most = 16LL * num_sms;
+  const long long copies = p.out_refs == p.refs ? 0 : (p.num_blocks + 4 * kForkThreads - 1) / (4 * kForkThreads);
+  const long long first = std::min(most, std::max(p.children, copies));
+  cudaError_t e = cudaSuccess;
+  if (first) e = launch(fork_rows_kernel, first, kForkThreads, false, stream, p);
+  if (e != cudaSuccess || p.t.requests == 0) return e;
+  return launch(fork_refs_kernel, std::min(most, p.t.requests), kForkThreads, first > 0, stream, p);
+}
+
+cudaError_t launch_resize(const ResizeLaunch& p, cudaStream_t stream) {
+  cudaError_t e = launch(resize_plan_kernel, 1 + p.s.chunks, kScanThreads, false, stream, p);
+  if (e != cudaSuccess || p.t.requests == 0) return e;
+  return launch(resize_apply_kernel, std::min(p.t.requests, 1LL << 16), kApplyThreads, true, stream, p);
+}
+
+cudaError_t launch_compact(const CompactLaunch& p, int num_sms, cudaStream_t stream) {
+  cudaError_t e = launch(compact_scan_kernel, p.s.chunks, kScanThreads, false, stream, p.s);
+  if (e == cudaSuccess) e = launch(compact_moves_kernel, p.s.chunks, kScanThreads, true, stream, p);
+  if (e != cudaSuccess || p.t.requests == 0) return e;
+  return launch(compact_rename_kernel, std::min(p.t.requests, 16LL * num_sms), kForkThreads, true, stream, p);
+}
+
+}  // namespace sai

@@ -12,6 +12,7 @@ enum DevStatusBits : int {
   kDevBadRowMeta = 1,      // a row's seq_len / row_start / row_to_batch was out of range
   kDevWaitTimeout = 2,     // a pipeline wait gave up (the affected rows are undefined)
   kDevBadPage = 4,         // a block-table entry was out of range (fused path)
+  kDevNoPages = 8,         // a request got no pages (resize_pages)
 };
 
 struct TopkLaunch {
@@ -199,5 +200,89 @@ bool attn_tiles_pay(long long rows, int q_heads, int heads, int dim, bool f8, lo
 size_t attn_tiles_workspace(long long rows, int q_heads, int heads, int dim, long long max_keys, int num_sms);
 cudaError_t launch_attn_tiles(const AttnLaunch& p, long long max_keys, void* workspace, int num_sms,
                               cudaStream_t stream);
+
+// ------------------------------------------------- pages of a pool
+// One array of the pool, axes joined where they are contiguous: a page is rows
+// of `row_units` units (16 or 4 bytes) in an outer and an inner (`inner`) axis.
+struct PageArray {
+  char* base;
+  long long page_stride, s0, s1;  // bytes between pages, outer rows, inner rows
+  uint32_t units;                 // of a page
+  uint32_t row_units, inner;
+  uint32_t m_row, m_inner;        // division by them: (u * m) >> (24 + sh), for u < 2^24
+  uint8_t sh_row, sh_inner;
+  uint8_t wide;                   // unit of 16 bytes (else 4)
+  int8_t cells;                   // the page's tokens are 0: outer, 1: inner rows, 2: cell_units of the row, -1: copied whole
+  uint32_t cell_units;
+};
+constexpr int kPageArrays = 32;  // of one launch
+struct PageCopy {
+  PageArray a[kPageArrays];
+  uint32_t first[kPageArrays + 1];  // pieces of a page before array i
+  int arrays;
+  const int* src;
+  const int* dst;
+  const int* cells;     // tokens of each pair, or null: whole pages
+  const int* count;     // number of pairs on the device, or null: `pairs`
+  long long pairs;
+  long long num_blocks;
+  int* status;
+};
+struct PageTable {
+  const int* table;
+  long long requests, width, stride;
+  const int* lens;
+  int* out;
+  long long out_stride;
+  int block_size;
+};
+// Free pages of the pool, chunk by chunk of `chunk` pages.
+struct PoolScan {
+  const int* refs;
+  int* out_refs;
+  long long num_blocks, chunk;
+  int chunks;
+  int* counts;       // [chunks] free pages of each
+  int* free_list;    // [num_blocks]: chunk c's from c * chunk on
+  uint32_t* held;    // a bit a page: refs above 0 (compact)
+};
+struct ForkLaunch {
+  PageTable t;
+  const int* refs;
+  int* out_refs;
+  long long num_blocks;
+  const int* parents;
+  long long children;
+  int* out_lens;
+  int* status;
+};
+struct ResizeLaunch {
+  PageTable t;
+  PoolScan s;
+  const int* new_lens;
+  int* out_lens;
+  int4* plan;        // [requests]: first of its free pages, their number, state, last page
+  int* last_shared;  // [requests]
+  int* src;          // copies: [requests]
+  int* dst;
+  int* cells;
+  int* count;
+  int* status;
+};
+struct CompactLaunch {
+  PageTable t;
+  PoolScan s;
+  int* moves;
+  int* src;  // [num_blocks / 2]
+  int* dst;
+  int* count;
+  int* status;
+};
+void pool_chunks(long long num_blocks, PoolScan* s);  // fills num_blocks, chunk, chunks
+cudaError_t launch_page_copy(const PageCopy& c, bool dependent, int num_sms, cudaStream_t stream);
+cudaError_t launch_fork(const ForkLaunch& p, int num_sms, cudaStream_t stream);
+cudaError_t launch_resize(const ResizeLaunch& p, cudaStream_t stream);
+// moves and renames; the pages are copied by launch_page_copy
+cudaError_t launch_compact(const CompactLaunch& p, int num_sms, cudaStream_t stream);
 
 }  // namespace sai
