@@ -496,6 +496,47 @@ int sai_sparse_attention(const uint16_t* q, int64_t q_row_stride, int32_t q_head
                          sai_stream_t stream);
 
 /*
+ * sai_paged_attention_mod, sai_sparse_attention_mod -- the same attentions with
+ * scores changed before the softmax, and masks by document and by prefix.
+ *
+ * With x = sm_scale * q[i, a].k_t, n = seq_lens[i]:
+ *   softcap > 0:   x becomes softcap * tanh(x / softcap)
+ *   slopes:        then x becomes x - slopes[a] * |n - 1 - t|
+ *   row_starts:    row i sees no key t < row_starts[i] (its document's first
+ *                  token); its `sinks` are the first tokens from there on
+ *   prefix_lens:   row i also sees the keys t < prefix_lens[i] at and behind its
+ *                  own position (not before its start or its window)
+ * so that row i, n > 0, with b = row_starts[i] and e = max(n, prefix_lens[i]),
+ * sees b <= t < e with (window = 0, or t >= n - window, or t < b + sinks); a
+ * start at or past e leaves it none. tanh is computed to fp32 (a few 2^-24), and
+ * the changed scores are fp32.
+ *
+ * softcap      0: none; else in [1e-30, 1e30].
+ * slopes       fp32 [q_heads] or NULL; row_starts, prefix_lens int32 [rows] or
+ *              NULL. A start or prefix outside [0, max_seq_len] makes a bad row,
+ *              as does a prefix past the table's columns.
+ * sai_sparse_attention_mod takes softcap alone (SAI_ERR_UNSUPPORTED otherwise:
+ * slots have no positions). mod = NULL or all unset: the plain call. Workspaces
+ * are those of the plain calls.
+ */
+typedef struct {
+  float softcap;
+  const float* slopes;
+  const int32_t* row_starts;
+  const int32_t* prefix_lens;
+} sai_score_mod;
+
+int sai_paged_attention_mod(const uint16_t* q, int64_t q_row_stride, int32_t q_heads, const sai_kv_cache* cache,
+                            const int32_t* block_table, int64_t bt_rows, int64_t bt_stride, const int32_t* row_to_batch,
+                            const int32_t* seq_lens, int64_t rows, int32_t max_seq_len, int32_t window, int32_t sinks,
+                            float sm_scale, int32_t packed, const sai_score_mod* mod, uint16_t* out, float* out_lse,
+                            void* workspace, size_t workspace_bytes, sai_stream_t stream);
+int sai_sparse_attention_mod(const uint16_t* q, int64_t q_row_stride, int32_t q_heads, const sai_kv_cache* cache,
+                             const int32_t* slots, int64_t slots_stride, int32_t k, int64_t rows, float sm_scale,
+                             const sai_score_mod* mod, uint16_t* out, float* out_lse, void* workspace,
+                             size_t workspace_bytes, sai_stream_t stream);
+
+/*
  * Pages of the caches: copying, forking, growing and ending requests, compacting.
  *
  * A pool of num_blocks pages (the blocks of the caches) is shared by all layers:

@@ -93,3 +93,33 @@ def attend(q: np.ndarray, k: np.ndarray, v: np.ndarray, sm_scale: float):
         mag[a] = w @ np.abs(v[:, a // group]) / total
         lse[a] = m + np.log(total)
     return out, lse, mag
+
+
+def span(n: int, window: int = 0, sinks: int = 0, start: int = 0, prefix: int = 0) -> np.ndarray:
+    """Positions that a row of length n sees from its document's start, with a prefix that it sees past its own."""
+    if n == 0:
+        return np.arange(0)
+    t = np.arange(start, max(n, prefix, start))
+    return t[(t >= n - window) | (t < start + sinks)] if window else t
+
+
+def attend_changed(q, k, v, sm_scale, softcap=0.0, slopes=None, dist=None):
+    """``attend`` with scores capped by tanh and lowered by slopes [q_heads] times dist [n]."""
+    hq, dim = q.shape
+    out, lse, mag = np.zeros((hq, dim)), np.full(hq, -np.inf), np.zeros((hq, dim))
+    if len(k) == 0:
+        return out, lse, mag
+    group = hq // k.shape[1]
+    for a in range(hq):
+        s = k[:, a // group] @ q[a] * sm_scale
+        if softcap:
+            s = softcap * np.tanh(s / softcap)
+        if slopes is not None:
+            s = s - float(slopes[a]) * dist
+        m = s.max()
+        w = np.exp(s - m)
+        total = w.sum()
+        out[a] = w @ v[:, a // group] / total
+        mag[a] = w @ np.abs(v[:, a // group]) / total
+        lse[a] = m + np.log(total)
+    return out, lse, mag

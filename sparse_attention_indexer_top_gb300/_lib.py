@@ -25,6 +25,12 @@ class KVCacheDesc(ctypes.Structure):
                 ("dim", _c_i32), ("dtype", _c_i32)]
 
 
+class ScoreMod(ctypes.Structure):
+    """sai_score_mod of include/sai.h."""
+
+    _fields_ = [("softcap", _f32), ("slopes", _vp), ("row_starts", _vp), ("prefix_lens", _vp)]
+
+
 class PageArrayDesc(ctypes.Structure):
     """sai_page_array of include/sai.h."""
 
@@ -75,6 +81,10 @@ SIGNATURES = {
     "sai_sparse_attention_workspace": (_c_size, [_c_i64, _c_i32, _c_i32, _c_i32, _c_i32, _c_i32]),
     "sai_sparse_attention": (ctypes.c_int, [_vp, _c_i64, _c_i32, _vp, _vp, _c_i64, _c_i32, _c_i64, _f32, _vp, _vp,
                                             _vp, _c_size, _vp]),
+    "sai_paged_attention_mod": (ctypes.c_int, [_vp, _c_i64, _c_i32, _vp, _vp, _c_i64, _c_i64, _vp, _vp, _c_i64, _c_i32,
+                                               _c_i32, _c_i32, _f32, _c_i32, _vp, _vp, _vp, _vp, _c_size, _vp]),
+    "sai_sparse_attention_mod": (ctypes.c_int, [_vp, _c_i64, _c_i32, _vp, _vp, _c_i64, _c_i32, _c_i64, _f32, _vp, _vp,
+                                                _vp, _vp, _c_size, _vp]),
     "sai_cache_page_arrays": (ctypes.c_int, [_vp, _vp]),
     "sai_copy_pages": (ctypes.c_int, [_vp, _c_i32, _c_i64, _vp, _vp, _c_i64, _vp]),
     "sai_fork_pages": (ctypes.c_int, [_vp, _c_i64, _c_i64, _c_i64, _vp, _c_i32, _vp, _c_i64, _vp, _c_i64, _vp, _c_i64,

@@ -113,7 +113,9 @@ def paged_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, 
                     max_seq_len: int, row_to_batch: Optional[torch.Tensor] = None, packed: int = False,
                     window: int = 0, sinks: int = 0, sm_scale: Optional[float] = None,
                     out: Optional[torch.Tensor] = None, want_lse: bool = False,
-                    out_lse: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None, stream=None):
+                    out_lse: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                    softcap: float = 0.0, slopes: Optional[torch.Tensor] = None,
+                    row_starts: Optional[torch.Tensor] = None, prefix_lens: Optional[torch.Tensor] = None, stream=None):
     """Attention of each row over the first ``seq_lens[i]`` keys of its request.
 
     ``q`` is bf16 ``[rows, q_heads, dim]`` (any row stride; ``q_heads`` a
@@ -124,19 +126,30 @@ def paged_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, 
     defaults to ``dim ** -0.5``. Returns ``out`` (bf16, like ``q``), or ``(out,
     lse)`` with ``want_lse`` or ``out_lse`` (fp32 ``[rows, q_heads]``). A row
     that sees no key gives zeros and -inf.
+
+    Scores ``x`` may be changed before the softmax: ``softcap`` above 0 makes
+    them ``softcap * tanh(x / softcap)``, then ``slopes`` (fp32 ``[q_heads]``)
+    takes ``slopes[a] * |seq_lens[i] - 1 - t|`` off key ``t``'s.
+    ``row_starts`` (int32 ``[rows]``) hides the keys before a row's document, whose
+    first tokens ``sinks`` then means; ``prefix_lens`` (int32 ``[rows]``) shows a
+    row the keys ``t < prefix_lens[i]`` past its own position too (a prefix that
+    all its tokens see). Starts and prefixes lie in ``[0, max_seq_len]``.
     """
     if stream is not None:
         with _on(stream, cache.device):
             return paged_attention(q, cache, block_table, seq_lens, max_seq_len=max_seq_len, row_to_batch=row_to_batch,
                                    packed=packed, window=window, sinks=sinks, sm_scale=sm_scale, out=out,
-                                   want_lse=want_lse, out_lse=out_lse, workspace=workspace)
+                                   want_lse=want_lse, out_lse=out_lse, workspace=workspace, softcap=softcap,
+                                   slopes=slopes, row_starts=row_starts, prefix_lens=prefix_lens)
     return binding().paged_attention(cache._ref, cache._index, q, block_table, seq_lens, max_seq_len, row_to_batch,
-                                     packed, window, sinks, sm_scale, out, want_lse, out_lse, workspace)
+                                     packed, window, sinks, sm_scale, out, want_lse, out_lse, workspace, softcap, slopes,
+                                     row_starts, prefix_lens)
 
 
 def sparse_attention(q: torch.Tensor, cache: KVCache, slots: torch.Tensor, *, sm_scale: Optional[float] = None,
                      out: Optional[torch.Tensor] = None, want_lse: bool = False,
-                     out_lse: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None, stream=None):
+                     out_lse: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                     softcap: float = 0.0, stream=None):
     """Attention of each row over the cache cells ``slots[i, j] >= 0`` (int32
     ``[rows, k]``, unit column stride: the slots of ``index_score_topk`` or of
     ``topk_transform`` with the cache's block size). Otherwise as
@@ -144,5 +157,6 @@ def sparse_attention(q: torch.Tensor, cache: KVCache, slots: torch.Tensor, *, sm
     if stream is not None:
         with _on(stream, cache.device):
             return sparse_attention(q, cache, slots, sm_scale=sm_scale, out=out, want_lse=want_lse, out_lse=out_lse,
-                                    workspace=workspace)
-    return binding().sparse_attention(cache._ref, cache._index, q, slots, sm_scale, out, want_lse, out_lse, workspace)
+                                    workspace=workspace, softcap=softcap)
+    return binding().sparse_attention(cache._ref, cache._index, q, slots, sm_scale, out, want_lse, out_lse, workspace,
+                                      softcap)

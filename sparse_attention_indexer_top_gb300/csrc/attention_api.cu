@@ -51,6 +51,22 @@ int check_cache(const sai_kv_cache* c, sai::CacheView* out) {
   return SAI_OK;
 }
 
+// The changes of scores and masks; NULL or nothing set: none.
+int check_mod(const sai_score_mod* mod, bool slots, sai::AttnLaunch* p) {
+  if (!mod) return SAI_OK;
+  if (!std::isfinite(mod->softcap) || mod->softcap < 0.f) return SAI_ERR_SHAPE;
+  // 1 / cap and what is capped stay normal numbers
+  if (mod->softcap != 0.f && (mod->softcap < 1e-30f || mod->softcap > 1e30f)) return SAI_ERR_SHAPE;
+  if (slots && (mod->slopes || mod->row_starts || mod->prefix_lens)) return SAI_ERR_UNSUPPORTED;
+  if (!aligned(mod->slopes, 4) || !aligned(mod->row_starts, 4) || !aligned(mod->prefix_lens, 4)) return SAI_ERR_ALIGN;
+  p->cap_log2 = mod->softcap * 1.44269504088896340736f;
+  p->slopes = mod->slopes;
+  p->row_starts = mod->row_starts;
+  p->prefix_lens = mod->prefix_lens;
+  p->modified = mod->softcap > 0.f || mod->slopes || mod->row_starts || mod->prefix_lens;
+  return SAI_OK;
+}
+
 int check_table(const int32_t* block_table, int64_t bt_rows, int64_t bt_stride, const int32_t* row_to_batch,
                 const int32_t* seq_lens, int64_t rows) {
   if (!block_table || !seq_lens) return SAI_ERR_NULL;
@@ -185,9 +201,20 @@ int sai_paged_attention(const uint16_t* q, int64_t q_row_stride, int32_t q_heads
                         const int32_t* seq_lens, int64_t rows, int32_t max_seq_len, int32_t window, int32_t sinks,
                         float sm_scale, int32_t packed, uint16_t* out, float* out_lse, void* workspace,
                         size_t workspace_bytes, sai_stream_t stream) {
+  return sai_paged_attention_mod(q, q_row_stride, q_heads, cache, block_table, bt_rows, bt_stride, row_to_batch, seq_lens,
+                                 rows, max_seq_len, window, sinks, sm_scale, packed, nullptr, out, out_lse, workspace,
+                                 workspace_bytes, stream);
+}
+
+int sai_paged_attention_mod(const uint16_t* q, int64_t q_row_stride, int32_t q_heads, const sai_kv_cache* cache,
+                            const int32_t* block_table, int64_t bt_rows, int64_t bt_stride, const int32_t* row_to_batch,
+                            const int32_t* seq_lens, int64_t rows, int32_t max_seq_len, int32_t window, int32_t sinks,
+                            float sm_scale, int32_t packed, const sai_score_mod* mod, uint16_t* out, float* out_lse,
+                            void* workspace, size_t workspace_bytes, sai_stream_t stream) {
   sai::AttnLaunch p{};
   int e = check_cache(cache, &p.c);
   if (e != SAI_OK) return e;
+  if ((e = check_mod(mod, false, &p)) != SAI_OK) return e;
   if (rows < 0 || rows > INT_MAX / 16 || max_seq_len < 0 || window < 0 || sinks < 0) return SAI_ERR_SHAPE;
   if ((e = check_attention(q, q_row_stride, q_heads, p.c, rows, sm_scale, out, out_lse)) != SAI_OK) return e;
   if (rows == 0) return SAI_OK;
@@ -234,9 +261,18 @@ int sai_sparse_attention(const uint16_t* q, int64_t q_row_stride, int32_t q_head
                          const int32_t* slots, int64_t slots_stride, int32_t k, int64_t rows, float sm_scale,
                          uint16_t* out, float* out_lse, void* workspace, size_t workspace_bytes,
                          sai_stream_t stream) {
+  return sai_sparse_attention_mod(q, q_row_stride, q_heads, cache, slots, slots_stride, k, rows, sm_scale, nullptr, out,
+                                  out_lse, workspace, workspace_bytes, stream);
+}
+
+int sai_sparse_attention_mod(const uint16_t* q, int64_t q_row_stride, int32_t q_heads, const sai_kv_cache* cache,
+                             const int32_t* slots, int64_t slots_stride, int32_t k, int64_t rows, float sm_scale,
+                             const sai_score_mod* mod, uint16_t* out, float* out_lse, void* workspace,
+                             size_t workspace_bytes, sai_stream_t stream) {
   sai::AttnLaunch p{};
   int e = check_cache(cache, &p.c);
   if (e != SAI_OK) return e;
+  if ((e = check_mod(mod, true, &p)) != SAI_OK) return e;
   if (rows < 0 || rows > INT_MAX / 16 || k < 1 || k > 65536) return SAI_ERR_SHAPE;
   if ((e = check_attention(q, q_row_stride, q_heads, p.c, rows, sm_scale, out, out_lse)) != SAI_OK) return e;
   if (rows == 0) return SAI_OK;

@@ -224,8 +224,15 @@ PyObject* attention_result(const at::Tensor& out, const at::Tensor& lse) {
   return r;
 }
 
+double softcap_of(PyObject* o) {
+  const double s = PyFloat_AsDouble(o);
+  if (s == -1.0 && PyErr_Occurred()) throw Raised{};
+  if (s != 0.0 && !(s >= 1e-30 && s <= 1e30)) refuse("softcap must be 0 (none) or in [1e-30, 1e30]");
+  return s;
+}
+
 // (cache, device, q, block_table, seq_lens, max_seq_len, row_to_batch, packed, window, sinks, sm_scale, out, want_lse,
-//  out_lse, workspace)
+//  out_lse, workspace, softcap, slopes, row_starts, prefix_lens)
 PyObject* paged_attention(PyObject* const* a) {
   const Cache c = cache_of(a[0], a[1]);
   const at::Tensor* qt = tensor(a[2], "q");
@@ -245,14 +252,22 @@ PyObject* paged_attention(PyObject* const* a) {
   const Space w = workspace_of(a[14], a[14] == Py_None ? sai_paged_attention_workspace(rows, q.heads, c.d->heads, c.d->dim,
                                                                                        c.d->dtype, most, window, sinks, packed)
                                                        : 0, c);
-  check(sai_paged_attention(q.p, q.stride, q.heads, c.d, bt.p, bt.rows, bt.stride, r2b, lens, rows, most, window, sinks,
-                            static_cast<float>(scale), packed, static_cast<uint16_t*>(out.data_ptr()),
-                            lse.defined() ? static_cast<float*>(lse.data_ptr()) : nullptr, w.p, w.bytes, stream_of(c)),
+  sai_score_mod mod{static_cast<float>(softcap_of(a[15])), nullptr, nullptr, nullptr};
+  if (a[16] != Py_None) {
+    const at::Tensor& t = need(a[16], "slopes", at::kFloat, 1, c.device);
+    if (t.size(0) != q.heads || !t.is_contiguous()) refuse("slopes must be contiguous [" + std::to_string(q.heads) + "]");
+    mod.slopes = static_cast<const float*>(t.data_ptr());
+  }
+  if (a[17] != Py_None) mod.row_starts = row_index(a[17], "row_starts", rows, c.device);
+  if (a[18] != Py_None) mod.prefix_lens = row_index(a[18], "prefix_lens", rows, c.device);
+  check(sai_paged_attention_mod(q.p, q.stride, q.heads, c.d, bt.p, bt.rows, bt.stride, r2b, lens, rows, most, window, sinks,
+                                static_cast<float>(scale), packed, &mod, static_cast<uint16_t*>(out.data_ptr()),
+                                lse.defined() ? static_cast<float*>(lse.data_ptr()) : nullptr, w.p, w.bytes, stream_of(c)),
         "sai_paged_attention");
   return attention_result(out, lse);
 }
 
-// (cache, device, q, slots, sm_scale, out, want_lse, out_lse, workspace)
+// (cache, device, q, slots, sm_scale, out, want_lse, out_lse, workspace, softcap)
 PyObject* sparse_attention(PyObject* const* a) {
   const Cache c = cache_of(a[0], a[1]);
   const at::Tensor* qt = tensor(a[2], "q");
@@ -271,10 +286,11 @@ PyObject* sparse_attention(PyObject* const* a) {
   const int32_t k32 = static_cast<int32_t>(k);
   const Space w = workspace_of(
       a[8], a[8] == Py_None ? sai_sparse_attention_workspace(rows, q.heads, c.d->heads, c.d->dim, c.d->dtype, k32) : 0, c);
-  check(sai_sparse_attention(q.p, q.stride, q.heads, c.d, static_cast<const int32_t*>(slots.data_ptr()),
-                             rows > 1 ? slots.stride(0) : std::max<int64_t>(k, 1), k32, rows, static_cast<float>(scale),
-                             static_cast<uint16_t*>(out.data_ptr()),
-                             lse.defined() ? static_cast<float*>(lse.data_ptr()) : nullptr, w.p, w.bytes, stream_of(c)),
+  const sai_score_mod mod{static_cast<float>(softcap_of(a[9])), nullptr, nullptr, nullptr};
+  check(sai_sparse_attention_mod(q.p, q.stride, q.heads, c.d, static_cast<const int32_t*>(slots.data_ptr()),
+                                 rows > 1 ? slots.stride(0) : std::max<int64_t>(k, 1), k32, rows, static_cast<float>(scale),
+                                 &mod, static_cast<uint16_t*>(out.data_ptr()),
+                                 lse.defined() ? static_cast<float*>(lse.data_ptr()) : nullptr, w.p, w.bytes, stream_of(c)),
         "sai_sparse_attention");
   return attention_result(out, lse);
 }
@@ -436,9 +452,9 @@ PyObject* guarded(PyObject*, PyObject* const* args, Py_ssize_t n) {
 
 PyMethodDef methods[] = {
     {"append_kv", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(&guarded<append_kv, 11>)), METH_FASTCALL, nullptr},
-    {"paged_attention", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(&guarded<paged_attention, 15>)), METH_FASTCALL,
+    {"paged_attention", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(&guarded<paged_attention, 19>)), METH_FASTCALL,
      nullptr},
-    {"sparse_attention", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(&guarded<sparse_attention, 9>)), METH_FASTCALL,
+    {"sparse_attention", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(&guarded<sparse_attention, 10>)), METH_FASTCALL,
      nullptr},
     {"copy_pages", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(&guarded<copy_pages, 7>)), METH_FASTCALL, nullptr},
     {"fork_pages", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(&guarded<fork_pages, 8>)), METH_FASTCALL, nullptr},

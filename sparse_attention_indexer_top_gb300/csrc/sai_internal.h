@@ -183,6 +183,12 @@ struct AttnLaunch {
   float* part_o;   // row kernel: [rows, q_heads, chunks, dim]; tile kernel: [slots, rows and heads of a unit, dim]
   float2* part_ml; // without dim: running maximum (log2 units) and sum
   int* status;
+  // changed scores and masks (`modified`: any of them)
+  bool modified;
+  float cap_log2;          // softcap * log2(e), 0: none
+  const float* slopes;     // [q_heads] or null
+  const int* row_starts;   // [rows] or null
+  const int* prefix_lens;  // [rows] or null
 };
 // Chunks per row of the row kernel, and its partial results' bytes.
 struct AttnPlan {
@@ -193,6 +199,7 @@ struct AttnPlan {
 };
 AttnPlan attn_rows_plan(long long rows, int q_heads, int heads, int dim, bool f8, long long max_keys, int num_sms);
 cudaError_t launch_attn_rows(const AttnLaunch& p, cudaStream_t stream);
+cudaError_t launch_attn_rows_mod(const AttnLaunch& p, cudaStream_t stream);
 // The tile kernel of packed rows: whether it takes a call, whether it beats the
 // row kernel on these sizes, its workspace, its launch.
 bool attn_tiles_apply(int group, float scale_log2);
@@ -200,6 +207,10 @@ bool attn_tiles_pay(long long rows, int q_heads, int heads, int dim, bool f8, lo
 size_t attn_tiles_workspace(long long rows, int q_heads, int heads, int dim, long long max_keys, int num_sms);
 cudaError_t launch_attn_tiles(const AttnLaunch& p, long long max_keys, void* workspace, int num_sms,
                               cudaStream_t stream);
+cudaError_t launch_attn_tiles_mod(const AttnLaunch& p, long long max_keys, void* workspace, int num_sms,
+                                  cudaStream_t stream);
+cudaError_t launch_attn_tiles_cap(const AttnLaunch& p, long long max_keys, void* workspace, int num_sms,
+                                  cudaStream_t stream);
 
 // ------------------------------------------------- pages of a pool
 // One array of the pool, axes joined where they are contiguous: a page is rows
