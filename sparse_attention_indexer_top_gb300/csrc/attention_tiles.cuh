@@ -420,6 +420,11 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
   return r;
 }
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   uint64_t r;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
@@ -661,67 +666,73 @@ __device__ __forceinline__ void rescale_o(uint32_t to, float f) {
   }
 }
 
-// Changes 32 columns of scores s, from column c0 of the tile at t0: the product
-// with `mul` in log2 units, capped, biased. Two elements to an instruction where
-// no score of the warp passes the cap and no key lies behind its row's position.
+// What a thread's row does to its scores, in log2 units, besides the multiplier.
+struct Change {
+  float cap, inv_cap;
+  float slope;
+  int ahead;  // the row's position less the tile's first token
+};
+
+// Changes 32 columns of scores s, from column c0 of the tile: times `mul`,
+// capped (no |x| above cap / 2), biased. Two elements to an instruction: with a
+// cap, 6 of them, which is what the cap costs beside the masks' and the sum's.
 template <int MOD>
-__device__ __forceinline__ void change32(uint32_t* s, float mul, float cap, float inv_cap, float slope, int ahead) {
-  // ahead: position less the token of column 0
-  const bool linear = !(MOD & kBias) || __all_sync(0xffffffffu, ahead >= 31);
-  bool near = true;
-  if (MOD & kCap) {
-    float top = 0.f;
+__device__ __forceinline__ void change32(uint32_t* s, int c0, float mul, const Change& ch) {
+  const float xm = mul * ch.inv_cap;
+  const uint64_t mul_2 = pair(mul, mul), x_2 = pair(xm, xm), slope_2 = pair(-ch.slope, -ch.slope);
+  // distances of the two columns, whole numbers, less 2 at each step
+  uint64_t d = pair(static_cast<float>(ch.ahead - c0), static_cast<float>(ch.ahead - c0 - 1));
+  const uint64_t step = pair(-2.f, -2.f);
+  uint64_t q_2[4];
 #pragma unroll
-    for (int c = 0; c < 32; c += 2) top = max3(top, fabsf(__uint_as_float(s[c])), fabsf(__uint_as_float(s[c + 1])));
-    near = __all_sync(0xffffffffu, top * (mul * inv_cap) <= 1.f);
-  }
-  const float d0 = static_cast<float>(ahead);
-  if (near && linear) {
-    const uint64_t mul2 = pair(mul, mul), x2 = pair(mul * inv_cap, mul * inv_cap), slope2 = pair(slope, slope);
-    const uint64_t cap2 = pair(cap, cap), zero = pair(0.f, 0.f);
-    const float b = -slope * d0;
-    const uint64_t b2 = pair(b, b);
+  for (int i = 0; i < 4; ++i) q_2[i] = pair(ch.cap * tanh_near(i), ch.cap * tanh_near(i));
 #pragma unroll
-    for (int c = 0; c < 32; c += 2) {
-      uint64_t v = pair(__uint_as_float(s[c]), __uint_as_float(s[c + 1]));
-      const uint64_t bias = (MOD & kBias) ? fma2(slope2, pair(static_cast<float>(c), static_cast<float>(c + 1)), b2) : zero;
-      if (MOD & kCap) {
-        const uint64_t x = fma2(v, x2, zero), y = fma2(x, x, zero);
-        uint64_t q = pair(tanh_q(6), tanh_q(6));
+  for (int c = 0; c < 32; c += 2) {
+    uint64_t v = pair(__uint_as_float(s[c]), __uint_as_float(s[c + 1]));
+    if (MOD & kCap) {
+      const uint64_t x = mul2(v, x_2), y = mul2(x, x);
+      uint64_t q = q_2[3];
 #pragma unroll
-        for (int i = 5; i >= 0; --i) q = fma2(q, y, pair(tanh_q(i), tanh_q(i)));
-        v = fma2(fma2(x, cap2, zero), q, bias);
-      } else {
-        v = fma2(v, mul2, bias);
-      }
-      float lo, hi;
-      unpair(v, lo, hi);
-      s[c] = __float_as_uint(lo);
-      s[c + 1] = __float_as_uint(hi);
+      for (int i = 2; i >= 0; --i) q = fma2(q, y, q_2[i]);
+      v = mul2(x, q);
+    } else {
+      v = mul2(v, mul_2);
     }
-    return;
-  }
-#pragma unroll
-  for (int c = 0; c < 32; ++c) {
-    float v = __uint_as_float(s[c]) * mul;
-    if (MOD & kCap) v = capped(v, cap, inv_cap);
-    if (MOD & kBias) v = fmaf(-slope, fabsf(d0 - static_cast<float>(c)), v);
-    s[c] = __float_as_uint(v);
+    if (MOD & kBias) {
+      v = fma2(slope_2, d & 0x7fffffff7fffffffull, v);
+      d = add2(d, step);
+    }
+    float lo, hi;
+    unpair(v, lo, hi);
+    s[c] = __float_as_uint(lo);
+    s[c + 1] = __float_as_uint(hi);
   }
 }
 
-// A tile of an e4m3 cache whose scales are not all in the tile's powers:
-// factors[g] are left over of 16 keys' scales. Out of line, and S is read twice
-// 32 columns at a time: beside the plain code it slowed that by half.
-template <int D, int MOD>
+// A tile of an e4m3 cache whose scales are not all in the tile's powers
+// (factors[g] are left over of 16 keys' scales; null: nothing is), or one with
+// scores near its cap. Out of line, and S is read twice 32 columns at a time:
+// beside the plain code it slowed that by half.
+template <int D, bool F8, int MOD>
 __device__ __noinline__ float2 rough_tile(uint32_t ts, uint32_t to, float2 ml, float mul, float ev, float un_ev,
-                                          const float2* factors, int4 sees, uint32_t bad, bool have_o, float3 mod, int ahead) {
+                                          const float2* factors, int4 sees, uint32_t bad, bool have_o, Change ch) {
   uint32_t s[32];
   // masked after the scaling: a scale may be 0, and 0 * -inf is NaN
   auto scaled = [&](int c0) {
+    if (!MOD || factors) {
 #pragma unroll
-    for (int c = 0; c < 32; ++c) s[c] = __float_as_uint(__uint_as_float(s[c]) * factors[(c0 + c) / 16].x);
-    if (MOD & (kCap | kBias)) change32<MOD>(s, mul, mod.x, mod.y, mod.z, ahead - c0);
+      for (int c = 0; c < 32; ++c) s[c] = __float_as_uint(__uint_as_float(s[c]) * factors[(c0 + c) / 16].x);
+    }
+    if (MOD & (kCap | kBias)) {
+      const float d0 = static_cast<float>(ch.ahead - c0);
+#pragma unroll
+      for (int c = 0; c < 32; ++c) {
+        float v = __uint_as_float(s[c]) * mul;
+        if (MOD & kCap) v = capped(v, ch.cap, ch.inv_cap);
+        if (MOD & kBias) v = fmaf(-ch.slope, fabsf(d0 - static_cast<float>(c)), v);
+        s[c] = __float_as_uint(v);
+      }
+    }
     mask32<MOD>(s, sees.x - c0, sees.y - c0, sees.z - c0, sees.w - c0, bad >> (c0 / 16));
   };
   const float mul1 = MOD & (kCap | kBias) ? 1.f : mul;
@@ -735,9 +746,9 @@ __device__ __noinline__ float2 rough_tile(uint32_t ts, uint32_t to, float2 ml, f
     for (int c = 0; c < 32; ++c) top = fmaxf(top, __uint_as_float(s[c]));
   }
   top = fmaf(top, mul1, ev);
-  const bool up = top > ml.x + kPassed<true>;
+  const bool up = top > ml.x + kPassed<F8>;
   if (__any_sync(0xffffffffu, up)) {
-    const float to_m = top - kLift<true>;
+    const float to_m = top - kLift<F8>;
     const float f = up ? (ml.x == -INFINITY ? 0.f : ex2(ml.x - to_m)) : 1.f;
     if (up) ml.x = to_m;
     ml.y *= f;
@@ -752,11 +763,11 @@ __device__ __noinline__ float2 rough_tile(uint32_t ts, uint32_t to, float2 ml, f
     scaled(c0);
 #pragma unroll
     for (int c = 0; c < 32; c += 2) {
-      const float f = factors[(c0 + c) / 16].y;
+      const float f = !MOD || factors ? factors[(c0 + c) / 16].y : 1.f;
       const float a = ex2(fmaf(__uint_as_float(s[c]), mul1, off));
       const float b = ex2(fmaf(__uint_as_float(s[c + 1]), mul1, off));
       sum += a + b;
-      s[c / 2] = pack_f16(a * f, b * f);
+      s[c / 2] = F8 ? pack_f16(a * f, b * f) : pack_bf16(a, b);
     }
     tmem_st16(ts + c0 / 2, s);
   }
@@ -893,10 +904,29 @@ __device__ __forceinline__ bool softmax_role(Shared<D, F8>& S, const TilesLaunch
         }
         return top;
       };
-      if (F8 && rough) {
-        const float2 ml = rough_tile<D, MOD>(ts, to, make_float2(m, l), mul, ev, un_ev, factors,
-                                             make_int4(ln.n - t0, ln.first - t0, ln.sinks - t0, ln.start - t0), bad,
-                                             i > ps.i0, make_float3(cap, inv_cap, ln.slope), ln.pos - t0);
+      const Change ch{cap, inv_cap, ln.slope, ln.pos - t0};
+      uint32_t s[kTile];
+      if ((MOD & kCap) && !rough) {
+        // scores near the cap: as a rough tile, which reads them again
+#pragma unroll
+        for (int c = 0; c < kTile; c += 32) tmem_ld32(ts + c, s + c);
+#pragma unroll
+        for (int c = 0; c < kTile; c += 32) tmem_ld_wait32(s + c);
+        float far[2] = {0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < kTile; c += 4) {
+          far[0] = max3(far[0], fabsf(__uint_as_float(s[c])), fabsf(__uint_as_float(s[c + 1])));
+          far[1] = max3(far[1], fabsf(__uint_as_float(s[c + 2])), fabsf(__uint_as_float(s[c + 3])));
+        }
+        if (!__all_sync(0xffffffffu, fmaxf(far[0], far[1]) * (mul * inv_cap) <= kNear)) {
+          rough = true;
+          factors = nullptr;
+        }
+      }
+      if ((F8 || (MOD & kCap)) && rough) {
+        const float2 ml = rough_tile<D, F8, MOD>(ts, to, make_float2(m, l), mul, ev, un_ev, factors,
+                                                 make_int4(ln.n - t0, ln.first - t0, ln.sinks - t0, ln.start - t0), bad,
+                                                 i > ps.i0, ch);
         m = ml.x;
         l = ml.y;
         tc_fence_before();
@@ -907,14 +937,18 @@ __device__ __forceinline__ bool softmax_role(Shared<D, F8>& S, const TilesLaunch
         }
         continue;
       }
-      uint32_t s[kTile];
+      if (!(MOD & kCap)) {
 #pragma unroll
-      for (int c = 0; c < kTile; c += 32) tmem_ld32(ts + c, s + c);
+        for (int c = 0; c < kTile; c += 32) tmem_ld32(ts + c, s + c);
 #pragma unroll
-      for (int c = 0; c < kTile; c += 32) tmem_ld_wait32(s + c);
-      if (MOD & (kCap | kBias)) {
+        for (int c = 0; c < kTile; c += 32) tmem_ld_wait32(s + c);
+      }
+      // the maximum of a tile that is only capped is that of the scores before;
+      // the cap then goes with the weights
+      const bool late = MOD & kCap && !(MOD & kBias) && !masked;
+      if ((MOD & (kCap | kBias)) && !late) {
 #pragma unroll
-        for (int c = 0; c < kTile; c += 32) change32<MOD>(s + c, mul, cap, inv_cap, ln.slope, ln.live ? ln.pos - t0 - c : 31);
+        for (int c = 0; c < kTile; c += 32) change32<MOD>(s + c, c, mul, ch);
         mul = 1.f;
       }
       if (masked) {
@@ -924,7 +958,12 @@ __device__ __forceinline__ bool softmax_role(Shared<D, F8>& S, const TilesLaunch
       float top = -INFINITY;
 #pragma unroll
       for (int c = 0; c < kTile; c += 32) top = largest(s + c, c, top);
-      top = fmaf(top, mul, ev);
+      if (late) {
+        const float x = top * (mul * inv_cap), y = x * x;
+        top = fmaf(cap * x, fmaf(fmaf(fmaf(tanh_near(3), y, tanh_near(2)), y, tanh_near(1)), y, tanh_near(0)), ev);
+      } else {
+        top = fmaf(top, mul, ev);
+      }
       const bool up = top > m + kPassed<F8>;
       if (__any_sync(0xffffffffu, up)) {
         top -= kLift<F8>;
@@ -955,17 +994,46 @@ __device__ __forceinline__ bool softmax_role(Shared<D, F8>& S, const TilesLaunch
         tile_l += a + b;
         tmem_st16(ts + c0 / 2, s);
       };
+      auto capped_weights = [&](uint32_t* s, int c0) {
+        uint64_t sum[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
+        const float off = ev - base, xm = mul * inv_cap;
+        float a, b;
+        const uint64_t x_2 = pair(xm, xm), off2 = pair(off, off);
+        uint64_t q_2[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) q_2[i] = pair(cap * tanh_near(i), cap * tanh_near(i));
+#pragma unroll
+        for (int c = 0; c < 32; c += 2) {
+          const uint64_t x = mul2(pair(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), x_2), y = mul2(x, x);
+          unpair(fma2(x, fma2(fma2(fma2(q_2[3], y, q_2[2]), y, q_2[1]), y, q_2[0]), off2), a, b);
+          a = ex2(a);
+          b = ex2(b);
+          sum[(c >> 1) & 1] = add2(sum[(c >> 1) & 1], pair(a, b));
+          s[c / 2] = F8 ? pack_f16(a, b) : pack_bf16(a, b);
+        }
+        unpair(add2(sum[0], sum[1]), a, b);
+        tile_l += a + b;
+        tmem_st16(ts + c0 / 2, s);
+      };
       auto hand_over = [&](int half) {
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) arrive_first<PAIR>(&S.p_ready[x][half]);
       };
-      weights(s, 0);
-      weights(s + 32, 32);
-      hand_over(0);
-      weights(s + 64, 64);
-      weights(s + 96, 96);
+      if (late) {
+        capped_weights(s, 0);
+        capped_weights(s + 32, 32);
+        hand_over(0);
+        capped_weights(s + 64, 64);
+        capped_weights(s + 96, 96);
+      } else {
+        weights(s, 0);
+        weights(s + 32, 32);
+        hand_over(0);
+        weights(s + 64, 64);
+        weights(s + 96, 96);
+      }
       hand_over(1);
       l = fmaf(tile_l, un_ev, l);
     }
