@@ -709,6 +709,58 @@ __device__ __forceinline__ void change32(uint32_t* s, int c0, float mul, const C
   }
 }
 
+// Weights 2^(changed score + off) of 32 columns from column c0, two to a word in
+// s[0..16), and what they add up to: the change, the maximum and the exponent in
+// one go. The bias is linear in the column, start + slope * column.
+template <bool F8, int MOD>
+__device__ __forceinline__ uint64_t changed_weights32(uint32_t* s, int c0, uint64_t mul_2, const uint64_t (&q_2)[4],
+                                                      uint64_t off_2, uint64_t slope_2) {
+  uint64_t sum[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
+  uint64_t col = pair(static_cast<float>(c0), static_cast<float>(c0 + 1));
+  const uint64_t two = pair(2.f, 2.f);
+#pragma unroll
+  for (int c = 0; c < 32; c += 8) {
+    uint64_t x[4], w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      w[j] = off_2;
+      if (MOD & kBias) {
+        w[j] = fma2(col, slope_2, off_2);
+        col = add2(col, two);
+      }
+      x[j] = pair(__uint_as_float(s[c + 2 * j]), __uint_as_float(s[c + 2 * j + 1]));
+    }
+    if (MOD & kCap) {
+      uint64_t y[4], q[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[j] = mul2(x[j], mul_2);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) y[j] = mul2(x[j], x[j]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) q[j] = fma2(q_2[3], y[j], q_2[2]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) q[j] = fma2(q[j], y[j], q_2[1]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) q[j] = fma2(q[j], y[j], q_2[0]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w[j] = fma2(x[j], q[j], w[j]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w[j] = fma2(x[j], mul_2, w[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float a, b;
+      unpair(w[j], a, b);
+      a = ex2(a);
+      b = ex2(b);
+      sum[j & 1] = add2(sum[j & 1], pair(a, b));
+      s[c / 2 + j] = F8 ? pack_f16(a, b) : pack_bf16(a, b);
+    }
+  }
+  return add2(sum[0], sum[1]);
+}
+
 // A tile of an e4m3 cache whose scales are not all in the tile's powers
 // (factors[g] are left over of 16 keys' scales; null: nothing is), or one with
 // scores near its cap. Out of line, and S is read twice 32 columns at a time:
@@ -883,7 +935,9 @@ __device__ __forceinline__ bool softmax_role(Shared<D, F8>& S, const TilesLaunch
       ++at.tiles;
       tc_fence_after();
       const int t0 = ps.tile0(i);
-      const bool whole = t0 + kTile <= ln.n && (t0 >= ln.first || t0 + kTile <= ln.sinks) && (!MOD || t0 >= ln.start);
+      // (MOD: whatever a lane without a row of the pass computes, nobody reads)
+      const bool whole = (MOD && !ln.live) ||
+                         (t0 + kTile <= ln.n && (t0 >= ln.first || t0 + kTile <= ln.sinks) && (!MOD || t0 >= ln.start));
       const bool masked = !__all_sync(0xffffffffu, whole) || bad;
       if (bad && lane == 0) atomicOr(p.status, kDevBadPage);
       auto mask = [&](uint32_t* s, int c0) {
@@ -905,25 +959,7 @@ __device__ __forceinline__ bool softmax_role(Shared<D, F8>& S, const TilesLaunch
         return top;
       };
       const Change ch{cap, inv_cap, ln.slope, ln.pos - t0};
-      uint32_t s[kTile];
-      if ((MOD & kCap) && !rough) {
-        // scores near the cap: as a rough tile, which reads them again
-#pragma unroll
-        for (int c = 0; c < kTile; c += 32) tmem_ld32(ts + c, s + c);
-#pragma unroll
-        for (int c = 0; c < kTile; c += 32) tmem_ld_wait32(s + c);
-        float far[2] = {0.f, 0.f};
-#pragma unroll
-        for (int c = 0; c < kTile; c += 4) {
-          far[0] = max3(far[0], fabsf(__uint_as_float(s[c])), fabsf(__uint_as_float(s[c + 1])));
-          far[1] = max3(far[1], fabsf(__uint_as_float(s[c + 2])), fabsf(__uint_as_float(s[c + 3])));
-        }
-        if (!__all_sync(0xffffffffu, fmaxf(far[0], far[1]) * (mul * inv_cap) <= kNear)) {
-          rough = true;
-          factors = nullptr;
-        }
-      }
-      if ((F8 || (MOD & kCap)) && rough) {
+      auto rough_path = [&](const float2* factors) {
         const float2 ml = rough_tile<D, F8, MOD>(ts, to, make_float2(m, l), mul, ev, un_ev, factors,
                                                  make_int4(ln.n - t0, ln.first - t0, ln.sinks - t0, ln.start - t0), bad,
                                                  i > ps.i0, ch);
@@ -935,35 +971,94 @@ __device__ __forceinline__ bool softmax_role(Shared<D, F8>& S, const TilesLaunch
           arrive_first<PAIR>(&S.p_ready[x][0]);
           arrive_first<PAIR>(&S.p_ready[x][1]);
         }
+      };
+      if (F8 && rough) {
+        rough_path(factors);
         continue;
       }
-      if (!(MOD & kCap)) {
+      auto hand_over = [&](int half) {
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_first<PAIR>(&S.p_ready[x][half]);
+      };
+      uint32_t s[kTile];
 #pragma unroll
-        for (int c = 0; c < kTile; c += 32) tmem_ld32(ts + c, s + c);
+      for (int c = 0; c < kTile; c += 32) tmem_ld32(ts + c, s + c);
 #pragma unroll
-        for (int c = 0; c < kTile; c += 32) tmem_ld_wait32(s + c);
-      }
-      // the maximum of a tile that is only capped is that of the scores before;
-      // the cap then goes with the weights
-      const bool late = MOD & kCap && !(MOD & kBias) && !masked;
-      if ((MOD & (kCap | kBias)) && !late) {
+      for (int c = 0; c < kTile; c += 32) tmem_ld_wait32(s + c);
+      if constexpr ((MOD & (kCap | kBias)) != 0) {
+        // A bound of the row's changed scores, cheaper than their maximum: while
+        // it does not pass the running maximum, that stays, and change and
+        // exponent go together. With a cap it is the cap of the largest
+        // magnitude (masked columns, which may hold anything, are left to the
+        // longer way), else the largest product; a bias is at most what it is
+        // at the tile's nearest (slope below 0: farthest) column.
+        float bound;
+        bool apart = false;  // the longer way
+        if (MOD & kCap) {
+          float far[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int c = 0; c < kTile; c += 2)
+            far[c / 2 & 3] = max3(far[c / 2 & 3], fabsf(__uint_as_float(s[c])), fabsf(__uint_as_float(s[c + 1])));
+          const float t = fmaxf(max3(far[0], far[1], far[2]), far[3]) * (mul * inv_cap), y = t * t;
+          if (!__all_sync(0xffffffffu, !ln.live || t <= kNear)) {  // scores near the cap
+            rough_path(nullptr);
+            continue;
+          }
+          bound = cap * (t * fmaf(fmaf(fmaf(tanh_near(3), y, tanh_near(2)), y, tanh_near(1)), y, tanh_near(0)));
+          apart = masked;
+        } else {
+          if (masked) {
+#pragma unroll
+            for (int c = 0; c < kTile; c += 32) mask(s + c, c);
+          }
+          bound = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < kTile; c += 32) bound = largest(s + c, c, bound);
+          bound *= mul;
+        }
+        float off = ev, slope = 0.f;
+        if (MOD & kBias) {
+          const float d0 = static_cast<float>(ch.ahead), d1 = d0 - (kTile - 1);
+          const float lo = d1 > 0.f ? d1 : d0 < 0.f ? -d0 : 0.f, hi = fmaxf(d0, -d1);
+          bound = fmaf(-ln.slope, ln.slope >= 0.f ? lo : hi, bound);
+          slope = d0 < 0.f ? -ln.slope : ln.slope;
+          off = fmaf(-slope, d0, ev);
+          apart = apart || (d0 >= 0.f && d1 < 0.f && ln.n > ln.pos + 1);  // keys on both sides of the position
+        }
+        if (__all_sync(0xffffffffu, !ln.live || (!apart && bound + ev <= m + kPassed<F8>))) {
+          off -= m == -INFINITY ? 0.f : m;
+          const float x1 = MOD & kCap ? mul * inv_cap : mul;
+          const uint64_t off_2 = pair(off, off), x_2 = pair(x1, x1), slope_2 = pair(slope, slope);
+          uint64_t q_2[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) q_2[j] = pair(cap * tanh_near(j), cap * tanh_near(j));
+          uint64_t sum = pair(0.f, 0.f);
+#pragma unroll
+          for (int c = 0; c < kTile; c += 32) {
+            sum = add2(sum, changed_weights32<F8, MOD>(s + c, c, x_2, q_2, off_2, slope_2));
+            tmem_st16(ts + c / 2, s + c);
+            if (c == 32) hand_over(0);
+          }
+          hand_over(1);
+          float a, b;
+          unpair(sum, a, b);
+          l = fmaf(a + b, un_ev, l);
+          continue;
+        }
 #pragma unroll
         for (int c = 0; c < kTile; c += 32) change32<MOD>(s + c, c, mul, ch);
         mul = 1.f;
       }
-      if (masked) {
+      if (masked && (!MOD || (MOD & kCap) || !(MOD & kBias))) {
 #pragma unroll
         for (int c = 0; c < kTile; c += 32) mask(s + c, c);
       }
       float top = -INFINITY;
 #pragma unroll
       for (int c = 0; c < kTile; c += 32) top = largest(s + c, c, top);
-      if (late) {
-        const float x = top * (mul * inv_cap), y = x * x;
-        top = fmaf(cap * x, fmaf(fmaf(fmaf(tanh_near(3), y, tanh_near(2)), y, tanh_near(1)), y, tanh_near(0)), ev);
-      } else {
-        top = fmaf(top, mul, ev);
-      }
+      top = fmaf(top, mul, ev);
       const bool up = top > m + kPassed<F8>;
       if (__any_sync(0xffffffffu, up)) {
         top -= kLift<F8>;
@@ -994,46 +1089,11 @@ __device__ __forceinline__ bool softmax_role(Shared<D, F8>& S, const TilesLaunch
         tile_l += a + b;
         tmem_st16(ts + c0 / 2, s);
       };
-      auto capped_weights = [&](uint32_t* s, int c0) {
-        uint64_t sum[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
-        const float off = ev - base, xm = mul * inv_cap;
-        float a, b;
-        const uint64_t x_2 = pair(xm, xm), off2 = pair(off, off);
-        uint64_t q_2[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) q_2[i] = pair(cap * tanh_near(i), cap * tanh_near(i));
-#pragma unroll
-        for (int c = 0; c < 32; c += 2) {
-          const uint64_t x = mul2(pair(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), x_2), y = mul2(x, x);
-          unpair(fma2(x, fma2(fma2(fma2(q_2[3], y, q_2[2]), y, q_2[1]), y, q_2[0]), off2), a, b);
-          a = ex2(a);
-          b = ex2(b);
-          sum[(c >> 1) & 1] = add2(sum[(c >> 1) & 1], pair(a, b));
-          s[c / 2] = F8 ? pack_f16(a, b) : pack_bf16(a, b);
-        }
-        unpair(add2(sum[0], sum[1]), a, b);
-        tile_l += a + b;
-        tmem_st16(ts + c0 / 2, s);
-      };
-      auto hand_over = [&](int half) {
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) arrive_first<PAIR>(&S.p_ready[x][half]);
-      };
-      if (late) {
-        capped_weights(s, 0);
-        capped_weights(s + 32, 32);
-        hand_over(0);
-        capped_weights(s + 64, 64);
-        capped_weights(s + 96, 96);
-      } else {
-        weights(s, 0);
-        weights(s + 32, 32);
-        hand_over(0);
-        weights(s + 64, 64);
-        weights(s + 96, 96);
-      }
+      weights(s, 0);
+      weights(s + 32, 32);
+      hand_over(0);
+      weights(s + 64, 64);
+      weights(s + 96, 96);
       hand_over(1);
       l = fmaf(tile_l, un_ev, l);
     }
