@@ -170,10 +170,11 @@ template <int MOD>
 struct PassMore {
   int base_tile;  // of the first tokens
   int high;       // highest first key of a window
+  int last;       // index of the last tile
 };
 template <>
 struct PassMore<0> {
-  static constexpr int base_tile = 0, high = 0;
+  static constexpr int base_tile = 0, high = 0, last = 0;
 };
 template <int MOD>
 struct Pass : PassMore<MOD> {
@@ -185,7 +186,10 @@ struct Pass : PassMore<MOD> {
   int low_tile;
   int i0, i1;      // tile indices of this piece
   bool act[2];     // MMA tile has rows of the pass
+  // With a bias the nearest tiles come first: from the first tile on, every
+  // nearer one would pass the running maximum by its 128 steps of the slope.
   __device__ __forceinline__ int tile0(int i) const {
+    if (MOD & kBias) i = this->last - i;
     return (i < first_tiles ? i + this->base_tile : i - first_tiles + low_tile) * kTile;
   }
   // does every row of the pass see all of the tile?
@@ -226,6 +230,7 @@ __device__ __forceinline__ Pass<MOD> get_pass(const Shared<D, F8>& S, const Tile
     } else if (r.low > 0) r.first_tiles = min((min(p.sinks, r.low) + kTile - 1) / kTile, r.low_tile);
     tiles = r.first_tiles + (r.most + kTile - 1) / kTile - r.low_tile;
   }
+  if constexpr (MOD != 0) r.last = tiles - 1;
   r.i0 = static_cast<int>(static_cast<long long>(tiles) * pc.from / pc.of);
   r.i1 = static_cast<int>(static_cast<long long>(tiles) * pc.to / pc.of);
   return r;
@@ -635,17 +640,23 @@ __device__ __forceinline__ float query_to_f16(unsigned char* tile, int r) {
   return __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
 }
 
-// Scores of 32 columns that the row does not see become -inf: columns from n
-// on, and those below `first` that are not below `sinks`; bits 0 and 1 of `bad`
-// take out 16 each; MOD: those below `start` too. One bit a column, so that an
-// element costs a test and a select.
+// Which of 32 columns the row sees, a bit each: those below n, except below
+// `first` that are not below `sinks` (MOD: and those below `start`); bits 0 and 1
+// of `bad` take out 16 each.
 template <int MOD>
-__device__ __forceinline__ void mask32(uint32_t* s, int n, int first, int sinks, int start, uint32_t bad) {
+__device__ __forceinline__ uint32_t seen32(int n, int first, int sinks, int start, uint32_t bad) {
   auto below = [](int x) { return x <= 0 ? 0u : x >= 32 ? ~0u : (1u << x) - 1u; };
   uint32_t see = below(n) & (~below(first) | below(sinks));
   if (MOD) see &= ~below(start);
   if (bad & 1) see &= 0xffff0000u;
   if (bad & 2) see &= 0x0000ffffu;
+  return see;
+}
+// Scores of 32 columns that the row does not see become -inf. One bit a column,
+// so that an element costs a test and a select.
+template <int MOD>
+__device__ __forceinline__ void mask32(uint32_t* s, int n, int first, int sinks, int start, uint32_t bad) {
+  const uint32_t see = seen32<MOD>(n, first, sinks, start, bad);
 #pragma unroll
   for (int c = 0; c < 32; ++c)
     if (!(see & (1u << c))) s[c] = 0xff800000u;
@@ -710,11 +721,12 @@ __device__ __forceinline__ void change32(uint32_t* s, int c0, float mul, const C
 }
 
 // Weights 2^(changed score + off) of 32 columns from column c0, two to a word in
-// s[0..16), and what they add up to: the change, the maximum and the exponent in
-// one go. The bias is linear in the column, start + slope * column.
-template <bool F8, int MOD>
+// s[0..16), and what they add up to: change and exponent in one go. The bias is
+// linear in the column, slope * column and part of `off`; MASKED: columns without
+// their bit in `see` get 0.
+template <bool F8, int MOD, bool MASKED>
 __device__ __forceinline__ uint64_t changed_weights32(uint32_t* s, int c0, uint64_t mul_2, const uint64_t (&q_2)[4],
-                                                      uint64_t off_2, uint64_t slope_2) {
+                                                      uint64_t off_2, uint64_t slope_2, uint32_t see) {
   uint64_t sum[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
   uint64_t col = pair(static_cast<float>(c0), static_cast<float>(c0 + 1));
   const uint64_t two = pair(2.f, 2.f);
@@ -754,6 +766,10 @@ __device__ __forceinline__ uint64_t changed_weights32(uint32_t* s, int c0, uint6
       unpair(w[j], a, b);
       a = ex2(a);
       b = ex2(b);
+      if (MASKED) {
+        a = see & (1u << (c + 2 * j)) ? a : 0.f;
+        b = see & (2u << (c + 2 * j)) ? b : 0.f;
+      }
       sum[j & 1] = add2(sum[j & 1], pair(a, b));
       s[c / 2 + j] = F8 ? pack_f16(a, b) : pack_bf16(a, b);
     }
@@ -761,41 +777,58 @@ __device__ __forceinline__ uint64_t changed_weights32(uint32_t* s, int c0, uint6
   return add2(sum[0], sum[1]);
 }
 
-// A tile of an e4m3 cache whose scales are not all in the tile's powers
-// (factors[g] are left over of 16 keys' scales; null: nothing is), or one with
-// scores near its cap. Out of line, and S is read twice 32 columns at a time:
-// beside the plain code it slowed that by half.
+// The largest magnitude of 32 columns and `top`.
+__device__ __forceinline__ float largest32(const uint32_t* s, float top) {
+  float a[4] = {top, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int c = 0; c < 32; c += 2)
+    a[c / 2 & 3] = max3(a[c / 2 & 3], fabsf(__uint_as_float(s[c])), fabsf(__uint_as_float(s[c + 1])));
+  return fmaxf(max3(a[0], a[1], a[2]), a[3]);
+}
+
+// Any tile, by the longer way: an e4m3 cache's whose scales are not all in the
+// tile's powers (factors[g] are left over of 16 keys' scales; null: nothing is),
+// and with changed scores one that may move the maximum, has scores near its
+// cap, or keys on both sides of a row's position. Out of line, and S is read
+// twice 32 columns at a time: beside the plain code it slowed that by half.
 template <int D, bool F8, int MOD>
 __device__ __noinline__ float2 rough_tile(uint32_t ts, uint32_t to, float2 ml, float mul, float ev, float un_ev,
-                                          const float2* factors, int4 sees, uint32_t bad, bool have_o, Change ch) {
+                                          const float2* factors, int4 sees, uint32_t bad, bool masked, bool have_o,
+                                          Change ch) {
+  constexpr bool kChanged = (MOD & (kCap | kBias)) != 0;
   uint32_t s[32];
   // masked after the scaling: a scale may be 0, and 0 * -inf is NaN
   auto scaled = [&](int c0) {
-    if (!MOD || factors) {
+    if (!kChanged || factors) {
 #pragma unroll
       for (int c = 0; c < 32; ++c) s[c] = __float_as_uint(__uint_as_float(s[c]) * factors[(c0 + c) / 16].x);
     }
-    if (MOD & (kCap | kBias)) {
-      const float d0 = static_cast<float>(ch.ahead - c0);
+    if (kChanged) {
+      if ((MOD & kCap) && !__all_sync(0xffffffffu, largest32(s, 0.f) * (mul * ch.inv_cap) <= kNear)) {
+        const float d0 = static_cast<float>(ch.ahead - c0);
 #pragma unroll
-      for (int c = 0; c < 32; ++c) {
-        float v = __uint_as_float(s[c]) * mul;
-        if (MOD & kCap) v = capped(v, ch.cap, ch.inv_cap);
-        if (MOD & kBias) v = fmaf(-ch.slope, fabsf(d0 - static_cast<float>(c)), v);
-        s[c] = __float_as_uint(v);
+        for (int c = 0; c < 32; ++c) {
+          float v = capped(__uint_as_float(s[c]) * mul, ch.cap, ch.inv_cap);
+          if (MOD & kBias) v = fmaf(-ch.slope, fabsf(d0 - static_cast<float>(c)), v);
+          s[c] = __float_as_uint(v);
+        }
+      } else {
+        change32<MOD>(s, c0, mul, ch);
       }
     }
-    mask32<MOD>(s, sees.x - c0, sees.y - c0, sees.z - c0, sees.w - c0, bad >> (c0 / 16));
+    if (!kChanged || masked) mask32<MOD>(s, sees.x - c0, sees.y - c0, sees.z - c0, sees.w - c0, bad >> (c0 / 16));
   };
-  const float mul1 = MOD & (kCap | kBias) ? 1.f : mul;
+  const float mul1 = kChanged ? 1.f : mul;
   float top = -INFINITY;
 #pragma unroll 1
   for (int c0 = 0; c0 < kTile; c0 += 32) {
     tmem_ld32(ts + c0, s);
     tmem_ld_wait32(s);
     scaled(c0);
+    float t[4] = {top, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-    for (int c = 0; c < 32; ++c) top = fmaxf(top, __uint_as_float(s[c]));
+    for (int c = 0; c < 32; c += 2) t[c / 2 & 3] = max3(t[c / 2 & 3], __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
+    top = fmaxf(max3(t[0], t[1], t[2]), t[3]);
   }
   top = fmaf(top, mul1, ev);
   const bool up = top > ml.x + kPassed<F8>;
@@ -815,7 +848,7 @@ __device__ __noinline__ float2 rough_tile(uint32_t ts, uint32_t to, float2 ml, f
     scaled(c0);
 #pragma unroll
     for (int c = 0; c < 32; c += 2) {
-      const float f = !MOD || factors ? factors[(c0 + c) / 16].y : 1.f;
+      const float f = !kChanged || factors ? factors[(c0 + c) / 16].y : 1.f;
       const float a = ex2(fmaf(__uint_as_float(s[c]), mul1, off));
       const float b = ex2(fmaf(__uint_as_float(s[c + 1]), mul1, off));
       sum += a + b;
@@ -962,7 +995,7 @@ __device__ __forceinline__ bool softmax_role(Shared<D, F8>& S, const TilesLaunch
       auto rough_path = [&](const float2* factors) {
         const float2 ml = rough_tile<D, F8, MOD>(ts, to, make_float2(m, l), mul, ev, un_ev, factors,
                                                  make_int4(ln.n - t0, ln.first - t0, ln.sinks - t0, ln.start - t0), bad,
-                                                 i > ps.i0, ch);
+                                                 masked, i > ps.i0, ch);
         m = ml.x;
         l = ml.y;
         tc_fence_before();
@@ -990,32 +1023,20 @@ __device__ __forceinline__ bool softmax_role(Shared<D, F8>& S, const TilesLaunch
       if constexpr ((MOD & (kCap | kBias)) != 0) {
         // A bound of the row's changed scores, cheaper than their maximum: while
         // it does not pass the running maximum, that stays, and change and
-        // exponent go together. With a cap it is the cap of the largest
-        // magnitude (masked columns, which may hold anything, are left to the
-        // longer way), else the largest product; a bias is at most what it is
-        // at the tile's nearest (slope below 0: farthest) column.
-        float bound;
-        bool apart = false;  // the longer way
+        // exponent go together. It is that of the largest magnitude (with a cap)
+        // or product, columns that are not seen among them, and of the bias at
+        // the tile's nearest (slope below 0: farthest) column. (Reading S twice, 32
+        // columns ahead of their use, leaves more registers and is slower: 1001
+        // against 873 us.)
+        float bound = MOD & kCap ? 0.f : -INFINITY;
+#pragma unroll
+        for (int c = 0; c < kTile; c += 32) bound = MOD & kCap ? largest32(s + c, bound) : largest(s + c, c, bound);
+        bool quick = true;
         if (MOD & kCap) {
-          float far[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int c = 0; c < kTile; c += 2)
-            far[c / 2 & 3] = max3(far[c / 2 & 3], fabsf(__uint_as_float(s[c])), fabsf(__uint_as_float(s[c + 1])));
-          const float t = fmaxf(max3(far[0], far[1], far[2]), far[3]) * (mul * inv_cap), y = t * t;
-          if (!__all_sync(0xffffffffu, !ln.live || t <= kNear)) {  // scores near the cap
-            rough_path(nullptr);
-            continue;
-          }
+          const float t = bound * (mul * inv_cap), y = t * t;
+          quick = t <= kNear;
           bound = cap * (t * fmaf(fmaf(fmaf(tanh_near(3), y, tanh_near(2)), y, tanh_near(1)), y, tanh_near(0)));
-          apart = masked;
         } else {
-          if (masked) {
-#pragma unroll
-            for (int c = 0; c < kTile; c += 32) mask(s + c, c);
-          }
-          bound = -INFINITY;
-#pragma unroll
-          for (int c = 0; c < kTile; c += 32) bound = largest(s + c, c, bound);
           bound *= mul;
         }
         float off = ev, slope = 0.f;
@@ -1025,33 +1046,43 @@ __device__ __forceinline__ bool softmax_role(Shared<D, F8>& S, const TilesLaunch
           bound = fmaf(-ln.slope, ln.slope >= 0.f ? lo : hi, bound);
           slope = d0 < 0.f ? -ln.slope : ln.slope;
           off = fmaf(-slope, d0, ev);
-          apart = apart || (d0 >= 0.f && d1 < 0.f && ln.n > ln.pos + 1);  // keys on both sides of the position
+          quick = quick && !(d0 >= 0.f && d1 < 0.f && ln.n > ln.pos + 1);  // no keys on both sides of the position
         }
-        if (__all_sync(0xffffffffu, !ln.live || (!apart && bound + ev <= m + kPassed<F8>))) {
-          off -= m == -INFINITY ? 0.f : m;
-          const float x1 = MOD & kCap ? mul * inv_cap : mul;
-          const uint64_t off_2 = pair(off, off), x_2 = pair(x1, x1), slope_2 = pair(slope, slope);
-          uint64_t q_2[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) q_2[j] = pair(cap * tanh_near(j), cap * tanh_near(j));
-          uint64_t sum = pair(0.f, 0.f);
-#pragma unroll
-          for (int c = 0; c < kTile; c += 32) {
-            sum = add2(sum, changed_weights32<F8, MOD>(s + c, c, x_2, q_2, off_2, slope_2));
-            tmem_st16(ts + c / 2, s + c);
-            if (c == 32) hand_over(0);
-          }
-          hand_over(1);
-          float a, b;
-          unpair(sum, a, b);
-          l = fmaf(a + b, un_ev, l);
+        if (!__all_sync(0xffffffffu, !ln.live || (quick && bound + ev <= m + kPassed<F8>))) {
+          rough_path(nullptr);
           continue;
         }
+        off -= m == -INFINITY ? 0.f : m;
+        const float x1 = MOD & kCap ? mul * inv_cap : mul;
+        const uint64_t off_2 = pair(off, off), x_2 = pair(x1, x1), slope_2 = pair(slope, slope);
+        uint64_t q_2[4];
 #pragma unroll
-        for (int c = 0; c < kTile; c += 32) change32<MOD>(s + c, c, mul, ch);
-        mul = 1.f;
+        for (int j = 0; j < 4; ++j) q_2[j] = pair(cap * tanh_near(j), cap * tanh_near(j));
+        uint64_t sum = pair(0.f, 0.f);
+        if (!masked) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            sum = add2(sum, changed_weights32<F8, MOD, false>(s + 32 * c, 32 * c, x_2, q_2, off_2, slope_2, ~0u));
+            tmem_st16(ts + 16 * c, s + 32 * c);
+            if (c == 1) hand_over(0);
+          }
+        } else {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const int at = t0 + 32 * c;
+            const uint32_t see = seen32<MOD>(ln.n - at, ln.first - at, ln.sinks - at, ln.start - at, bad >> (2 * c));
+            sum = add2(sum, changed_weights32<F8, MOD, true>(s + 32 * c, 32 * c, x_2, q_2, off_2, slope_2, see));
+            tmem_st16(ts + 16 * c, s + 32 * c);
+            if (c == 1) hand_over(0);
+          }
+        }
+        hand_over(1);
+        float a, b;
+        unpair(sum, a, b);
+        l = fmaf(a + b, un_ev, l);
+        continue;
       }
-      if (masked && (!MOD || (MOD & kCap) || !(MOD & kBias))) {
+      if (masked) {
 #pragma unroll
         for (int c = 0; c < kTile; c += 32) mask(s + c, c);
       }
