@@ -745,7 +745,8 @@ __device__ __forceinline__ uint64_t changed_weights32(uint32_t* s, int c0, uint6
     if (MOD & kCap) {
       uint64_t y[4], q[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) x[j] = mul2(x[j], mul_2);
+      for (int j = 0; j < 4; ++j)
+        if (F8) x[j] = mul2(x[j], mul_2);
 #pragma unroll
       for (int j = 0; j < 4; ++j) y[j] = mul2(x[j], x[j]);
 #pragma unroll
@@ -825,11 +826,16 @@ __device__ __noinline__ float2 rough_tile(uint32_t ts, uint32_t to, float2 ml, f
     tmem_ld32(ts + c0, s);
     tmem_ld_wait32(s);
     scaled(c0);
+    if (kChanged) {  // the second time they are read as they are
+      tmem_st16(ts + c0, s);
+      tmem_st16(ts + c0 + 16, s + 16);
+    }
     float t[4] = {top, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
     for (int c = 0; c < 32; c += 2) t[c / 2 & 3] = max3(t[c / 2 & 3], __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
     top = fmaxf(max3(t[0], t[1], t[2]), t[3]);
   }
+  if (kChanged) tmem_st_wait();
   top = fmaf(top, mul1, ev);
   const bool up = top > ml.x + kPassed<F8>;
   if (__any_sync(0xffffffffu, up)) {
@@ -845,7 +851,7 @@ __device__ __noinline__ float2 rough_tile(uint32_t ts, uint32_t to, float2 ml, f
   for (int c0 = 0; c0 < kTile; c0 += 32) {  // weights of chunk c go over scores of chunk c / 2
     tmem_ld32(ts + c0, s);
     tmem_ld_wait32(s);
-    scaled(c0);
+    if (!kChanged) scaled(c0);
 #pragma unroll
     for (int c = 0; c < 32; c += 2) {
       const float f = !kChanged || factors ? factors[(c0 + c) / 16].y : 1.f;
@@ -1015,11 +1021,6 @@ __device__ __forceinline__ bool softmax_role(Shared<D, F8>& S, const TilesLaunch
         __syncwarp();
         if (lane == 0) arrive_first<PAIR>(&S.p_ready[x][half]);
       };
-      uint32_t s[kTile];
-#pragma unroll
-      for (int c = 0; c < kTile; c += 32) tmem_ld32(ts + c, s + c);
-#pragma unroll
-      for (int c = 0; c < kTile; c += 32) tmem_ld_wait32(s + c);
       if constexpr ((MOD & (kCap | kBias)) != 0) {
         // A bound of the row's changed scores, cheaper than their maximum: while
         // it does not pass the running maximum, that stays, and change and
@@ -1029,12 +1030,18 @@ __device__ __forceinline__ bool softmax_role(Shared<D, F8>& S, const TilesLaunch
         // columns ahead of their use, leaves more registers and is slower: 1001
         // against 873 us.)
         float bound = MOD & kCap ? 0.f : -INFINITY;
+        uint32_t u[2][32];
+        tmem_ld32(ts, u[0]);
 #pragma unroll
-        for (int c = 0; c < kTile; c += 32) bound = MOD & kCap ? largest32(s + c, bound) : largest(s + c, c, bound);
+        for (int c = 0; c < 4; ++c) {
+          tmem_ld_wait32(u[c & 1]);
+          tmem_ld32(ts + 32 * (c + 1) % kTile, u[(c + 1) & 1]);  // at last the first again
+          bound = MOD & kCap ? largest32(u[c & 1], bound) : largest(u[c & 1], 0, bound);
+        }
         bool quick = true;
         if (MOD & kCap) {
           const float t = bound * (mul * inv_cap), y = t * t;
-          quick = t <= kNear;
+          quick = t <= kNear && (F8 || (mul * inv_cap > 0x1p-17f && mul * inv_cap < 0x1p17f));  // whose 7th power is normal
           bound = cap * (t * fmaf(fmaf(fmaf(tanh_near(3), y, tanh_near(2)), y, tanh_near(1)), y, tanh_near(0)));
         } else {
           bound *= mul;
@@ -1048,31 +1055,50 @@ __device__ __forceinline__ bool softmax_role(Shared<D, F8>& S, const TilesLaunch
           off = fmaf(-slope, d0, ev);
           quick = quick && !(d0 >= 0.f && d1 < 0.f && ln.n > ln.pos + 1);  // no keys on both sides of the position
         }
+        tmem_ld_wait32(u[0]);
         if (!__all_sync(0xffffffffu, !ln.live || (quick && bound + ev <= m + kPassed<F8>))) {
           rough_path(nullptr);
           continue;
         }
         off -= m == -INFINITY ? 0.f : m;
         const float x1 = MOD & kCap ? mul * inv_cap : mul;
+        // the polynomial in the scores themselves, or (e4m3, whose products are of any
+        // size) in the scores over the cap
+        float qc[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) qc[j] = cap * tanh_near(j);
+        if (!F8) {
+          const float y1 = x1 * x1;
+          float f = x1;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            qc[j] *= f;
+            f *= y1;
+          }
+        }
         const uint64_t off_2 = pair(off, off), x_2 = pair(x1, x1), slope_2 = pair(slope, slope);
         uint64_t q_2[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) q_2[j] = pair(cap * tanh_near(j), cap * tanh_near(j));
+        for (int j = 0; j < 4; ++j) q_2[j] = pair(qc[j], qc[j]);
         uint64_t sum = pair(0.f, 0.f);
         if (!masked) {
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            sum = add2(sum, changed_weights32<F8, MOD, false>(s + 32 * c, 32 * c, x_2, q_2, off_2, slope_2, ~0u));
-            tmem_st16(ts + 16 * c, s + 32 * c);
+            if (c) tmem_ld_wait32(u[c & 1]);
+            if (c < 3) tmem_ld32(ts + 32 * (c + 1), u[(c + 1) & 1]);
+            sum = add2(sum, changed_weights32<F8, MOD, false>(u[c & 1], 32 * c, x_2, q_2, off_2, slope_2, ~0u));
+            tmem_st16(ts + 16 * c, u[c & 1]);
             if (c == 1) hand_over(0);
           }
         } else {
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
+            if (c) tmem_ld_wait32(u[c & 1]);
+            if (c < 3) tmem_ld32(ts + 32 * (c + 1), u[(c + 1) & 1]);
             const int at = t0 + 32 * c;
             const uint32_t see = seen32<MOD>(ln.n - at, ln.first - at, ln.sinks - at, ln.start - at, bad >> (2 * c));
-            sum = add2(sum, changed_weights32<F8, MOD, true>(s + 32 * c, 32 * c, x_2, q_2, off_2, slope_2, see));
-            tmem_st16(ts + 16 * c, s + 32 * c);
+            sum = add2(sum, changed_weights32<F8, MOD, true>(u[c & 1], 32 * c, x_2, q_2, off_2, slope_2, see));
+            tmem_st16(ts + 16 * c, u[c & 1]);
             if (c == 1) hand_over(0);
           }
         }
@@ -1082,6 +1108,11 @@ __device__ __forceinline__ bool softmax_role(Shared<D, F8>& S, const TilesLaunch
         l = fmaf(a + b, un_ev, l);
         continue;
       }
+      uint32_t s[kTile];
+#pragma unroll
+      for (int c = 0; c < kTile; c += 32) tmem_ld32(ts + c, s + c);
+#pragma unroll
+      for (int c = 0; c < kTile; c += 32) tmem_ld_wait32(s + c);
       if (masked) {
 #pragma unroll
         for (int c = 0; c < kTile; c += 32) mask(s + c, c);
