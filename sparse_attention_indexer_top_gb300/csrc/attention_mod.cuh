@@ -38,12 +38,17 @@ __host__ __device__ constexpr float tanh_q(int i) {
   return q[i];
 }
 
-// The same with four coefficients for |t| <= 1/2, where most scores lie:
-// relative error 5.5e-7, a score moved by 2^-20.8 of itself, which is below what
-// an fp32 sum of 64 or 128 products may be off by.
-constexpr float kNear = 0.5f;
+// The same with four coefficients for |t| <= 1/2, where most scores lie
+// (relative error 5.5e-7), and with three for |t| <= 1/4 (4.0e-7): a score is
+// moved by 2^-20.8 of itself, which is below what an fp32 sum of 64 or 128
+// products may be off by.
+constexpr float kNear = 0.5f, kNearest = 0.25f;
 __host__ __device__ constexpr float tanh_near(int i) {
   constexpr float q[4] = {0.9999994558f, -0.3332631794f, 0.1319029659f, -0.04440222584f};
+  return q[i];
+}
+__host__ __device__ constexpr float tanh_nearest(int i) {
+  constexpr float q[3] = {0.9999996043f, -0.3332190823f, 0.1284161343f};
   return q[i];
 }
 

@@ -62,6 +62,7 @@
 #include <algorithm>
 #include <climits>
 #include <cmath>
+#include <type_traits>
 
 #include "attention_mod.cuh"
 #include "sai_internal.h"
@@ -724,8 +725,8 @@ __device__ __forceinline__ void change32(uint32_t* s, int c0, float mul, const C
 // s[0..16), and what they add up to: change and exponent in one go. The bias is
 // linear in the column, slope * column and part of `off`; MASKED: columns without
 // their bit in `see` get 0.
-template <bool F8, int MOD, bool MASKED>
-__device__ __forceinline__ uint64_t changed_weights32(uint32_t* s, int c0, uint64_t mul_2, const uint64_t (&q_2)[4],
+template <bool F8, int MOD, int Q, bool MASKED>
+__device__ __forceinline__ uint64_t changed_weights32(uint32_t* s, int c0, uint64_t mul_2, const uint64_t (&q_2)[Q],
                                                       uint64_t off_2, uint64_t slope_2, uint32_t see) {
   uint64_t sum[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
   uint64_t col = pair(static_cast<float>(c0), static_cast<float>(c0 + 1));
@@ -750,11 +751,11 @@ __device__ __forceinline__ uint64_t changed_weights32(uint32_t* s, int c0, uint6
 #pragma unroll
       for (int j = 0; j < 4; ++j) y[j] = mul2(x[j], x[j]);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) q[j] = fma2(q_2[3], y[j], q_2[2]);
+      for (int j = 0; j < 4; ++j) q[j] = q_2[Q - 1];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) q[j] = fma2(q[j], y[j], q_2[1]);
+      for (int k = Q - 2; k >= 0; --k)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) q[j] = fma2(q[j], y[j], q_2[0]);
+        for (int j = 0; j < 4; ++j) q[j] = fma2(q[j], y[j], q_2[k]);
 #pragma unroll
       for (int j = 0; j < 4; ++j) w[j] = fma2(x[j], q[j], w[j]);
     } else {
@@ -1038,9 +1039,10 @@ __device__ __forceinline__ bool softmax_role(Shared<D, F8>& S, const TilesLaunch
           tmem_ld32(ts + 32 * (c + 1) % kTile, u[(c + 1) & 1]);  // at last the first again
           bound = MOD & kCap ? largest32(u[c & 1], bound) : largest(u[c & 1], 0, bound);
         }
-        bool quick = true;
+        bool quick = true, nearest = false;
         if (MOD & kCap) {
           const float t = bound * (mul * inv_cap), y = t * t;
+          nearest = __all_sync(0xffffffffu, !ln.live || t <= kNearest);
           quick = t <= kNear && (F8 || (mul * inv_cap > 0x1p-17f && mul * inv_cap < 0x1p17f));  // whose 7th power is normal
           bound = cap * (t * fmaf(fmaf(fmaf(tanh_near(3), y, tanh_near(2)), y, tanh_near(1)), y, tanh_near(0)));
         } else {
@@ -1062,45 +1064,45 @@ __device__ __forceinline__ bool softmax_role(Shared<D, F8>& S, const TilesLaunch
         }
         off -= m == -INFINITY ? 0.f : m;
         const float x1 = MOD & kCap ? mul * inv_cap : mul;
+        const uint64_t off_2 = pair(off, off), x_2 = pair(x1, x1), slope_2 = pair(slope, slope);
+        uint64_t sum = pair(0.f, 0.f);
         // the polynomial in the scores themselves, or (e4m3, whose products are of any
         // size) in the scores over the cap
-        float qc[4];
+        auto coefficients = [&](auto& q_2, auto value) {
+          constexpr int Q = sizeof(q_2) / sizeof(q_2[0]);
+          float f = F8 ? cap : cap * x1;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) qc[j] = cap * tanh_near(j);
-        if (!F8) {
-          const float y1 = x1 * x1;
-          float f = x1;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            qc[j] *= f;
-            f *= y1;
+          for (int j = 0; j < Q; ++j) {
+            q_2[j] = pair(f * value(j), f * value(j));
+            if (!F8) f *= x1 * x1;
           }
-        }
-        const uint64_t off_2 = pair(off, off), x_2 = pair(x1, x1), slope_2 = pair(slope, slope);
-        uint64_t q_2[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) q_2[j] = pair(qc[j], qc[j]);
-        uint64_t sum = pair(0.f, 0.f);
-        if (!masked) {
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            if (c) tmem_ld_wait32(u[c & 1]);
-            if (c < 3) tmem_ld32(ts + 32 * (c + 1), u[(c + 1) & 1]);
-            sum = add2(sum, changed_weights32<F8, MOD, false>(u[c & 1], 32 * c, x_2, q_2, off_2, slope_2, ~0u));
-            tmem_st16(ts + 16 * c, u[c & 1]);
-            if (c == 1) hand_over(0);
-          }
-        } else {
+        };
+        auto go = [&](const auto& q_2, auto masks) {
+          constexpr int Q = sizeof(q_2) / sizeof(q_2[0]);
+          constexpr bool MASKED = decltype(masks)::value;
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             if (c) tmem_ld_wait32(u[c & 1]);
             if (c < 3) tmem_ld32(ts + 32 * (c + 1), u[(c + 1) & 1]);
             const int at = t0 + 32 * c;
-            const uint32_t see = seen32<MOD>(ln.n - at, ln.first - at, ln.sinks - at, ln.start - at, bad >> (2 * c));
-            sum = add2(sum, changed_weights32<F8, MOD, true>(u[c & 1], 32 * c, x_2, q_2, off_2, slope_2, see));
+            const uint32_t see =
+                MASKED ? seen32<MOD>(ln.n - at, ln.first - at, ln.sinks - at, ln.start - at, bad >> (2 * c)) : ~0u;
+            sum = add2(sum, changed_weights32<F8, MOD, Q, MASKED>(u[c & 1], 32 * c, x_2, q_2, off_2, slope_2, see));
             tmem_st16(ts + 16 * c, u[c & 1]);
             if (c == 1) hand_over(0);
           }
+        };
+        if (MOD & kCap && !masked && nearest) {
+          uint64_t q_2[3];
+          coefficients(q_2, [](int j) { return tanh_nearest(j); });
+          go(q_2, std::false_type());
+        } else {
+          uint64_t q_2[4];
+          coefficients(q_2, [](int j) { return tanh_near(j); });
+          if (masked)
+            go(q_2, std::true_type());
+          else
+            go(q_2, std::false_type());
         }
         hand_over(1);
         float a, b;
