@@ -5,8 +5,14 @@
 // one kernel over 16-byte units, spread over all SMs whatever the number of
 // pages, and the decisions are prefix sums over the pool's counts (which pages
 // are free) and over the requests (how many each wants), which make the answer
-// independent of the order in which CTAs run. A call is a chain of two or three
-// kernels; each is launched while the one before ends, and waits for it.
+// independent of the order in which CTAs run.
+//
+// The decisions are phases, each of which needs the whole of the one before. A
+// small call runs them in one kernel, as a cluster of eight CTAs with a barrier
+// of the cluster between phases: what such a call costs is its launches, about
+// 2 us each on the host and as much on the GPU. A large one runs a kernel for
+// each, as wide as the GPU; every kernel is launched while the one before ends,
+// and waits for it.
 #include "sai_internal.h"
 #include "sai_ptx.cuh"
 
@@ -193,43 +199,81 @@ __device__ __forceinline__ int free_page(const PoolScan& s, const int (&before)[
   return s.free_list[lo * s.chunk + k - before[lo]];
 }
 
+// Rows are dealt out to teams of TEAM threads: warps in a cluster, whole CTAs in
+// a launch as wide as the GPU. This thread's team, how many there are, and its
+// place in the team.
+struct Team {
+  int me, all, lane;
+};
+template <int TEAM>
+__device__ __forceinline__ Team team_here() {
+  const int per = blockDim.x / TEAM;
+  return Team{static_cast<int>(blockIdx.x) * per + static_cast<int>(threadIdx.x) / TEAM, static_cast<int>(gridDim.x) * per,
+              static_cast<int>(threadIdx.x) % TEAM};
+}
+template <int TEAM>
+__device__ __forceinline__ int team_sum(int x) {
+  if (TEAM == 32) return __reduce_add_sync(0xffffffffu, x);
+  int total;
+  block_scan<TEAM>(x, &total);
+  return total;
+}
+template <int TEAM>
+__device__ __forceinline__ void team_sync() {
+  if (TEAM == 32)
+    __syncwarp();
+  else
+    __syncthreads();
+}
+// End of a phase in a cluster: what its CTAs wrote is there for all of them.
+__device__ __forceinline__ void phase_end() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+constexpr int kCluster = 8;
+constexpr long long kSmallEntries = 1 << 16;
+
 // ------------------------------------------------------------------ forks
 constexpr int kForkThreads = 128;
 
 // Children's rows and lengths, and the counts before the change.
-__global__ void __launch_bounds__(kForkThreads) fork_rows_kernel(const ForkLaunch p) {
+template <int TEAM>
+__device__ __forceinline__ void fork_rows(const ForkLaunch& p) {
   if (p.out_refs != p.refs)
-    for (long long i = blockIdx.x * static_cast<long long>(kForkThreads) + threadIdx.x; i < p.num_blocks;
-         i += static_cast<long long>(gridDim.x) * kForkThreads)
+    for (long long i = blockIdx.x * static_cast<long long>(blockDim.x) + threadIdx.x; i < p.num_blocks;
+         i += static_cast<long long>(gridDim.x) * blockDim.x)
       p.out_refs[i] = p.refs[i];
-  pdl_trigger();
-  for (long long i = blockIdx.x; i < p.children; i += gridDim.x) {
+  const Team w = team_here<TEAM>();
+  for (long long i = w.me; i < p.children; i += w.all) {
     long long r = p.parents[i];
     const bool bad = r < -1 || r >= p.t.requests;
     const int len = bad || r < 0 ? 0 : p.t.lens[r];
-    if (bad && threadIdx.x == 0) atomicOr(p.status, kDevBadRowMeta);
+    if (bad && w.lane == 0) atomicOr(p.status, kDevBadRowMeta);
     if (bad || !good_len(len, p.t)) r = -1;
-    for (long long c = threadIdx.x; c < p.t.width; c += kForkThreads)
+#pragma unroll 4
+    for (long long c = w.lane; c < p.t.width; c += TEAM)
       p.t.out[i * p.t.out_stride + c] = r < 0 ? -1 : p.t.table[r * p.t.stride + c];
-    if (threadIdx.x == 0) p.out_lens[i] = r < 0 ? 0 : len;
+    if (w.lane == 0) p.out_lens[i] = r < 0 ? 0 : len;
   }
 }
 
 // Each old request's pages are held once for each child.
-__global__ void __launch_bounds__(kForkThreads) fork_refs_kernel(const ForkLaunch p) {
-  pdl_wait();
-  for (long long r = blockIdx.x; r < p.t.requests; r += gridDim.x) {
+template <int TEAM>
+__device__ __forceinline__ void fork_refs(const ForkLaunch& p) {
+  const Team w = team_here<TEAM>();
+  for (long long r = w.me; r < p.t.requests; r += w.all) {
     const int len = p.t.lens[r];
     if (!good_len(len, p.t)) {
-      if (threadIdx.x == 0) atomicOr(p.status, kDevBadRowMeta);
+      if (w.lane == 0) atomicOr(p.status, kDevBadRowMeta);
       continue;
     }
-    int mine = 0, children;
-    for (long long i = threadIdx.x; i < p.children; i += kForkThreads) mine += p.parents[i] == r;
-    block_scan<kForkThreads>(mine, &children);
+    int children = 0;
+#pragma unroll 4
+    for (long long i = w.lane; i < p.children; i += TEAM) children += p.parents[i] == r;
+    children = team_sum<TEAM>(children);
     const int pages = static_cast<int>(pages_of(len, p.t.block_size));
     bool bad = false;
-    for (int c = threadIdx.x; c < pages; c += kForkThreads) {
+#pragma unroll 4
+    for (int c = w.lane; c < pages; c += TEAM) {
       const int page = p.t.table[r * p.t.stride + c];
       if (page < 0 || page >= p.num_blocks)
         bad = true;
@@ -238,6 +282,20 @@ __global__ void __launch_bounds__(kForkThreads) fork_refs_kernel(const ForkLaunc
     }
     if (bad) atomicOr(p.status, kDevBadPage);
   }
+}
+
+__global__ void __launch_bounds__(kForkThreads) fork_rows_kernel(const ForkLaunch p) {
+  pdl_trigger();
+  fork_rows<kForkThreads>(p);
+}
+__global__ void __launch_bounds__(kForkThreads) fork_refs_kernel(const ForkLaunch p) {
+  pdl_wait();
+  fork_refs<kForkThreads>(p);
+}
+__global__ void __cluster_dims__(kCluster) __launch_bounds__(kScanThreads) fork_kernel(const ForkLaunch p) {
+  fork_rows<32>(p);
+  phase_end();
+  fork_refs<32>(p);
 }
 
 // ------------------------------------------------- growing and shrinking
@@ -313,23 +371,12 @@ __device__ __forceinline__ void plan_requests(const ResizeLaunch& p) {
   }
 }
 
-__global__ void __launch_bounds__(kScanThreads) resize_plan_kernel(const ResizeLaunch p) {
-  pdl_trigger();
-  if (blockIdx.x == 0)
-    plan_requests(p);
-  else
-    scan_chunk(p.s, blockIdx.x - 1);
-}
-
-constexpr int kApplyThreads = 128;
-
-__global__ void __launch_bounds__(kApplyThreads) resize_apply_kernel(const ResizeLaunch p) {
-  __shared__ int before[kMostChunks];
+template <int THREADS, int TEAM>
+__device__ __forceinline__ void apply_plan(const ResizeLaunch& p, int (&before)[kMostChunks]) {
   const PageTable& t = p.t;
-  pdl_wait();
-  pdl_trigger();
-  const int free = free_before<kApplyThreads>(p.s, before);
-  for (long long r = blockIdx.x; r < t.requests; r += gridDim.x) {
+  const int free = free_before<THREADS>(p.s, before);
+  const Team w = team_here<TEAM>();
+  for (long long r = w.me; r < t.requests; r += w.all) {
     const int4 x = p.plan[r];
     const int len = t.lens[r], want = p.new_lens[r], bs = t.block_size;
     const bool wants = x.y > 0 || (x.z & kKeeps);
@@ -337,7 +384,8 @@ __global__ void __launch_bounds__(kApplyThreads) resize_apply_kernel(const Resiz
     const int have = static_cast<int>(pages_of(len, bs)), to = static_cast<int>(pages_of(want, bs));
     const int copies = (x.z & kCopies) ? 1 : 0;
     bool bad = false;
-    for (long long c = threadIdx.x; c < t.width; c += kApplyThreads) {
+#pragma unroll 4
+    for (long long c = w.lane; c < t.width; c += TEAM) {
       const int old = t.table[r * t.stride + c];
       int page = old;
       if (served) {
@@ -362,32 +410,90 @@ __global__ void __launch_bounds__(kApplyThreads) resize_apply_kernel(const Resiz
       if (page != old || t.out != t.table) t.out[r * t.out_stride + c] = page;
     }
     if (bad) atomicOr(p.status, kDevBadPage);
-    __syncthreads();  // out_lens may be the lengths that the other threads read
-    if (threadIdx.x == 0) {
+    team_sync<TEAM>();  // out_lens may be the lengths that the others read
+    if (w.lane == 0) {
       p.out_lens[r] = served ? want : len;
       if ((x.z & kGood) && !served) atomicOr(p.status, kDevNoPages);
     }
   }
 }
 
-// ------------------------------------------------------------- compacting
-__global__ void __launch_bounds__(kScanThreads) compact_scan_kernel(const PoolScan s) {
-  pdl_trigger();
-  scan_chunk(s, blockIdx.x);
-}
+constexpr int kApplyThreads = 128;
 
-// Every held page's new id; the counts move, and the copies are written down.
-__global__ void __launch_bounds__(kScanThreads) compact_moves_kernel(const CompactLaunch p) {
+__global__ void __launch_bounds__(kScanThreads) resize_plan_kernel(const ResizeLaunch p) {
+  pdl_trigger();
+  if (blockIdx.x == 0)
+    plan_requests(p);
+  else
+    scan_chunk(p.s, blockIdx.x - 1);
+}
+__global__ void __launch_bounds__(kApplyThreads) resize_apply_kernel(const ResizeLaunch p) {
   __shared__ int before[kMostChunks];
-  __shared__ int below;
-  const PoolScan& s = p.s;
   pdl_wait();
   pdl_trigger();
-  const int free = free_before<kScanThreads>(s, before);
-  const int held = static_cast<int>(s.num_blocks) - free;
+  apply_plan<kApplyThreads, kApplyThreads>(p, before);
+}
+__global__ void __cluster_dims__(kCluster) __launch_bounds__(kScanThreads) resize_kernel(const ResizeLaunch p) {
+  __shared__ int before[kMostChunks];
+  pdl_trigger();
+  if (blockIdx.x == 0)
+    plan_requests(p);
+  else
+    for (int c = blockIdx.x - 1; c < p.s.chunks; c += kCluster - 1) scan_chunk(p.s, c);
+  phase_end();
+  apply_plan<kScanThreads, 32>(p, before);
+}
+
+// ------------------------------------------------------------- compacting
+// New ids of one chunk's held pages; the counts move, and the copies are written
+// down. `held` pages in all, of which `moving` move.
+__device__ __forceinline__ void move_chunk(const CompactLaunch& p, const int (&before)[kMostChunks], int held, int moving,
+                                           int chunk) {
+  __shared__ uint32_t word[kChunk / 32];
+  __shared__ int first[kChunk / 32];  // held pages before the word's
+  const PoolScan& s = p.s;
+  const long long c0 = chunk * s.chunk;
+  int rank = static_cast<int>(c0) - before[chunk];  // held pages before the chunk
+  for (long long base = c0; base < min(c0 + s.chunk, s.num_blocks); base += kChunk) {
+    const int n = static_cast<int>(min(kChunk, s.num_blocks - base));
+    const uint32_t bits = threadIdx.x * 32 < n ? s.held[base / 32 + threadIdx.x] : 0u;
+    int total;
+    const int x = rank + block_scan<kScanThreads>(__popc(bits), &total);
+    if (threadIdx.x * 32 < n) {
+      word[threadIdx.x] = bits;
+      first[threadIdx.x] = x;
+    }
+    __syncthreads();
+#pragma unroll 4
+    for (int i = threadIdx.x; i < n; i += kScanThreads) {
+      const int page = static_cast<int>(base) + i;
+      const uint32_t w = word[i / 32], bit = 1u << (i & 31);
+      int to = -1;
+      if (w & bit) {
+        to = page;
+        if (page >= held) {
+          const int j = first[i / 32] + __popc(w & (bit - 1)) - (held - moving);  // number among the pages that move
+          to = free_page(s, before, j);
+          p.src[j] = page;
+          p.dst[j] = to;
+          s.out_refs[to] = s.refs[page];
+          s.out_refs[page] = 0;
+        }
+      }
+      p.moves[page] = to;
+    }
+    rank += total;
+    __syncthreads();  // the words are written again
+  }
+}
+
+// How many pages are held, and how many of them move: as many as there are free
+// pages below that number.
+__device__ __forceinline__ int2 count_moves(const PoolScan& s, int (&before)[kMostChunks]) {
+  __shared__ int below;
+  const int held = static_cast<int>(s.num_blocks) - free_before<kScanThreads>(s, before);
   if (threadIdx.x == 0) below = 0;
   __syncthreads();
-  // free pages below `held` = pages that move
   const int last = held == s.num_blocks ? -1 : static_cast<int>(held / s.chunk);
   if (last >= 0) {
     int n = 0;
@@ -399,47 +505,21 @@ __global__ void __launch_bounds__(kScanThreads) compact_moves_kernel(const Compa
     if ((threadIdx.x & 31) == 0 && n) atomicAdd(&below, n);
   }
   __syncthreads();
-  const int moving = last < 0 ? 0 : before[last] + below;
-  if (blockIdx.x == 0 && threadIdx.x == 0) *p.count = moving;
-  const long long c0 = blockIdx.x * s.chunk;
-  int rank = static_cast<int>(c0) - before[blockIdx.x];  // held pages before the chunk
-  for (long long base = c0; base < min(c0 + s.chunk, s.num_blocks); base += kChunk) {
-    const long long p0 = base + threadIdx.x * kScanPages;
-    const uint32_t bits = p0 < s.num_blocks ? (s.held[p0 / 32] >> (p0 & 16)) & 0xffffu : 0u;
-    int total;
-    int at = rank + block_scan<kScanThreads>(__popc(bits), &total);
-    for (int i = 0; i < kScanPages && p0 + i < s.num_blocks; ++i) {
-      const int page = static_cast<int>(p0) + i;
-      int to = -1;
-      if ((bits >> i) & 1) {
-        to = page;
-        if (page >= held) {
-          const int j = at - (held - moving);  // number among the pages that move
-          to = free_page(s, before, j);
-          p.src[j] = page;
-          p.dst[j] = to;
-          s.out_refs[to] = s.refs[page];
-          s.out_refs[page] = 0;
-        }
-        ++at;
-      }
-      p.moves[page] = to;
-    }
-    rank += total;
-  }
+  return make_int2(held, last < 0 ? 0 : before[last] + below);
 }
 
-__global__ void __launch_bounds__(kForkThreads) compact_rename_kernel(const CompactLaunch p) {
+template <int TEAM>
+__device__ __forceinline__ void rename_rows(const CompactLaunch& p) {
   const PageTable& t = p.t;
-  pdl_wait();
-  pdl_trigger();
-  for (long long r = blockIdx.x; r < t.requests; r += gridDim.x) {
+  const Team w = team_here<TEAM>();
+  for (long long r = w.me; r < t.requests; r += w.all) {
     const int len = t.lens[r];
     const bool good = good_len(len, t);
-    if (!good && threadIdx.x == 0) atomicOr(p.status, kDevBadRowMeta);
+    if (!good && w.lane == 0) atomicOr(p.status, kDevBadRowMeta);
     const long long pages = good ? pages_of(len, t.block_size) : 0;
     bool bad = false;
-    for (long long c = threadIdx.x; c < t.width; c += kForkThreads) {
+#pragma unroll 4
+    for (long long c = w.lane; c < t.width; c += TEAM) {
       const int old = t.table[r * t.stride + c];
       int page = old;
       if (c < pages) {
@@ -453,6 +533,35 @@ __global__ void __launch_bounds__(kForkThreads) compact_rename_kernel(const Comp
     }
     if (bad) atomicOr(p.status, kDevBadPage);
   }
+}
+
+__global__ void __launch_bounds__(kScanThreads) compact_scan_kernel(const PoolScan s) {
+  pdl_trigger();
+  scan_chunk(s, blockIdx.x);
+}
+__global__ void __launch_bounds__(kScanThreads) compact_moves_kernel(const CompactLaunch p) {
+  __shared__ int before[kMostChunks];
+  pdl_wait();
+  pdl_trigger();
+  const int2 n = count_moves(p.s, before);
+  if (blockIdx.x == 0 && threadIdx.x == 0) *p.count = n.y;
+  move_chunk(p, before, n.x, n.y, blockIdx.x);
+}
+__global__ void __launch_bounds__(kForkThreads) compact_rename_kernel(const CompactLaunch p) {
+  pdl_wait();
+  pdl_trigger();
+  rename_rows<kForkThreads>(p);
+}
+__global__ void __cluster_dims__(kCluster) __launch_bounds__(kScanThreads) compact_kernel(const CompactLaunch p) {
+  __shared__ int before[kMostChunks];
+  pdl_trigger();
+  for (int c = blockIdx.x; c < p.s.chunks; c += kCluster) scan_chunk(p.s, c);
+  phase_end();
+  const int2 n = count_moves(p.s, before);
+  if (blockIdx.x == 0 && threadIdx.x == 0) *p.count = n.y;
+  for (int c = blockIdx.x; c < p.s.chunks; c += kCluster) move_chunk(p, before, n.x, n.y, c);
+  phase_end();
+  rename_rows<32>(p);
 }
 
 template <typename... P>
@@ -469,6 +578,9 @@ cudaError_t launch(void (*kernel)(P...), long long grid, int threads, bool depen
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
+// Whether one cluster does a call: by the entries of its tables and counts.
+bool small_call(long long entries) { return entries <= kSmallEntries; }
+
 }  // namespace
 
 void pool_chunks(long long num_blocks, PoolScan* s) {
@@ -484,6 +596,9 @@ cudaError_t launch_page_copy(const PageCopy& c, bool dependent, int num_sms, cud
 }
 
 cudaError_t launch_fork(const ForkLaunch& p, int num_sms, cudaStream_t stream) {
+  if (p.children == 0 && p.t.requests == 0 && p.out_refs == p.refs) return cudaSuccess;
+  if (small_call((p.t.requests + p.children) * p.t.width + p.num_blocks))
+    return launch(fork_kernel, kCluster, kScanThreads, false, stream, p);
   const long long most = 16LL * num_sms;
   const long long copies = p.out_refs == p.refs ? 0 : (p.num_blocks + 4 * kForkThreads - 1) / (4 * kForkThreads);
   const long long first = std::min(most, std::max(p.children, copies));
@@ -493,17 +608,21 @@ cudaError_t launch_fork(const ForkLaunch& p, int num_sms, cudaStream_t stream) {
   return launch(fork_refs_kernel, std::min(most, p.t.requests), kForkThreads, first > 0, stream, p);
 }
 
-cudaError_t launch_resize(const ResizeLaunch& p, cudaStream_t stream) {
+cudaError_t launch_resize(const ResizeLaunch& p, int num_sms, cudaStream_t stream) {
+  if (small_call(p.t.requests * p.t.width + p.s.num_blocks))
+    return launch(resize_kernel, kCluster, kScanThreads, false, stream, p);
   cudaError_t e = launch(resize_plan_kernel, 1 + p.s.chunks, kScanThreads, false, stream, p);
   if (e != cudaSuccess || p.t.requests == 0) return e;
-  return launch(resize_apply_kernel, std::min(p.t.requests, 1LL << 16), kApplyThreads, true, stream, p);
+  return launch(resize_apply_kernel, std::min(16LL * num_sms, p.t.requests), kApplyThreads, true, stream, p);
 }
 
 cudaError_t launch_compact(const CompactLaunch& p, int num_sms, cudaStream_t stream) {
+  if (small_call(p.t.requests * p.t.width + p.s.num_blocks))
+    return launch(compact_kernel, kCluster, kScanThreads, false, stream, p);
   cudaError_t e = launch(compact_scan_kernel, p.s.chunks, kScanThreads, false, stream, p.s);
   if (e == cudaSuccess) e = launch(compact_moves_kernel, p.s.chunks, kScanThreads, true, stream, p);
   if (e != cudaSuccess || p.t.requests == 0) return e;
-  return launch(compact_rename_kernel, std::min(p.t.requests, 16LL * num_sms), kForkThreads, true, stream, p);
+  return launch(compact_rename_kernel, std::min(16LL * num_sms, p.t.requests), kForkThreads, true, stream, p);
 }
 
 }  // namespace sai

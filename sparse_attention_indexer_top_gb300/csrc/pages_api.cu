@@ -22,8 +22,7 @@ constexpr uint32_t kPieceUnits = 1024;  // of page_copy_kernel's pieces
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 void divisor(uint32_t d, uint32_t* m, uint8_t* sh) {
-  int s = 0;
-  while ((1u << s) < d) ++s;
+  const int s = d > 1 ? 32 - __builtin_clz(d - 1) : 0;
   *sh = static_cast<uint8_t>(s);
   *m = static_cast<uint32_t>(((1ull << (24 + s)) + d - 1) / d);
 }
@@ -86,27 +85,27 @@ int describe(const sai_page_array& in, int32_t block_size, sai::PageArray* out) 
 }
 
 // block_size 0: pages are copied whole.
-int check_arrays(const sai_page_array* arrays, int32_t n, int64_t num_blocks, int32_t block_size) {
+// Leaves the first launch's arrays in c.
+int check_arrays(const sai_page_array* arrays, int32_t n, int64_t num_blocks, int32_t block_size, sai::PageCopy* c) {
   if (n < 0 || n > kMostArrays || num_blocks < 1 || num_blocks > kMostPages) return SAI_ERR_SHAPE;
   if (n && !arrays) return SAI_ERR_NULL;
+  c->arrays = std::min(n, sai::kPageArrays);
+  c->first[0] = 0;
   for (int32_t i = 0; i < n; ++i) {
-    sai::PageArray a;
-    const int e = describe(arrays[i], block_size, &a);
+    sai::PageArray beyond, *a = i < sai::kPageArrays ? &c->a[i] : &beyond;
+    const int e = describe(arrays[i], block_size, a);
     if (e != SAI_OK) return e;
+    if (i < sai::kPageArrays) c->first[i + 1] = c->first[i] + (a->units + kPieceUnits - 1) / kPieceUnits;
   }
   return SAI_OK;
 }
 
-// Copies the pairs in every array, as many arrays at a time as a launch takes.
+// Copies the pairs in every array, as many arrays at a time as a launch takes
+// (c has the first of them).
 int copy_arrays(sai::PageCopy& c, const sai_page_array* arrays, int32_t n, int32_t block_size, bool dependent, int sms,
                 cudaStream_t stream) {
   for (int32_t i0 = 0; i0 < n; i0 += sai::kPageArrays) {
-    c.arrays = std::min(n - i0, sai::kPageArrays);
-    c.first[0] = 0;
-    for (int i = 0; i < c.arrays; ++i) {
-      describe(arrays[i0 + i], block_size, &c.a[i]);
-      c.first[i + 1] = c.first[i] + (c.a[i].units + kPieceUnits - 1) / kPieceUnits;
-    }
+    if (i0) check_arrays(arrays + i0, n - i0, 1, block_size, &c);
     const cudaError_t e = sai::launch_page_copy(c, dependent && i0 == 0, sms, stream);
     if (e != cudaSuccess) return cuda_status(e);
   }
@@ -195,17 +194,18 @@ int sai_cache_page_arrays(const sai_kv_cache* c, sai_page_array* out) {
 
 int sai_copy_pages(const sai_page_array* arrays, int32_t num_arrays, int64_t num_blocks, const int32_t* src,
                    const int32_t* dst, int64_t pairs, sai_stream_t stream) {
-  int e = check_arrays(arrays, num_arrays, num_blocks, 0);
+  sai::PageCopy c;
+  const int e = check_arrays(arrays, num_arrays, num_blocks, 0, &c);
   if (e != SAI_OK) return e;
   if (pairs < 0 || pairs > INT_MAX) return SAI_ERR_SHAPE;
   if (pairs == 0 || num_arrays == 0) return SAI_OK;
   if (!src || !dst) return SAI_ERR_NULL;
   if (!aligned(src, 4) || !aligned(dst, 4)) return SAI_ERR_ALIGN;
-  sai::PageCopy c{};
   int dev, sms;
   if (!device_setup(&dev, &c.status, &sms)) return SAI_ERR_CUDA;
   c.src = src;
   c.dst = dst;
+  c.cells = c.count = nullptr;
   c.pairs = pairs;
   c.num_blocks = num_blocks;
   return copy_arrays(c, arrays, num_arrays, 0, false, sms, reinterpret_cast<cudaStream_t>(stream));
@@ -251,7 +251,8 @@ int sai_resize_pages(const sai_page_array* arrays, int32_t num_arrays, int64_t n
   sai::ResizeLaunch p{};
   int e = check_table(block_table, requests, width, bt_stride, seq_lens, block_size, out_table, out_stride, requests, &p.t);
   if (e != SAI_OK) return e;
-  if ((e = check_arrays(arrays, num_arrays, num_blocks, block_size)) != SAI_OK) return e;
+  sai::PageCopy c;
+  if ((e = check_arrays(arrays, num_arrays, num_blocks, block_size, &c)) != SAI_OK) return e;
   if (!refs || !out_refs || (requests && (!new_lens || !out_lens))) return SAI_ERR_NULL;
   if (!aligned(refs, 4) || !aligned(out_refs, 4) || !aligned(new_lens, 4) || !aligned(out_lens, 4)) return SAI_ERR_ALIGN;
   if ((out_table != block_table &&
@@ -261,7 +262,6 @@ int sai_resize_pages(const sai_page_array* arrays, int32_t num_arrays, int64_t n
     return SAI_ERR_SHAPE;
   if (!workspace || !aligned(workspace, 16) || workspace_bytes < sai_resize_pages_workspace(num_blocks, requests))
     return SAI_ERR_WORKSPACE;
-  sai::PageCopy c{};
   int dev, sms;
   if (!device_setup(&dev, &p.status, &sms)) return SAI_ERR_CUDA;
   lay_out(&p, num_blocks, requests, static_cast<char*>(workspace));
@@ -270,7 +270,7 @@ int sai_resize_pages(const sai_page_array* arrays, int32_t num_arrays, int64_t n
   p.new_lens = new_lens;
   p.out_lens = out_lens;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if ((e = cuda_status(sai::launch_resize(p, s))) != SAI_OK || requests == 0) return e;
+  if ((e = cuda_status(sai::launch_resize(p, sms, s))) != SAI_OK || requests == 0) return e;
   c.src = p.src;
   c.dst = p.dst;
   c.cells = p.cells;
@@ -295,7 +295,8 @@ int sai_compact_pages(const sai_page_array* arrays, int32_t num_arrays, int64_t 
   sai::CompactLaunch p{};
   int e = check_table(block_table, requests, width, bt_stride, seq_lens, block_size, out_table, out_stride, requests, &p.t);
   if (e != SAI_OK) return e;
-  if ((e = check_arrays(arrays, num_arrays, num_blocks, 0)) != SAI_OK) return e;
+  sai::PageCopy c;
+  if ((e = check_arrays(arrays, num_arrays, num_blocks, 0, &c)) != SAI_OK) return e;
   if (!refs || !out_refs || !out_moves) return SAI_ERR_NULL;
   if (!aligned(refs, 4) || !aligned(out_refs, 4) || !aligned(out_moves, 4)) return SAI_ERR_ALIGN;
   if ((out_table != block_table &&
@@ -305,7 +306,6 @@ int sai_compact_pages(const sai_page_array* arrays, int32_t num_arrays, int64_t 
     return SAI_ERR_SHAPE;
   if (!workspace || !aligned(workspace, 16) || workspace_bytes < sai_compact_pages_workspace(num_blocks))
     return SAI_ERR_WORKSPACE;
-  sai::PageCopy c{};
   int dev, sms;
   if (!device_setup(&dev, &p.status, &sms)) return SAI_ERR_CUDA;
   lay_out(&p, num_blocks, static_cast<char*>(workspace));
@@ -316,6 +316,7 @@ int sai_compact_pages(const sai_page_array* arrays, int32_t num_arrays, int64_t 
   if ((e = cuda_status(sai::launch_compact(p, sms, s))) != SAI_OK) return e;
   c.src = p.src;
   c.dst = p.dst;
+  c.cells = nullptr;
   c.count = p.count;
   c.pairs = num_blocks / 2 + 1;
   c.num_blocks = num_blocks;

@@ -292,7 +292,7 @@ struct CompactLaunch {
 void pool_chunks(long long num_blocks, PoolScan* s);  // fills num_blocks, chunk, chunks
 cudaError_t launch_page_copy(const PageCopy& c, bool dependent, int num_sms, cudaStream_t stream);
 cudaError_t launch_fork(const ForkLaunch& p, int num_sms, cudaStream_t stream);
-cudaError_t launch_resize(const ResizeLaunch& p, cudaStream_t stream);
+cudaError_t launch_resize(const ResizeLaunch& p, int num_sms, cudaStream_t stream);
 // moves and renames; the pages are copied by launch_page_copy
 cudaError_t launch_compact(const CompactLaunch& p, int num_sms, cudaStream_t stream);
 

@@ -105,7 +105,8 @@ def test_copy_more_arrays_than_a_launch_takes():
 
 @pytest.mark.parametrize("in_place", [False, True])
 @pytest.mark.parametrize("requests,children,blocks,bs,width", [(1, 1, 1, 16, 1), (5, 9, 300, 16, 20), (70, 3, 9001, 1, 40),
-                                                              (40, 130, 5000, 128, 33), (3, 0, 100, 16, 9)])
+                                                              (40, 130, 5000, 128, 33), (3, 0, 100, 16, 9),
+                                                              (300, 520, 90001, 16, 70)])
 def test_fork(requests, children, blocks, bs, width, in_place):
     table, lens, refs = _state(requests, requests, blocks, bs, width)
     rng = random.Random(children)
@@ -131,13 +132,13 @@ def test_fork_bad_metadata():
 
 def _resize_case(seed, requests, blocks, bs, width, *, nhd=False, in_place=False, free=None):
     rng = random.Random(seed)
-    table, lens, refs = _state(seed, requests, blocks, bs, width, most=max(1, blocks * bs // (2 * requests)))
+    table, lens, refs = _state(seed, requests, blocks, bs, width, most=max(1, min(width * bs, blocks * bs // (2 * requests))))
     top = width * bs
     new = [min(top, rng.choice([n, n + 1, n + 1, n + 1, 0, rng.randint(0, n), n + rng.randint(0, 3 * bs)])) for n in lens]
     if free is not None:  # all but so many of the free pages are held by others
         for page in [p for p, r in enumerate(refs) if r == 0][free:]:
             refs[page] = 1
-    p = Pool(seed, blocks, bs=bs, nhd=nhd, kinds=("bf16", "e4m3") if bs >= 16 else ())
+    p = Pool(seed, blocks, bs=bs, nhd=nhd, kinds=("bf16", "e4m3") if blocks < 50000 else ())
     before = p.snapshot()
     want = O.resize(table, lens, new, refs, bs)
     tt, tl, tn, tr = _t(table), _t(lens), _t(new), _t(refs)
@@ -154,7 +155,7 @@ def _resize_case(seed, requests, blocks, bs, width, *, nhd=False, in_place=False
 
 @pytest.mark.parametrize("nhd,in_place", [(False, False), (True, False), (False, True)])
 @pytest.mark.parametrize("requests,blocks,bs,width", [(1, 1, 16, 1), (7, 90, 16, 30), (60, 900, 32, 40), (33, 200, 128, 9),
-                                                      (600, 20000, 16, 70)])
+                                                      (600, 20000, 16, 70), (1100, 20000, 32, 60), (50, 90001, 16, 30)])
 def test_resize(requests, blocks, bs, width, nhd, in_place):
     for seed in range(3):
         _resize_case(100 * seed + requests, requests, blocks, bs, width, nhd=nhd, in_place=in_place)
@@ -198,14 +199,14 @@ def test_resize_bad_metadata():
 
 @pytest.mark.parametrize("in_place", [False, True])
 @pytest.mark.parametrize("requests,blocks,bs,width", [(1, 1, 16, 1), (4, 33, 16, 9), (30, 500, 32, 20), (9, 8193, 16, 70),
-                                                      (90, 30000, 16, 100)])
+                                                      (90, 30000, 16, 100), (200, 80000, 16, 90)])
 def test_compact(requests, blocks, bs, width, in_place):
     for seed in range(3):
         table, lens, refs = _state(seed, requests, blocks, bs, width)
         if seed == 1:  # most of the pool held by others
             rng = random.Random(5)
             refs = [r or int(rng.random() < 0.7) for r in refs]
-        p = Pool(seed, blocks, bs=bs, kinds=("e4m3",))
+        p = Pool(seed, blocks, bs=bs, kinds=("e4m3",) if blocks < 50000 else ())
         before = p.snapshot()
         want = O.compact(table, lens, refs, bs)
         tt, tr = _t(table), _t(refs)
