@@ -8,7 +8,8 @@
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
-#include <ATen/ops/empty.h>
+#include <ATen/EmptyTensor.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -130,14 +131,17 @@ sai_stream_t stream_of(const Cache& c) {
   return reinterpret_cast<sai_stream_t>(c10::cuda::getCurrentCUDAStream(c.device).stream());
 }
 
-at::Tensor fresh(at::IntArrayRef shape, at::ScalarType type, const Cache& c) {
-  return at::empty(shape, at::TensorOptions().dtype(type).device(at::Device(at::kCUDA, c.device)));
+// What at::empty gives on the current device (the cache's, which is checked
+// before), without its way through the dispatcher: 0.6 instead of 1.6 us each.
+at::Tensor fresh(at::IntArrayRef shape, at::ScalarType type) {
+  return at::detail::empty_generic(shape, c10::cuda::CUDACachingAllocator::get(),
+                                   c10::DispatchKeySet(c10::DispatchKey::CUDA), type, std::nullopt);
 }
 
 // A given output, or a new one: contiguous, of this type and shape.
 at::Tensor output(PyObject* o, const char* name, at::IntArrayRef shape, at::ScalarType type, const Cache& c) {
   const at::Tensor* t = tensor(o, name);
-  if (!t) return fresh(shape, type, c);
+  if (!t) return fresh(shape, type);
   if (!t->is_cuda() || t->get_device() != c.device || t->scalar_type() != type || t->sizes() != shape || !t->is_contiguous()) {
     std::string s;
     for (int64_t x : shape) s += (s.empty() ? "" : ", ") + std::to_string(x);
@@ -147,7 +151,7 @@ at::Tensor output(PyObject* o, const char* name, at::IntArrayRef shape, at::Scal
 }
 
 struct Space {
-  at::Tensor hold;
+  c10::DataPtr hold;
   void* p = nullptr;
   size_t bytes = 0;
 };
@@ -159,8 +163,8 @@ Space workspace_of(PyObject* o, size_t bytes, const Cache& c) {
     w.p = t->data_ptr();
     w.bytes = t->nbytes();
   } else if (bytes) {
-    w.hold = fresh({static_cast<int64_t>(bytes)}, at::kByte, c);
-    w.p = w.hold.data_ptr();
+    w.hold = c10::cuda::CUDACachingAllocator::get()->allocate(bytes);
+    w.p = w.hold.get();
     w.bytes = bytes;
   }
   return w;
@@ -338,7 +342,7 @@ Plane plane_of(const at::Tensor& t, const char* name) {
 }
 Plane plane(PyObject* o, const char* name, const Cache& c) { return plane_of(need(o, name, at::kInt, 2, c.device), name); }
 Plane out_plane(PyObject* o, int64_t rows, int64_t width, const Cache& c) {
-  if (o == Py_None) return Plane{fresh({rows, width}, at::kInt, c), rows, width, width};
+  if (o == Py_None) return Plane{fresh({rows, width}, at::kInt), rows, width, width};
   const Plane p = plane(o, "out_table", c);
   if (p.rows != rows || p.width != width)
     refuse("out_table must be [" + std::to_string(rows) + ", " + std::to_string(width) + "]");

@@ -16,8 +16,7 @@ using sai::device_setup;
 
 constexpr int64_t kMostPages = 1 << 28;
 constexpr int32_t kMostArrays = 1 << 16;
-constexpr uint32_t kMostUnits = (1u << 24) - 1024;
-constexpr uint32_t kPieceUnits = 1024;  // of page_copy_kernel's pieces
+constexpr uint32_t kMostUnits = (1u << 24) - sai::kPagePiece;
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
@@ -95,7 +94,7 @@ int check_arrays(const sai_page_array* arrays, int32_t n, int64_t num_blocks, in
     sai::PageArray beyond, *a = i < sai::kPageArrays ? &c->a[i] : &beyond;
     const int e = describe(arrays[i], block_size, a);
     if (e != SAI_OK) return e;
-    if (i < sai::kPageArrays) c->first[i + 1] = c->first[i] + (a->units + kPieceUnits - 1) / kPieceUnits;
+    if (i < sai::kPageArrays) c->first[i + 1] = c->first[i] + (a->units + sai::kPagePiece - 1) / sai::kPagePiece;
   }
   return SAI_OK;
 }

@@ -226,7 +226,8 @@ struct PageArray {
   int8_t cells;                   // the page's tokens are 0: outer, 1: inner rows, 2: cell_units of the row, -1: copied whole
   uint32_t cell_units;
 };
-constexpr int kPageArrays = 32;  // of one launch
+constexpr int kPageArrays = 32;       // of one launch
+constexpr uint32_t kPagePiece = 1024;  // units that a CTA copies at a time
 struct PageCopy {
   PageArray a[kPageArrays];
   uint32_t first[kPageArrays + 1];  // pieces of a page before array i
