@@ -425,15 +425,47 @@ __global__ void __launch_bounds__(kThreads) attn_rows_kernel(const AttnLaunch p)
     if (head_in_group + h0 < p.group) slope0 = p.slopes[head0 + h0] * 1.44269504088896340736f;
     if (head_in_group + h1 < p.group) slope1 = p.slopes[head0 + h1] * 1.44269504088896340736f;
   }
-  const int pos = biased ? p.seq_lens[row] - 1 : 0;
-  // distance of key `key` of group kg of stage s
-  auto distance = [&](int s, int kg, int key) -> float {
-    const int j = k_begin + (first + s * STEP) * SK + kg * 16 + key;
-    return static_cast<float>(abs(pos - (j < rk.low ? j + rk.start : j + rk.shift)));
+  // distance of key 0 of the first stage's first group, were all keys behind the
+  // row's first tokens
+  const int ahead0 = biased ? p.seq_lens[row] - 1 - rk.shift - k_begin - first * SK : 0;
+  // distances of the lane's key `key` of group kg of stage s, and of key + step
+  auto distances = [&](int s, int kg, int key, int step, float& d0, float& d1) {
+    const int j = s * STEP * SK + kg * 16 + key;  // behind key 0
+    const int a = ahead0 - j;
+    d0 = fabsf(static_cast<float>(a));
+    d1 = fabsf(static_cast<float>(a - step));
+    if (rk.low > 0) {  // first tokens before the window
+      const int at = k_begin + first * SK + j, back = rk.shift - rk.start;
+      if (at < rk.low) d0 = fabsf(static_cast<float>(a + back));
+      if (at + step < rk.low) d1 = fabsf(static_cast<float>(a - step + back));
+    }
   };
-  auto changed = [&](float x, float slope, float dist) -> float {
-    if (cap > 0.f) x = capped(x, cap, inv_cap);
-    return biased ? fmaf(-slope, dist, x) : x;
+  // The lane's four scores, two keys of two heads: x[head][key]
+  auto change = [&](float (&x)[2][2], float d0, float d1) {
+    if (cap > 0.f) {
+      float t[4], most = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        t[i] = x[i / 2][i % 2] * inv_cap;
+        most = fmaxf(most, fabsf(t[i]));
+      }
+      if (__all_sync(0xffffffffu, most <= kNear)) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float y = t[i] * t[i];
+          x[i / 2][i % 2] *= fmaf(fmaf(fmaf(tanh_near(3), y, tanh_near(2)), y, tanh_near(1)), y, tanh_near(0));
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i / 2][i % 2] = capped(x[i / 2][i % 2], cap, inv_cap);
+      }
+    }
+    if (biased) {
+      x[0][0] = fmaf(-slope0, d0, x[0][0]);
+      x[0][1] = fmaf(-slope0, d1, x[0][1]);
+      x[1][0] = fmaf(-slope1, d0, x[1][0]);
+      x[1][1] = fmaf(-slope1, d1, x[1][1]);
+    }
   };
 
   constexpr int NO = FEW ? 1 : 2;  // accumulator tiles per 16 dims
@@ -510,13 +542,20 @@ __global__ void __launch_bounds__(kThreads) attn_rows_kernel(const AttnLaunch p)
             }
             c[2 * n] *= k0;
             c[2 * n + 1] *= k1;
-            if (MOD) {
-              const float dist = biased ? distance(s, kg, key) : 0.f;
-              c[2 * n] = changed(c[2 * n], slope0, dist);
-              c[2 * n + 1] = changed(c[2 * n + 1], slope1, dist);
+            if (!MOD) {
+              c[2 * n] = on ? c[2 * n] : -INFINITY;
+              c[2 * n + 1] = on ? c[2 * n + 1] : -INFINITY;
             }
-            c[2 * n] = on ? c[2 * n] : -INFINITY;
-            c[2 * n + 1] = on ? c[2 * n + 1] : -INFINITY;
+          }
+          if (MOD) {
+            float x[2][2] = {{c[0], c[2]}, {c[1], c[3]}}, d0 = 0.f, d1 = 0.f;
+            if (biased) distances(s, kg, g, 8, d0, d1);
+            change(x, d0, d1);
+            const bool on0 = (live >> g) & 1, on1 = (live >> (g + 8)) & 1;
+            c[0] = on0 ? x[0][0] : -INFINITY;
+            c[1] = on0 ? x[1][0] : -INFINITY;
+            c[2] = on1 ? x[0][1] : -INFINITY;
+            c[3] = on1 ? x[1][1] : -INFINITY;
           }
           float x0 = fmaxf(c[0] + ev[0], c[2] + ev[1]), x1 = fmaxf(c[1] + ev[0], c[3] + ev[1]);
           if (__any_sync(0xffffffffu, x0 > m0 + kPassed<F8> || x1 > m1 + kPassed<F8>)) {
@@ -612,9 +651,9 @@ __global__ void __launch_bounds__(kThreads) attn_rows_kernel(const AttnLaunch p)
         // that multiply v codes then fit f16 whatever the scales; l adds the
         // same weights without the scale.
         float x0 = -INFINITY, x1 = -INFINITY;
-        float vs[2][2];
+        float vs[2][2], evs[2][2];
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
+        for (int n = 0; n < 2; ++n) {
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const int key = 8 * n + 2 * t + e;
@@ -628,16 +667,29 @@ __global__ void __launch_bounds__(kThreads) attn_rows_kernel(const AttnLaunch p)
             const bool on = (live >> key) & 1;
             c[n][e] *= sc0 * ks;
             c[n][e + 2] *= sc1 * ks;
-            if (MOD) {
-              const float dist = biased ? distance(s, kg, key) : 0.f;
-              c[n][e] = changed(c[n][e], slope0, dist);
-              c[n][e + 2] = changed(c[n][e + 2], slope1, dist);
+            evs[n][e] = ev;
+            if (!MOD) {
+              c[n][e] = on ? c[n][e] : -INFINITY;
+              c[n][e + 2] = on ? c[n][e + 2] : -INFINITY;
             }
-            c[n][e] = on ? c[n][e] : -INFINITY;
-            c[n][e + 2] = on ? c[n][e + 2] : -INFINITY;
-            x0 = fmaxf(x0, c[n][e] + ev);
-            x1 = fmaxf(x1, c[n][e + 2] + ev);
           }
+          if (MOD) {
+            float x[2][2] = {{c[n][0], c[n][1]}, {c[n][2], c[n][3]}}, d0 = 0.f, d1 = 0.f;
+            if (biased) distances(s, kg, 8 * n + 2 * t, 1, d0, d1);
+            change(x, d0, d1);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const bool on = (live >> (8 * n + 2 * t + e)) & 1;
+              c[n][e] = on ? x[0][e] : -INFINITY;
+              c[n][e + 2] = on ? x[1][e] : -INFINITY;
+            }
+          }
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            x0 = fmaxf(x0, c[n][e] + evs[n][e]);
+            x1 = fmaxf(x1, c[n][e + 2] + evs[n][e]);
+          }
+        }
         if (__any_sync(0xffffffffu, x0 > m0 + kPassed<F8> || x1 > m1 + kPassed<F8>)) {
 #pragma unroll
           for (int f = 1; f < 4; f <<= 1) {
