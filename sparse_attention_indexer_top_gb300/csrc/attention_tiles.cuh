@@ -906,7 +906,14 @@ __device__ __forceinline__ bool softmax_role(Shared<D, F8>& S, const TilesLaunch
     ln.n = ln.live ? S.row_n[local] : 0;
     ln.first = p.window > 0 ? max(0, ln.n - p.window) : 0;
     ln.sinks = min(p.sinks, ln.first);
-    ln.head = static_cast<long long>(ln.row) * p.q_heads + pc.kvh * p.group + r % p.group;
+    // the row's head, and its place among the partial results (-1: final). MOD: known
+    // at the end alone, the loop has no registers to keep them in.
+    long long part = -1;
+    auto place = [&]() {
+      ln.head = static_cast<long long>(ln.row) * p.q_heads + pc.kvh * p.group + r % p.group;
+      part = pc.slot < 0 ? -1 : (static_cast<long long>(pc.slot) * 2 * PAIR * L.rows_per_tile + local) * p.group + r % p.group;
+    };
+    if (!MOD) place();
     if constexpr (MOD != 0) {
       ln.start = ln.pos = 0;
       ln.slope = 0.f;
@@ -920,10 +927,9 @@ __device__ __forceinline__ bool softmax_role(Shared<D, F8>& S, const TilesLaunch
         if (MOD & kBias) ln.slope = p.slopes[pc.kvh * p.group + r % p.group] * 1.44269504088896340736f;
       }
     }
-    // -1: final
-    const long long part = pc.slot < 0 ? -1 : (static_cast<long long>(pc.slot) * 2 * PAIR * L.rows_per_tile + local) * p.group + r % p.group;
     float m = -INFINITY, l = 0.f;
     if (ps.i0 == ps.i1) {
+      if (MOD) place();
       const float o[32] = {};
 #pragma unroll 1
       for (int c = 0; c < D; c += 32) write_columns<D, MOD>(p, ln, part, l, c, o, S.stage[warp]);
@@ -1165,6 +1171,7 @@ __device__ __forceinline__ bool softmax_role(Shared<D, F8>& S, const TilesLaunch
     __syncwarp();
     ++at.passes;
     tc_fence_after();
+    if (MOD) place();
     bool extra = *reinterpret_cast<volatile int*>(&S.nonfinite) != 0;
     if (PAIR == 2) {
       int other;
