@@ -7,12 +7,13 @@
 // are free) and over the requests (how many each wants), which make the answer
 // independent of the order in which CTAs run.
 //
-// The decisions are phases, each of which needs the whole of the one before. A
-// small call runs them in one kernel, as a cluster of eight CTAs with a barrier
-// of the cluster between phases: what such a call costs is its launches, about
-// 2 us each on the host and as much on the GPU. A large one runs a kernel for
-// each, as wide as the GPU; every kernel is launched while the one before ends,
-// and waits for it.
+// The decisions are phases, each of which needs the whole of the one before. What
+// a small call costs is its launches, about 2 us each on the host and as much on
+// the GPU, and a trip to L2 for each step of a phase. So tables are written by the
+// same launch as the copies, beside them, and the phases before are one kernel
+// for small calls, a cluster of eight CTAs with a barrier of the cluster between
+// them; for large ones each is a kernel as wide as the GPU. Every kernel is
+// launched while the one before ends, and waits for it.
 #include "sai_internal.h"
 #include "sai_ptx.cuh"
 
@@ -52,35 +53,18 @@ __device__ __forceinline__ void copy_piece(const PageArray& a, long long src, lo
     if (at[i] >= 0) *reinterpret_cast<V*>(a.base + dst * a.page_stride + at[i]) = x[i];
 }
 
-__global__ void __launch_bounds__(kCopyThreads) page_copy_kernel(const __grid_constant__ PageCopy c) {
-  pdl_wait();
-  const long long pairs = c.count ? *c.count : c.pairs;
-  const uint32_t pieces = c.first[c.arrays];
-  const uint32_t step_pair = gridDim.x / pieces, step_piece = gridDim.x % pieces;
-  long long pair = blockIdx.x / pieces;
-  uint32_t piece = blockIdx.x % pieces;
-  while (pair < pairs) {
-    const int src = c.src[pair], dst = c.dst[pair];
-    if (src >= 0 && dst >= 0 && src != dst) {
-      if (src < c.num_blocks && dst < c.num_blocks) {
-        int lo = 0, hi = c.arrays - 1;  // the array with first[i] <= piece < first[i + 1]
-        while (lo < hi) {
-          const int mid = (lo + hi + 1) >> 1;
-          if (c.first[mid] <= piece)
-            lo = mid;
-          else
-            hi = mid - 1;
-        }
-        const uint32_t u0 = (piece - c.first[lo]) * kPagePiece;
-        const uint32_t cells = c.cells ? static_cast<uint32_t>(c.cells[pair]) : 1u << 16;
-        if (c.a[lo].wide)
-          copy_piece<uint4>(c.a[lo], src, dst, u0, cells);
-        else
-          copy_piece<uint32_t>(c.a[lo], src, dst, u0, cells);
-      } else if (piece == 0 && threadIdx.x == 0) {
-        atomicOr(c.status, kDevBadPage);
-      }
-    }
+// What a CTA copies at a time: pair, and piece of the pair's pages.
+struct CopyWalk {
+  long long pair;
+  uint32_t piece, pieces, step_pair, step_piece;
+  __device__ __forceinline__ CopyWalk(const PageCopy& c, uint32_t cta, uint32_t ctas) {
+    pieces = c.first[c.arrays];
+    step_pair = ctas / pieces;
+    step_piece = ctas % pieces;
+    pair = cta / pieces;
+    piece = cta % pieces;
+  }
+  __device__ __forceinline__ void next() {
     pair += step_pair;
     piece += step_piece;
     if (piece >= pieces) {
@@ -88,6 +72,43 @@ __global__ void __launch_bounds__(kCopyThreads) page_copy_kernel(const __grid_co
       ++pair;
     }
   }
+};
+
+__device__ __forceinline__ void copy_page(const PageCopy& c, uint32_t piece, int src, int dst, uint32_t cells) {
+  int lo = 0, hi = c.arrays - 1;  // the array with first[i] <= piece < first[i + 1]
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (c.first[mid] <= piece)
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  const uint32_t u0 = (piece - c.first[lo]) * kPagePiece;
+  if (c.a[lo].wide)
+    copy_piece<uint4>(c.a[lo], src, dst, u0, cells);
+  else
+    copy_piece<uint32_t>(c.a[lo], src, dst, u0, cells);
+}
+
+// The pairs of c.src and c.dst, by `ctas` CTAs of which this is number `cta`.
+__device__ __forceinline__ void copy_pairs(const PageCopy& c, uint32_t cta, uint32_t ctas) {
+  CopyWalk w(c, cta, ctas);
+  const long long pairs = c.count ? *c.count : c.pairs;
+  // there is room for c.pairs: the first pair is read along with their number
+  for (bool go = w.pair < c.pairs; go; w.next(), go = w.pair < pairs) {
+    const int src = c.src[w.pair], dst = c.dst[w.pair];
+    if (w.pair >= pairs) return;
+    if (src < 0 || dst < 0 || src == dst) continue;
+    if (src < c.num_blocks && dst < c.num_blocks)
+      copy_page(c, w.piece, src, dst, 0);
+    else if (w.piece == 0 && threadIdx.x == 0)
+      atomicOr(c.status, kDevBadPage);
+  }
+}
+
+__global__ void __launch_bounds__(kCopyThreads) page_copy_kernel(const __grid_constant__ PageCopy c) {
+  pdl_wait();
+  copy_pairs(c, blockIdx.x, gridDim.x);
 }
 
 // ------------------------------------------------------- sums over a CTA
@@ -203,15 +224,15 @@ __device__ __forceinline__ int free_page(const PoolScan& s, const int (&before)[
 }
 
 // Rows are dealt out to teams of TEAM threads: warps in a cluster, whole CTAs in
-// a launch as wide as the GPU. This thread's team, how many there are, and its
-// place in the team.
+// a launch as wide as the GPU. This thread's team, how many there are in `ctas`
+// CTAs, and its place in the team.
 struct Team {
   int me, all, lane;
 };
 template <int TEAM>
-__device__ __forceinline__ Team team_here() {
+__device__ __forceinline__ Team team_here(int ctas) {
   const int per = blockDim.x / TEAM;
-  return Team{static_cast<int>(blockIdx.x) * per + static_cast<int>(threadIdx.x) / TEAM, static_cast<int>(gridDim.x) * per,
+  return Team{static_cast<int>(blockIdx.x) * per + static_cast<int>(threadIdx.x) / TEAM, ctas * per,
               static_cast<int>(threadIdx.x) % TEAM};
 }
 template <int TEAM>
@@ -245,7 +266,7 @@ __device__ __forceinline__ void fork_rows(const ForkLaunch& p) {
     for (long long i = blockIdx.x * static_cast<long long>(blockDim.x) + threadIdx.x; i < p.num_blocks;
          i += static_cast<long long>(gridDim.x) * blockDim.x)
       p.out_refs[i] = p.refs[i];
-  const Team w = team_here<TEAM>();
+  const Team w = team_here<TEAM>(gridDim.x);
   for (long long i = w.me; i < p.children; i += w.all) {
     long long r = p.parents[i];
     const bool bad = r < -1 || r >= p.t.requests;
@@ -262,7 +283,7 @@ __device__ __forceinline__ void fork_rows(const ForkLaunch& p) {
 // Each old request's pages are held once for each child.
 template <int TEAM>
 __device__ __forceinline__ void fork_refs(const ForkLaunch& p) {
-  const Team w = team_here<TEAM>();
+  const Team w = team_here<TEAM>(gridDim.x);
   for (long long r = w.me; r < p.t.requests; r += w.all) {
     const int len = p.t.lens[r];
     if (!good_len(len, p.t)) {
@@ -309,7 +330,6 @@ __device__ __forceinline__ void plan_requests(const ResizeLaunch& p) {
   const PageTable& t = p.t;
   constexpr int kTile = 2048;
   __shared__ int others[kTile];
-  if (threadIdx.x == 0) *p.count = 0;
   int any = 0;
   for (long long r0 = 0; r0 < t.requests; r0 += kScanThreads) {
     const long long r = r0 + threadIdx.x;
@@ -339,6 +359,7 @@ __device__ __forceinline__ void plan_requests(const ResizeLaunch& p) {
     any |= __syncthreads_or(shared >= 0);
   }
   long long upto = 0;
+  int copied = 0;
   for (long long r0 = 0; r0 < t.requests; r0 += kScanThreads) {
     const long long r = r0 + threadIdx.x;
     int4 x = r < t.requests ? p.plan[r] : make_int4(0, 0, 0, 0);
@@ -371,15 +392,21 @@ __device__ __forceinline__ void plan_requests(const ResizeLaunch& p) {
     x.x = static_cast<int>(min(upto + before, 1LL << 30));  // past every pool's end
     if (r < t.requests) p.plan[r] = x;
     upto += total;
+    if (any) {
+      int more;
+      const bool copies = x.z & kCopies;
+      const int k = copied + block_scan<kScanThreads>(copies ? 1 : 0, &more);
+      if (copies) p.copies[k] = make_int4(x.w, x.x, x.y, t.lens[r] % t.block_size);
+      copied += more;
+    }
   }
+  if (threadIdx.x == 0) p.copies[t.requests] = make_int4(copied, 0, 0, 0);
 }
 
-template <int THREADS, int TEAM>
-__device__ __forceinline__ void apply_plan(const ResizeLaunch& p, int (&before)[kMostChunks]) {
+// The rows of the table, by the first `ctas` CTAs. `free` pages in all.
+__device__ __forceinline__ void apply_plan(const ResizeLaunch& p, const int (&before)[kMostChunks], int free, int ctas) {
   const PageTable& t = p.t;
-  const int free = free_before<THREADS>(p.s, before);
-  const Team w = team_here<TEAM>();
-  for (long long r = w.me; r < t.requests; r += w.all) {
+  for (long long r = blockIdx.x; r < t.requests; r += ctas) {
     const int4 x = p.plan[r];
     const int len = t.lens[r], want = p.new_lens[r], bs = t.block_size;
     const bool wants = x.y > 0 || (x.z & kKeeps);
@@ -388,16 +415,12 @@ __device__ __forceinline__ void apply_plan(const ResizeLaunch& p, int (&before)[
     const int copies = (x.z & kCopies) ? 1 : 0;
     bool bad = false;
 #pragma unroll 4
-    for (long long c = w.lane; c < t.width; c += TEAM) {
+    for (long long c = threadIdx.x; c < t.width; c += kCopyThreads) {
       const int old = t.table[r * t.stride + c];
       int page = old;
       if (served) {
         if (copies && c == have - 1) {
           page = free_page(p.s, before, x.x);
-          const int k = atomicAdd(p.count, 1);
-          p.src[k] = old;
-          p.dst[k] = page;
-          p.cells[k] = len % bs;
           atomicAdd(p.s.out_refs + old, -1);
         } else if (c >= have && c < to) {
           page = free_page(p.s, before, x.x + copies + static_cast<int>(c) - have);
@@ -413,15 +436,13 @@ __device__ __forceinline__ void apply_plan(const ResizeLaunch& p, int (&before)[
       if (page != old || t.out != t.table) t.out[r * t.out_stride + c] = page;
     }
     if (bad) atomicOr(p.status, kDevBadPage);
-    team_sync<TEAM>();  // out_lens may be the lengths that the others read
-    if (w.lane == 0) {
+    __syncthreads();  // out_lens may be the lengths that the others read
+    if (threadIdx.x == 0) {
       p.out_lens[r] = served ? want : len;
       if ((x.z & kGood) && !served) atomicOr(p.status, kDevNoPages);
     }
   }
 }
-
-constexpr int kApplyThreads = 128;
 
 __global__ void __launch_bounds__(kScanThreads) resize_plan_kernel(const ResizeLaunch p) {
   pdl_trigger();
@@ -430,21 +451,22 @@ __global__ void __launch_bounds__(kScanThreads) resize_plan_kernel(const ResizeL
   else
     scan_chunk(p.s, blockIdx.x - 1);
 }
-__global__ void __launch_bounds__(kApplyThreads) resize_apply_kernel(const ResizeLaunch p) {
+
+// The table's rows by the first `rows_ctas` CTAs, the copies by the others.
+__global__ void __launch_bounds__(kCopyThreads)
+    resize_apply_kernel(const __grid_constant__ PageCopy c, const __grid_constant__ ResizeLaunch p, const int rows_ctas) {
   __shared__ int before[kMostChunks];
   pdl_wait();
-  pdl_trigger();
-  apply_plan<kApplyThreads, kApplyThreads>(p, before);
-}
-__global__ void __cluster_dims__(kCluster) __launch_bounds__(kScanThreads) resize_kernel(const ResizeLaunch p) {
-  __shared__ int before[kMostChunks];
-  pdl_trigger();
-  if (blockIdx.x == 0)
-    plan_requests(p);
-  else
-    for (int c = blockIdx.x - 1; c < p.s.chunks; c += kCluster - 1) scan_chunk(p.s, c);
-  phase_end();
-  apply_plan<kScanThreads, 32>(p, before);
+  const int4 first = blockIdx.x < rows_ctas ? make_int4(0, 0, 0, 0) : p.copies[p.t.requests];  // their number
+  const int free = free_before<kCopyThreads>(p.s, before);
+  if (blockIdx.x < rows_ctas) {
+    apply_plan(p, before, free, rows_ctas);
+    return;
+  }
+  for (CopyWalk w(c, blockIdx.x - rows_ctas, gridDim.x - rows_ctas); w.pair < first.x; w.next()) {
+    const int4 x = p.copies[w.pair];  // page, first of the request's free pages, their number, filled cells
+    if (static_cast<long long>(x.y) + x.z <= free) copy_page(c, w.piece, x.x, free_page(p.s, before, x.y), x.w);
+  }
 }
 
 // ------------------------------------------------------------- compacting
@@ -511,18 +533,17 @@ __device__ __forceinline__ int2 count_moves(const PoolScan& s, int (&before)[kMo
   return make_int2(held, last < 0 ? 0 : before[last] + below);
 }
 
-template <int TEAM>
-__device__ __forceinline__ void rename_rows(const CompactLaunch& p) {
+// The rows of the table, by the first `ctas` CTAs.
+__device__ __forceinline__ void rename_rows(const CompactLaunch& p, int ctas) {
   const PageTable& t = p.t;
-  const Team w = team_here<TEAM>();
-  for (long long r = w.me; r < t.requests; r += w.all) {
+  for (long long r = blockIdx.x; r < t.requests; r += ctas) {
     const int len = t.lens[r];
     const bool good = good_len(len, t);
-    if (!good && w.lane == 0) atomicOr(p.status, kDevBadRowMeta);
+    if (!good && threadIdx.x == 0) atomicOr(p.status, kDevBadRowMeta);
     const long long pages = good ? pages_of(len, t.block_size) : 0;
     bool bad = false;
 #pragma unroll 4
-    for (long long c = w.lane; c < t.width; c += TEAM) {
+    for (long long c = threadIdx.x; c < t.width; c += kCopyThreads) {
       const int old = t.table[r * t.stride + c];
       int page = old;
       if (c < pages) {
@@ -550,11 +571,6 @@ __global__ void __launch_bounds__(kScanThreads) compact_moves_kernel(const Compa
   if (blockIdx.x == 0 && threadIdx.x == 0) *p.count = n.y;
   move_chunk(p, before, n.x, n.y, blockIdx.x);
 }
-__global__ void __launch_bounds__(kForkThreads) compact_rename_kernel(const CompactLaunch p) {
-  pdl_wait();
-  pdl_trigger();
-  rename_rows<kForkThreads>(p);
-}
 __global__ void __cluster_dims__(kCluster) __launch_bounds__(kScanThreads) compact_kernel(const CompactLaunch p) {
   __shared__ int before[kMostChunks];
   pdl_trigger();
@@ -563,8 +579,16 @@ __global__ void __cluster_dims__(kCluster) __launch_bounds__(kScanThreads) compa
   const int2 n = count_moves(p.s, before);
   if (blockIdx.x == 0 && threadIdx.x == 0) *p.count = n.y;
   for (int c = blockIdx.x; c < p.s.chunks; c += kCluster) move_chunk(p, before, n.x, n.y, c);
-  phase_end();
-  rename_rows<32>(p);
+}
+
+// The table's rows by the first `rows_ctas` CTAs, the copies by the others.
+__global__ void __launch_bounds__(kCopyThreads)
+    compact_apply_kernel(const __grid_constant__ PageCopy c, const __grid_constant__ CompactLaunch p, const int rows_ctas) {
+  pdl_wait();
+  if (blockIdx.x < rows_ctas)
+    rename_rows(p, rows_ctas);
+  else
+    copy_pairs(c, blockIdx.x - rows_ctas, gridDim.x - rows_ctas);
 }
 
 template <typename... P>
@@ -581,8 +605,10 @@ cudaError_t launch(void (*kernel)(P...), long long grid, int threads, bool depen
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-// Whether one cluster does a call: by the entries of its tables and counts.
-bool small_call(long long entries) { return entries <= kSmallEntries; }
+// CTAs of a launch that copy; c.pairs is at least the number of pairs.
+long long copy_ctas(const PageCopy& c, int num_sms) {
+  return c.arrays ? std::min<long long>(static_cast<long long>(kCopyCtas) * num_sms, c.pairs * c.first[c.arrays]) : 0;
+}
 
 }  // namespace
 
@@ -593,14 +619,13 @@ void pool_chunks(long long num_blocks, PoolScan* s) {
   s->chunks = static_cast<int>((num_blocks + s->chunk - 1) / s->chunk);
 }
 
-cudaError_t launch_page_copy(const PageCopy& c, bool dependent, int num_sms, cudaStream_t stream) {
-  const long long grid = std::min<long long>(static_cast<long long>(kCopyCtas) * num_sms, c.pairs * c.first[c.arrays]);
-  return launch(page_copy_kernel, grid, kCopyThreads, dependent, stream, c);
+cudaError_t launch_page_copy(const PageCopy& c, int num_sms, cudaStream_t stream) {
+  return launch(page_copy_kernel, copy_ctas(c, num_sms), kCopyThreads, false, stream, c);
 }
 
 cudaError_t launch_fork(const ForkLaunch& p, int num_sms, cudaStream_t stream) {
   if (p.children == 0 && p.t.requests == 0 && p.out_refs == p.refs) return cudaSuccess;
-  if (small_call((p.t.requests + p.children) * p.t.width + p.num_blocks))
+  if ((p.t.requests + p.children) * p.t.width + p.num_blocks <= kSmallEntries)
     return launch(fork_kernel, kCluster, kScanThreads, false, stream, p);
   const long long most = 16LL * num_sms;
   const long long copies = p.out_refs == p.refs ? 0 : (p.num_blocks + 4 * kForkThreads - 1) / (4 * kForkThreads);
@@ -611,21 +636,24 @@ cudaError_t launch_fork(const ForkLaunch& p, int num_sms, cudaStream_t stream) {
   return launch(fork_refs_kernel, std::min(most, p.t.requests), kForkThreads, first > 0, stream, p);
 }
 
-cudaError_t launch_resize(const ResizeLaunch& p, int num_sms, cudaStream_t stream) {
-  if (small_call(p.t.requests * p.t.width + p.s.num_blocks))
-    return launch(resize_kernel, kCluster, kScanThreads, false, stream, p);
-  cudaError_t e = launch(resize_plan_kernel, 1 + p.s.chunks, kScanThreads, false, stream, p);
-  if (e != cudaSuccess || p.t.requests == 0) return e;
-  return launch(resize_apply_kernel, std::min(16LL * num_sms, p.t.requests), kApplyThreads, true, stream, p);
+cudaError_t launch_resize(const ResizeLaunch& p, cudaStream_t stream) {
+  return launch(resize_plan_kernel, 1 + p.s.chunks, kScanThreads, false, stream, p);
+}
+cudaError_t launch_resize_apply(const PageCopy& c, const ResizeLaunch& p, bool rows, int num_sms, cudaStream_t stream) {
+  const int rows_ctas = rows ? static_cast<int>(std::min<long long>(p.t.requests, 16LL * num_sms)) : 0;
+  const long long ctas = rows_ctas + copy_ctas(c, num_sms);
+  return ctas ? launch(resize_apply_kernel, ctas, kCopyThreads, rows, stream, c, p, rows_ctas) : cudaSuccess;
 }
 
-cudaError_t launch_compact(const CompactLaunch& p, int num_sms, cudaStream_t stream) {
-  if (small_call(p.t.requests * p.t.width + p.s.num_blocks))
-    return launch(compact_kernel, kCluster, kScanThreads, false, stream, p);
-  cudaError_t e = launch(compact_scan_kernel, p.s.chunks, kScanThreads, false, stream, p.s);
-  if (e == cudaSuccess) e = launch(compact_moves_kernel, p.s.chunks, kScanThreads, true, stream, p);
-  if (e != cudaSuccess || p.t.requests == 0) return e;
-  return launch(compact_rename_kernel, std::min(16LL * num_sms, p.t.requests), kForkThreads, true, stream, p);
+cudaError_t launch_compact(const CompactLaunch& p, cudaStream_t stream) {
+  if (p.s.num_blocks <= kSmallEntries) return launch(compact_kernel, kCluster, kScanThreads, false, stream, p);
+  const cudaError_t e = launch(compact_scan_kernel, p.s.chunks, kScanThreads, false, stream, p.s);
+  return e == cudaSuccess ? launch(compact_moves_kernel, p.s.chunks, kScanThreads, true, stream, p) : e;
+}
+cudaError_t launch_compact_apply(const PageCopy& c, const CompactLaunch& p, bool rows, int num_sms, cudaStream_t stream) {
+  const int rows_ctas = rows ? static_cast<int>(std::min<long long>(p.t.requests, 16LL * num_sms)) : 0;
+  const long long ctas = rows_ctas + copy_ctas(c, num_sms);
+  return ctas ? launch(compact_apply_kernel, ctas, kCopyThreads, rows, stream, c, p, rows_ctas) : cudaSuccess;
 }
 
 }  // namespace sai

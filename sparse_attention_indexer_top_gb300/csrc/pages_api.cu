@@ -99,15 +99,17 @@ int check_arrays(const sai_page_array* arrays, int32_t n, int64_t num_blocks, in
   return SAI_OK;
 }
 
-// Copies the pairs in every array, as many arrays at a time as a launch takes
-// (c has the first of them).
-int copy_arrays(sai::PageCopy& c, const sai_page_array* arrays, int32_t n, int32_t block_size, bool dependent, int sms,
-                cudaStream_t stream) {
-  for (int32_t i0 = 0; i0 < n; i0 += sai::kPageArrays) {
+// One launch for as many arrays as it takes: launch(first). c has the first of
+// them; one launch at least.
+template <typename F>
+int each_arrays(sai::PageCopy& c, const sai_page_array* arrays, int32_t n, int32_t block_size, F launch) {
+  int32_t i0 = 0;
+  do {
     if (i0) check_arrays(arrays + i0, n - i0, 1, block_size, &c);
-    const cudaError_t e = sai::launch_page_copy(c, dependent && i0 == 0, sms, stream);
+    const cudaError_t e = launch(i0 == 0);
     if (e != cudaSuccess) return cuda_status(e);
-  }
+    i0 += sai::kPageArrays;
+  } while (i0 < n);
   return SAI_OK;
 }
 
@@ -148,14 +150,11 @@ struct Space {
 size_t lay_out(sai::ResizeLaunch* p, int64_t num_blocks, int64_t requests, char* base) {
   Space w{base};
   sai::pool_chunks(num_blocks, &p->s);
-  p->count = w.take<int>(4);
   p->s.counts = w.take<int>(p->s.chunks);
   p->s.free_list = w.take<int>(num_blocks);
   p->plan = w.take<int4>(requests);
+  p->copies = w.take<int4>(requests + 1);
   p->last_shared = w.take<int>(requests);
-  p->src = w.take<int>(requests);
-  p->dst = w.take<int>(requests);
-  p->cells = w.take<int>(requests);
   return w.used;
 }
 size_t lay_out(sai::CompactLaunch* p, int64_t num_blocks, char* base) {
@@ -204,10 +203,11 @@ int sai_copy_pages(const sai_page_array* arrays, int32_t num_arrays, int64_t num
   if (!device_setup(&dev, &c.status, &sms)) return SAI_ERR_CUDA;
   c.src = src;
   c.dst = dst;
-  c.cells = c.count = nullptr;
+  c.count = nullptr;
   c.pairs = pairs;
   c.num_blocks = num_blocks;
-  return copy_arrays(c, arrays, num_arrays, 0, false, sms, reinterpret_cast<cudaStream_t>(stream));
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  return each_arrays(c, arrays, num_arrays, 0, [&](bool) { return sai::launch_page_copy(c, sms, s); });
 }
 
 int sai_fork_pages(const int32_t* block_table, int64_t requests, int64_t width, int64_t bt_stride,
@@ -269,15 +269,10 @@ int sai_resize_pages(const sai_page_array* arrays, int32_t num_arrays, int64_t n
   p.new_lens = new_lens;
   p.out_lens = out_lens;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if ((e = cuda_status(sai::launch_resize(p, sms, s))) != SAI_OK || requests == 0) return e;
-  c.src = p.src;
-  c.dst = p.dst;
-  c.cells = p.cells;
-  c.count = p.count;
+  if ((e = cuda_status(sai::launch_resize(p, s))) != SAI_OK || requests == 0) return e;
   c.pairs = requests;
-  c.num_blocks = num_blocks;
-  c.status = p.status;
-  return copy_arrays(c, arrays, num_arrays, block_size, true, sms, s);
+  return each_arrays(c, arrays, num_arrays, block_size,
+                     [&](bool first) { return sai::launch_resize_apply(c, p, first, sms, s); });
 }
 
 size_t sai_compact_pages_workspace(int64_t num_blocks) {
@@ -312,15 +307,14 @@ int sai_compact_pages(const sai_page_array* arrays, int32_t num_arrays, int64_t 
   p.s.out_refs = out_refs;
   p.moves = out_moves;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if ((e = cuda_status(sai::launch_compact(p, sms, s))) != SAI_OK) return e;
+  if ((e = cuda_status(sai::launch_compact(p, s))) != SAI_OK) return e;
   c.src = p.src;
   c.dst = p.dst;
-  c.cells = nullptr;
   c.count = p.count;
   c.pairs = num_blocks / 2 + 1;
   c.num_blocks = num_blocks;
   c.status = p.status;
-  return copy_arrays(c, arrays, num_arrays, 0, true, sms, s);
+  return each_arrays(c, arrays, num_arrays, 0, [&](bool first) { return sai::launch_compact_apply(c, p, first, sms, s); });
 }
 
 }  // extern "C"

@@ -234,7 +234,6 @@ struct PageCopy {
   int arrays;
   const int* src;
   const int* dst;
-  const int* cells;     // tokens of each pair, or null: whole pages
   const int* count;     // number of pairs on the device, or null: `pairs`
   long long pairs;
   long long num_blocks;
@@ -275,10 +274,7 @@ struct ResizeLaunch {
   int* out_lens;
   int4* plan;        // [requests]: first of its free pages, their number, state, last page
   int* last_shared;  // [requests]
-  int* src;          // copies: [requests]
-  int* dst;
-  int* cells;
-  int* count;
+  int4* copies;      // [requests + 1]: page, first of its request's free pages, their number, filled cells; last: number
   int* status;
 };
 struct CompactLaunch {
@@ -291,10 +287,12 @@ struct CompactLaunch {
   int* status;
 };
 void pool_chunks(long long num_blocks, PoolScan* s);  // fills num_blocks, chunk, chunks
-cudaError_t launch_page_copy(const PageCopy& c, bool dependent, int num_sms, cudaStream_t stream);
+cudaError_t launch_page_copy(const PageCopy& c, int num_sms, cudaStream_t stream);
 cudaError_t launch_fork(const ForkLaunch& p, int num_sms, cudaStream_t stream);
-cudaError_t launch_resize(const ResizeLaunch& p, int num_sms, cudaStream_t stream);
-// moves and renames; the pages are copied by launch_page_copy
-cudaError_t launch_compact(const CompactLaunch& p, int num_sms, cudaStream_t stream);
+// What is decided; then the table's rows (`rows`) and the copies in c's arrays.
+cudaError_t launch_resize(const ResizeLaunch& p, cudaStream_t stream);
+cudaError_t launch_resize_apply(const PageCopy& c, const ResizeLaunch& p, bool rows, int num_sms, cudaStream_t stream);
+cudaError_t launch_compact(const CompactLaunch& p, cudaStream_t stream);
+cudaError_t launch_compact_apply(const PageCopy& c, const CompactLaunch& p, bool rows, int num_sms, cudaStream_t stream);
 
 }  // namespace sai
