@@ -200,6 +200,12 @@ __device__ __forceinline__ void scan_chunk(const PoolScan& s, int chunk) {
 template <int THREADS>
 __device__ __forceinline__ int free_before(const PoolScan& s, int (&before)[kMostChunks]) {
   int sum = 0;
+  if (s.chunks == 1) {
+    if (threadIdx.x == 0) before[0] = 0;
+    sum = s.counts[0];
+    __syncthreads();
+    return sum;
+  }
   for (int c0 = 0; c0 < s.chunks; c0 += THREADS) {
     const int c = c0 + threadIdx.x;
     int total;
@@ -325,78 +331,88 @@ __global__ void __cluster_dims__(kCluster) __launch_bounds__(kScanThreads) fork_
 // ------------------------------------------------- growing and shrinking
 enum : int { kGood = 1, kCopies = 2, kKeeps = 4 };
 
-// What each request wants, and which free pages (by number) are for it. One CTA.
+// What each request wants, and which free pages (by number) are for it. One CTA,
+// a request to a thread, in rounds where there are more; the first round's stay
+// in registers, and the shared last pages of up to kShared requests in shared
+// memory.
 __device__ __forceinline__ void plan_requests(const ResizeLaunch& p) {
   const PageTable& t = p.t;
-  constexpr int kTile = 2048;
-  __shared__ int others[kTile];
+  constexpr int kShared = 2048;
+  __shared__ int others[kShared];
+  struct Wish {
+    int need, state, last, shared, refs;  // shared: the last page, if others hold it too, else -1
+  };
+  auto wish = [&](long long r) -> Wish {
+    Wish w{0, 0, -1, -1, 0};
+    if (r >= t.requests) return w;
+    const int len = t.lens[r], want = p.new_lens[r];
+    if (!good_len(len, t) || !good_len(want, t)) {
+      atomicOr(p.status, kDevBadRowMeta);
+      return w;
+    }
+    if (want > len && len % t.block_size) {
+      w.last = t.table[r * t.stride + len / t.block_size];
+      if (w.last < 0 || w.last >= p.s.num_blocks) {
+        atomicOr(p.status, kDevBadPage);
+        return w;
+      }
+      w.refs = p.s.refs[w.last];
+      if (w.refs > 1) w.shared = w.last;
+    }
+    w.state = kGood | (w.shared >= 0 ? kCopies : 0);
+    w.need = static_cast<int>(max(0LL, pages_of(want, t.block_size) - pages_of(len, t.block_size)));
+    return w;
+  };
+  const bool few = t.requests <= kShared;
+  const Wish first = wish(threadIdx.x);
   int any = 0;
   for (long long r0 = 0; r0 < t.requests; r0 += kScanThreads) {
     const long long r = r0 + threadIdx.x;
-    int shared = -1;
-    if (r < t.requests) {
-      const int len = t.lens[r], want = p.new_lens[r];
-      int state = 0, need = 0, last = -1;
-      if (!good_len(len, t) || !good_len(want, t)) {
-        atomicOr(p.status, kDevBadRowMeta);
-      } else {
-        state = kGood;
-        need = static_cast<int>(max(0LL, pages_of(want, t.block_size) - pages_of(len, t.block_size)));
-        if (want > len && len % t.block_size) {
-          last = t.table[r * t.stride + len / t.block_size];
-          if (last < 0 || last >= p.s.num_blocks) {
-            atomicOr(p.status, kDevBadPage);
-            state = need = 0;
-          } else if (p.s.refs[last] > 1) {
-            state |= kCopies;
-            shared = last;
-          }
-        }
-      }
-      p.plan[r] = make_int4(0, need, state, last);
-      p.last_shared[r] = shared;
-    }
-    any |= __syncthreads_or(shared >= 0);
+    const Wish w = r0 == 0 ? first : wish(r);
+    if (r < t.requests) (few ? others : p.last_shared)[r] = w.shared;
+    any |= __syncthreads_or(w.shared >= 0);
   }
   long long upto = 0;
   int copied = 0;
   for (long long r0 = 0; r0 < t.requests; r0 += kScanThreads) {
     const long long r = r0 + threadIdx.x;
-    int4 x = r < t.requests ? p.plan[r] : make_int4(0, 0, 0, 0);
+    Wish w = r0 == 0 ? first : wish(r);
     if (any) {
-      const int mine = r < t.requests ? p.last_shared[r] : -1;
       int same = 0;
       bool later = false;
-      for (long long k0 = 0; k0 < t.requests; k0 += kTile) {
-        const int n = static_cast<int>(min(static_cast<long long>(kTile), t.requests - k0));
-        __syncthreads();
-        for (int k = threadIdx.x; k < n; k += kScanThreads) others[k] = p.last_shared[k0 + k];
-        __syncthreads();
-        if (mine >= 0)
+      for (long long k0 = 0; k0 < t.requests; k0 += kShared) {
+        const int n = static_cast<int>(min(static_cast<long long>(kShared), t.requests - k0));
+        if (!few) {
+          __syncthreads();
+          for (int k = threadIdx.x; k < n; k += kScanThreads) others[k] = p.last_shared[k0 + k];
+          __syncthreads();
+        }
+        if (w.shared >= 0)
+#pragma unroll 8
           for (int k = 0; k < n; ++k)
-            if (others[k] == mine) {
+            if (others[k] == w.shared) {
               ++same;
               later = later || k0 + k > r;
             }
       }
-      if (mine >= 0) {
+      if (w.shared >= 0) {
         // the last of all its holders keeps the page: those before it leave it, or it is not served either
-        if (!later && same == p.s.refs[mine])
-          x.z = (x.z & ~kCopies) | kKeeps;
+        if (!later && same == w.refs)
+          w.state = (w.state & ~kCopies) | kKeeps;
         else
-          ++x.y;
+          ++w.need;
       }
     }
     long long total;
-    const long long before = block_scan<kScanThreads>(static_cast<long long>(x.y), &total);
-    x.x = static_cast<int>(min(upto + before, 1LL << 30));  // past every pool's end
-    if (r < t.requests) p.plan[r] = x;
+    const long long before = block_scan<kScanThreads>(static_cast<long long>(w.need), &total);
+    const int at = static_cast<int>(min(upto + before, 1LL << 30));  // past every pool's end
+    if (r < t.requests) p.plan[r] = make_int4(at, w.need, w.state, w.last);
     upto += total;
     if (any) {
       int more;
-      const bool copies = x.z & kCopies;
+      const bool copies = w.state & kCopies;
       const int k = copied + block_scan<kScanThreads>(copies ? 1 : 0, &more);
-      if (copies) p.copies[k] = make_int4(x.w, x.x, x.y, t.lens[r] % t.block_size);
+      if (copies) p.copies[k] = make_int4(w.last, at, w.need, t.lens[r] % t.block_size);
       copied += more;
     }
   }
