@@ -508,8 +508,9 @@ int sai_sparse_attention(const uint16_t* q, int64_t q_row_stride, int32_t q_head
  *                  own position (not before its start or its window)
  * so that row i, n > 0, with b = row_starts[i] and e = max(n, prefix_lens[i]),
  * sees b <= t < e with (window = 0, or t >= n - window, or t < b + sinks); a
- * start at or past e leaves it none. tanh is computed to fp32 (a few 2^-24), and
- * the changed scores are fp32.
+ * start at or past e leaves it none. The changed scores are fp32; a capped one is
+ * off by at most 2^-20 of itself (2^-22 of the cap beyond it). Slopes are finite,
+ * and so are their products with distances.
  *
  * softcap      0: none; else in [1e-30, 1e30].
  * slopes       fp32 [q_heads] or NULL; row_starts, prefix_lens int32 [rows] or
@@ -554,7 +555,8 @@ int sai_sparse_attention_mod(const uint16_t* q, int64_t q_row_stride, int32_t q_
  * rows of row_bytes contiguous bytes, stride[] apart, at base + p * page_stride
  * (all in bytes, multiples of 4). cells names the axis (0 or 1) that counts the
  * page's tokens, so that a partly filled page may be copied in part; -1: it is
- * copied whole. sai_cache_page_arrays writes the arrays of a cache (k, v, and
+ * copied whole. A page has fewer than 2^24 units of 16 bytes (of 4 where an
+ * address, stride or row is no multiple of 16). sai_cache_page_arrays writes the arrays of a cache (k, v, and
  * for e4m3 k_scale, v_scale) to out[4] and returns how many they are, or an
  * error below 0. Pages of one array must not overlap.
  */

@@ -29,7 +29,7 @@ class PageSet:
     ``caches`` are the layers' ``KVCache`` objects (keys, values and their
     scales). ``arrays`` are any other CUDA tensors ``[num_blocks, ...]`` of the
     same pool, such as the indexer's keys and their scales: each page contiguous
-    and of a multiple of 4 bytes, pages any distance apart. ``block_size`` is
+    and of a multiple of 4 bytes (below 256 MB), pages any distance apart. ``block_size`` is
     that of the caches, or is given where there are none. The object keeps the
     tensors.
     """
@@ -45,8 +45,8 @@ class PageSet:
                 raise ValueError(f"arrays[{i}] must be [num_blocks, ...]")
             if not t[0].is_contiguous():
                 raise ValueError(f"arrays[{i}] needs contiguous pages")
-            if t[0].nbytes % 4 or t[0].nbytes > 2 ** 31 - 4:
-                raise ValueError(f"arrays[{i}] needs pages of a multiple of 4 bytes, below 2 GiB")
+            if t[0].nbytes % 4 or t[0].nbytes > 2 ** 28 - 2 ** 16:
+                raise ValueError(f"arrays[{i}] needs pages of a multiple of 4 bytes, below 2^28 - 2^16")
             if t.shape[0] > 1 and t.stride(0) < t[0].numel():
                 raise ValueError(f"arrays[{i}] needs pages that do not overlap")
             every.append((f"arrays[{i}]", t.device, t.shape[0]))
@@ -73,6 +73,8 @@ class PageSet:
             step = t.stride(0) * t.element_size() if t.shape[0] > 1 else page
             descs.append(PageArrayDesc(t.data_ptr(), step, (0, 0), (1, 1), page, -1))
         self._descs = (PageArrayDesc * len(descs))(*descs)
+        # an empty copy: the checks of the arrays alone
+        check(load().sai_copy_pages(ctypes.addressof(self._descs), len(descs), self.num_blocks, None, None, 0, None), "PageSet")
         self._args = (ctypes.addressof(self._descs), len(descs), self.num_blocks, self.block_size, self.device.index)
 
 
