@@ -403,6 +403,11 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -686,12 +691,14 @@ struct Change {
 };
 
 // Changes 32 columns of scores s, from column c0 of the tile: times `mul`,
-// capped (no |x| above cap / 2), biased. Two elements to an instruction: with a
-// cap, 6 of them, which is what the cap costs beside the masks' and the sum's.
-template <int MOD>
+// capped, biased. Two elements to an instruction. FAR: scores above half the cap
+// are cap (1 - 2 / (1 + e^(2x / cap))), off by 2^-22 of the cap; without, there are
+// none.
+template <int MOD, bool FAR>
 __device__ __forceinline__ void change32(uint32_t* s, int c0, float mul, const Change& ch) {
-  const float xm = mul * ch.inv_cap;
-  const uint64_t mul_2 = pair(mul, mul), x_2 = pair(xm, xm), slope_2 = pair(-ch.slope, -ch.slope);
+  const float xm = mul * ch.inv_cap, em = xm * 2.885390081777927f;
+  const uint64_t mul_2 = pair(mul, mul), x_2 = pair(xm, xm), e_2 = pair(em, em), slope_2 = pair(-ch.slope, -ch.slope);
+  const uint64_t cap_2 = pair(ch.cap, ch.cap), less_2 = pair(-2.f * ch.cap, -2.f * ch.cap), one_2 = pair(1.f, 1.f);
   // distances of the two columns, whole numbers, less 2 at each step
   uint64_t d = pair(static_cast<float>(ch.ahead - c0), static_cast<float>(ch.ahead - c0 - 1));
   const uint64_t step = pair(-2.f, -2.f);
@@ -706,7 +713,17 @@ __device__ __forceinline__ void change32(uint32_t* s, int c0, float mul, const C
       uint64_t q = q_2[3];
 #pragma unroll
       for (int i = 2; i >= 0; --i) q = fma2(q, y, q_2[i]);
-      v = mul2(x, q);
+      q = mul2(x, q);
+      if (FAR) {
+        float a, b, xa, xb, na, nb;
+        unpair(mul2(v, e_2), a, b);
+        unpair(add2(pair(ex2(a), ex2(b)), one_2), a, b);
+        unpair(fma2(pair(rcp(a), rcp(b)), less_2, cap_2), a, b);
+        unpair(x, xa, xb);
+        unpair(q, na, nb);
+        q = pair(fabsf(xa) <= kNear ? na : a, fabsf(xb) <= kNear ? nb : b);
+      }
+      v = q;
     } else {
       v = mul2(v, mul_2);
     }
@@ -806,17 +823,10 @@ __device__ __noinline__ float2 rough_tile(uint32_t ts, uint32_t to, float2 ml, f
       for (int c = 0; c < 32; ++c) s[c] = __float_as_uint(__uint_as_float(s[c]) * factors[(c0 + c) / 16].x);
     }
     if (kChanged) {
-      if ((MOD & kCap) && !__all_sync(0xffffffffu, largest32(s, 0.f) * (mul * ch.inv_cap) <= kNear)) {
-        const float d0 = static_cast<float>(ch.ahead - c0);
-#pragma unroll
-        for (int c = 0; c < 32; ++c) {
-          float v = capped(__uint_as_float(s[c]) * mul, ch.cap, ch.inv_cap);
-          if (MOD & kBias) v = fmaf(-ch.slope, fabsf(d0 - static_cast<float>(c)), v);
-          s[c] = __float_as_uint(v);
-        }
-      } else {
-        change32<MOD>(s, c0, mul, ch);
-      }
+      if ((MOD & kCap) && !__all_sync(0xffffffffu, largest32(s, 0.f) * (mul * ch.inv_cap) <= kNear))
+        change32<MOD, true>(s, c0, mul, ch);
+      else
+        change32<MOD, false>(s, c0, mul, ch);
     }
     if (!kChanged || masked) mask32<MOD>(s, sees.x - c0, sees.y - c0, sees.z - c0, sees.w - c0, bad >> (c0 / 16));
   };
