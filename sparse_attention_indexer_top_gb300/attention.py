@@ -3,7 +3,9 @@
 ``KVCache`` names one layer's cache arrays; ``append_kv`` rotates the step's
 keys and queries and writes keys and values into it, ``sparse_attention``
 attends over the slots that ``index_score_topk`` or ``topk_transform`` picked,
-and ``paged_attention`` over all keys of a row or a sliding window of them.
+and ``paged_attention`` over all keys of a row or a sliding window of them;
+both can cap the scores, and the latter biases them by distance and masks by
+document and prefix. The pages themselves are moved by ``pages.py``.
 Rows, ``seq_lens``, ``row_to_batch`` and ``block_table`` mean what they mean
 for ``index_score_topk``; the table may be columns of a wider one, and a length
 past its columns makes a bad row. As everywhere in this package, the

@@ -54,7 +54,10 @@
 // MOD: rows see a document or a prefix of their request (kMasks), and scores are
 // capped (kCap) and biased by distance (kBias) before the softmax
 // (attention_mod.cuh). These instances are apart, in attention_tiles_mod.cu and
-// attention_tiles_cap.cu.
+// attention_tiles_cap.cu. Bound: the softmax warps, whose two-element FMAs a pair
+// of scores go from 2 to 3 (bias), 6 (cap below a quarter) or 7. 2048 rows on
+// 32768 keys, 32 / 4 heads, bf16 (e4m3), us: plain 628 (787), masks 646 (859), bias
+// 655 (856), cap 750 (922), both 834 (1083).
 #pragma once
 #include <cuda.h>
 #include <cuda_fp16.h>

@@ -14,6 +14,11 @@
 // for small calls, a cluster of eight CTAs with a barrier of the cluster between
 // them; for large ones each is a kernel as wide as the GPU. Every kernel is
 // launched while the one before ends, and waits for it.
+//
+// On the GPU, us: copy of 3 pages 2.3, of 500 pages of 24 arrays 167 (6.68 TB/s, a
+// plain copy's rate); fork of 8 requests 3.3, of 512 to 600 with a pool of 131072
+// pages 6.2; resize of 16 beams with their copies 9.0, of 160 requests 6.5; compact of
+// 512 pages 7.0, of 4096 pages of 12 arrays 84 (72 are its bytes).
 #include "sai_internal.h"
 #include "sai_ptx.cuh"
 
@@ -260,6 +265,9 @@ __device__ __forceinline__ void phase_end() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 constexpr int kCluster = 8;
+// Entries of tables and counts that one cluster takes: a fork of 8 requests with a
+// pool of 1024 takes 3.3 us with it and 3.7 in two launches (and 2 us less of the
+// host); one of 512 requests, 0.6 million entries, 10.8 and 6.2.
 constexpr long long kSmallEntries = 1 << 16;
 
 // ------------------------------------------------------------------ forks
