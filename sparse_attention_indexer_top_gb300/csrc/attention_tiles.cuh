@@ -699,7 +699,7 @@ struct Change {
 // none.
 template <int MOD, bool FAR>
 __device__ __forceinline__ void change32(uint32_t* s, int c0, float mul, const Change& ch) {
-  const float xm = mul * ch.inv_cap, em = xm * 2.885390081777927f;
+  const float xm = fminf(mul * ch.inv_cap, 1e38f), em = xm * 2.885390081777927f;  // finite: a score of 0 stays 0
   const uint64_t mul_2 = pair(mul, mul), x_2 = pair(xm, xm), e_2 = pair(em, em), slope_2 = pair(-ch.slope, -ch.slope);
   const uint64_t cap_2 = pair(ch.cap, ch.cap), less_2 = pair(-2.f * ch.cap, -2.f * ch.cap), one_2 = pair(1.f, 1.f);
   // distances of the two columns, whole numbers, less 2 at each step

@@ -152,6 +152,33 @@ def test_caps_far_below_and_above_the_scores(packed, dtype, any_scales, cap, sig
 
 
 @pytest.mark.parametrize("packed", [0, sai.PACKED_TILES])
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("cap", [0.0, 7.0, 60.0])
+def test_slopes_of_either_sign_and_zero(packed, dtype, cap):
+    """Slopes below 0 favour far keys: every tile then moves the maximum; prefixes put keys on both sides of the position."""
+    totals = [900, 500]
+    c = Case(91, totals, dtype=dtype, bs=64, hkv=1)
+    rows = [(0, n, 0) for n in range(850, 901, 7)] + [(0, 300, 900), (0, 1, 900), (0, 129, 260)] + [(1, n, 0) for n in (1, 2, 130, 500)]
+    q, q64 = c.queries(len(rows), 6)
+    slopes = torch.tensor([-0.05, -0.001, 0.0, 0.001, 0.3, -2.0], device=DEV)
+    b, n, prefix = (_lens(list(x)) for x in zip(*rows))
+    out, lse = sai.paged_attention(q, c.cache, c.t_table, n, max_seq_len=900, row_to_batch=b, packed=packed, want_lse=True,
+                                   softcap=cap, slopes=slopes, prefix_lens=prefix)
+    _check(c, q64, [(b, n, A.span(n, prefix=p)) for b, n, p in rows], out, lse, 128 ** -0.5, softcap=cap, slopes=slopes)
+
+
+@pytest.mark.parametrize("packed", [0, sai.PACKED_TILES])
+def test_scores_of_zero_under_the_least_cap(packed):
+    c = Case(92, [50], dtype="bf16", bs=16, hkv=1)
+    q = torch.zeros((1, 2, 128), dtype=torch.bfloat16, device=DEV)
+    out, lse = sai.paged_attention(q, c.cache, c.t_table, _lens([50]), max_seq_len=50, row_to_batch=_lens([0]), packed=packed,
+                                   want_lse=True, softcap=1e-30, sm_scale=1e15)
+    assert torch.allclose(lse, torch.full_like(lse, float(np.log(50))), atol=1e-5)
+    mean = c.kv[0][1].mean(0)
+    assert np.abs(out[0].float().cpu().numpy() - mean).max() <= 2.0 ** -6 * np.abs(c.kv[0][1]).mean()
+
+
+@pytest.mark.parametrize("packed", [0, sai.PACKED_TILES])
 def test_infinite_scores_are_capped(packed):
     """A key of infinities: the product is +inf, its capped score the cap; without a cap such a row is NaN."""
     c = Case(95, [60], dtype="bf16", bs=64, hkv=1)
