@@ -28,8 +28,8 @@
 // sees a document or a prefix of its request. These instances are apart, in
 // attention_rows_mod.cu, so that the plain ones hold none of it; what is done is
 // chosen at run time, since reading the keys takes longer: 64 rows of 4096-32768
-// keys, 64 / 8 heads, e4m3, 396 us plain, 405 capped, 419 biased, 436 both; bf16 712
-// to 714.
+// keys, 64 / 8 heads, e4m3, 399 us plain, 412 capped, 404 biased, 414 both; bf16 721
+// to 723.
 #pragma once
 #include "attention_mod.cuh"
 #include "sai_internal.h"
@@ -360,9 +360,13 @@ __global__ void __launch_bounds__(kThreads) attn_rows_kernel(const AttnLaunch p)
   const int my_stages = stages > first ? (stages - first + STEP - 1) / STEP : 0;
   bool bad_slot = false;
 
+  // With a bias the nearest keys come first: from the first group on, every
+  // nearer one would pass the running maximum by its 16 steps of the slope.
+  const bool biased = MOD && p.slopes;
+  auto place_of = [&](int s) { return biased ? stages - 1 - first - s * STEP : first + s * STEP; };
   // slot of this lane's key (lane & 15) in the team's stage s, -1: none
   auto slot_of = [&](int s) -> int {
-    const int j = k_begin + (first + s * STEP) * SK + mt * 16 + (lane & 15);
+    const int j = k_begin + place_of(s) * SK + mt * 16 + (lane & 15);
     if (s >= my_stages || j >= k_end) return -1;
     long long slot;
     if (p.slots) {
@@ -421,23 +425,21 @@ __global__ void __launch_bounds__(kThreads) attn_rows_kernel(const AttnLaunch p)
   // MOD: the cap, and the slopes of the lane's two heads
   const float cap = MOD ? p.cap_log2 : 0.f, inv_cap = MOD && cap > 0.f ? 1.f / cap : 0.f;
   float slope0 = 0.f, slope1 = 0.f;
-  const bool biased = MOD && p.slopes;
   if (biased) {
     const int h0 = FEW ? 2 * t : g, h1 = FEW ? 2 * t + 1 : g + 8;
     if (head_in_group + h0 < p.group) slope0 = p.slopes[head0 + h0] * 1.44269504088896340736f;
     if (head_in_group + h1 < p.group) slope1 = p.slopes[head0 + h1] * 1.44269504088896340736f;
   }
-  // distance of key 0 of the first stage's first group, were all keys behind the
-  // row's first tokens
-  const int ahead0 = biased ? p.seq_lens[row] - 1 - rk.shift - k_begin - first * SK : 0;
-  // distances of the lane's key `key` of group kg of stage s, and of key + step
-  auto distances = [&](int s, int kg, int key, int step, float& d0, float& d1) {
-    const int j = s * STEP * SK + kg * 16 + key;  // behind key 0
-    const int a = ahead0 - j;
+  // distance of key 0 of the group at work, were all keys behind the row's first tokens
+  const int behind = biased ? p.seq_lens[row] - 1 - rk.shift : 0;
+  int ahead = behind - k_begin - place_of(0) * SK;
+  // distances of the lane's key `key` of the group, and of key + step
+  auto distances = [&](int key, int step, float& d0, float& d1) {
+    const int a = ahead - key;
     d0 = fabsf(static_cast<float>(a));
     d1 = fabsf(static_cast<float>(a - step));
     if (rk.low > 0) {  // first tokens before the window
-      const int at = k_begin + first * SK + j, back = rk.shift - rk.start;
+      const int at = behind - a, back = rk.shift - rk.start;
       if (at < rk.low) d0 = fabsf(static_cast<float>(a + back));
       if (at + step < rk.low) d1 = fabsf(static_cast<float>(a - step + back));
     }
@@ -486,7 +488,7 @@ __global__ void __launch_bounds__(kThreads) attn_rows_kernel(const AttnLaunch p)
     for (int s = 0; s < DEPTH - 1; ++s) issue(s, sl[s]);
     int next = sl[DEPTH - 1];
 
-    for (int s = 0; s < my_stages; ++s) {
+    for (int s = 0; s < my_stages; ++s, ahead += MOD ? (STEP + 1) * SK : 0) {
       cp_wait<DEPTH - 2>();
       team_sync();  // the stage is whole for every lane, and the place refilled below is free
       const int after = slot_of(s + DEPTH);
@@ -495,7 +497,7 @@ __global__ void __launch_bounds__(kThreads) attn_rows_kernel(const AttnLaunch p)
       const uint32_t st = ring_u + (s % DEPTH) * STAGE;
       const unsigned char* stp = ring + (s % DEPTH) * STAGE;
 #pragma unroll 1
-      for (int kg = 0; kg < MT; ++kg) {
+      for (int kg = 0; kg < MT; ++kg, ahead -= MOD ? 16 : 0) {
         const uint32_t live = *reinterpret_cast<const uint32_t*>(stp + 2 * KB + SK * 8 + kg * 4);
         if (live == 0) continue;
         const uint32_t kb = st + kg * 16 * RB, vb = kb + KB;
@@ -551,7 +553,7 @@ __global__ void __launch_bounds__(kThreads) attn_rows_kernel(const AttnLaunch p)
           }
           if (MOD) {
             float x[2][2] = {{c[0], c[2]}, {c[1], c[3]}}, d0 = 0.f, d1 = 0.f;
-            if (biased) distances(s, kg, g, 8, d0, d1);
+            if (biased) distances(g, 8, d0, d1);
             change(x, d0, d1);
             const bool on0 = (live >> g) & 1, on1 = (live >> (g + 8)) & 1;
             c[0] = on0 ? x[0][0] : -INFINITY;
@@ -677,7 +679,7 @@ __global__ void __launch_bounds__(kThreads) attn_rows_kernel(const AttnLaunch p)
           }
           if (MOD) {
             float x[2][2] = {{c[n][0], c[n][1]}, {c[n][2], c[n][3]}}, d0 = 0.f, d1 = 0.f;
-            if (biased) distances(s, kg, 8 * n + 2 * t, 1, d0, d1);
+            if (biased) distances(8 * n + 2 * t, 1, d0, d1);
             change(x, d0, d1);
 #pragma unroll
             for (int e = 0; e < 2; ++e) {

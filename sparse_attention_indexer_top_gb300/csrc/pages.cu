@@ -267,19 +267,23 @@ __device__ __forceinline__ void phase_end() {
 constexpr int kCluster = 8;
 // Entries of tables and counts that one cluster takes: a fork of 8 requests with a
 // pool of 1024 takes 3.3 us with it and 3.7 in two launches (and 2 us less of the
-// host); one of 512 requests, 0.6 million entries, 10.8 and 6.2.
+// host); one of 512 requests, 0.6 million entries, 10.8 and 5.8.
 constexpr long long kSmallEntries = 1 << 16;
 
 // ------------------------------------------------------------------ forks
 constexpr int kForkThreads = 128;
 
-// Children's rows and lengths, and the counts before the change.
-template <int TEAM>
-__device__ __forceinline__ void fork_rows(const ForkLaunch& p) {
+// The counts before the change.
+__device__ __forceinline__ void fork_counts(const ForkLaunch& p) {
   if (p.out_refs != p.refs)
     for (long long i = blockIdx.x * static_cast<long long>(blockDim.x) + threadIdx.x; i < p.num_blocks;
          i += static_cast<long long>(gridDim.x) * blockDim.x)
       p.out_refs[i] = p.refs[i];
+}
+
+// Children's rows and lengths.
+template <int TEAM>
+__device__ __forceinline__ void fork_rows(const ForkLaunch& p) {
   const Team w = team_here<TEAM>(gridDim.x);
   for (long long i = w.me; i < p.children; i += w.all) {
     long long r = p.parents[i];
@@ -294,10 +298,12 @@ __device__ __forceinline__ void fork_rows(const ForkLaunch& p) {
   }
 }
 
-// Each old request's pages are held once for each child.
-template <int TEAM>
+// Each old request's pages are held once for each child. WAIT: the counts are
+// there after pdl_wait, which every thread calls.
+template <int TEAM, bool WAIT>
 __device__ __forceinline__ void fork_refs(const ForkLaunch& p) {
   const Team w = team_here<TEAM>(gridDim.x);
+  bool waited = !WAIT;
   for (long long r = w.me; r < p.t.requests; r += w.all) {
     const int len = p.t.lens[r];
     if (!good_len(len, p.t)) {
@@ -308,6 +314,8 @@ __device__ __forceinline__ void fork_refs(const ForkLaunch& p) {
 #pragma unroll 4
     for (long long i = w.lane; i < p.children; i += TEAM) children += p.parents[i] == r;
     children = team_sum<TEAM>(children);
+    if (!waited) pdl_wait();
+    waited = true;
     const int pages = static_cast<int>(pages_of(len, p.t.block_size));
     bool bad = false;
 #pragma unroll 4
@@ -320,20 +328,23 @@ __device__ __forceinline__ void fork_refs(const ForkLaunch& p) {
     }
     if (bad) atomicOr(p.status, kDevBadPage);
   }
+  if (!waited) pdl_wait();
 }
 
-__global__ void __launch_bounds__(kForkThreads) fork_rows_kernel(const ForkLaunch p) {
+__global__ void __launch_bounds__(kForkThreads) fork_counts_kernel(const ForkLaunch p) {
   pdl_trigger();
-  fork_rows<kForkThreads>(p);
+  fork_counts(p);
 }
-__global__ void __launch_bounds__(kForkThreads) fork_refs_kernel(const ForkLaunch p) {
-  pdl_wait();
-  fork_refs<kForkThreads>(p);
+// The rows, and the numbers of children, do not wait for the counts.
+__global__ void __launch_bounds__(kForkThreads) fork_rows_kernel(const ForkLaunch p) {
+  fork_rows<kForkThreads>(p);
+  fork_refs<kForkThreads, true>(p);
 }
 __global__ void __cluster_dims__(kCluster) __launch_bounds__(kScanThreads) fork_kernel(const ForkLaunch p) {
+  fork_counts(p);
   fork_rows<32>(p);
   phase_end();
-  fork_refs<32>(p);
+  fork_refs<32, false>(p);
 }
 
 // ------------------------------------------------- growing and shrinking
@@ -652,12 +663,10 @@ cudaError_t launch_fork(const ForkLaunch& p, int num_sms, cudaStream_t stream) {
   if ((p.t.requests + p.children) * p.t.width + p.num_blocks <= kSmallEntries)
     return launch(fork_kernel, kCluster, kScanThreads, false, stream, p);
   const long long most = 16LL * num_sms;
-  const long long copies = p.out_refs == p.refs ? 0 : (p.num_blocks + 4 * kForkThreads - 1) / (4 * kForkThreads);
-  const long long first = std::min(most, std::max(p.children, copies));
-  cudaError_t e = cudaSuccess;
-  if (first) e = launch(fork_rows_kernel, first, kForkThreads, false, stream, p);
-  if (e != cudaSuccess || p.t.requests == 0) return e;
-  return launch(fork_refs_kernel, std::min(most, p.t.requests), kForkThreads, first > 0, stream, p);
+  const long long copies = p.out_refs == p.refs ? 0 : std::min(most, (p.num_blocks + 4 * kForkThreads - 1) / (4 * kForkThreads));
+  const long long rows = std::min(most, std::max(p.children, p.t.requests));
+  const cudaError_t e = copies ? launch(fork_counts_kernel, copies, kForkThreads, false, stream, p) : cudaSuccess;
+  return e == cudaSuccess && rows ? launch(fork_rows_kernel, rows, kForkThreads, copies > 0, stream, p) : e;
 }
 
 cudaError_t launch_resize(const ResizeLaunch& p, cudaStream_t stream) {
