@@ -492,15 +492,21 @@ __global__ void __launch_bounds__(kCopyThreads)
     resize_apply_kernel(const __grid_constant__ PageCopy c, const __grid_constant__ ResizeLaunch p, const int rows_ctas) {
   __shared__ int before[kMostChunks];
   pdl_wait();
-  const int4 first = blockIdx.x < rows_ctas ? make_int4(0, 0, 0, 0) : p.copies[p.t.requests];  // their number
-  const int free = free_before<kCopyThreads>(p.s, before);
   if (blockIdx.x < rows_ctas) {
+    const int free = free_before<kCopyThreads>(p.s, before);
     apply_plan(p, before, free, rows_ctas);
     return;
   }
-  for (CopyWalk w(c, blockIdx.x - rows_ctas, gridDim.x - rows_ctas); w.pair < first.x; w.next()) {
-    const int4 x = p.copies[w.pair];  // page, first of the request's free pages, their number, filled cells
+  CopyWalk w(c, blockIdx.x - rows_ctas, gridDim.x - rows_ctas);
+  // the number of copies and the first one are read together (there is room for one a request)
+  const int copies = p.copies[p.t.requests].x;
+  int4 x = w.pair < p.t.requests ? p.copies[w.pair] : make_int4(0, 0, 0, 0);
+  const int free = free_before<kCopyThreads>(p.s, before);
+  while (w.pair < copies) {
+    // x: page, first of the request's free pages, their number, filled cells
     if (static_cast<long long>(x.y) + x.z <= free) copy_page(c, w.piece, x.x, free_page(p.s, before, x.y), x.w);
+    w.next();
+    if (w.pair < copies) x = p.copies[w.pair];
   }
 }
 
