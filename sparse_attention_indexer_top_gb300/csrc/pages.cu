@@ -612,6 +612,16 @@ __global__ void __launch_bounds__(kScanThreads) compact_moves_kernel(const Compa
   if (blockIdx.x == 0 && threadIdx.x == 0) *p.count = n.y;
   move_chunk(p, before, n.x, n.y, blockIdx.x);
 }
+// A pool of one chunk: one CTA, whose phases end by its own barrier.
+__global__ void __launch_bounds__(kScanThreads) compact_chunk_kernel(const CompactLaunch p) {
+  __shared__ int before[kMostChunks];
+  pdl_trigger();
+  scan_chunk(p.s, 0);
+  __syncthreads();
+  const int2 n = count_moves(p.s, before);
+  if (threadIdx.x == 0) *p.count = n.y;
+  move_chunk(p, before, n.x, n.y, 0);
+}
 __global__ void __cluster_dims__(kCluster) __launch_bounds__(kScanThreads) compact_kernel(const CompactLaunch p) {
   __shared__ int before[kMostChunks];
   pdl_trigger();
@@ -685,6 +695,7 @@ cudaError_t launch_resize_apply(const PageCopy& c, const ResizeLaunch& p, bool r
 }
 
 cudaError_t launch_compact(const CompactLaunch& p, cudaStream_t stream) {
+  if (p.s.chunks == 1) return launch(compact_chunk_kernel, 1, kScanThreads, false, stream, p);
   if (p.s.num_blocks <= kSmallEntries) return launch(compact_kernel, kCluster, kScanThreads, false, stream, p);
   const cudaError_t e = launch(compact_scan_kernel, p.s.chunks, kScanThreads, false, stream, p.s);
   return e == cudaSuccess ? launch(compact_moves_kernel, p.s.chunks, kScanThreads, true, stream, p) : e;
