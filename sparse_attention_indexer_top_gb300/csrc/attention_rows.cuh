@@ -242,6 +242,10 @@ __global__ void __launch_bounds__(kThreads) attn_rows_kernel(const AttnLaunch p)
   constexpr int STAGE = 2 * KB + SK * 8 + MT * 4 + (16 - MT * 4 % 16) % 16;
   constexpr int NS = D / 16;        // k16 steps of q.k, and 16-dim column groups of O
   constexpr int HT = FEW ? 8 : 16;  // heads of a tile
+  // Changed scores, bf16: the weights go to the MMA as two bf16 terms, 2^-17
+  // together, so that the result is off by its own rounding alone; the time is that
+  // of the keys. (Masks alone change nothing, the last bit included.)
+  const bool split = MOD && !F8 && (p.cap_log2 > 0.f || p.slopes);
   static_assert(!FEW || MT == 1, "one tile of few heads");
 
   extern __shared__ __align__(128) unsigned char smem[];
@@ -586,7 +590,7 @@ __global__ void __launch_bounds__(kThreads) attn_rows_kernel(const AttnLaunch p)
             }
           }
           const float b0 = m0 == -INFINITY ? 0.f : m0, b1 = m1 == -INFINITY ? 0.f : m1;
-          uint32_t pb[2];
+          uint32_t pb[2], rest[2] = {0u, 0u};
 #pragma unroll
           for (int n = 0; n < 2; ++n) {
             float w0 = ex2(c[2 * n] - b0), w1 = ex2(c[2 * n + 1] - b1);
@@ -596,7 +600,9 @@ __global__ void __launch_bounds__(kThreads) attn_rows_kernel(const AttnLaunch p)
               w0 *= vs[n];
               w1 *= vs[n];
             }
-            pb[n] = transpose8x8(F8 ? pack_f16(w0, w1) : pack_bf16(w0, w1));
+            pb[n] = F8 ? pack_f16(w0, w1) : pack_bf16(w0, w1);
+            if (split) rest[n] = transpose8x8(pack_bf16(w0 - bf16_lo(pb[n]), w1 - bf16_hi(pb[n])));
+            pb[n] = transpose8x8(pb[n]);
           }
           if (!F8) {
             const int vrow = (lane & 7) + (lane >> 4) * 8, vhalf = (lane >> 3) & 1;
@@ -605,6 +611,7 @@ __global__ void __launch_bounds__(kThreads) attn_rows_kernel(const AttnLaunch p)
               uint32_t r[4];
               ldsm4_t(vb + vrow * RB + (((2 * s2 + vhalf) ^ (vrow & 7)) << 4), r);
               mma16816<false>(o[s2][0], r, pb[0], pb[1]);
+              if (split) mma16816<false>(o[s2][0], r, rest[0], rest[1]);
             }
           } else {
             // transposed 16-bit pairs hold two dims of keys 2t and 2t + 1; a
@@ -734,9 +741,9 @@ __global__ void __launch_bounds__(kThreads) attn_rows_kernel(const AttnLaunch p)
             }
           }
         // the weights as bf16 (f16 with e4m3 values): the MMA's other operand
-        // is the cache's type; relative error 2^-9 (2^-12 and the absolute term
-        // of kLift), under the output's
-        uint32_t pa[4];
+        // is the cache's type; relative error 2^-9 (split: 2^-17; f16 2^-12 and the
+        // absolute term of kLift), under the output's
+        uint32_t pa[4], rest[4] = {0u, 0u, 0u, 0u};
         if (F8) {
           pa[0] = pack_f16(c[0][0], c[0][1]);
           pa[1] = pack_f16(c[0][2], c[0][3]);
@@ -748,6 +755,11 @@ __global__ void __launch_bounds__(kThreads) attn_rows_kernel(const AttnLaunch p)
           pa[2] = pack_bf16(c[1][0], c[1][1]);
           pa[3] = pack_bf16(c[1][2], c[1][3]);
         }
+        if (split) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            rest[i] = pack_bf16(c[i / 2][i % 2 * 2] - bf16_lo(pa[i]), c[i / 2][i % 2 * 2 + 1] - bf16_hi(pa[i]));
+        }
         const int vrow = lane & 15, vhalf = lane >> 4;
         if (!F8) {
 #pragma unroll
@@ -756,6 +768,10 @@ __global__ void __launch_bounds__(kThreads) attn_rows_kernel(const AttnLaunch p)
             ldsm4_t(vb + vrow * RB + (((2 * s2 + vhalf) ^ (vrow & 7)) << 4), r);
             mma16816<false>(o[s2][0], pa, r[0], r[1]);
             mma16816<false>(o[s2][NO - 1], pa, r[2], r[3]);
+            if (split) {
+              mma16816<false>(o[s2][0], rest, r[0], r[1]);
+              mma16816<false>(o[s2][NO - 1], rest, r[2], r[3]);
+            }
           }
         } else {
           // transposed 16-bit pairs hold two dims of keys 2t and 2t + 1; a
