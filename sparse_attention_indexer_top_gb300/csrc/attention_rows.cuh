@@ -28,8 +28,8 @@
 // sees a document or a prefix of its request. These instances are apart, in
 // attention_rows_mod.cu, so that the plain ones hold none of it; what is done is
 // chosen at run time, since reading the keys takes longer: 64 rows of 4096-32768
-// keys, 64 / 8 heads, e4m3, 399 us plain, 412 capped, 404 biased, 414 both; bf16 721
-// to 723.
+// keys, 64 / 8 heads, e4m3, 399 us plain, 411 capped, 404 biased, 412 both; bf16 723
+// for all of them.
 #pragma once
 #include "attention_mod.cuh"
 #include "sai_internal.h"

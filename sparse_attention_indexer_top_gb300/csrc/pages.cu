@@ -17,8 +17,8 @@
 //
 // On the GPU, us: copy of 3 pages 2.3, of 500 pages of 24 arrays 167 (6.68 TB/s, a
 // plain copy's rate); fork of 8 requests 3.3, of 512 to 600 with a pool of 131072
-// pages 6.2; resize of 16 beams with their copies 9.0, of 160 requests 6.5; compact of
-// 512 pages 7.0, of 4096 pages of 12 arrays 84 (72 are its bytes).
+// pages 5.7; resize of 16 beams with their copies 8.8, of 160 requests 6.5; compact of
+// 512 pages 6.2, of 4096 pages of 12 arrays 83 (72 are its bytes).
 #include "sai_internal.h"
 #include "sai_ptx.cuh"
 
