@@ -18,7 +18,7 @@
 // On the GPU, us: copy of 3 pages 2.3, of 500 pages of 24 arrays 167 (6.68 TB/s, a
 // plain copy's rate); fork of 8 requests 3.3, of 512 to 600 with a pool of 131072
 // pages 5.7; resize of 16 beams with their copies 8.8, of 160 requests 6.5; compact of
-// 512 pages 6.2, of 4096 pages of 12 arrays 83 (72 are its bytes).
+// 512 pages 6.2, of 4096 pages of 16 arrays 83 (72 are its bytes).
 #include "sai_internal.h"
 #include "sai_ptx.cuh"
 
@@ -253,13 +253,6 @@ __device__ __forceinline__ int team_sum(int x) {
   block_scan<TEAM>(x, &total);
   return total;
 }
-template <int TEAM>
-__device__ __forceinline__ void team_sync() {
-  if (TEAM == 32)
-    __syncwarp();
-  else
-    __syncthreads();
-}
 // End of a phase in a cluster: what its CTAs wrote is there for all of them.
 __device__ __forceinline__ void phase_end() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -351,7 +344,7 @@ __global__ void __cluster_dims__(kCluster) __launch_bounds__(kScanThreads) fork_
 enum : int { kGood = 1, kCopies = 2, kKeeps = 4 };
 
 // What each request wants, and which free pages (by number) are for it. One CTA,
-// a request to a thread, in rounds where there are more; the first round's stay
+// a request to a thread, in turns where there are more; those of the first turn stay
 // in registers, and the shared last pages of up to kShared requests in shared
 // memory.
 __device__ __forceinline__ void plan_requests(const ResizeLaunch& p) {
