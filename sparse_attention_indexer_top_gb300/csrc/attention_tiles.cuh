@@ -811,12 +811,13 @@ __device__ __forceinline__ float largest32(const uint32_t* s, float top) {
 // Any tile, by the longer way: an e4m3 cache's whose scales are not all in the
 // tile's powers (factors[g] are left over of 16 keys' scales; null: nothing is),
 // and with changed scores one that may move the maximum, has scores near its
-// cap, or keys on both sides of a row's position. Out of line, and S is read
-// twice 32 columns at a time: beside the plain code it slowed that by half.
+// cap, or keys on both sides of a row's position (`keep`: the maximum is known to
+// stay, and one reading does). Out of line, and S is read twice 32 columns at a
+// time: beside the plain code it slowed that by half.
 template <int D, bool F8, int MOD>
 __device__ __noinline__ float2 rough_tile(uint32_t ts, uint32_t to, float2 ml, float mul, float ev, float un_ev,
                                           const float2* factors, int4 sees, uint32_t bad, bool masked, bool have_o,
-                                          Change ch) {
+                                          bool keep, Change ch) {
   constexpr bool kChanged = (MOD & (kCap | kBias)) != 0;
   uint32_t s[32];
   // masked after the scaling: a scale may be 0, and 0 * -inf is NaN
@@ -836,7 +837,7 @@ __device__ __noinline__ float2 rough_tile(uint32_t ts, uint32_t to, float2 ml, f
   const float mul1 = kChanged ? 1.f : mul;
   float top = -INFINITY;
 #pragma unroll 1
-  for (int c0 = 0; c0 < kTile; c0 += 32) {
+  for (int c0 = 0; c0 < kTile && !(kChanged && keep); c0 += 32) {
     tmem_ld32(ts + c0, s);
     tmem_ld_wait32(s);
     scaled(c0);
@@ -865,7 +866,7 @@ __device__ __noinline__ float2 rough_tile(uint32_t ts, uint32_t to, float2 ml, f
   for (int c0 = 0; c0 < kTile; c0 += 32) {  // weights of chunk c go over scores of chunk c / 2
     tmem_ld32(ts + c0, s);
     tmem_ld_wait32(s);
-    if (!kChanged) scaled(c0);
+    if (!kChanged || keep) scaled(c0);
 #pragma unroll
     for (int c = 0; c < 32; c += 2) {
       const float f = !kChanged || factors ? factors[(c0 + c) / 16].y : 1.f;
@@ -1018,10 +1019,10 @@ __device__ __forceinline__ bool softmax_role(Shared<D, F8>& S, const TilesLaunch
         return top;
       };
       const Change ch{cap, inv_cap, ln.slope, ln.pos - t0};
-      auto rough_path = [&](const float2* factors) {
+      auto rough_path = [&](const float2* factors, bool keep) {
         const float2 ml = rough_tile<D, F8, MOD>(ts, to, make_float2(m, l), mul, ev, un_ev, factors,
                                                  make_int4(ln.n - t0, ln.first - t0, ln.sinks - t0, ln.start - t0), bad,
-                                                 masked, i > ps.i0, ch);
+                                                 masked, i > ps.i0, keep, ch);
         m = ml.x;
         l = ml.y;
         tc_fence_before();
@@ -1032,7 +1033,7 @@ __device__ __forceinline__ bool softmax_role(Shared<D, F8>& S, const TilesLaunch
         }
       };
       if (F8 && rough) {
-        rough_path(factors);
+        rough_path(factors, false);
         continue;
       }
       auto hand_over = [&](int half) {
@@ -1059,8 +1060,10 @@ __device__ __forceinline__ bool softmax_role(Shared<D, F8>& S, const TilesLaunch
           bound = MOD & kCap ? largest32(u[c & 1], bound) : largest(u[c & 1], 0, bound);
         }
         bool quick = true, nearest = false;
+        float far = 0.f, most = 0.f;  // largest magnitude over the cap; the most that the bias adds
         if (MOD & kCap) {
           const float t = bound * (mul * inv_cap), y = t * t;
+          far = t;
           nearest = __all_sync(0xffffffffu, !ln.live || t <= kNearest);
           quick = t <= kNear && (F8 || (mul * inv_cap > 0x1p-17f && mul * inv_cap < 0x1p17f));  // whose 7th power is normal
           bound = cap * (t * fmaf(fmaf(fmaf(tanh_near(3), y, tanh_near(2)), y, tanh_near(1)), y, tanh_near(0)));
@@ -1071,14 +1074,16 @@ __device__ __forceinline__ bool softmax_role(Shared<D, F8>& S, const TilesLaunch
         if (MOD & kBias) {
           const float d0 = static_cast<float>(ch.ahead), d1 = d0 - (kTile - 1);
           const float lo = d1 > 0.f ? d1 : d0 < 0.f ? -d0 : 0.f, hi = fmaxf(d0, -d1);
-          bound = fmaf(-ln.slope, ln.slope >= 0.f ? lo : hi, bound);
+          most = -ln.slope * (ln.slope >= 0.f ? lo : hi);
+          bound += most;
           slope = d0 < 0.f ? -ln.slope : ln.slope;
           off = fmaf(-slope, d0, ev);
           quick = quick && !(d0 >= 0.f && d1 < 0.f && ln.n > ln.pos + 1);  // no keys on both sides of the position
         }
         tmem_ld_wait32(u[0]);
         if (!__all_sync(0xffffffffu, !ln.live || (quick && bound + ev <= m + kPassed<F8>))) {
-          rough_path(nullptr);
+          if (MOD & kCap && far > kNear) bound = fmaf(cap, tanh_far(far), most);
+          rough_path(nullptr, __all_sync(0xffffffffu, !ln.live || bound + ev <= m + kPassed<F8>));
           continue;
         }
         off -= m == -INFINITY ? 0.f : m;
