@@ -694,10 +694,11 @@ struct Change {
 };
 
 // Changes 32 columns of scores s, from column c0 of the tile: times `mul`,
-// capped, biased. Two elements to an instruction. FAR: scores above half the cap
-// are cap (1 - 2 / (1 + e^(2x / cap))), off by 2^-22 of the cap; without, there are
-// none.
-template <int MOD, bool FAR>
+// capped, biased. Two elements to an instruction. FAR 0: no score is above half
+// the cap; 1: none above the cap (three coefficients more, but no exponentials and
+// reciprocals, of which a pair would take as long as two dozen FMAs); 2: those above
+// half of it are cap (1 - 2 / (1 + e^(2x / cap))), off by 2^-22 of the cap.
+template <int MOD, int FAR>
 __device__ __forceinline__ void change32(uint32_t* s, int c0, float mul, const Change& ch) {
   const float xm = fminf(mul * ch.inv_cap, 1e38f), em = xm * 2.885390081777927f;  // finite: a score of 0 stays 0
   const uint64_t mul_2 = pair(mul, mul), x_2 = pair(xm, xm), e_2 = pair(em, em), slope_2 = pair(-ch.slope, -ch.slope);
@@ -705,19 +706,23 @@ __device__ __forceinline__ void change32(uint32_t* s, int c0, float mul, const C
   // distances of the two columns, whole numbers, less 2 at each step
   uint64_t d = pair(static_cast<float>(ch.ahead - c0), static_cast<float>(ch.ahead - c0 - 1));
   const uint64_t step = pair(-2.f, -2.f);
-  uint64_t q_2[4];
+  constexpr int Q = FAR == 1 ? 7 : 4;
+  uint64_t q_2[Q];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) q_2[i] = pair(ch.cap * tanh_near(i), ch.cap * tanh_near(i));
+  for (int i = 0; i < Q; ++i) {
+    const float f = ch.cap * (FAR == 1 ? tanh_q(i) : tanh_near(i < 4 ? i : 0));
+    q_2[i] = pair(f, f);
+  }
 #pragma unroll
   for (int c = 0; c < 32; c += 2) {
     uint64_t v = pair(__uint_as_float(s[c]), __uint_as_float(s[c + 1]));
     if (MOD & kCap) {
       const uint64_t x = mul2(v, x_2), y = mul2(x, x);
-      uint64_t q = q_2[3];
+      uint64_t q = q_2[Q - 1];
 #pragma unroll
-      for (int i = 2; i >= 0; --i) q = fma2(q, y, q_2[i]);
+      for (int i = Q - 2; i >= 0; --i) q = fma2(q, y, q_2[i]);
       q = mul2(x, q);
-      if (FAR) {
+      if (FAR == 2) {
         float a, b, xa, xb, na, nb;
         unpair(mul2(v, e_2), a, b);
         unpair(add2(pair(ex2(a), ex2(b)), one_2), a, b);
@@ -827,10 +832,13 @@ __device__ __noinline__ float2 rough_tile(uint32_t ts, uint32_t to, float2 ml, f
       for (int c = 0; c < 32; ++c) s[c] = __float_as_uint(__uint_as_float(s[c]) * factors[(c0 + c) / 16].x);
     }
     if (kChanged) {
-      if ((MOD & kCap) && !__all_sync(0xffffffffu, largest32(s, 0.f) * (mul * ch.inv_cap) <= kNear))
-        change32<MOD, true>(s, c0, mul, ch);
+      const float far = MOD & kCap ? largest32(s, 0.f) * (mul * ch.inv_cap) : 0.f;
+      if (!(MOD & kCap) || __all_sync(0xffffffffu, far <= kNear))
+        change32<MOD, 0>(s, c0, mul, ch);
+      else if (__all_sync(0xffffffffu, far <= 1.f))
+        change32<MOD, 1>(s, c0, mul, ch);
       else
-        change32<MOD, false>(s, c0, mul, ch);
+        change32<MOD, 2>(s, c0, mul, ch);
     }
     if (!kChanged || masked) mask32<MOD>(s, sees.x - c0, sees.y - c0, sees.z - c0, sees.w - c0, bad >> (c0 / 16));
   };
