@@ -126,6 +126,16 @@ __device__ __forceinline__ float ex2(float x) {
 }
 __device__ __forceinline__ float bf16_lo(uint32_t x) { return __uint_as_float(x << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t x) { return __uint_as_float(x & 0xffff0000u); }
+// Two weights w >= 0 as two bf16 terms each, off by 2^-15 of w at most together: the
+// upper half of w's bits (2^-7), and the rest, rounded (2^-8 of it). The rest of a weight above 0 is above 0 too
+// (2^-126 at least): both terms multiply the same values, and 0, or anything
+// below it, times an infinite one would turn the sum into NaN.
+__device__ __forceinline__ uint32_t upper_bf16(float a, float b) {
+  return __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
+}
+__device__ __forceinline__ uint32_t rest_bf16(float a, float b, uint32_t upper) {
+  return pack_bf16(fmaxf(a - bf16_lo(upper), fminf(a, 0x1p-126f)), fmaxf(b - bf16_hi(upper), fminf(b, 0x1p-126f)));
+}
 
 // Ring depth of each warp's (team's) 16-key (16 * MT keys) stages. A group's
 // work is a chain of dependent steps, so more warps beat deeper rings: at dim
@@ -242,7 +252,7 @@ __global__ void __launch_bounds__(kThreads) attn_rows_kernel(const AttnLaunch p)
   constexpr int STAGE = 2 * KB + SK * 8 + MT * 4 + (16 - MT * 4 % 16) % 16;
   constexpr int NS = D / 16;        // k16 steps of q.k, and 16-dim column groups of O
   constexpr int HT = FEW ? 8 : 16;  // heads of a tile
-  // Changed scores, bf16: the weights go to the MMA as two bf16 terms, 2^-17
+  // Changed scores, bf16: the weights go to the MMA as two bf16 terms, 2^-15
   // together, so that the result is off by its own rounding alone; the time is that
   // of the keys. (Masks alone change nothing, the last bit included.)
   const bool split = MOD && !F8 && (p.cap_log2 > 0.f || p.slopes);
@@ -600,8 +610,8 @@ __global__ void __launch_bounds__(kThreads) attn_rows_kernel(const AttnLaunch p)
               w0 *= vs[n];
               w1 *= vs[n];
             }
-            pb[n] = F8 ? pack_f16(w0, w1) : pack_bf16(w0, w1);
-            if (split) rest[n] = transpose8x8(pack_bf16(w0 - bf16_lo(pb[n]), w1 - bf16_hi(pb[n])));
+            pb[n] = F8 ? pack_f16(w0, w1) : split ? upper_bf16(w0, w1) : pack_bf16(w0, w1);
+            if (split) rest[n] = transpose8x8(rest_bf16(w0, w1, pb[n]));
             pb[n] = transpose8x8(pb[n]);
           }
           if (!F8) {
@@ -741,24 +751,26 @@ __global__ void __launch_bounds__(kThreads) attn_rows_kernel(const AttnLaunch p)
             }
           }
         // the weights as bf16 (f16 with e4m3 values): the MMA's other operand
-        // is the cache's type; relative error 2^-9 (split: 2^-17; f16 2^-12 and the
-        // absolute term of kLift), under the output's
+        // is the cache's type; relative error 2^-8, as the output's own rounding
+        // (split: 2^-15; f16 2^-11 and the absolute term of kLift)
         uint32_t pa[4], rest[4] = {0u, 0u, 0u, 0u};
         if (F8) {
           pa[0] = pack_f16(c[0][0], c[0][1]);
           pa[1] = pack_f16(c[0][2], c[0][3]);
           pa[2] = pack_f16(c[1][0], c[1][1]);
           pa[3] = pack_f16(c[1][2], c[1][3]);
+        } else if (split) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float a = c[i / 2][i % 2 * 2], b = c[i / 2][i % 2 * 2 + 1];
+            pa[i] = upper_bf16(a, b);
+            rest[i] = rest_bf16(a, b, pa[i]);
+          }
         } else {
           pa[0] = pack_bf16(c[0][0], c[0][1]);
           pa[1] = pack_bf16(c[0][2], c[0][3]);
           pa[2] = pack_bf16(c[1][0], c[1][1]);
           pa[3] = pack_bf16(c[1][2], c[1][3]);
-        }
-        if (split) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            rest[i] = pack_bf16(c[i / 2][i % 2 * 2] - bf16_lo(pa[i]), c[i / 2][i % 2 * 2 + 1] - bf16_hi(pa[i]));
         }
         const int vrow = lane & 15, vhalf = lane >> 4;
         if (!F8) {

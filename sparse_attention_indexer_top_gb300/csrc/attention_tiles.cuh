@@ -1169,8 +1169,8 @@ __device__ __forceinline__ bool softmax_role(Shared<D, F8>& S, const TilesLaunch
         if (i > ps.i0) rescale_o<D>(to, f);
       }
       const float base = m == -INFINITY ? 0.f : m;
-      // weights of 32 columns in 16 bits (relative error 2^-9, under the output's
-      // own; f16 2^-12 and the absolute term of kLift), over the scores' TMEM
+      // weights of 32 columns in 16 bits (relative error 2^-8, as the output's own
+      // rounding; f16 2^-11 and the absolute term of kLift), over the scores' TMEM
       // columns
       float tile_l = 0.f;
       auto weights = [&](uint32_t* s, int c0) {

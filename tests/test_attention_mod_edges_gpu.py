@@ -1,0 +1,83 @@
+"""GPU tests of the attention with changed scores and masks where it went wrong or slow: infinite values, large scales,
+first tokens of several documents, long prefixes under short windows, rows that see nothing, the cap's own error.
+
+Bounds of time compare two calls on the same machine with about the same keys to read; they are far above what the calls
+differ by and far below what they differed by while the second one walked keys that no row sees, or walked them alone.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+import sparse_attention_indexer_top_gb300 as sai
+from oracle import attention as A
+from test_attention_gpu import DEV, Case, _lens
+from test_attention_mod_gpu import _check, _slopes
+
+pytestmark = pytest.mark.gpu
+
+
+def _infinite(c, n, dim):
+    """Value cell (t, t % dim) becomes infinite, even t up, odd t down: every dim meets one infinity at least, of one sign
+    (dim is even), with a weight of its own."""
+    for t in range(n):
+        inf = float("inf") if t % 2 == 0 else -float("inf")
+        c.v[int(c.table[0, t // c.bs]), :, t % c.bs, t % dim] = inf
+
+
+def _all_infinite(out, dim):
+    sign = torch.where(torch.arange(dim, device=DEV) % 2 == 0, float("inf"), -float("inf"))
+    return bool((out.float() == sign).all())
+
+
+INF_MODS = [dict(), dict(softcap=30.0), dict(softcap=5.0, slopes=0.02), dict(slopes=0.02)]
+
+
+@pytest.mark.parametrize("mod", INF_MODS)
+@pytest.mark.parametrize("group,dim", [(1, 128), (8, 64), (12, 128), (17, 64), (70, 128)])
+@pytest.mark.parametrize("packed", [0, 1, sai.PACKED_TILES])
+def test_visible_infinite_values_stay_infinite(mod, group, dim, packed):
+    """A sum of positive weights times values with infinities of one sign is infinite, the key of the largest weight among
+    them; scores lie within 60 of one another, so no weight is 0."""
+    n = 2 * dim
+    c = Case(20 + dim + group, [n], dtype="bf16", hkv=1, dim=dim, bs=64)
+    _infinite(c, n, dim)
+    q, _ = c.queries(3, group, sigma=1.0)
+    kw = dict(mod)
+    if "slopes" in kw:
+        kw["slopes"] = kw["slopes"] * _slopes(group)
+    out = sai.paged_attention(q, c.cache, c.t_table, _lens([n, n - 1, n]), max_seq_len=n, row_to_batch=_lens([0, 0, 0]),
+                              packed=packed, **kw)
+    assert _all_infinite(out, dim)
+
+
+@pytest.mark.parametrize("cap", [0.0, 4.0])
+@pytest.mark.parametrize("group", [4, 16, 64])
+def test_sparse_infinite_values_stay_infinite(cap, group):
+    c = Case(30 + group, [256], dtype="bf16", hkv=1, bs=64)
+    _infinite(c, 256, 128)
+    q, _ = c.queries(2, group, sigma=1.0)
+    slots = torch.tensor([[c.slot(0, t) for t in range(256)], [c.slot(0, t) for t in range(128)] + [-1] * 128],
+                         dtype=torch.int32, device=DEV)
+    assert _all_infinite(sai.sparse_attention(q, c.cache, slots, softcap=cap), 128)
+
+
+@pytest.mark.parametrize("packed", [0, sai.PACKED_TILES])
+def test_an_infinite_value_reaches_its_dim_alone(packed):
+    """One infinity on a row that is split over chunks, and another row that does not see it."""
+    c = Case(40, [3000], dtype="bf16", hkv=2, bs=128)
+    q, q64 = c.queries(2, 8, sigma=1.0)
+    at = 2500
+    c.v[int(c.table[0, at // 128]), :, at % 128, 9] = float("inf")
+    slopes = 0.001 * _slopes(8)
+    out, lse = sai.paged_attention(q, c.cache, c.t_table, _lens([3000, 2400]), max_seq_len=3000, row_to_batch=_lens([0, 0]),
+                                   packed=packed, want_lse=True, softcap=20.0, slopes=slopes)
+    assert (out[0, :, 9] == float("inf")).all() and torch.isfinite(out[1]).all()
+    out[0, :, 9] = 0.0
+    c.kv[0][1][at, :, 9] = 0.0
+    for i, n in enumerate((3000, 2400)):
+        k, v = (x[:n] for x in c.kv[0])
+        ref, _, mag = A.attend_changed(q64[i], k, v, 128 ** -0.5, 20.0, slopes.double().cpu().numpy(), np.arange(n)[::-1])
+        if i == 0:
+            ref[:, 9] = mag[:, 9] = 0.0
+        assert (np.abs(out[i].float().cpu().numpy() - ref) <= 2.0 ** -8 * np.abs(ref) + 2.0 ** -7 * mag).all(), i
