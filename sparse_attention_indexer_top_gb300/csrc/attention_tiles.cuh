@@ -911,6 +911,12 @@ __device__ __forceinline__ bool softmax_role(Shared<D, F8>& S, const TilesLaunch
   float scale = p.scale_log2;
   bool lost = false;  // as in the MMA role: no way out of the loop
   const float cap = MOD & kCap ? p.cap_log2 : 0.f, inv_cap = MOD & kCap ? 1.f / cap : 0.f;
+  // bf16: may the polynomial be one in the products themselves? Its last coefficient
+  // has the 7th power of the scale over the cap, times the cap: normal numbers are
+  // needed, and a cap below 2^17 times the scale (11,585 at dim 128; above it every
+  // tile goes the longer way).
+  const float over = MOD & kCap ? scale * inv_cap : 1.f, over3 = over * over * over;
+  const bool in_products = F8 || (over > 0x1p-17f && over < 0x1p17f && scale * over3 * over3 < 0x1p126f);
   if (F8) {
     lost = !mbar_wait(&S.q_full, at.pieces & 1);
     scale *= query_to_f16<D>(S.q[x], r);
@@ -1073,7 +1079,7 @@ __device__ __forceinline__ bool softmax_role(Shared<D, F8>& S, const TilesLaunch
           const float t = bound * (mul * inv_cap), y = t * t;
           far = t;
           nearest = __all_sync(0xffffffffu, !ln.live || t <= kNearest);
-          quick = t <= kNear && (F8 || (mul * inv_cap > 0x1p-17f && mul * inv_cap < 0x1p17f));  // whose 7th power is normal
+          quick = t <= kNear && in_products;
           bound = cap * (t * fmaf(fmaf(fmaf(tanh_near(3), y, tanh_near(2)), y, tanh_near(1)), y, tanh_near(0)));
         } else {
           bound *= mul;

@@ -81,3 +81,25 @@ def test_an_infinite_value_reaches_its_dim_alone(packed):
         if i == 0:
             ref[:, 9] = mag[:, 9] = 0.0
         assert (np.abs(out[i].float().cpu().numpy() - ref) <= 2.0 ** -8 * np.abs(ref) + 2.0 ** -7 * mag).all(), i
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("packed", [0, sai.PACKED_TILES])
+@pytest.mark.parametrize("slopes", [False, True])
+@pytest.mark.parametrize("sm,cap", [(1e20, 1e15), (1e30, 1e26), (2.0 ** 60, 2.0 ** 50), (1e-25, 1e-29)])
+def test_large_and_small_scales_under_a_cap(dtype, packed, slopes, sm, cap):
+    """Scores of 0 at any sm_scale: the weights are even (biased: those of the distances alone)."""
+    n = 300
+    c = Case(41, [n], dtype=dtype, bs=16, hkv=1)
+    q = torch.zeros((2, 2, 128), dtype=torch.bfloat16, device=DEV)
+    sl = _slopes(2) if slopes else None
+    out, lse = sai.paged_attention(q, c.cache, c.t_table, _lens([n, 200]), max_seq_len=n, row_to_batch=_lens([0, 0]),
+                                   packed=packed, want_lse=True, softcap=cap, sm_scale=sm, slopes=sl)
+    for i, m in enumerate((n, 200)):
+        w = np.exp(-(sl.double().cpu().numpy() if slopes else np.zeros(2))[:, None] * np.arange(m)[::-1])
+        ref = w @ c.kv[0][1][:m, 0] / w.sum(1, keepdims=True)
+        mag = w @ np.abs(c.kv[0][1][:m, 0]) / w.sum(1, keepdims=True)
+        # weights in 16 bits (2^-8 of each at most) and the result's own rounding
+        assert (np.abs(out[i].float().cpu().numpy() - ref) <= 2.0 ** -8 * np.abs(ref) + 2.0 ** -7 * mag).all(), i
+        # distances' products 2^-22 of at most 150, exponentials and sums 2^-20
+        assert np.abs(lse[i].cpu().numpy() - np.log(w.sum(1))).max() <= 2.0 ** -14, i
