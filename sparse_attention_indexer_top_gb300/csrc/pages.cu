@@ -345,12 +345,15 @@ enum : int { kGood = 1, kCopies = 2, kKeeps = 4 };
 
 // What each request wants, and which free pages (by number) are for it. One CTA,
 // a request to a thread, in turns where there are more; those of the first turn stay
-// in registers, and the shared last pages of up to kShared requests in shared
-// memory.
+// in registers. How many share a last page, and which is the last of them: up to
+// kPlanShared requests keep their pages in shared memory, and each looks at all of
+// them; more are counted page by page in memory, so that the time grows with the
+// requests and not with their square. Pairs on one page, all growing, a call in us,
+// looking at all (counting): 128 requests 13.8 (14.4), 256 15.8 (14.4), 512 29
+// (14), 2048 314 (28), 131072 1 s (1.35 ms).
 __device__ __forceinline__ void plan_requests(const ResizeLaunch& p) {
   const PageTable& t = p.t;
-  constexpr int kShared = 2048;
-  __shared__ int others[kShared];
+  __shared__ int others[kPlanShared];
   struct Wish {
     int need, state, last, shared, refs;  // shared: the last page, if others hold it too, else -1
   };
@@ -375,14 +378,24 @@ __device__ __forceinline__ void plan_requests(const ResizeLaunch& p) {
     w.need = static_cast<int>(max(0LL, pages_of(want, t.block_size) - pages_of(len, t.block_size)));
     return w;
   };
-  const bool few = t.requests <= kShared;
+  const bool few = t.requests <= kPlanShared;
   const Wish first = wish(threadIdx.x);
   int any = 0;
   for (long long r0 = 0; r0 < t.requests; r0 += kScanThreads) {
     const long long r = r0 + threadIdx.x;
     const Wish w = r0 == 0 ? first : wish(r);
-    if (r < t.requests) (few ? others : p.last_shared)[r] = w.shared;
+    if (few && r < t.requests) others[r] = w.shared;
+    if (!few && w.shared >= 0) p.sharers[w.shared] = make_int2(0, -1);
     any |= __syncthreads_or(w.shared >= 0);
+  }
+  if (!few && any) {
+    for (long long r = threadIdx.x; r < t.requests; r += kScanThreads) {
+      const Wish w = r < kScanThreads ? first : wish(r);
+      if (w.shared < 0) continue;
+      atomicAdd(&p.sharers[w.shared].x, 1);
+      atomicMax(&p.sharers[w.shared].y, static_cast<int>(r));
+    }
+    __syncthreads();
   }
   long long upto = 0;
   int copied = 0;
@@ -392,20 +405,17 @@ __device__ __forceinline__ void plan_requests(const ResizeLaunch& p) {
     if (any) {
       int same = 0;
       bool later = false;
-      for (long long k0 = 0; k0 < t.requests; k0 += kShared) {
-        const int n = static_cast<int>(min(static_cast<long long>(kShared), t.requests - k0));
-        if (!few) {
-          __syncthreads();
-          for (int k = threadIdx.x; k < n; k += kScanThreads) others[k] = p.last_shared[k0 + k];
-          __syncthreads();
-        }
-        if (w.shared >= 0)
+      if (w.shared >= 0 && few) {
 #pragma unroll 8
-          for (int k = 0; k < n; ++k)
-            if (others[k] == w.shared) {
-              ++same;
-              later = later || k0 + k > r;
-            }
+        for (int k = 0; k < static_cast<int>(t.requests); ++k)
+          if (others[k] == w.shared) {
+            ++same;
+            later = later || k > r;
+          }
+      } else if (w.shared >= 0) {
+        const int2 x = __ldcg(p.sharers + w.shared);
+        same = x.x;
+        later = x.y > r;
       }
       if (w.shared >= 0) {
         // the last of all its holders keeps the page: those before it leave it, or it is not served either

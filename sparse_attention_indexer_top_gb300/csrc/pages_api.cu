@@ -154,7 +154,7 @@ size_t lay_out(sai::ResizeLaunch* p, int64_t num_blocks, int64_t requests, char*
   p->s.free_list = w.take<int>(num_blocks);
   p->plan = w.take<int4>(requests);
   p->copies = w.take<int4>(requests + 1);
-  p->last_shared = w.take<int>(requests);
+  p->sharers = w.take<int2>(requests > sai::kPlanShared ? num_blocks : 0);
   return w.used;
 }
 size_t lay_out(sai::CompactLaunch* p, int64_t num_blocks, char* base) {

@@ -267,13 +267,14 @@ struct ForkLaunch {
   int* out_lens;
   int* status;
 };
+constexpr int kPlanShared = 128;
 struct ResizeLaunch {
   PageTable t;
   PoolScan s;
   const int* new_lens;
   int* out_lens;
   int4* plan;        // [requests]: first of its free pages, their number, state, last page
-  int* last_shared;  // [requests]
+  int2* sharers;     // [num_blocks], above kPlanShared requests: growing requests whose shared last page it is, last of them
   int4* copies;      // [requests + 1]: page, first of its request's free pages, their number, filled cells; last: number
   int* status;
 };
