@@ -60,3 +60,48 @@ def test_resize_time_grows_with_the_requests_alone():
 
     small, large = us(16384), us(131072)
     assert large < 20 * small, (small, large)  # eight times the requests
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("requests,children", [(3, 5000), (300, 320), (300, 321), (5000, 9000)])
+def test_fork_of_many_children(requests, children, in_place):
+    bs, width, blocks = 16, 5, 2 * requests + 50  # 64 children a column
+    table, lens, refs = _state(requests, requests, blocks, bs, width, most=30)
+    rng = random.Random(children)
+    parents = [rng.randrange(-1, requests) for _ in range(children)]
+    counts = [0] * requests
+    for r in parents:
+        if r >= 0:
+            counts[r] += 1
+    want = list(refs)
+    for r, row in enumerate(table):
+        for page in row[:O.pages_of(lens[r], bs)]:
+            want[page] += counts[r] - 1
+    t_refs = _t(refs)
+    got = sai.fork_pages(_t(table), _t(lens), t_refs, _t(parents), block_size=bs, out_refs=t_refs if in_place else None)
+    assert got[0].tolist() == [table[r] if r >= 0 else [-1] * width for r in parents]
+    assert got[1].tolist() == [lens[r] if r >= 0 else 0 for r in parents] and got[2].tolist() == want
+    assert sai.device_status() == 0
+
+
+def test_fork_of_many_children_with_bad_metadata():
+    table, lens, refs = [[0, 1], [2, 99], [3, -7]], [20, 32, 40], [1, 1, 1, 1, 0]
+    parents = [0, 1, 2, 3, -2] + [0] * 5000 + [1] * 9
+    got = sai.fork_pages(_t(table), _t(lens), _t(refs), _t(parents), block_size=16)
+    # request 2 is too long, 3 and -2 are no requests, page 99 is none
+    assert got[0][:6].tolist() == [[0, 1], [2, 99], [-1, -1], [-1, -1], [-1, -1], [0, 1]] and got[0][-1].tolist() == [2, 99]
+    assert got[1][:6].tolist() == [20, 32, 0, 0, 0, 20] and got[2].tolist() == [5001, 5001, 10, 1, 0]
+    assert sai.device_status() == 1 + 4
+
+
+def test_fork_time_grows_with_the_requests_alone():
+    def us(n):
+        table = torch.arange(n, dtype=torch.int32, device=DEV)[:, None].contiguous()
+        lens, refs = torch.full((n,), 5, dtype=torch.int32, device=DEV), torch.ones(n, dtype=torch.int32, device=DEV)
+        parents = torch.arange(n, dtype=torch.int32, device=DEV).flip(0).contiguous()
+        got = sai.fork_pages(table, lens, refs, parents, block_size=16)
+        assert torch.equal(got[0], table.flip(0)) and torch.equal(got[2], refs)
+        return least_us(lambda: sai.fork_pages(table, lens, refs, parents, block_size=16))
+
+    small, large = us(65536), us(524288)
+    assert large < 20 * small, (small, large)  # eight times the requests
