@@ -258,13 +258,15 @@ __device__ __forceinline__ void phase_end() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 constexpr int kCluster = 8;
-// Entries of tables and counts that one cluster takes: a fork of 8 requests with a
-// pool of 1024 takes 3.3 us with it and 3.7 in two launches (and 2 us less of the
-// host); one of 512 requests, 0.6 million entries, 10.8 and 5.8.
-constexpr long long kSmallEntries = 1 << 16;
 
 // ------------------------------------------------------------------ forks
 constexpr int kForkThreads = 128;
+// Entries of tables and counts, and columns, that one cluster takes: there the host
+// saves 1 us by one launch less. On the GPU (called one after another), us, as a
+// cluster: 1536 entries of 32 columns 3.6 (5.5), 6144 of 32 4.0 (5.9), 12288 of 64
+// 4.6 (6.4), 8192 of 256 6.1 (8.3), 32768 of 512 9.4 (10.6); in two launches 3.6
+// (6.9), 4.0 (7.0), 4.0 (7.0), 4.3 (7.1), 5.2 (6.8).
+constexpr long long kForkSmall = 1 << 13, kForkNarrow = 64;
 
 // The counts before the change.
 __device__ __forceinline__ void fork_counts(const ForkLaunch& p) {
@@ -645,8 +647,8 @@ __global__ void __launch_bounds__(kScanThreads) compact_moves_kernel(const Compa
   if (blockIdx.x == 0 && threadIdx.x == 0) *p.count = n.y;
   move_chunk(p, before, n.x, n.y, blockIdx.x);
 }
-// A pool of one chunk: one CTA, whose phases end by its own barrier (512 pages
-// 6.2 us, as a cluster 7.4).
+// A pool of one chunk: one CTA, whose phases end by its own barrier (64 pages 6.0
+// us, 512 6.2, 2048 7.9, 8192 15.3; as a cluster 6.8, 7.4, 8.8, 17.3).
 __global__ void __launch_bounds__(kScanThreads) compact_chunk_kernel(const CompactLaunch p) {
   __shared__ int before[kMostChunks];
   pdl_trigger();
@@ -656,6 +658,9 @@ __global__ void __launch_bounds__(kScanThreads) compact_chunk_kernel(const Compa
   if (threadIdx.x == 0) *p.count = n.y;
   move_chunk(p, before, n.x, n.y, 0);
 }
+// A pool of a few chunks, as a cluster: as long on the GPU as two launches (16384
+// pages 23.6 us, 65536 43.5 and 43.1), and 2 us less of the host at 16384 pages.
+constexpr long long kCompactSmall = 1 << 16;
 __global__ void __cluster_dims__(kCluster) __launch_bounds__(kScanThreads) compact_kernel(const CompactLaunch p) {
   __shared__ int before[kMostChunks];
   pdl_trigger();
@@ -710,7 +715,7 @@ cudaError_t launch_page_copy(const PageCopy& c, int num_sms, cudaStream_t stream
 
 cudaError_t launch_fork(const ForkLaunch& p, int num_sms, cudaStream_t stream) {
   if (p.children == 0 && p.t.requests == 0 && p.out_refs == p.refs) return cudaSuccess;
-  if ((p.t.requests + p.children) * p.t.width + p.num_blocks <= kSmallEntries)
+  if (p.t.width <= kForkNarrow && (p.t.requests + p.children) * p.t.width + p.num_blocks <= kForkSmall)
     return launch(fork_kernel, kCluster, kScanThreads, false, stream, p);
   const long long most = 16LL * num_sms;
   const long long copies = p.out_refs == p.refs ? 0 : std::min(most, (p.num_blocks + 4 * kForkThreads - 1) / (4 * kForkThreads));
@@ -730,7 +735,7 @@ cudaError_t launch_resize_apply(const PageCopy& c, const ResizeLaunch& p, bool r
 
 cudaError_t launch_compact(const CompactLaunch& p, cudaStream_t stream) {
   if (p.s.chunks == 1) return launch(compact_chunk_kernel, 1, kScanThreads, false, stream, p);
-  if (p.s.num_blocks <= kSmallEntries) return launch(compact_kernel, kCluster, kScanThreads, false, stream, p);
+  if (p.s.num_blocks <= kCompactSmall) return launch(compact_kernel, kCluster, kScanThreads, false, stream, p);
   const cudaError_t e = launch(compact_scan_kernel, p.s.chunks, kScanThreads, false, stream, p.s);
   return e == cudaSuccess ? launch(compact_moves_kernel, p.s.chunks, kScanThreads, true, stream, p) : e;
 }

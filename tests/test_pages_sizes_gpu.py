@@ -63,7 +63,7 @@ def test_resize_time_grows_with_the_requests_alone():
 
 
 @pytest.mark.parametrize("in_place", [False, True])
-@pytest.mark.parametrize("requests,children", [(3, 5000), (300, 320), (300, 321), (5000, 9000)])
+@pytest.mark.parametrize("requests,children", [(3, 5000), (300, 320), (300, 321), (5000, 9000), (200, 300)])
 def test_fork_of_many_children(requests, children, in_place):
     bs, width, blocks = 16, 5, 2 * requests + 50  # 64 children a column
     table, lens, refs = _state(requests, requests, blocks, bs, width, most=30)
@@ -81,6 +81,19 @@ def test_fork_of_many_children(requests, children, in_place):
     got = sai.fork_pages(_t(table), _t(lens), t_refs, _t(parents), block_size=bs, out_refs=t_refs if in_place else None)
     assert got[0].tolist() == [table[r] if r >= 0 else [-1] * width for r in parents]
     assert got[1].tolist() == [lens[r] if r >= 0 else 0 for r in parents] and got[2].tolist() == want
+    assert sai.device_status() == 0
+
+
+@pytest.mark.parametrize("blocks,width", [(6912, 20), (6913, 20), (2000, 64), (2000, 65)])
+def test_fork_in_a_cluster_and_in_two_launches(blocks, width):
+    """Up to 8192 entries, of the 64 rows among them, and 64 columns are one launch."""
+    table, lens, refs = _state(blocks, 30, blocks, 16, width)
+    rng = random.Random(blocks)
+    for _ in range(3):
+        parents = [rng.randrange(-1, 30) for _ in range(34)]
+        want = O.fork(table, lens, refs, parents, 16)
+        got = sai.fork_pages(_t(table), _t(lens), _t(refs), _t(parents), block_size=16)
+        assert [x.tolist() for x in got] == list(want)
     assert sai.device_status() == 0
 
 
