@@ -518,7 +518,9 @@ int sai_sparse_attention(const uint16_t* q, int64_t q_row_stride, int32_t q_head
  *              as does a prefix past the table's columns.
  * sai_sparse_attention_mod takes softcap alone (SAI_ERR_UNSUPPORTED otherwise:
  * slots have no positions). mod = NULL or all unset: the plain call. Workspaces
- * are those of the plain calls.
+ * are those of the plain calls; with prefix_lens that of window = 0, so that long
+ * prefixes are split over CTAs (that of the window itself is taken too, for rows
+ * split as the window alone would be).
  */
 typedef struct {
   float softcap;

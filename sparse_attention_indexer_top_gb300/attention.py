@@ -101,7 +101,7 @@ def append_kv(cache: KVCache, k: torch.Tensor, v: torch.Tensor, block_table: tor
 
 def paged_attention_workspace(rows: int, q_heads: int, cache: KVCache, *, max_seq_len: int, window: int = 0,
                               sinks: int = 0, packed: int = False) -> int:
-    """Workspace bytes of ``paged_attention`` for these sizes."""
+    """Workspace bytes of ``paged_attention`` for these sizes (with ``prefix_lens``: of ``window=0``)."""
     return int(load().sai_paged_attention_workspace(rows, q_heads, cache.heads, cache.dim, cache.dtype, max_seq_len,
                                                     window, sinks, int(packed)))
 

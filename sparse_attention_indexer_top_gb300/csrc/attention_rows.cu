@@ -4,7 +4,8 @@
 
 namespace sai {
 
-AttnPlan attn_rows_plan(long long rows, int q_heads, int heads, int dim, bool f8, long long max_keys, int num_sms) {
+AttnPlan attn_rows_plan(long long rows, int q_heads, int heads, int dim, bool f8, long long max_keys, int num_sms,
+                        bool even_out) {
   const int group = q_heads / heads;
   const long long units = rows * heads * (group <= 64 ? 1 : (group + 63) / 64);
   // Chunks of at least 128 keys until a wave of CTAs (three per SM) is full:
@@ -15,13 +16,13 @@ AttnPlan attn_rows_plan(long long rows, int q_heads, int heads, int dim, bool f8
   // 412 with four, 389 with sixteen.
   auto up = [](long long a, long long b) { return (a + b - 1) / b; };
   const long long wave = 3LL * num_sms;
-  const long long fill = std::min(up(wave, std::max(1LL, units)), up(max_keys, 128));
-  const long long even = std::min(up(8 * wave, std::max(1LL, units)), up(max_keys, 512));
+  const long long fill = std::min(even_out ? up(wave, std::max(1LL, units)) : wave / std::max(1LL, units), up(max_keys, 128));
+  const long long even = even_out ? std::min(up(8 * wave, std::max(1LL, units)), up(max_keys, 512)) : 1;
   const long long chunks = std::max(1LL, std::min(64LL, std::max(fill, even)));
   // a cluster only within the first wave: beyond it, waiting for as many free
   // places at once costs more than the second kernel (37 windowed rows: 67 us
   // clustered, 59 joined)
-  AttnPlan pl{static_cast<int>(chunks), 0, false, chunks > 1 && chunks <= 8 && units * chunks <= wave};
+  AttnPlan pl{static_cast<int>(chunks), 0, false, chunks > 1 && chunks <= 8 && units * chunks <= wave, 2 * units * chunks <= wave};
   // enough units for every team to have its own: no joining
   const int teams = group <= 16 ? 4 : group <= 32 ? 2 : 1;
   pl.own = chunks == 1 && units >= 4LL * num_sms * teams;

@@ -192,7 +192,9 @@ __device__ __forceinline__ RowKeys row_keys(const AttnLaunch& p, int row) {
 }
 
 // Keys of each chunk when a row's keys are split: even shares in 64-key steps.
-__device__ __forceinline__ int chunk_keys(int count, int chunks) {
+template <bool MOD>
+__device__ __forceinline__ int chunk_keys(const AttnLaunch& p, int count) {
+  const int chunks = MOD && count <= p.short_keys ? p.short_chunks : p.chunks;
   return ((count + chunks - 1) / chunks + 63) & ~63;
 }
 
@@ -289,7 +291,7 @@ __global__ void __launch_bounds__(kThreads) attn_rows_kernel(const AttnLaunch p)
   }
   int k_begin = 0, k_end = rk.count;
   if (p.chunks > 1) {
-    const int per = chunk_keys(rk.count, p.chunks);
+    const int per = chunk_keys<MOD>(p, rk.count);
     k_begin = min(rk.count, chunk * per);
     k_end = min(rk.count, k_begin + per);
     if (!p.clustered && k_begin >= k_end) return;  // the joining kernel knows which chunks there are
@@ -952,7 +954,7 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const AttnLaunch p) {
   const RowKeys rk = row_keys<MOD>(p, static_cast<int>(head / p.q_heads));
   int used = 0;
   if (rk.count > 0) {
-    const int per = chunk_keys(rk.count, p.chunks);
+    const int per = chunk_keys<MOD>(p, rk.count);
     used = (rk.count + per - 1) / per;
   }
   pdl_wait();

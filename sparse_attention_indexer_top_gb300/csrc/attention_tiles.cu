@@ -23,6 +23,11 @@ bool attn_tiles_pay(long long rows, int q_heads, int heads, int dim, bool f8, lo
   return 5 + mb / (f8 ? 5.5 : 9.0) > 1.25 * tile_us;
 }
 
+bool attn_tiles_fill(long long rows, int q_heads, int heads, int dim, int num_sms) {
+  const Work w = work_of(rows, q_heads / heads, heads, dim, 0, num_sms);
+  return static_cast<long long>(w.row_tiles) * heads >= w.shares;
+}
+
 size_t attn_tiles_workspace(long long rows, int q_heads, int heads, int dim, long long max_keys, int num_sms) {
   const int group = q_heads / heads;
   const Work w = work_of(rows, group, heads, dim, max_keys, num_sms);

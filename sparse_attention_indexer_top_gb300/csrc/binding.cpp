@@ -253,9 +253,12 @@ PyObject* paged_attention(PyObject* const* a) {
   const at::Tensor out = output(a[11], "out", {rows, q.heads, c.d->dim}, at::kBFloat16, c);
   at::Tensor lse;
   if (truth(a[12]) || a[13] != Py_None) lse = output(a[13], "out_lse", {rows, q.heads}, at::kFloat, c);
-  const Space w = workspace_of(a[14], a[14] == Py_None ? sai_paged_attention_workspace(rows, q.heads, c.d->heads, c.d->dim,
-                                                                                       c.d->dtype, most, window, sinks, packed)
-                                                       : 0, c);
+  // a prefix is seen whole, whatever the window
+  const size_t need_bytes =
+      a[14] == Py_None ? sai_paged_attention_workspace(rows, q.heads, c.d->heads, c.d->dim, c.d->dtype, most,
+                                                       a[18] == Py_None ? window : std::min(window, 0), sinks, packed)
+                       : 0;
+  const Space w = workspace_of(a[14], need_bytes, c);
   sai_score_mod mod{static_cast<float>(softcap_of(a[15])), nullptr, nullptr, nullptr};
   if (a[16] != Py_None) {
     const at::Tensor& t = need(a[16], "slopes", at::kFloat, 1, c.device);

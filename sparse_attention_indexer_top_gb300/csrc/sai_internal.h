@@ -189,6 +189,8 @@ struct AttnLaunch {
   const float* slopes;     // [q_heads] or null
   const int* row_starts;   // [rows] or null
   const int* prefix_lens;  // [rows] or null
+  // prefix_lens under a window: rows of up to so many keys (the window's) are split as without prefixes
+  int short_keys, short_chunks;
 };
 // Chunks per row of the row kernel, and its partial results' bytes.
 struct AttnPlan {
@@ -196,14 +198,18 @@ struct AttnPlan {
   size_t workspace_bytes;
   bool own;        // a unit for each team of warps instead of each CTA
   bool clustered;  // a unit's chunks are a cluster and need no workspace
+  bool idle;       // half of the GPU is
 };
-AttnPlan attn_rows_plan(long long rows, int q_heads, int heads, int dim, bool f8, long long max_keys, int num_sms);
+// `even_out`: long rows are cut past a full wave too, else within one.
+AttnPlan attn_rows_plan(long long rows, int q_heads, int heads, int dim, bool f8, long long max_keys, int num_sms,
+                        bool even_out = true);
 cudaError_t launch_attn_rows(const AttnLaunch& p, cudaStream_t stream);
 cudaError_t launch_attn_rows_mod(const AttnLaunch& p, cudaStream_t stream);
 // The tile kernel of packed rows: whether it takes a call, whether it beats the
 // row kernel on these sizes, its workspace, its launch.
 bool attn_tiles_apply(int group, float scale_log2);
 bool attn_tiles_pay(long long rows, int q_heads, int heads, int dim, bool f8, long long max_keys, int num_sms);
+bool attn_tiles_fill(long long rows, int q_heads, int heads, int dim, int num_sms);  // a unit for every CTA (pair)
 size_t attn_tiles_workspace(long long rows, int q_heads, int heads, int dim, long long max_keys, int num_sms);
 cudaError_t launch_attn_tiles(const AttnLaunch& p, long long max_keys, void* workspace, int num_sms,
                               cudaStream_t stream);

@@ -13,6 +13,7 @@ import sparse_attention_indexer_top_gb300 as sai
 from oracle import attention as A
 from test_attention_gpu import DEV, Case, _lens
 from test_attention_mod_gpu import _check, _slopes
+from timing import least_us
 
 pytestmark = pytest.mark.gpu
 
@@ -103,3 +104,33 @@ def test_large_and_small_scales_under_a_cap(dtype, packed, slopes, sm, cap):
         assert (np.abs(out[i].float().cpu().numpy() - ref) <= 2.0 ** -8 * np.abs(ref) + 2.0 ** -7 * mag).all(), i
         # distances' products 2^-22 of at most 150, exponentials and sums 2^-20
         assert np.abs(lse[i].cpu().numpy() - np.log(w.sum(1))).max() <= 2.0 ** -14, i
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("packed", [0, 1])
+def test_a_long_prefix_under_a_short_window_is_split(dtype, packed):
+    """The row sees the keys from its window's first one to the prefix's end, far more than the window."""
+    c = Case(44, [30000], dtype=dtype, bs=128, hkv=1)
+    q, q64 = c.queries(1, 8)
+    n, prefix = _lens([200]), _lens([30000])
+    kw = dict(max_seq_len=30000, row_to_batch=_lens([0]), packed=packed, prefix_lens=prefix)
+    out, lse = sai.paged_attention(q, c.cache, c.t_table, n, want_lse=True, window=128, **kw)
+    _check(c, q64, [(0, 200, A.span(200, 128, 0, 0, 30000))], out, lse, 128 ** -0.5)
+    whole = least_us(lambda: sai.paged_attention(q, c.cache, c.t_table, n, **kw))
+    windowed = least_us(lambda: sai.paged_attention(q, c.cache, c.t_table, n, window=128, **kw))
+    assert windowed < 2 * whole, (windowed, whole)
+
+
+def test_workspaces_of_a_long_prefix():
+    """The plain call's workspace for its window is enough; that without a window lets the row be split."""
+    c = Case(45, [5000], dtype="bf16", bs=128, hkv=1)
+    q, q64 = c.queries(2, 8)
+    n, prefix = _lens([100, 4000]), _lens([5000, 0])
+    cells = [(0, 100, A.span(100, 64, 0, 0, 5000)), (0, 4000, A.span(4000, 64))]
+    for window in (64, 0):
+        need = sai.paged_attention_workspace(2, 8, c.cache, max_seq_len=5000, window=window)
+        ws = torch.empty(max(need, 16), dtype=torch.uint8, device=DEV)
+        out, lse = sai.paged_attention(q, c.cache, c.t_table, n, max_seq_len=5000, row_to_batch=_lens([0, 0]), window=64,
+                                       want_lse=True, prefix_lens=prefix, workspace=ws)
+        _check(c, q64, cells, out, lse, 128 ** -0.5)
+    assert sai.device_status() == 0
