@@ -158,22 +158,44 @@ struct Shared {
   int nonfinite;
   int stop;       // a wait gave up: no further piece
   int segs;
-  int high, start_min, sinks_max;  // MOD, of all rows here: highest first key, lowest start, highest end of first tokens
+  int gap;  // with the piece at a multiple of 16 bytes plain e4m3 tiles take 803 us for 782
   Piece piece;             // at work on
   long long step, begin, end;  // dealt: next step, and the share
   int more;                // a piece follows
   int deal[kMaxDealt + 2];  // dealt: the row tiles' weights, summed up, and the number of shares
   int warp_starts[16];
   int row_n[kMaxRows<D>], row_b[kMaxRows<D>];
+  // of each run of rows of one request. MOD has more to keep in them, in tiles (pack_segment).
   int seg_start[kMaxRows<D> + 1], seg_most[kMaxRows<D>], seg_least[kMaxRows<D>], seg_low[kMaxRows<D>];
   float2 factors[F8 ? kSoftmaxWarps : 1][8];  // per softmax warp: what the tiles leave of the k and v scales of 16 keys
 };
+
+// MOD: what a segment keeps, three words of it: tiles of 128 keys, the counts in 8
+// bits each, 255 meaning as many as there are. Exact counts of a long document or
+// window would not fit shared memory; more tiles than needed are masked.
+struct Segment {
+  int low_tile;     // of the least first key
+  int high_tiles;   // tiles from there on that some row does not see the start of
+  int base_tile;    // of the first tokens that lie before low_tile, and of how many tiles
+  int first_tiles;
+  int least_tiles;  // last tiles that some row does not see the end of
+};
+__device__ __forceinline__ int count8(int n) { return max(0, min(n, 255)); }
+__device__ __forceinline__ void pack_segment(const Segment& g, int& start, int& least, int& low) {
+  low = g.low_tile << 8 | count8(g.high_tiles);
+  least = g.base_tile << 8 | count8(g.first_tiles);
+  start |= count8(g.least_tiles) << 16;
+}
+__device__ __forceinline__ Segment unpack_segment(int start, int least, int low) {
+  return Segment{static_cast<int>(static_cast<uint32_t>(low) >> 8), low & 255,
+                 static_cast<int>(static_cast<uint32_t>(least) >> 8), least & 255, start >> 16};
+}
 
 // One request's rows of the CTA (pair) and the tiles that the piece walks.
 template <int MOD>
 struct PassMore {
   int base_tile;  // of the first tokens
-  int high;       // highest first key of a window
+  int high;       // up to there, some row does not see a tile's start
   int last;       // index of the last tile
 };
 template <>
@@ -184,7 +206,7 @@ template <int MOD>
 struct Pass : PassMore<MOD> {
   int s, e;        // rows [s, e) of the pair
   int batch;
-  int most, least; // longest and shortest (above 0) row
+  int most, least; // longest and shortest (above 0) row (MOD: in whole tiles)
   int low;         // least first key of a row's window (0: no window)
   int first_tiles; // tiles that hold the first `sinks` tokens before the window's tiles
   int low_tile;
@@ -210,8 +232,9 @@ __device__ __forceinline__ Pass<MOD> get_pass(const Shared<D, F8>& S, const Tile
   const AttnLaunch& p = L.a;
   const Piece& pc = S.piece;
   Pass<MOD> r;
-  r.s = S.seg_start[seg];
-  r.e = S.seg_start[seg + 1];
+  constexpr int kStart = MOD ? 0xffff : -1;
+  r.s = S.seg_start[seg] & kStart;
+  r.e = S.seg_start[seg + 1] & kStart;
   r.batch = S.row_b[r.s];
   r.most = S.seg_most[seg];
   r.least = S.seg_least[seg];
@@ -222,16 +245,17 @@ __device__ __forceinline__ Pass<MOD> get_pass(const Shared<D, F8>& S, const Tile
   int tiles = 0;
   r.first_tiles = r.low_tile = 0;
   if constexpr (MOD != 0) {
-    r.base_tile = 0;
-    r.high = S.high;
-  }
-  if (r.most > 0) {
+    const Segment g = unpack_segment(S.seg_start[seg], r.least, r.low);
+    const int end = (r.most + kTile - 1) / kTile;
+    r.base_tile = g.base_tile;
+    r.low_tile = g.low_tile;
+    r.first_tiles = g.first_tiles < 255 ? g.first_tiles : g.low_tile - g.base_tile;
+    r.high = g.high_tiles < 255 ? (g.low_tile + g.high_tiles) * kTile : INT_MAX;
+    r.least = g.least_tiles < 255 ? (end - g.least_tiles) * kTile : 0;
+    tiles = r.first_tiles + end - r.low_tile;
+  } else if (r.most > 0) {
     r.low_tile = r.low / kTile;
-    if constexpr (MOD != 0) {
-      // first tokens of all the rows here, whatever their request: a tile too many is masked
-      r.base_tile = min(S.start_min / kTile, r.low_tile);
-      r.first_tiles = max(0, min((S.sinks_max + kTile - 1) / kTile, r.low_tile) - r.base_tile);
-    } else if (r.low > 0) r.first_tiles = min((min(p.sinks, r.low) + kTile - 1) / kTile, r.low_tile);
+    if (r.low > 0) r.first_tiles = min((min(p.sinks, r.low) + kTile - 1) / kTile, r.low_tile);
     tiles = r.first_tiles + (r.most + kTile - 1) / kTile - r.low_tile;
   }
   if constexpr (MOD != 0) r.last = tiles - 1;
@@ -1678,29 +1702,21 @@ __device__ __forceinline__ Piece next_piece(const Shared<D, F8>& S, const TilesL
 
 // The rows of the piece: lengths, and the runs of one request. Both CTAs of a
 // pair look at all its rows. Every thread calls it; ends with a barrier.
-template <int MOD, int D, bool F8>
+template <int D, bool F8>
 __device__ __forceinline__ void set_up_rows(Shared<D, F8>& S, const TilesLaunch& L) {
   const Piece& pc = S.piece;
   constexpr int kRows = kMaxRows<D>, kGroups = kRows / 32;
   const AttnLaunch& p = L.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rows_here = 2 * kPair<D> * L.rows_per_tile;
-  if (tid == 0) {
-    S.nonfinite = 0;
-    S.high = S.sinks_max = 0;
-    S.start_min = INT_MAX;
-  }
+  if (tid == 0) S.nonfinite = 0;
   for (int i = tid; i < kRows; i += kThreads) {
     int n = 0, b = -1;
     const int row = pc.row0 + i;
     if (i < rows_here && row < p.rows) {
       n = p.seq_lens[row];
       b = p.row_to_batch[row];
-      if (MOD) {
-        const RowSpan span = row_span(p, row, n);
-        n = span.good ? span.end : -1;
-      }
-      if (n < 0 || (!MOD && n > p.max_len) || b < 0 || b >= p.bt_rows ||
+      if (n < 0 || n > p.max_len || b < 0 || b >= p.bt_rows ||
           ((static_cast<long long>(n) - 1) >> p.c.bs_log2) >= p.bt_stride) {
         atomicOr(p.status, kDevBadRowMeta);
         n = 0;
@@ -1735,18 +1751,111 @@ __device__ __forceinline__ void set_up_rows(Shared<D, F8>& S, const TilesLaunch&
     if (i < rows_here && n > 0) {
       atomicMax(&S.seg_most[id], n);
       atomicMin(&S.seg_least[id], n);
-      if (MOD) {
-        const RowSpan span = row_span(p, pc.row0 + i, p.seq_lens[pc.row0 + i]);
-        atomicMin(&S.seg_low[id], span.first);
-        atomicMax(&S.high, span.first);
-        if (span.sinks_end > span.start) {
-          atomicMin(&S.start_min, span.start);
-          atomicMax(&S.sinks_max, span.sinks_end);
-        }
-      } else {
-        atomicMin(&S.seg_low[id], p.window > 0 ? max(0, n - p.window) : 0);
+      atomicMin(&S.seg_low[id], p.window > 0 ? max(0, n - p.window) : 0);
+    }
+  }
+  named_bar(kSetUpBar, kThreads);
+}
+
+// The same with documents and prefixes; a thread's rows' spans stay in registers
+// over the steps.
+template <int D, bool F8>
+__device__ __forceinline__ void set_up_spans(Shared<D, F8>& S, const TilesLaunch& L) {
+  const Piece& pc = S.piece;
+  constexpr int kRows = kMaxRows<D>, kGroups = kRows / 32;
+  const AttnLaunch& p = L.a;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rows_here = 2 * kPair<D> * L.rows_per_tile;
+  // bounds of the segments' keys, where rows leave later: least length, least and
+  // highest first key, least and highest first token before the former's tile
+  int(*bounds)[kRows] = reinterpret_cast<int(*)[kRows]>(S.stage);
+  static_assert(5 * kRows * sizeof(int) <= sizeof(S.stage), "bounds fit");
+  int *least = bounds[0], *low = bounds[1], *high = bounds[2], *first = bounds[3], *behind = bounds[4];
+  if (tid == 0) S.nonfinite = 0;
+  constexpr int kTurns = (kRows + kThreads - 1) / kThreads;
+  RowSpan spans[kTurns];  // of the rows tid + t * kThreads
+#pragma unroll
+  for (int t = 0; t < kTurns; ++t) {
+    const int i = tid + t * kThreads;
+    if (i >= kRows) break;
+    int n = 0, b = -1;
+    const int row = pc.row0 + i;
+    if (i < rows_here && row < p.rows) {
+      n = p.seq_lens[row];
+      b = p.row_to_batch[row];
+      spans[t] = row_span(p, row, n);
+      n = spans[t].good ? spans[t].end : -1;
+      if (n < 0 || b < 0 || b >= p.bt_rows ||
+          ((static_cast<long long>(n) - 1) >> p.c.bs_log2) >= p.bt_stride) {
+        atomicOr(p.status, kDevBadRowMeta);
+        n = 0;
+        b = -1;
       }
     }
+    S.row_n[i] = n;
+    S.row_b[i] = b;
+    S.seg_most[i] = 0;
+    least[i] = low[i] = first[i] = INT_MAX;
+    high[i] = behind[i] = 0;
+  }
+  named_bar(kSetUpBar, kThreads);
+  for (int w = warp; w < kGroups; w += kThreads / 32) {
+    const int i = 32 * w + lane;
+    const uint32_t starts = __ballot_sync(0xffffffffu, i < rows_here && (i == 0 || S.row_b[i - 1] != S.row_b[i]));
+    if (lane == 0) S.warp_starts[w] = __popc(starts);
+  }
+  named_bar(kSetUpBar, kThreads);
+  int ids[kTurns];  // segments of this thread's rows
+#pragma unroll
+  for (int t = 0; t < kTurns; ++t) {
+    const int w = warp + t * (kThreads / 32);
+    if (w >= kGroups) break;
+    const int i = 32 * w + lane;
+    const bool start = i < rows_here && (i == 0 || S.row_b[i - 1] != S.row_b[i]);
+    const uint32_t starts = __ballot_sync(0xffffffffu, start);
+    int id = -1;
+    for (int v = 0; v < w; ++v) id += S.warp_starts[v];
+    id += __popc(starts & ((2u << lane) - 1u));
+    ids[t] = id;
+    if (start) S.seg_start[id] = i;
+    if (i == rows_here - 1) {
+      S.segs = id + 1;
+      S.seg_start[id + 1] = rows_here;
+    }
+    const int n = S.row_n[i];
+    if (i < rows_here && n > 0) {
+      atomicMax(&S.seg_most[id], n);
+      atomicMin(&least[id], n);
+      atomicMin(&low[id], spans[t].first);
+      atomicMax(&high[id], spans[t].first);
+    }
+  }
+  named_bar(kSetUpBar, kThreads);
+  if (p.window > 0 && p.sinks > 0) {
+    // First tokens in the window's tiles, a later document's say, are walked anyway.
+#pragma unroll
+    for (int t = 0; t < kTurns; ++t) {
+      const int i = tid + t * kThreads;
+      if (i >= rows_here || S.row_n[i] <= 0) continue;
+      const RowSpan& span = spans[t];
+      if (span.sinks_end > span.start && span.start / kTile < low[ids[t]] / kTile) {
+        atomicMin(&first[ids[t]], span.start);
+        atomicMax(&behind[ids[t]], span.sinks_end);
+      }
+    }
+    named_bar(kSetUpBar, kThreads);
+  }
+  for (int g = tid; g < S.segs; g += kThreads) {
+    Segment sg{0, 0, 0, 0, 0};
+    const int most = S.seg_most[g];
+    if (most > 0) {
+      sg.low_tile = low[g] / kTile;
+      sg.high_tiles = (high[g] + kTile - 1) / kTile - sg.low_tile;
+      sg.base_tile = min(first[g] / kTile, sg.low_tile);
+      sg.first_tiles = min((behind[g] + kTile - 1) / kTile, sg.low_tile) - sg.base_tile;
+      sg.least_tiles = (most + kTile - 1) / kTile - least[g] / kTile;
+    }
+    pack_segment(sg, S.seg_start[g], S.seg_least[g], S.seg_low[g]);
   }
   named_bar(kSetUpBar, kThreads);
 }
@@ -1822,7 +1931,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto pieces = [&](auto role) {
     Progress at;
     while (S.more) {
-      set_up_rows<MOD>(S, L);
+      if constexpr (MOD != 0)
+        set_up_spans(S, L);
+      else
+        set_up_rows(S, L);
       const bool ok = role(at);
       ++at.pieces;
       if (!ok) {

@@ -107,6 +107,25 @@ def test_large_and_small_scales_under_a_cap(dtype, packed, slopes, sm, cap):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("rows", ["two requests", "two documents"])
+def test_first_tokens_of_one_document_cost_no_other(dtype, rows):
+    """Rows of a window with first tokens: tiles between one row's first tokens and another's are not walked."""
+    c = Case(43, [30000, 200], dtype=dtype, bs=128, hkv=1)
+    if rows == "two requests":  # a late document of one, a short other one
+        spans = [(0, n, 29000) for n in range(29985, 30001)] + [(1, n, 0) for n in range(185, 201)]
+    else:
+        spans = [(0, n, 0) for n in range(28985, 29001)] + [(0, n, 29000) for n in range(29140, 29156)]
+    b, n, start = (_lens(list(x)) for x in zip(*spans))
+    q, q64 = c.queries(len(spans), 8)
+    kw = dict(max_seq_len=30000, row_to_batch=b, packed=sai.PACKED_TILES, window=128, sinks=4)
+    out, lse = sai.paged_attention(q, c.cache, c.t_table, n, want_lse=True, row_starts=start, **kw)
+    _check(c, q64, [(b, n, A.span(n, 128, 4, s)) for b, n, s in spans], out, lse, 128 ** -0.5)
+    plain = least_us(lambda: sai.paged_attention(q, c.cache, c.t_table, n, **kw))
+    masked = least_us(lambda: sai.paged_attention(q, c.cache, c.t_table, n, row_starts=start, **kw))
+    assert masked < 3 * plain, (masked, plain)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
 @pytest.mark.parametrize("packed", [0, 1])
 def test_a_long_prefix_under_a_short_window_is_split(dtype, packed):
     """The row sees the keys from its window's first one to the prefix's end, far more than the window."""
@@ -133,4 +152,47 @@ def test_workspaces_of_a_long_prefix():
         out, lse = sai.paged_attention(q, c.cache, c.t_table, n, max_seq_len=5000, row_to_batch=_lens([0, 0]), window=64,
                                        want_lse=True, prefix_lens=prefix, workspace=ws)
         _check(c, q64, cells, out, lse, 128 ** -0.5)
+    assert sai.device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("mod", ["masks", "bias", "cap"])
+@pytest.mark.parametrize("dim,hkv,group", [(128, 1, 4), (64, 1, 4)])
+def test_each_change_alone_on_long_rows(dtype, mod, dim, hkv, group):
+    """Few rows, long enough that their tiles are dealt out and joined, for each instance of the tile kernel."""
+    total, rows = 9000, 6
+    c = Case(47, [total], dtype=dtype, bs=64, hkv=hkv, dim=dim)
+    q, q64 = c.queries(rows, group, sigma=3.0)
+    n = list(range(total - rows + 1, total + 1))
+    start, prefix = [0, 4000, 8990, 17, 9000, 1], [0, 0, 9000, 8999, 0, 0]
+    kw, plain = {}, dict(softcap=0.0, slopes=None)
+    if mod == "masks":
+        kw = dict(row_starts=_lens(start), prefix_lens=_lens(prefix))
+    else:
+        start = prefix = [0] * rows
+        kw = dict(slopes=0.01 * _slopes(group)) if mod == "bias" else dict(softcap=20.0)
+        plain.update(kw)
+    for w, s in ((0, 0), (3001, 200)):
+        out, lse = sai.paged_attention(q, c.cache, c.t_table, _lens(n), max_seq_len=total, row_to_batch=_lens([0] * rows),
+                                       packed=sai.PACKED_TILES, want_lse=True, window=w, sinks=s, **kw)
+        _check(c, q64, [(0, m, A.span(m, w, s, a, p)) for m, a, p in zip(n, start, prefix)], out, lse, dim ** -0.5, **plain)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("dim,hkv,group,bs", [(64, 2, 1, 16), (64, 1, 33, 128), (128, 1, 64, 64), (128, 2, 5, 16)])
+@pytest.mark.parametrize("window,sinks", [(130, 70), (3, 300)])
+def test_masks_with_windows_of_other_heads(dtype, dim, hkv, group, bs, window, sinks):
+    from test_attention_mod_gpu import _spans
+
+    totals = [700, 2, 333]
+    c = Case(48 + group, totals, dtype=dtype, bs=bs, hkv=hkv, dim=dim)
+    spans = _spans(window + group, totals, 40)
+    q, q64 = c.queries(len(spans), hkv * group)
+    b, n, start, prefix = (_lens(list(x)) for x in zip(*spans))
+    cells = [(b, n, A.span(n, window, sinks, s, p)) for b, n, s, p in spans]
+    for packed in (0, sai.PACKED_TILES):
+        for mod in (dict(), dict(softcap=10.0), dict(slopes=_slopes(hkv * group))):
+            out, lse = sai.paged_attention(q, c.cache, c.t_table, n, max_seq_len=700, row_to_batch=b, packed=packed,
+                                           window=window, sinks=sinks, want_lse=True, row_starts=start, prefix_lens=prefix, **mod)
+            _check(c, q64, cells, out, lse, dim ** -0.5, **mod)
     assert sai.device_status() == 0
