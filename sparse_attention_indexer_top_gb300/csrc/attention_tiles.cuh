@@ -953,20 +953,32 @@ __device__ __forceinline__ bool softmax_role(Shared<D, F8>& S, const TilesLaunch
     const Pass<MOD> ps = get_pass<MOD>(S, L, seg);
     if (!ps.act[x]) continue;
     Lane<MOD> ln;
+    float m = -INFINITY, l = 0.f;
     ln.row = pc.row0 + local;
     ln.live = in_tile && local >= ps.s && local < ps.e && ln.row < p.rows;
     ln.n = ln.live ? S.row_n[local] : 0;
     ln.first = p.window > 0 ? max(0, ln.n - p.window) : 0;
     ln.sinks = min(p.sinks, ln.first);
     // the row's head, and its place among the partial results (-1: final). MOD: known
-    // at the end alone, the loop has no registers to keep them in.
+    // at the end alone, the loop has no registers to keep them in. Until then a row that
+    // sees nothing, padding say, is not live: it would have no maximum to keep, and send
+    // all its unit's tiles the longer way (2048 rows on 32768 keys, every 50th of
+    // them padding, softcap 50: 1535 us for 761).
     long long part = -1;
     auto place = [&]() {
+      if (MOD) {
+        ln.live = in_tile && local >= ps.s && local < ps.e && ln.row < p.rows;
+        if (ln.n == 0) {
+          m = -INFINITY;
+          l = 0.f;
+        }
+      }
       ln.head = static_cast<long long>(ln.row) * p.q_heads + pc.kvh * p.group + r % p.group;
       part = pc.slot < 0 ? -1 : (static_cast<long long>(pc.slot) * 2 * PAIR * L.rows_per_tile + local) * p.group + r % p.group;
     };
     if (!MOD) place();
     if constexpr (MOD != 0) {
+      ln.live = ln.n > 0;
       ln.start = ln.pos = 0;
       ln.slope = 0.f;
       if (ln.n > 0) {
@@ -979,7 +991,6 @@ __device__ __forceinline__ bool softmax_role(Shared<D, F8>& S, const TilesLaunch
         if (MOD & kBias) ln.slope = p.slopes[pc.kvh * p.group + r % p.group] * 1.44269504088896340736f;
       }
     }
-    float m = -INFINITY, l = 0.f;
     if (ps.i0 == ps.i1) {
       if (MOD) place();
       const float o[32] = {};
@@ -1791,6 +1802,7 @@ __device__ __forceinline__ void set_up_spans(Shared<D, F8>& S, const TilesLaunch
         n = 0;
         b = -1;
       }
+      if (spans[t].start == spans[t].end) n = 0;  // sees nothing
     }
     S.row_n[i] = n;
     S.row_b[i] = b;

@@ -156,6 +156,36 @@ def test_workspaces_of_a_long_prefix():
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("mod", ["cap", "bias", "both"])
+@pytest.mark.parametrize("empty", ["lengths", "starts"])
+def test_rows_that_see_nothing_slow_no_others(dtype, mod, empty):
+    """Padding, or documents that start behind their rows, among packed rows with changed scores: NaN queries too."""
+    total, rows = 32768, 1024
+    c = Case(46, [total], dtype=dtype, bs=128, hkv=1)
+    q, q64 = c.queries(rows, 8)
+    none = [i for i in range(rows) if i % 50 == 3]
+    full = list(range(total - rows + 1, total + 1))
+    lens = [0 if i in none and empty == "lengths" else n for i, n in enumerate(full)]
+    kw = dict(max_seq_len=total, row_to_batch=_lens([0] * rows), packed=sai.PACKED_TILES, softcap=0.0 if mod == "bias" else 50.0,
+              slopes=None if mod == "cap" else 0.01 * _slopes(8))
+    starts = _lens([0] * rows)
+    n = _lens(full)
+    whole = least_us(lambda: sai.paged_attention(q, c.cache, c.t_table, n, row_starts=starts, **kw))
+    if empty == "starts":
+        starts[none] = total
+    n = _lens(lens)
+    holes = least_us(lambda: sai.paged_attention(q, c.cache, c.t_table, n, row_starts=starts, **kw))
+    assert holes < 1.25 * whole, (holes, whole)
+    q[none[0]] = float("nan")
+    q[none[1]] = float("inf")
+    out, lse = sai.paged_attention(q, c.cache, c.t_table, n, want_lse=True, row_starts=starts, **kw)
+    few = [0, 2, 4, 200, rows - 1]
+    _check(c, q64[few], [(0, full[i], A.span(full[i])) for i in few], out[few], lse[few], 128 ** -0.5, softcap=kw["softcap"],
+           slopes=kw["slopes"])
+    assert (out[none] == 0).all() and (lse[none] == -float("inf")).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
 @pytest.mark.parametrize("mod", ["masks", "bias", "cap"])
 @pytest.mark.parametrize("dim,hkv,group", [(128, 1, 4), (64, 1, 4)])
 def test_each_change_alone_on_long_rows(dtype, mod, dim, hkv, group):
