@@ -557,10 +557,10 @@ int sai_sparse_attention_mod(const uint16_t* q, int64_t q_row_stride, int32_t q_
  * rows of row_bytes contiguous bytes, stride[] apart, at base + p * page_stride
  * (all in bytes, multiples of 4). cells names the axis (0 or 1) that counts the
  * page's tokens, so that a partly filled page may be copied in part; -1: it is
- * copied whole. A page has fewer than 2^24 units of 16 bytes (of 4 where an
- * address, stride or row is no multiple of 16). sai_cache_page_arrays writes the arrays of a cache (k, v, and
- * for e4m3 k_scale, v_scale) to out[4] and returns how many they are, or an
- * error below 0. Pages of one array must not overlap.
+ * copied whole. A page has at most 2^24 - 1024 units of 16 bytes (of 4 where
+ * an address, stride or row is no multiple of 16). sai_cache_page_arrays writes
+ * the arrays of a cache (k, v, and for e4m3 k_scale, v_scale) to out[4] and
+ * returns how many they are, or an error below 0. Pages of one array must not overlap.
  */
 typedef struct {
   void* base;

@@ -22,6 +22,8 @@ import torch
 from ._lib import PageArrayDesc, binding, check, load
 from .attention import KVCache, _on
 
+PAGE_UNITS = 2 ** 24 - 1024  # of a page of one array
+
 
 class PageSet:
     """The arrays whose blocks are the pages of one pool.
@@ -29,9 +31,10 @@ class PageSet:
     ``caches`` are the layers' ``KVCache`` objects (keys, values and their
     scales). ``arrays`` are any other CUDA tensors ``[num_blocks, ...]`` of the
     same pool, such as the indexer's keys and their scales: each page contiguous
-    and of a multiple of 4 bytes (below 256 MB), pages any distance apart. ``block_size`` is
-    that of the caches, or is given where there are none. The object keeps the
-    tensors.
+    and of a multiple of 4 bytes, pages any distance apart; of at most 2^24 - 1024
+    units of 16 bytes, or of 4 where an address, distance or size is no multiple of
+    16 (256 or 64 MB). ``block_size`` is that of the caches, or is given where there
+    are none. The object keeps the tensors.
     """
 
     def __init__(self, caches: Sequence[KVCache] = (), arrays: Sequence[torch.Tensor] = (), *,
@@ -45,10 +48,14 @@ class PageSet:
                 raise ValueError(f"arrays[{i}] must be [num_blocks, ...]")
             if not t[0].is_contiguous():
                 raise ValueError(f"arrays[{i}] needs contiguous pages")
-            if t[0].nbytes % 4 or t[0].nbytes > 2 ** 28 - 2 ** 16:
-                raise ValueError(f"arrays[{i}] needs pages of a multiple of 4 bytes, below 2^28 - 2^16")
+            if t[0].nbytes % 4:
+                raise ValueError(f"arrays[{i}] needs pages of a multiple of 4 bytes")
             if t.shape[0] > 1 and t.stride(0) < t[0].numel():
                 raise ValueError(f"arrays[{i}] needs pages that do not overlap")
+            step = t.stride(0) * t.element_size() if t.shape[0] > 1 else 0
+            unit = 4 if (t.data_ptr() | step | t[0].nbytes) % 16 else 16
+            if t[0].nbytes > unit * PAGE_UNITS:
+                raise ValueError(f"arrays[{i}] needs pages of {unit * PAGE_UNITS} bytes at most, got {t[0].nbytes}")
             every.append((f"arrays[{i}]", t.device, t.shape[0]))
         if not every:
             raise ValueError("a pool needs at least one cache or array")

@@ -118,3 +118,16 @@ def test_fork_time_grows_with_the_requests_alone():
 
     small, large = us(65536), us(524288)
     assert large < 20 * small, (small, large)  # eight times the requests
+
+
+def test_page_sizes_are_refused_by_their_units():
+    """Pages of 2^24 - 1024 units at most, of 16 bytes, or of 4 where something is no multiple of 16."""
+    wide, narrow = 16 * (2 ** 24 - 1024), 4 * (2 ** 24 - 1024)
+    raw = torch.zeros(wide + 64, dtype=torch.uint8, device=DEV)
+    sai.PageSet(arrays=[raw[:wide][None]], block_size=1)
+    sai.PageSet(arrays=[raw[4:4 + narrow][None]], block_size=1)
+    sai.PageSet(arrays=[raw[:narrow][None]], block_size=1)
+    for x in (raw[:wide + 16][None], raw[4:8 + narrow][None], raw[:narrow + 4][None], raw[4:4 + wide][None],
+              torch.as_strided(raw, (2, narrow + 16), (narrow + 20, 1))):
+        with pytest.raises(ValueError, match="bytes at most"):
+            sai.PageSet(arrays=[x], block_size=1)
