@@ -3,9 +3,10 @@
 //
 // tanh is odd: for |t| <= 1 it is t Q(t^2) with a polynomial Q, the minimax
 // approximation (Remez exchange) of tanh(sqrt y) / sqrt y on [0, 1], relative
-// error 5e-8; beyond, 1 - 2 / (1 + e^(2|t|)), whose terms are then of like size.
-// A score is off by a few 2^-24 of itself, as one rounding of it. The hardware's
-// one-instruction tanh is off by 2^-11 of the cap: half a percent of a weight.
+// error 7e-8; beyond, 1 - 2 / (1 + e^(2|t|)), whose terms are then of like size.
+// A capped score is off by 2^-20 of itself at most, 2^-22 of the cap beyond it, most of
+// it the coefficients left out below 1/2 (tanh_near). The hardware's one-instruction
+// tanh is off by 2^-11 of the cap: half a percent of a weight.
 #pragma once
 #include <cstdint>
 
@@ -39,9 +40,9 @@ __host__ __device__ constexpr float tanh_q(int i) {
 }
 
 // The same with four coefficients for |t| <= 1/2, where most scores lie
-// (relative error 5.5e-7), and with three for |t| <= 1/4 (4.0e-7): a score is
-// moved by 2^-20.8 of itself, which is below what an fp32 sum of 64 or 128
-// products may be off by.
+// (relative error 5.6e-7, 9.3 2^-24), and with three for |t| <= 1/4 (4.2e-7, 7.1
+// 2^-24): a score is moved by 2^-20.7 of itself, which is below what an fp32 sum of
+// 64 or 128 products may be off by (2^-17, 2^-16 of the sum of their sizes).
 constexpr float kNear = 0.5f, kNearest = 0.25f;
 __host__ __device__ constexpr float tanh_near(int i) {
   constexpr float q[4] = {0.9999994558f, -0.3332631794f, 0.1319029659f, -0.04440222584f};

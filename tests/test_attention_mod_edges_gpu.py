@@ -107,6 +107,41 @@ def test_large_and_small_scales_under_a_cap(dtype, packed, slopes, sm, cap):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("packed", [0, sai.PACKED_TILES])
+@pytest.mark.parametrize("near", [0.01, 0.2, 0.25, 0.5, 1.0, 2.0, 9.0])
+def test_the_cap_alone(dtype, packed, near):
+    """256 equal keys with exact products, so that the log-sum-exp is the capped score plus log 256, on both sides of where
+    the polynomials change.
+
+    The score may be off by 2^-20 of itself (of the cap, 2^-22, beyond it). The rest is the way through log2 units: scale,
+    cap, its inverse, the product, the sum with the logarithm and ln 2 are a rounding each, of at most the log-sum-exp and
+    log 256, doubled: 16 * 2^-24."""
+    n, cap = 256, 30.0
+    c = Case(42, [n], dtype=dtype, bs=128, hkv=1, dim=64)
+    blocks = [int(x) for x in c.table[0]]
+    one = torch.zeros(64)
+    one[:2] = 1.0
+    c.k[blocks] = one.to(c.k.dtype).to(DEV)
+    if dtype == "e4m3":
+        c.ks[blocks] = 1.0
+    at = [near * cap * f for f in (0.97, 0.996, 1.0, 1.004, 1.03)]
+    q = torch.zeros((len(at) * 2, 1, 64))
+    for i, x in enumerate(at):
+        hi = torch.tensor(x).bfloat16().float()
+        q[2 * i, 0, 0], q[2 * i, 0, 1] = hi, torch.tensor(x - float(hi)).bfloat16().float()
+        q[2 * i + 1] = -q[2 * i]
+    q = q.to(torch.bfloat16).to(DEV)
+    x = q.double().sum(-1).cpu().numpy()[:, 0]
+    rows = len(x)
+    _, lse = sai.paged_attention(q, c.cache, c.t_table, _lens([n] * rows), max_seq_len=n, row_to_batch=_lens([0] * rows),
+                                 packed=packed, want_lse=True, softcap=cap, sm_scale=1.0)
+    ref = cap * np.tanh(x / cap) + np.log(n)
+    tol = np.where(np.abs(x) <= cap, 2.0 ** -20 * np.abs(x), 2.0 ** -22 * cap) + 2.0 ** -20 * (np.abs(ref) + 2 * np.log(n))
+    err = np.abs(lse.cpu().double().numpy()[:, 0] - ref)
+    assert (err <= tol).all(), (err / tol).max()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
 @pytest.mark.parametrize("rows", ["two requests", "two documents"])
 def test_first_tokens_of_one_document_cost_no_other(dtype, rows):
     """Rows of a window with first tokens: tiles between one row's first tokens and another's are not walked."""
