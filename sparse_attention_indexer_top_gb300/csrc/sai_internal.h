@@ -189,8 +189,8 @@ struct AttnLaunch {
   const float* slopes;     // [q_heads] or null
   const int* row_starts;   // [rows] or null
   const int* prefix_lens;  // [rows] or null
-  // prefix_lens under a window: rows of up to so many keys (the window's) are split as without prefixes
-  int short_keys, short_chunks;
+  // prefix_lens under a window: rows of up to so many keys (the window's) are split as without prefixes (-1: none)
+  int short_keys = -1, short_chunks = 1;
 };
 // Chunks per row of the row kernel, and its partial results' bytes.
 struct AttnPlan {
