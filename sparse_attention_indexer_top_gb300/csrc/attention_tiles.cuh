@@ -54,10 +54,12 @@
 // MOD: rows see a document or a prefix of their request (kMasks), and scores are
 // capped (kCap) and biased by distance (kBias) before the softmax
 // (attention_mod.cuh). These instances are apart, in attention_tiles_mod.cu and
-// attention_tiles_cap.cu. Bound: the softmax warps, whose two-element FMAs a pair
-// of scores go from 2 to 3 (bias), 6 (cap below a quarter) or 7. 2048 rows on
-// 32768 keys, 32 / 4 heads, bf16 (e4m3), us: plain 628 (787), masks 646 (859), bias
-// 655 (856), cap 750 (922), both 834 (1083).
+// attention_tiles_cap.cu. Bound: the softmax warps, whose two-element operations a
+// pair of scores go from 2 to 4 (bias), 5 (cap, scores below a quarter of it; e4m3 6), 6
+// (below half; 7) or, with both, 2 more; scores above go the longer way (rough_tile). 2048
+// rows on 32768 keys, 32 / 4 heads, bf16 (e4m3), us: plain 623 (783), masks 647 (813),
+// bias 672 (818), cap 760 (884), 862 (946), 1541 (1801) with scores below a quarter, below
+// half, above half of it, both 820 (1042).
 #pragma once
 #include <cuda.h>
 #include <cuda_fp16.h>
@@ -771,7 +773,10 @@ __device__ __forceinline__ void change32(uint32_t* s, int c0, float mul, const C
 }
 
 // Weights 2^(changed score + off) of 32 columns from column c0, two to a word in
-// s[0..16), and what they add up to: change and exponent in one go. The bias is
+// s[0..16), and what they add up to: change and exponent in one go. One 16-bit term
+// each, off by 2^-8 (f16 2^-11) as in the plain kernel, which leaves bf16 results off by
+// 0.0023 for 0.0017 with exact weights (2048 rows on 32768 keys): the second term that
+// the row kernel takes would be half as many products again here. The bias is
 // linear in the column, slope * column and part of `off`; MASKED: columns without
 // their bit in `see` get 0.
 template <bool F8, int MOD, int Q, bool MASKED>
