@@ -172,9 +172,9 @@ struct Shared {
   float2 factors[F8 ? kSoftmaxWarps : 1][8];  // per softmax warp: what the tiles leave of the k and v scales of 16 keys
 };
 
-// MOD: what a segment keeps, three words of it: tiles of 128 keys, the counts in 8
-// bits each, 255 meaning as many as there are. Exact counts of a long document or
-// window would not fit shared memory; more tiles than needed are masked.
+// MOD: what a segment's three words hold: tiles of 128 keys, and counts of them in 8
+// bits each, 255 meaning as many as there are (shared memory has no room for whole
+// words; a tile more than needed is masked).
 struct Segment {
   int low_tile;     // of the least first key
   int high_tiles;   // tiles from there on that some row does not see the start of
